@@ -70,8 +70,9 @@ typedef enum {
     KDA_ERR_TIMEOUT = 4,          /* a bounded on-device wait gave up (device status only) */
     KDA_ERR_BAD_SEQLENS = 5,      /* cu_seqlens not 0 = c_0 <= c_1 <= ... <= c_N = T_tot (device status) */
     KDA_ERR_WORKSPACE = 6,        /* workspace missing or smaller than kda_prefill_workspace_bytes */
-    KDA_ERR_BAD_SNAPSHOT = 7      /* a snapshot request off its sequence, off a chunk boundary, or
+    KDA_ERR_BAD_SNAPSHOT = 7,     /* a snapshot request off its sequence, off a chunk boundary, or
                                      repeated (device status, kda_prefill_snapshots) */
+    KDA_ERR_BAD_PAGE = 8          /* a page number outside the cache (device status, kda_latent_decode) */
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -286,6 +287,153 @@ KDA_API int kda_prefill_noalloc(const kda_desc *desc,
  * 256 bytes); returns KDA_ERR_INVALID_ARGUMENT for a limit outside the range.
  */
 KDA_API int kda_selftest_wait_timeout(const kda_desc *desc, int64_t timeout_ns, kda_stream_t stream);
+
+/* ===========================================================================
+ * Operators around the recurrent layers: the norm and the 8-bit products of
+ * their projections, and the attention over shared latents of the layers of
+ * full attention that a KDA stack alternates with (deep dive, section 04).
+ *
+ * They keep the conventions above (device pointers, caller-owned memory, no
+ * allocation, no synchronisation, synchronous return codes) with these
+ * differences: rows may be strided where a desc has a stride for them (in
+ * elements, the last dimension always dense), and pointers need the alignment
+ * of their element only (wider alignment selects wider accesses).
+ * ======================================================================== */
+
+/* Root-mean-square norm of rows, with the residual's addition before it and
+ * an 8-bit output behind it:
+ *
+ *     h = x + residual                       (x alone when residual is NULL)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *     scales[b] = max(max |y| over block b, 1e-12) / 448
+ *     quantized = e4m3(y / scales[b])        (to nearest even, saturating)
+ *
+ * with blocks of 128 consecutive elements of a row, the last one short where
+ * dim is no multiple of 128.  h, the mean and y are fp32; the mean is taken of
+ * the unrounded h.  A row that holds an infinity or a NaN has unspecified
+ * values of y, scales and quantized; other rows are not affected. */
+typedef struct kda_norm_desc {
+    int64_t rows;            /* >= 0 */
+    int32_t dim;             /* elements of a row, >= 1 */
+    int32_t dtype;           /* kda_dtype of x, weight, residual, residual_out, normed */
+    int64_t x_stride;        /* elements between rows of x, >= dim */
+    int64_t residual_stride; /* elements between rows of residual, >= dim */
+    float eps;               /* >= 0 */
+} kda_norm_desc;
+
+/* weight [dim] or NULL (ones); residual [rows, dim] or NULL.  Written, each
+ * unless NULL, dense: residual_out = h in dtype, normed = y in dtype,
+ * quantized (e4m3 bytes) with scales fp32 [rows, ceil(dim / 128)] (both or
+ * neither).  residual_out may be x or residual itself if that is dense; no
+ * other output may overlap an input or another output. */
+KDA_API int kda_rms_norm(const kda_norm_desc *desc, const void *x, const void *weight, const void *residual,
+                         void *residual_out, void *normed, uint8_t *quantized, float *scales,
+                         kda_stream_t stream);
+
+/* Product of e4m3 matrices with scales:
+ *
+ *     c[m, n] = sum over k of a[m, k] a_scale[m, k / 128] b[n, k] b_scale[n / 128, k / 128]
+ *
+ * Products of one k block are summed in fp32 by the tensor cores and scaled and
+ * added in fp32 after that. */
+typedef struct kda_matmul_desc {
+    int64_t m;               /* rows of a and c, >= 0 */
+    int32_t n, k;            /* rows of b; length of the sum; n >= 0, k >= 1 */
+    int64_t a_stride;        /* elements between rows of a, >= k */
+    int64_t b_stride;        /* elements between rows of b, >= k */
+    int64_t c_stride;        /* elements between rows of c, >= n */
+    int32_t dtype;           /* kda_dtype of c */
+    int32_t flags;           /* 0 or KDA_FLAG_CUDA_CORE_PREFILL (fp32 CUDA cores, for cross-checking) */
+} kda_matmul_desc;
+
+/* a [m, k], b [n, k] e4m3 bytes; a_scale fp32 [m, ceil(k / 128)], b_scale fp32
+ * [ceil(n / 128), ceil(k / 128)], both dense; c [m, n] written, overlapping no
+ * input.  a and b with 16-byte aligned rows (address and stride) run on the
+ * tensor cores, others on CUDA cores. */
+KDA_API int kda_matmul_fp8(const kda_matmul_desc *desc, const uint8_t *a, const float *a_scale, const uint8_t *b,
+                           const float *b_scale, void *c, kda_stream_t stream);
+
+/* kda_latent_desc.flags bits, beside KDA_FLAG_CUDA_CORE_PREFILL. */
+enum {
+    /* kda_latent_prefill: every key of its sequence is visible to a query. */
+    KDA_FLAG_NO_CAUSAL = 4
+};
+
+/* Attention whose keys and values come from one latent vector c_s and one
+ * rotary key r_s a token, both shared by all heads.  Expanded form (prompts):
+ * keys [k_s,h | r_s] and values v_s,h, the up-projections of c_s, are given.
+ * Absorbed form (decoding): the up-projections are folded into the queries and
+ * the output, keys are [c_s | r_s] and values c_s.  bf16 with the sizes (d_k,
+ * d_rope, d_v) = (128, 64, 128) expanded and rank 512, d_rope 64 absorbed runs
+ * on the tensor cores; fp32, KDA_FLAG_CUDA_CORE_PREFILL, other sizes up to the
+ * limits below, and strides or addresses that are no multiple of 16 bytes run
+ * on CUDA cores in fp32. */
+typedef struct kda_latent_desc {
+    int32_t num_seqs;        /* N >= 0 */
+    int32_t num_heads;       /* H >= 1 */
+    int32_t dtype;           /* kda_dtype of everything but lse */
+    int32_t flags;
+    float scale;             /* factor of the scores before the softmax, finite and > 0 */
+    int32_t d_k;             /* expanded: per-head key channels; absorbed: rank of the latent */
+    int32_t d_rope;          /* shared rotary key channels, >= 0; d_k + d_rope <= 256 / 640 */
+    int32_t d_v;             /* expanded: value channels <= 256; absorbed: must equal d_k <= 512 */
+    /* expanded form */
+    int64_t total_q, total_k;                /* cu_seqlens_q[N], cu_seqlens_k[N] */
+    int64_t q_token_stride, q_head_stride;   /* both forms (absorbed: a token is one (sequence, query)) */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride, rope_token_stride;
+    /* absorbed form */
+    int32_t num_queries;     /* queries a sequence, >= 1 */
+    int32_t page_size;       /* tokens of a page, >= 1 */
+    int32_t num_pages;       /* pages of the cache */
+    int32_t max_pages;       /* row length of the page table, >= 1 */
+    int64_t page_stride;     /* elements between pages; tokens of a page are dense, d_k + d_rope apart */
+    void *workspace;         /* 256-byte aligned device scratch */
+    size_t workspace_bytes;
+} kda_latent_desc;
+
+/* Bytes of device workspace for each form (0 for an invalid desc).  They do not
+ * depend on the contents of any device array. */
+KDA_API size_t kda_latent_prefill_workspace_bytes(const kda_latent_desc *desc);
+KDA_API size_t kda_latent_decode_workspace_bytes(const kda_latent_desc *desc);
+
+/* Expanded form over a packed batch: query i of a sequence with Lq queries and
+ * Lk keys sees keys 0 .. Lk - Lq + i (all with KDA_FLAG_NO_CAUSAL).
+ *
+ *   q        [total_q, H, d_k + d_rope]     k_nope [total_k, H, d_k]
+ *   k_rope   [total_k, d_rope] (NULL iff d_rope = 0)    v [total_k, H, d_v]
+ *   cu_seqlens_q, cu_seqlens_k  int32 [N+1], device; NULL for one sequence.
+ *   out      [total_q, H, d_v] dense, written; lse fp32 [total_q, H] or NULL:
+ *            log of the sum of exp(score).  A query that sees no key gets a zero
+ *            row and lse = -infinity.
+ *
+ * A malformed cu_seqlens is recorded as KDA_ERR_BAD_SEQLENS in the device
+ * status word (kda_latent_status); out is then unspecified. */
+KDA_API int kda_latent_prefill(const kda_latent_desc *desc, const void *q, const void *k_nope, const void *k_rope,
+                               const void *v, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, void *out,
+                               float *lse, kda_stream_t stream);
+
+/* Absorbed form for the last num_queries (Lq) tokens of each sequence over a
+ * paged cache: query i of a sequence of length L sees cached tokens 0 ..
+ * L - Lq + i.
+ *
+ *   q          [N, Lq, H, d_k + d_rope]
+ *   cache      [num_pages, page_size, d_k + d_rope]
+ *   page_table int32 [N, max_pages], device: token t of sequence n is row
+ *              t % page_size of page page_table[n, t / page_size]; entries
+ *              behind a sequence's length are not read
+ *   lengths    int32 [N], device, 0 <= lengths[n] <= max_pages * page_size
+ *   out        [N, Lq, H, d_k] dense, written; lse fp32 [N, Lq, H] or NULL, as above
+ *
+ * A page number outside the cache (KDA_ERR_BAD_PAGE) or a length outside its
+ * range (KDA_ERR_BAD_SEQLENS) is recorded in the device status word and never
+ * dereferenced; the outputs of that sequence are then unspecified. */
+KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const void *cache,
+                              const int32_t *page_table, const int32_t *lengths, void *out, float *lse,
+                              kda_stream_t stream);
+
+/* Synchronises `stream`, then returns the status word that the last
+ * kda_latent_* call on this workspace recorded. */
+KDA_API int kda_latent_status(const kda_latent_desc *desc, kda_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 KDA_API const char *kda_status_string(int status);

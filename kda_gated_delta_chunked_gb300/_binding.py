@@ -12,6 +12,7 @@ _LIB_PATH = os.environ.get("KDA_LIBRARY", os.path.join(_HERE, "_build", "libkda.
 
 KDA_OK, KDA_ERR_INVALID_ARGUMENT, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA = 0, 1, 2, 3
 KDA_ERR_TIMEOUT, KDA_ERR_BAD_SEQLENS, KDA_ERR_WORKSPACE, KDA_ERR_BAD_SNAPSHOT = 4, 5, 6, 7
+KDA_ERR_BAD_PAGE = 8
 KDA_F32, KDA_BF16 = 0, 1
 KDA_FLAG_CUDA_CORE_PREFILL = 1
 KDA_FLAG_SCALAR_GATE = 2
@@ -19,7 +20,8 @@ KDA_FLAG_SCALAR_GATE = 2
 EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step", "kda_get_device_status",
            "kda_status_string", "kda_last_cuda_error", "kda_version", "kda_prefill_noalloc",
            "kda_selftest_wait_timeout", "kda_prefill_snapshots", "kda_backward_workspace_bytes",
-           "kda_prefill_backward")
+           "kda_prefill_backward", "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes",
+           "kda_latent_decode_workspace_bytes", "kda_latent_prefill", "kda_latent_decode", "kda_latent_status")
 KDA_PREFILL_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 

@@ -10,7 +10,7 @@ namespace kda {
 
 static thread_local int g_last_cuda_error = 0;
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
     g_last_cuda_error = (int)e;
     return KDA_ERR_CUDA;
 }
@@ -187,6 +187,7 @@ const char* kda_status_string(int s) {
         case KDA_ERR_BAD_SEQLENS: return "KDA_ERR_BAD_SEQLENS";
         case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE";
         case KDA_ERR_BAD_SNAPSHOT: return "KDA_ERR_BAD_SNAPSHOT";
+        case KDA_ERR_BAD_PAGE: return "KDA_ERR_BAD_PAGE";
         default: return "KDA_ERR_UNKNOWN";
     }
 }

@@ -39,6 +39,10 @@ __device__ __forceinline__ void record_status(DeviceHeader* hdr, int code) {
     atomicCAS(&hdr->status, (int)KDA_OK, code);
 }
 
+__device__ __forceinline__ void record_status(int32_t* status, int code) {
+    atomicCAS(status, (int)KDA_OK, code);
+}
+
 // Index of the sequence that owns global chunk `c`, given the exclusive prefix
 // of chunk counts chunk_first[0..N] (chunk_first[N] = total chunks).
 __device__ __forceinline__ int chunk_owner(const int32_t* chunk_first, int N, int c) {
@@ -48,6 +52,20 @@ __device__ __forceinline__ int chunk_owner(const int32_t* chunk_first, int N, in
         if (chunk_first[mid] <= c) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Run by all threads of one block: records KDA_ERR_BAD_SEQLENS unless both
+// arrays (nullptr: one sequence, nothing to check) run 0 = c_0 <= ... <= c_N = total.
+__device__ __forceinline__ void check_cu_seqlens(const int32_t* cu_q, const int32_t* cu_k, int N, int64_t tq,
+                                                 int64_t tk, int32_t* status) {
+    if (!cu_q) return;
+    bool bad = false;
+    for (int n = threadIdx.x; n <= N; n += blockDim.x) {
+        if (n == 0) bad |= cu_q[0] != 0 || cu_k[0] != 0;
+        else bad |= cu_q[n] < cu_q[n - 1] || cu_k[n] < cu_k[n - 1];
+        if (n == N) bad |= cu_q[N] != tq || cu_k[N] != tk;
+    }
+    if (bad) record_status(status, KDA_ERR_BAD_SEQLENS);
 }
 
 }  // namespace kda

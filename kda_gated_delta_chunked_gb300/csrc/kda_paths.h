@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/kda.h"
+
 namespace kda {
 
 enum PrefillPath { kPathSimt = 0, kPathTensorCore = 1 };
@@ -77,5 +79,45 @@ bool tc_make_tile_map(CUtensorMap* m, const void* base, int64_t T, int H);
 // Tensor-core backward (kda_backward_tc.cu): bf16 inputs, head size 128.
 size_t backward_tc_bytes(int N, int H, int64_t T, int64_t chunks_ub);
 cudaError_t backward_tc_launch(const BackwardArgs& a, int64_t chunks_ub, void* region, cudaStream_t stream);
+
+// ---------------------------------------------------------------- operators around the recurrent layers
+cudaError_t rms_norm_launch(const kda_norm_desc& d, const void* x, const void* weight, const void* residual,
+                            void* residual_out, void* normed, uint8_t* quantized, float* scales, cudaStream_t stream);
+
+struct MatmulArgs {
+    int64_t m, lda, ldb, ldc;
+    int n, k, dtype;
+    const uint8_t *a, *b;
+    const float *sa, *sb;
+    void* c;
+};
+cudaError_t matmul_simt_launch(const MatmulArgs& a, cudaStream_t stream);
+
+struct LatentPrefillArgs {
+    int dtype, N, H, dk, dr, dv, causal;
+    float scale;
+    int64_t tq, tk;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, r_ts;
+    const void *q, *k, *r, *v;
+    const int32_t *cu_q, *cu_k;      // nullptr: one sequence
+    void* out;
+    float* lse;
+    int32_t* status;                 // OK on entry
+};
+cudaError_t latent_prefill_simt_launch(const LatentPrefillArgs& a, cudaStream_t stream);
+
+struct LatentDecodeArgs {
+    int dtype, N, H, Lq, dk, dr;
+    float scale;
+    int64_t q_ts, q_hs, page_stride;
+    int page_size, num_pages, max_pages;
+    const void *q, *cache;
+    const int32_t *table, *lens;
+    void* out;
+    float* lse;
+    int32_t* status;                 // OK on entry (CUDA cores), written whole (tensor cores)
+    void* scratch;
+};
+cudaError_t latent_decode_simt_launch(const LatentDecodeArgs& a, cudaStream_t stream);
 
 }  // namespace kda

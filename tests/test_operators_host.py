@@ -1,0 +1,133 @@
+"""Refusals of the operators around the recurrent layers: every call here is
+turned back by the checks of the C entry, before any CUDA work."""
+import ctypes
+
+import pytest
+import torch
+
+kda = pytest.importorskip("kda_gated_delta_chunked_gb300",
+                          reason="libkda.so not built (run __graft_entry__.build())")
+
+BAD, UNSUP, WS = kda.KDA_ERR_INVALID_ARGUMENT, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_WORKSPACE
+
+
+class Ptr:
+    """Stands in for a tensor in a pointer slot; never dereferenced."""
+    def __init__(self, addr):
+        self.addr = addr
+
+    def data_ptr(self):
+        return self.addr
+
+    def __add__(self, n):
+        return Ptr(self.addr + n)
+
+
+P = [Ptr((1 << 20) + i * (1 << 24)) for i in range(10)]
+
+
+def test_struct_sizes_match_the_header(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    c = tmp_path / "s.c"
+    c.write_text('#include <stdio.h>\n#include "kda.h"\nint main(void){printf("%zu %zu %zu %zu", sizeof(kda_norm_desc),'
+                 'sizeof(kda_matmul_desc), sizeof(kda_latent_desc), offsetof(kda_latent_desc, workspace));return 0;}\n')
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(c), "-o", str(tmp_path / "s")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()]
+    L = kda.KdaLatentDesc
+    assert got == [ctypes.sizeof(kda.KdaNormDesc), ctypes.sizeof(kda.KdaMatmulDesc), ctypes.sizeof(L), L.workspace.offset]
+
+
+def norm(d=None, x=P[0], w=P[1], r=P[2], h=P[3], y=P[4], q=P[5], s=P[6], **kw):
+    f = dict(rows=10, dim=256, dtype=kda.KDA_BF16, x_stride=256, residual_stride=256, eps=1e-6)
+    f.update(kw)
+    return kda.kda_rms_norm(kda.KdaNormDesc(**f), x, w, r, h, y, q, s, 0)
+
+
+def test_norm_refusals():
+    assert norm(rows=-1) == BAD and norm(dim=0) == BAD and norm(dtype=2) == BAD
+    assert norm(x_stride=255) == BAD and norm(residual_stride=255) == BAD
+    assert norm(eps=-1.0) == BAD and norm(eps=float("nan")) == BAD and norm(eps=float("inf")) == BAD
+    assert norm(q=None) == BAD and norm(s=None) == BAD                       # both or neither
+    assert norm(x=None) == BAD and norm(h=None, y=None, q=None, s=None) == BAD
+    assert norm(x=P[0] + 1) == BAD and norm(s=P[6] + 2) == BAD
+    assert norm(y=P[0] + 512) == BAD and norm(q=P[2]) == BAD and norm(y=P[3]) == BAD and norm(y=P[1]) == BAD
+    assert norm(h=P[0] + 512) == BAD and norm(h=P[0], x_stride=300) == BAD    # in place only exactly
+    assert norm(rows=1 << 31, dim=1, x_stride=1, residual_stride=1) == UNSUP
+    assert norm(rows=0, x=None, h=None, y=None, q=None, s=None) == kda.KDA_OK
+
+
+def matmul(a=P[0], sa=P[1], b=P[2], sb=P[3], c=P[4], **kw):
+    f = dict(m=10, n=300, k=256, a_stride=256, b_stride=256, c_stride=300, dtype=kda.KDA_BF16, flags=0)
+    f.update(kw)
+    return kda.kda_matmul_fp8(kda.KdaMatmulDesc(**f), a, sa, b, sb, c, 0)
+
+
+def test_matmul_refusals():
+    assert matmul(m=-1) == BAD and matmul(n=-1) == BAD and matmul(k=0) == BAD and matmul(dtype=7) == BAD
+    assert matmul(a_stride=255) == BAD and matmul(b_stride=255) == BAD and matmul(c_stride=299) == BAD
+    assert matmul(flags=2) == BAD
+    assert matmul(a=None) == BAD and matmul(sa=None) == BAD and matmul(b=None) == BAD and matmul(sb=None) == BAD
+    assert matmul(c=None) == BAD and matmul(c=P[4] + 1) == BAD and matmul(sa=P[1] + 2) == BAD
+    assert matmul(c=P[0] + 64) == BAD and matmul(c=P[1]) == BAD
+    assert matmul(m=1 << 31) == UNSUP
+    assert matmul(m=0, a=None, c=None) == kda.KDA_OK and matmul(n=0, c_stride=0, b=None) == kda.KDA_OK
+
+
+def latent(**kw):
+    f = dict(num_seqs=2, num_heads=4, dtype=kda.KDA_BF16, flags=0, scale=0.1, d_k=128, d_rope=64, d_v=128, total_q=50, total_k=60,
+             q_token_stride=768, q_head_stride=192, k_token_stride=512, k_head_stride=128, v_token_stride=512, v_head_stride=128,
+             rope_token_stride=64, workspace=P[9].addr, workspace_bytes=1 << 24)
+    f.update(kw)
+    return kda.KdaLatentDesc(**f)
+
+
+def prefill(q=P[0], k=P[1], r=P[2], v=P[3], cq=P[4], ck=P[5], out=P[6], lse=P[7], **kw):
+    return kda.kda_latent_prefill(latent(**kw), q, k, r, v, cq, ck, out, lse, 0)
+
+
+def test_prefill_refusals():
+    assert prefill(num_seqs=-1) == BAD and prefill(num_heads=0) == BAD and prefill(dtype=3) == BAD and prefill(flags=8) == BAD
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert prefill(scale=s) == BAD
+    assert prefill(d_k=0) == BAD and prefill(d_rope=-1) == BAD and prefill(d_v=0) == BAD and prefill(total_q=-1) == BAD
+    assert prefill(d_k=200) == UNSUP and prefill(d_v=257) == UNSUP and prefill(num_heads=70000) == UNSUP
+    assert prefill(q_token_stride=-1) == BAD
+    assert prefill(cq=None) == BAD and prefill(cq=None, ck=None) == BAD          # no lengths: one sequence only
+    assert prefill(q=None) == BAD and prefill(k=None) == BAD and prefill(r=None) == BAD and prefill(out=None) == BAD
+    assert prefill(d_rope=0) == BAD                                               # a rotary key without channels
+    assert prefill(q=P[0] + 1) == BAD and prefill(lse=P[7] + 2) == BAD and prefill(cq=P[4] + 1) == BAD
+    assert prefill(out=P[3]) == BAD and prefill(lse=P[6]) == BAD and prefill(out=P[9]) == BAD
+    assert prefill(workspace=None) == WS and prefill(workspace_bytes=8) == WS and prefill(workspace=P[9].addr + 8) == WS
+    assert prefill(num_seqs=0) == kda.KDA_OK and prefill(total_q=0, q=None, out=None) == kda.KDA_OK
+
+
+def decode(q=P[0], cache=P[1], table=P[2], lens=P[3], out=P[4], lse=P[5], **kw):
+    f = dict(d_k=512, d_rope=64, d_v=512, q_token_stride=4 * 576, q_head_stride=576, num_queries=1, page_size=64, num_pages=10,
+             max_pages=5, page_stride=64 * 576)
+    f.update(kw)
+    return kda.kda_latent_decode(latent(**f), q, cache, table, lens, out, lse, 0)
+
+
+def test_decode_refusals():
+    assert decode(num_queries=0) == BAD and decode(page_size=0) == BAD and decode(max_pages=0) == BAD and decode(num_pages=-1) == BAD
+    assert decode(d_v=256) == BAD and decode(page_stride=64 * 576 - 1) == BAD and decode(flags=kda.KDA_FLAG_NO_CAUSAL) == BAD
+    assert decode(d_k=513, d_v=513, page_stride=64 * 577) == UNSUP and decode(d_rope=129, page_stride=64 * 641) == UNSUP
+    assert decode(max_pages=1 << 30) == UNSUP
+    assert decode(q=None) == BAD and decode(cache=None) == BAD and decode(table=None) == BAD and decode(lens=None) == BAD
+    assert decode(out=None) == BAD and decode(out=P[4] + 1) == BAD and decode(table=P[2] + 2) == BAD
+    assert decode(out=P[1] + 64) == BAD and decode(lse=P[0]) == BAD and decode(out=P[9] + 64) == BAD
+    assert decode(workspace=None) == WS and decode(workspace_bytes=8) == WS
+    assert decode(num_seqs=0) == kda.KDA_OK
+    d = latent(d_k=512, d_v=512, num_queries=1, page_size=64, num_pages=10, max_pages=5, page_stride=64 * 576)
+    assert kda.kda_latent_decode_workspace_bytes(d) > 0 and kda.kda_latent_prefill_workspace_bytes(d) == 0
+
+
+def test_python_refusals():
+    """What the torch layer turns back: here, anything that is not on a CUDA device."""
+    x = torch.zeros(4, 256)
+    for call in (lambda: kda.rms_norm(x), lambda: kda.matmul_fp8(x, x, x, x), lambda: kda.latent_prefill(x, x, x, x, scale=1.0),
+                 lambda: kda.latent_decode(x, x, x, x, scale=1.0)):
+        with pytest.raises(ValueError):
+            call()
