@@ -1,0 +1,450 @@
+// kda_matmul_tc.cu -- the scaled e4m3 product on the tensor cores.
+//
+//     c[m, n] = sum_j  sa[m, j] sb[n / 128, j]  D_j[m, n],   D_j = sum_{k in block j} a b
+//
+// The scales change with every 128 values of k, so each block's product D_j is
+// formed on its own in TMEM (4 instructions of 32 k) and read back, scaled and
+// added to fp32 registers while the next block's runs into the other half of a
+// TMEM double buffer.  Two shapes of the same loop:
+//
+//  wide  rows of a along M.  A pair of CTAs (cta_group::2) owns a 256 x BN tile;
+//        each loads its 128 rows of a and half of b's rows, so a byte from L2
+//        feeds twice the products of a single CTA's tile.  One row of a per
+//        lane: its scale and b's block scale make one factor a thread.
+//        Persistent: a pair walks tiles in an order that keeps both operands
+//        in L2.
+//  thin  few rows of a: b's rows along M, a's along N, so b streams through
+//        once at full height.  The k blocks are split over the CTAs of a
+//        cluster, whose sums meet in distributed shared memory in rank order.
+//
+// Every wait is bounded; a tile whose wait gave up is filled with NaN.
+#include <math.h>
+
+#include "kda_common.cuh"
+#include "kda_paths.h"
+#include "kda_sm100_ops.cuh"
+#include "kda_tensor_map.h"
+
+namespace kda {
+using namespace sm100;
+
+constexpr int kMmEpiWarps = 8;
+
+// ------------------------------------------------------------------- wide
+template <int BN>
+struct WideShape {
+    static constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;
+    static constexpr int kThreads = 32 * (kMmEpiWarps + 4);        // whole warpgroups: registers move between them
+};
+
+// 32 consecutive values of a row at p (32-byte aligned).
+template <typename T>
+__device__ __forceinline__ void store32(T* p, const float* v) {
+    constexpr int per = 32 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 32; i += per) {
+        uint32_t w[8];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                w[j] = *(const uint32_t*)&b;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+        }
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + i), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    }
+}
+
+template <typename T, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WideShape<BN>::kThreads, 1)
+kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const MatmulArgs g, const int tiles_m, const int tiles_n) {
+    using S = WideShape<BN>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* after = raw + (base - smem_u32(raw)) + kStages * S::kStage;
+    uint64_t* full = (uint64_t*)after;             // leader: both CTAs' pieces of a stage have landed
+    uint64_t* empty = full + kStages;              // the MMAs reading a stage are done
+    uint64_t* tfull = empty + kStages;             // [2] a block's product is in TMEM
+    uint64_t* tempty = tfull + 2;                  // [2] leader: all epilogue warps of the pair have read it
+    uint32_t* tmem_at = (uint32_t*)(tempty + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 2 * kMmEpiWarps); }
+        fence_mbar_init();
+    }
+    if (warp == 0) { tmem_alloc_pair(tmem_at, 2 * BN); tmem_relinquish_pair(); }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_at;
+
+    const int kb = (g.k + 127) / 128;
+    const int tiles = tiles_m * tiles_n, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    // 8 tiles of rows beside each other: the tiles in flight form a near square, which reads the least
+    auto place = [&](int t, int& tm, int& tn) {
+        const int per = 8 * tiles_n, grp = t / per, rows = min(8, tiles_m - grp * 8), r = t - grp * per;
+        tm = grp * 8 + r % rows;
+        tn = r / rows;
+    };
+
+    // 384 threads x 168 registers at launch = 256 x 232 + 128 x 40
+    if (warp < kMmEpiWarps) {                                      // scale, add, store
+        regs_inc<232>();
+        constexpr int kCols = BN / 2;                              // columns of a thread
+        const int quarter = warp & 3, half = warp >> 2;
+        const int nb_all = (g.n + 127) / 128;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles; t += pairs) {
+            int tm, tn;
+            place(t, tm, tn);
+            const int64_t row = (int64_t)tm * 256 + rank * 128 + quarter * 32 + lane;
+            const int col = tn * BN + half * kCols;
+            const float* sa = g.sa + (row < g.m ? row : 0) * kb;
+            const float* sb = g.sb + (int64_t)min(col / 128, nb_all - 1) * kb;
+            float acc[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+            float next = sa[0] * sb[0];
+            for (int j = 0; j < kb; ++j, ++it) {
+                const float s = next;
+                if (j + 1 < kb) next = sa[j + 1] * sb[j + 1];
+                const uint32_t d = it & 1, dph = (it >> 1) & 1;
+                if (ok) ok = mbar_wait_spin(&tfull[d], dph);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t at = tmem_addr(tmem, 32 * quarter, d * BN + half * kCols);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    float f[32];
+                    tmem_ld32(at + c, f);
+                    tmem_wait_ld();
+                    tmem_ready(f);
+                    if (c + 32 == kCols) {                         // the buffer is read: free it before the last sums
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(map_cta(smem_u32(&tempty[d]), 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(f[i], s, acc[c + i]);
+                }
+            }
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[i] = NAN;
+            }
+            if (row < g.m && col < g.n) {
+                T* p = (T*)g.c + row * g.ldc + col;
+                const int n = min(kCols, g.n - col);
+                if (n == kCols && ((uintptr_t)p & 31) == 0) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) store32(p + c, acc + c);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        if (i < n) p[i] = from_f32<T>(acc[i]);
+                }
+            }
+        }
+    } else {
+        regs_dec<40>();
+        if (warp == kMmEpiWarps) {                                 // producer
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    int tm, tn;
+                    place(t, tm, tn);
+                    for (int j = 0; j < kb; ++j, ++it) {
+                        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                        if (it >= kStages && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
+                        const uint32_t at = base + s * S::kStage, bar = map_cta(smem_u32(&full[s]), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+                        tma_load_2d_pair(at, &map_a, j * 128, tm * 256 + (int)rank * 128, bar);
+                        tma_load_2d_pair(at + S::kA, &map_b, j * 128, tn * BN + (int)rank * (BN / 2), bar);
+                    }
+                }
+                if (!ok) drain_copies();
+            }
+        } else if (warp == kMmEpiWarps + 1) {                      // matrix instructions, by the leader
+            if (rank == 0 && lane == 0) {
+                const uint32_t idesc = idesc_e4m3(256, BN);
+                uint32_t it = 0;
+                bool ok = true;
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    for (int j = 0; j < kb; ++j, ++it) {
+                        const uint32_t s = it % kStages, ph = (it / kStages) & 1, d = it & 1, dph = (it >> 1) & 1;
+                        if (it >= 2 && !(ok = mbar_wait_spin(&tempty[d], dph ^ 1))) break;
+                        if (!(ok = mbar_wait_spin(&full[s], ph))) break;
+                        tc_fence_after_sync();
+                        const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
+                        const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma_f8_ss_pair(tmem + d * BN, da + 2 * q, db + 2 * q, idesc, q > 0);
+                        mma_commit_pair(&empty[s], 3);
+                        mma_commit_pair(&tfull[d], 3);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();                                                // the peer may still read or signal this CTA
+    if (warp == 0) tmem_dealloc_pair(tmem, 2 * BN);
+}
+
+// ------------------------------------------------------------------- thin
+// BT rows of a (tokens) a CTA; `splits` CTAs of a cluster share a 128 x BT tile.
+constexpr int kThinThreads = 32 * 6;
+
+template <int BT>
+struct ThinShape {
+    static constexpr uint32_t kA = 128 * 128, kB = BT * 128, kStage = kA + kB;
+    static constexpr int kStages = (int)(160 * 1024 / kStage) > 9 ? 9 : (int)(160 * 1024 / kStage);
+    static constexpr uint32_t kTmem = 2 * BT < 32 ? 32 : 2 * BT;
+    static constexpr uint32_t kScales = kStages * kStage;          // then factors [k blocks of the CTA][BT]
+    // sums [BT][128] of the cluster's CTAs: over the stages, which are read by then
+    static uint32_t smem(int blocks) { return kScales + (uint32_t)blocks * BT * 4 + 1024 + 256; }
+};
+
+template <typename T, int BT>
+__global__ void __launch_bounds__(kThinThreads, 1)
+kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const MatmulArgs g, const int blocks_per) {
+    using S = ThinShape<BT>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    float* factors = (float*)(mem + S::kScales);
+    uint64_t* full = (uint64_t*)(factors + (size_t)blocks_per * BT);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* tmem_at = (uint32_t*)(tempty + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int splits = gridDim.x;                                  // = the cluster
+    const int rank = blockIdx.x, n0 = blockIdx.y * 128;
+    const int64_t m0 = (int64_t)blockIdx.z * BT;
+    const int kb = (g.k + 127) / 128;
+    const int j0 = rank * blocks_per, count = max(0, min(kb, j0 + blocks_per) - j0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 4); }
+        fence_mbar_init();
+    }
+    if (warp == 0) { tmem_alloc(tmem_at, S::kTmem); tmem_relinquish(); }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_at;
+
+    float acc[BT];
+#pragma unroll
+    for (int i = 0; i < BT; ++i) acc[i] = 0.f;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int i = 0; i < count; ++i) {
+                const uint32_t s = i % kStages, ph = (i / kStages) & 1;
+                if (i >= kStages && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
+                const uint32_t at = base + s * S::kStage, bar = smem_u32(&full[s]);
+                mbar_arrive_expect_tx(&full[s], S::kStage);
+                tma_load_2d(at, &map_b, (j0 + i) * 128, n0, bar);
+                tma_load_2d(at + S::kA, &map_a, (j0 + i) * 128, (int)m0, bar);
+            }
+            if (!ok) drain_copies();
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(128, BT);
+            bool ok = true;
+            for (int i = 0; i < count; ++i) {
+                const uint32_t s = i % kStages, ph = (i / kStages) & 1, d = i & 1, dph = (i >> 1) & 1;
+                if (i >= 2 && !(ok = mbar_wait_spin(&tempty[d], dph ^ 1))) break;
+                if (!(ok = mbar_wait_spin(&full[s], ph))) break;
+                tc_fence_after_sync();
+                const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
+                const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mma_f8_ss(tmem + d * BT, da + 2 * q, db + 2 * q, idesc, q > 0);
+                mma_commit(&empty[s]);
+                mma_commit(&tfull[d]);
+            }
+        }
+    } else {
+        // factors of the CTA's blocks: sa of every token times sb of the 128 rows of b
+        const float* sb = g.sb + (int64_t)blockIdx.y * kb + j0;
+        for (int i = threadIdx.x; i < count * BT; i += 128) {
+            const int j = i % count, t = i / count;                // neighbouring threads: neighbouring blocks of a row
+            factors[j * BT + t] = m0 + t < g.m ? g.sa[(m0 + t) * kb + j0 + j] * sb[j] : 0.f;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            const uint32_t d = i & 1, dph = (i >> 1) & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(&tfull[d], dph));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t at = tmem_addr(tmem, 32 * warp, d * BT);
+#pragma unroll
+            for (int c = 0; c < BT; c += 16) {
+                float f[16];
+                tmem_ld16(at + c, f);
+                tmem_wait_ld();
+                tmem_ready(f);
+                if (c + 16 == BT) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[d]);
+                }
+                const float4* w = (const float4*)(factors + i * BT + c);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 x = w[q];
+                    acc[c + 4 * q] = fmaf(f[4 * q], x.x, acc[c + 4 * q]);
+                    acc[c + 4 * q + 1] = fmaf(f[4 * q + 1], x.y, acc[c + 4 * q + 1]);
+                    acc[c + 4 * q + 2] = fmaf(f[4 * q + 2], x.z, acc[c + 4 * q + 2]);
+                    acc[c + 4 * q + 3] = fmaf(f[4 * q + 3], x.w, acc[c + 4 * q + 3]);
+                }
+            }
+        }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < BT; ++i) acc[i] = NAN;
+        }
+    }
+    // All copies have landed and all MMAs are done (their products were waited for): the stages become sums[t][r].
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, S::kTmem);
+    const int r = threadIdx.x;                                     // row of b within the tile
+    if (splits == 1) {
+        if (r < 128 && n0 + r < g.n) {
+#pragma unroll
+            for (int t = 0; t < BT; ++t)
+                if (m0 + t < g.m) ((T*)g.c)[(m0 + t) * g.ldc + n0 + r] = from_f32<T>(acc[t]);
+        }
+        return;
+    }
+    float* sums = (float*)mem;
+    if (r < 128) {
+#pragma unroll
+        for (int t = 0; t < BT; ++t) sums[t * 128 + r] = acc[t];
+    }
+    cluster_sync();
+    // each CTA joins and stores its share of the tokens, the splits in rank order
+    const int live = (int)min64(BT, g.m - m0);
+    for (int i = rank * kThinThreads + threadIdx.x; i < live * 128; i += splits * kThinThreads) {
+        const uint32_t at = base + i * 4;
+        float x = 0.f;
+        for (int c = 0; c < splits; ++c) x += ld_cluster_f32(map_cta(at, c));
+        const int64_t m = m0 + i / 128;
+        const int n = n0 + i % 128;
+        if (n < g.n) ((T*)g.c)[m * g.ldc + n] = from_f32<T>(x);
+    }
+    cluster_sync();
+}
+
+// ------------------------------------------------------------------- host
+static bool make_operand(CUtensorMap* m, const uint8_t* p, int64_t rows, int k, int64_t ld, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows}, strides[1] = {(uint64_t)ld};
+    const uint32_t box[2] = {128, (uint32_t)box_rows};
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box);
+}
+
+template <typename T, int BN>
+static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
+    using S = WideShape<BN>;
+    auto kern = kda_matmul_fp8_wide<T, BN>;
+    static int resident = 0;                       // pairs that run at once: a property of the device and the kernel
+    if (!resident) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * 1024); cfg.blockDim = dim3(S::kThreads); cfg.dynamicSmemBytes = S::kSmem;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        resident = n > 0 ? n : 1;
+    }
+    CUtensorMap ma, mb;
+    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, BN / 2))
+        return cudaErrorInvalidValue;
+    const int tm = (int)((a.m + 255) / 256), tn = (a.n + BN - 1) / BN;
+    const int64_t tiles = (int64_t)tm * tn;
+    const int pairs = (int)min64(tiles, resident);
+    kern<<<2 * pairs, S::kThreads, S::kSmem, stream>>>(ma, mb, a, tm, tn);
+    return cudaGetLastError();
+}
+
+template <typename T, int BT>
+static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
+    using S = ThinShape<BT>;
+    auto kern = kda_matmul_fp8_thin<T, BT>;
+    const int kb = (a.k + 127) / 128, tn = (a.n + 127) / 128, tm = (int)((a.m + BT - 1) / BT);
+    int splits = 152 / (tn * tm);
+    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+    splits = splits > kb ? kb : splits;
+    const int per = (kb + splits - 1) / splits;
+    splits = (kb + per - 1) / per;
+    const uint32_t smem = S::smem(per);
+    static bool ready = false;
+    if (!ready) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        ready = true;
+    }
+    if (smem > 227 * 1024) return cudaErrorInvalidValue;
+    CUtensorMap ma, mb;
+    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, BT) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, 128))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, tn, tm); cfg.blockDim = dim3(kThinThreads); cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = splits; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    cfg.attrs = at; cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, a, per);
+}
+
+template <typename T>
+static cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t stream) {
+    const int blocks = (a.k + 127) / 128;
+    // the factors of a CTA's k blocks lie in shared memory
+    const bool thin_fits = blocks <= 96;
+    if (a.m <= 16 && thin_fits) return launch_thin<T, 16>(a, stream);
+    if (a.m <= 32 && thin_fits) return launch_thin<T, 32>(a, stream);
+    if (a.m <= 64 && thin_fits) return launch_thin<T, 64>(a, stream);
+    if (a.m <= 128 && thin_fits) return launch_thin<T, 128>(a, stream);
+    if ((a.m + 255) / 256 * ((a.n + 255) / 256) < 64) return launch_wide<T, 128>(a, stream);
+    return launch_wide<T, 256>(a, stream);
+}
+
+bool matmul_tc_takes(const MatmulArgs& a) {
+    return (((uintptr_t)a.a | (uintptr_t)a.b | (uintptr_t)a.lda | (uintptr_t)a.ldb) & 15) == 0 &&
+           a.lda < (1ll << 40) && a.ldb < (1ll << 40);
+}
+
+cudaError_t matmul_tc_launch(const MatmulArgs& a, cudaStream_t stream) {
+    return a.dtype == KDA_BF16 ? launch_matmul<__nv_bfloat16>(a, stream) : launch_matmul<float>(a, stream);
+}
+
+}  // namespace kda

@@ -128,7 +128,8 @@ int kda_matmul_fp8(const kda_matmul_desc* d, const uint8_t* a, const float* a_sc
     m.m = d->m; m.lda = d->a_stride; m.ldb = d->b_stride; m.ldc = d->c_stride;
     m.n = d->n; m.k = d->k; m.dtype = d->dtype;
     m.a = a; m.b = b; m.sa = a_scale; m.sb = b_scale; m.c = c;
-    const cudaError_t err = matmul_simt_launch(m, (cudaStream_t)stream);
+    const bool tc = (d->flags & KDA_FLAG_CUDA_CORE_PREFILL) == 0 && matmul_tc_takes(m);
+    const cudaError_t err = tc ? matmul_tc_launch(m, (cudaStream_t)stream) : matmul_simt_launch(m, (cudaStream_t)stream);
     return err == cudaSuccess ? KDA_OK : cuda_fail(err);
 }
 

@@ -92,6 +92,8 @@ struct MatmulArgs {
     void* c;
 };
 cudaError_t matmul_simt_launch(const MatmulArgs& a, cudaStream_t stream);
+bool matmul_tc_takes(const MatmulArgs& a);          // rows of a and b start on 16-byte boundaries
+cudaError_t matmul_tc_launch(const MatmulArgs& a, cudaStream_t stream);
 
 struct LatentPrefillArgs {
     int dtype, N, H, dk, dr, dv, causal;
