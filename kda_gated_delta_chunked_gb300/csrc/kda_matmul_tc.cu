@@ -72,15 +72,15 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint8_t* after = raw + (base - smem_u32(raw)) + kStages * S::kStage;
     uint64_t* full = (uint64_t*)after;             // leader: both CTAs' pieces of a stage have landed
     uint64_t* empty = full + kStages;              // the MMAs reading a stage are done
-    uint64_t* tfull = empty + kStages;             // [2] a block's product is in TMEM
-    uint64_t* tempty = tfull + 2;                  // [2] leader: all epilogue warps of the pair have read it
-    uint32_t* tmem_at = (uint32_t*)(tempty + 2);
+    uint64_t* tfull = empty + kStages;             // [2][2] half of a block's product is in TMEM
+    uint64_t* tempty = tfull + 4;                  // [2][2] leader: the pair's epilogue warps of that half have read it
+    uint32_t* tmem_at = (uint32_t*)(tempty + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 2 * kMmEpiWarps); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
+        for (int i = 0; i < 4; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], kMmEpiWarps); }
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc_pair(tmem_at, 2 * BN); tmem_relinquish_pair(); }
@@ -88,7 +88,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     __syncthreads();
     cluster_sync();
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
 
     const int kb = (g.k + 127) / 128;
     const int tiles = tiles_m * tiles_n, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
@@ -117,29 +117,37 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-            float next = sa[0] * sb[0];
+            float xa = sa[0], xb = sb[0];                          // loaded a block ahead
             for (int j = 0; j < kb; ++j, ++it) {
-                const float s = next;
-                if (j + 1 < kb) next = sa[j + 1] * sb[j + 1];
-                const uint32_t d = it & 1, dph = (it >> 1) & 1;
+                const float s = xa * xb;
+                const uint32_t d = (it & 1) * 2 + half, dph = (it >> 1) & 1;
                 if (ok) ok = mbar_wait_spin(&tfull[d], dph);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t at = tmem_addr(tmem, 32 * quarter, d * BN + half * kCols);
+                const uint32_t at = tmem_addr(tmem, 32 * quarter, d * kCols);
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    float f[32];
+                for (int c = 0; c < kCols; c += 64) {              // two loads in flight
+                    float f[32], e[32];
                     tmem_ld32(at + c, f);
+                    tmem_ld32(at + c + 32, e);
+                    if (c == 0) {
+                        const int jn = j + 1 < kb ? j + 1 : j;
+                        xa = sa[jn];
+                        xb = sb[jn];
+                    }
                     tmem_wait_ld();
                     tmem_ready(f);
-                    if (c + 32 == kCols) {                         // the buffer is read: free it before the last sums
+                    tmem_ready(e);
+                    if (c + 64 == kCols) {                         // the buffer is read: free it before the last sums
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(map_cta(smem_u32(&tempty[d]), 0));
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(f[i], s, acc[c + i]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[c + 32 + i] = fmaf(e[i], s, acc[c + 32 + i]);
                 }
             }
             if (!ok) {
@@ -174,28 +182,39 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         const uint32_t at = base + s * S::kStage, bar = map_cta(smem_u32(&full[s]), 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
                         tma_load_2d_pair(at, &map_a, j * 128, tm * 256 + (int)rank * 128, bar);
-                        tma_load_2d_pair(at + S::kA, &map_b, j * 128, tn * BN + (int)rank * (BN / 2), bar);
+                        // each half of the tile's columns takes half of its rows of b from either CTA
+                        tma_load_2d_pair(at + S::kA, &map_b, j * 128, tn * BN + (int)rank * (BN / 4), bar);
+                        tma_load_2d_pair(at + S::kA + S::kB / 2, &map_b, j * 128, tn * BN + BN / 2 + (int)rank * (BN / 4), bar);
                     }
                 }
                 if (!ok) drain_copies();
             }
-        } else if (warp == kMmEpiWarps + 1) {                      // matrix instructions, by the leader
-            if (rank == 0 && lane == 0) {
-                const uint32_t idesc = idesc_e4m3(256, BN);
+        } else if (warp <= kMmEpiWarps + 2) {
+            // Matrix instructions, by the leader: a warp for each half of the columns.  One warp needs about
+            // 500 cycles for the waits, 4 instructions and a commit, as long as the instructions of a whole
+            // block take.
+            if (rank == 0) {
+                const int h = warp - kMmEpiWarps - 1;
+                const uint32_t idesc = idesc_e4m3(256, BN / 2);
                 uint32_t it = 0;
                 bool ok = true;
                 for (int t = pair; t < tiles && ok; t += pairs) {
-                    for (int j = 0; j < kb; ++j, ++it) {
-                        const uint32_t s = it % kStages, ph = (it / kStages) & 1, d = it & 1, dph = (it >> 1) & 1;
-                        if (it >= 2 && !(ok = mbar_wait_spin(&tempty[d], dph ^ 1))) break;
-                        if (!(ok = mbar_wait_spin(&full[s], ph))) break;
-                        tc_fence_after_sync();
+                    for (int j = 0; j < kb && ok; ++j, ++it) {
+                        const uint32_t s = it % kStages, ph = (it / kStages) & 1, dph = (it >> 1) & 1, d = (it & 1) * 2 + h;
+                        ok = mbar_wait_warp(&full[s], ph);
+                        if (ok && it >= 2) ok = mbar_wait_warp(&tempty[d], dph ^ 1);
+                        if (!ok) break;
                         const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
-                        const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+                        const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA + h * (S::kB / 2));
+                        tc_fence_after_sync();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) mma_f8_ss_pair(tmem + d * BN, da + 2 * q, db + 2 * q, idesc, q > 0);
-                        mma_commit_pair(&empty[s], 3);
-                        mma_commit_pair(&tfull[d], 3);
+                            for (int q = 0; q < 4; ++q)
+                                mma_f8_ss_pair(tmem + d * (BN / 2), da + 2 * q, db + 2 * q, idesc, q > 0);
+                            mma_commit_pair(&tfull[d], 3);
+                            mma_commit_pair(&empty[s], 3);
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -252,7 +271,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
 
     float acc[BT];
 #pragma unroll
@@ -272,21 +291,23 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             if (!ok) drain_copies();
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3(128, BT);
-            bool ok = true;
-            for (int i = 0; i < count; ++i) {
-                const uint32_t s = i % kStages, ph = (i / kStages) & 1, d = i & 1, dph = (i >> 1) & 1;
-                if (i >= 2 && !(ok = mbar_wait_spin(&tempty[d], dph ^ 1))) break;
-                if (!(ok = mbar_wait_spin(&full[s], ph))) break;
-                tc_fence_after_sync();
-                const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
-                const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+        const uint32_t idesc = idesc_e4m3(128, BT);
+        bool ok = true;
+        for (int i = 0; i < count && ok; ++i) {
+            const uint32_t s = i % kStages, ph = (i / kStages) & 1, d = i & 1, dph = (i >> 1) & 1;
+            ok = mbar_wait_warp(&full[s], ph);
+            if (ok && i >= 2) ok = mbar_wait_warp(&tempty[d], dph ^ 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
+            const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+            if (elect_one()) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mma_f8_ss(tmem + d * BT, da + 2 * q, db + 2 * q, idesc, q > 0);
                 mma_commit(&empty[s]);
                 mma_commit(&tfull[d]);
             }
+            __syncwarp();
         }
     } else {
         // factors of the CTA's blocks: sa of every token times sb of the 128 rows of b
@@ -385,7 +406,7 @@ static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
         resident = n > 0 ? n : 1;
     }
     CUtensorMap ma, mb;
-    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, BN / 2))
+    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, BN / 4))
         return cudaErrorInvalidValue;
     const int tm = (int)((a.m + 255) / 256), tn = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)tm * tn;
