@@ -34,42 +34,40 @@ constexpr int kMmEpiWarps = 8;
 template <int BN>
 struct WideShape {
     static constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
-    static constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;
+    static constexpr int kStages = BN == 256 ? 5 : 7;
+    static constexpr uint32_t kOut = 128 * BN * 2;                 // a tile's output on its way to c
+    static constexpr uint32_t kSmem = kStages * kStage + kOut + 1024 + 256;
     static constexpr int kThreads = 32 * (kMmEpiWarps + 4);        // whole warpgroups: registers move between them
 };
 
-// 32 consecutive values of a row at p (32-byte aligned).
+// 8 or 16 consecutive values of a row at p (32-byte aligned).
 template <typename T>
-__device__ __forceinline__ void store32(T* p, const float* v) {
-    constexpr int per = 32 / sizeof(T);
+__device__ __forceinline__ void store_row32b(T* p, const f32x2* v) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 32; i += per) {
-        uint32_t w[8];
+    for (int j = 0; j < 8; ++j) {
         if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
-                w[j] = *(const uint32_t*)&b;
-            }
+            w[j] = bf16x2(v[j]);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+            float lo, hi;
+            unpack2(v[j / 2], lo, hi);
+            w[j] = __float_as_uint(j & 1 ? hi : lo);
         }
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + i), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
     }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
 template <typename T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WideShape<BN>::kThreads, 1)
 kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const MatmulArgs g, const int tiles_m, const int tiles_n) {
+                    const __grid_constant__ CUtensorMap map_c, const int use_map_c, const MatmulArgs g,
+                    const int tiles_m, const int tiles_n) {
     using S = WideShape<BN>;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    uint8_t* after = raw + (base - smem_u32(raw)) + kStages * S::kStage;
+    uint8_t* after = raw + (base - smem_u32(raw)) + kStages * S::kStage + S::kOut;
     uint64_t* full = (uint64_t*)after;             // leader: both CTAs' pieces of a stage have landed
     uint64_t* empty = full + kStages;              // the MMAs reading a stage are done
     uint64_t* tfull = empty + kStages;             // [2][2] half of a block's product is in TMEM
@@ -114,12 +112,13 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             const int col = tn * BN + half * kCols;
             const float* sa = g.sa + (row < g.m ? row : 0) * kb;
             const float* sb = g.sb + (int64_t)min(col / 128, nb_all - 1) * kb;
-            float acc[kCols];
+            f32x2 acc[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+            for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
             float xa = sa[0], xb = sb[0];                          // loaded a block ahead
             for (int j = 0; j < kb; ++j, ++it) {
-                const float s = xa * xb;
+                const float s1 = xa * xb;
+                const f32x2 s = pack2(s1, s1);
                 const uint32_t d = (it & 1) * 2 + half, dph = (it >> 1) & 1;
                 if (ok) ok = mbar_wait_spin(&tfull[d], dph);
                 ok = __all_sync(0xffffffffu, ok);
@@ -145,28 +144,56 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         if (lane == 0) mbar_arrive_cluster(map_cta(smem_u32(&tempty[d]), 0));
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(f[i], s, acc[c + i]);
+                    for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(f[2 * i], f[2 * i + 1]), s, acc[c / 2 + i]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c + 32 + i] = fmaf(e[i], s, acc[c + 32 + i]);
+                    for (int i = 0; i < 16; ++i)
+                        acc[c / 2 + 16 + i] = fma2(pack2(e[2 * i], e[2 * i + 1]), s, acc[c / 2 + 16 + i]);
                 }
             }
             if (!ok) {
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) acc[i] = NAN;
+                for (int i = 0; i < kCols / 2; ++i) acc[i] = pack2(NAN, NAN);
             }
-            if (row < g.m && col < g.n) {
+            if (sizeof(T) == 2 && use_map_c) {
+                // Through shared memory and out by TMA: the stores of all SMs' tiles come at once, and the
+                // next tile's products need not wait for them.  Boxes of 64 columns, 128-byte swizzle.
+                const uint32_t own = base + kStages * S::kStage + half * (S::kOut / 2);
+                const int r = quarter * 32 + lane;
+                if (threadIdx.x % 128 == 0) bulk_wait_read_all();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+#pragma unroll
+                for (int c = 0; c < kCols; c += 8) {
+                    const uint32_t at = own + c / 64 * 16384 + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(bf16x2(acc[c / 2])),
+                                 "r"(bf16x2(acc[c / 2 + 1])), "r"(bf16x2(acc[c / 2 + 2])), "r"(bf16x2(acc[c / 2 + 3]))
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                if (threadIdx.x % 128 == 0) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 64)
+                        if (col + c < g.n) tma_store_2d(&map_c, own + c / 64 * 16384, col + c, tm * 256 + rank * 128);
+                    bulk_commit();
+                }
+            } else if (row < g.m && col < g.n) {
                 T* p = (T*)g.c + row * g.ldc + col;
                 const int n = min(kCols, g.n - col);
                 if (n == kCols && ((uintptr_t)p & 31) == 0) {
+                    constexpr int per = 32 / sizeof(T);
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32) store32(p + c, acc + c);
+                    for (int c = 0; c < kCols; c += per) store_row32b(p + c, acc + c / 2);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        if (i < n) p[i] = from_f32<T>(acc[i]);
+                    for (int i = 0; i < kCols; ++i) {
+                        float lo, hi;
+                        unpack2(acc[i / 2], lo, hi);
+                        if (i < n) p[i] = from_f32<T>(i & 1 ? hi : lo);
+                    }
                 }
             }
         }
+        if (sizeof(T) == 2 && use_map_c && threadIdx.x % 128 == 0) bulk_wait_all();
     } else {
         regs_dec<40>();
         if (warp == kMmEpiWarps) {                                 // producer
@@ -408,10 +435,18 @@ static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
     CUtensorMap ma, mb;
     if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, BN / 4))
         return cudaErrorInvalidValue;
+    // c by TMA where its rows start on 16-byte boundaries
+    CUtensorMap mc = ma;
+    const bool use_mc = sizeof(T) == 2 && (((uintptr_t)a.c | (uintptr_t)(a.ldc * 2)) & 15) == 0 && a.ldc < (1ll << 38);
+    if (use_mc) {
+        const uint64_t dims[2] = {(uint64_t)a.n, (uint64_t)a.m}, strides[1] = {(uint64_t)a.ldc * 2};
+        const uint32_t box[2] = {64, 128};
+        if (!make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims, strides, box)) return cudaErrorInvalidValue;
+    }
     const int tm = (int)((a.m + 255) / 256), tn = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)tm * tn;
     const int pairs = (int)min64(tiles, resident);
-    kern<<<2 * pairs, S::kThreads, S::kSmem, stream>>>(ma, mb, a, tm, tn);
+    kern<<<2 * pairs, S::kThreads, S::kSmem, stream>>>(ma, mb, mc, use_mc, a, tm, tn);
     return cudaGetLastError();
 }
 
