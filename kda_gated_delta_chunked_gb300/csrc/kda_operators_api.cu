@@ -70,6 +70,10 @@ static int decode_desc(const kda_latent_desc* d) {
     if ((int64_t)d->num_seqs * d->num_queries > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
+static bool decode_tc(const kda_latent_desc* d) {
+    return (d->flags & KDA_FLAG_CUDA_CORE_PREFILL) == 0 &&
+           latent_decode_tc_takes(d->dtype, d->d_k, d->d_rope, d->num_heads, d->num_queries, d->page_size);
+}
 static int workspace_fault(const kda_latent_desc* d, size_t need) {
     return !d->workspace || d->workspace_bytes < need || misaligned(d->workspace, 256);
 }
@@ -138,7 +142,9 @@ size_t kda_latent_prefill_workspace_bytes(const kda_latent_desc* d) {
 }
 
 size_t kda_latent_decode_workspace_bytes(const kda_latent_desc* d) {
-    return decode_desc(d) ? 0 : kStatusBytes;
+    if (decode_desc(d)) return 0;
+    const bool tc = decode_tc(d);
+    return kStatusBytes + (tc ? latent_decode_tc_bytes(d->num_seqs, d->num_queries, d->num_heads, d->page_size, d->max_pages) : 0);
 }
 
 int kda_latent_prefill(const kda_latent_desc* d, const void* q, const void* k_nope, const void* k_rope,
@@ -204,8 +210,13 @@ int kda_latent_decode(const kda_latent_desc* d, const void* q, const void* cache
     a.q = q; a.cache = cache; a.table = page_table; a.lens = lengths; a.out = out; a.lse = lse;
     a.status = (int32_t*)d->workspace; a.scratch = (char*)d->workspace + kStatusBytes;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t err = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
-    if (err == cudaSuccess) err = latent_decode_simt_launch(a, s);
+    cudaError_t err;
+    if (decode_tc(d) && latent_decode_tc_aligned(a)) {
+        err = latent_decode_tc_launch(a, s);
+    } else {
+        err = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
+        if (err == cudaSuccess) err = latent_decode_simt_launch(a, s);
+    }
     return err == cudaSuccess ? KDA_OK : cuda_fail(err);
 }
 

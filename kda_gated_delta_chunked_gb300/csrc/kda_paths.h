@@ -121,5 +121,10 @@ struct LatentDecodeArgs {
     void* scratch;
 };
 cudaError_t latent_decode_simt_launch(const LatentDecodeArgs& a, cudaStream_t stream);
+// Tensor cores: what sizes and layouts they take, their scratch.
+bool latent_decode_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_size);
+bool latent_decode_tc_aligned(const LatentDecodeArgs& a);
+size_t latent_decode_tc_bytes(int N, int Lq, int H, int page_size, int max_pages);
+cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& a, cudaStream_t stream);
 
 }  // namespace kda
