@@ -1,0 +1,372 @@
+// kda_latent_prefill_tc.cu -- expanded latent attention over packed prompts on
+// the tensor cores (bf16; keys 128 + 64 shared rotary channels, values 128).
+//
+//     S = Q K^T (192 channels),  P = exp2(scale' S - ref),  O += P V
+//
+// A CTA owns 256 query rows of one head as two tiles of 128 and walks the key
+// tiles of 128 that they see.  While the softmax of one tile runs on its own
+// warpgroup (a thread a row), the tensor core works on the other:
+//
+//     PV_j(0)  S_{j+1}(0)  PV_j(1)  S_{j+1}(1)  PV_{j+1}(0) ...
+//
+// TMEM holds S0 S1 O0 O1 (4 x 128 columns); P overwrites its S as bf16 and is
+// read from there, so only V passes through shared memory for the second
+// product.  The reference of a row moves only when a score exceeds it by 2^8
+// (then the row of O is rescaled), which is rare after the first tiles.
+// K (three pieces of 64 channels) and V (two of 64 keys) share one ring of eight
+// 16 KB pieces, in the order of their use; with the queries' 96 KB that fills
+// shared memory.
+//
+// Bound by the tensor pipe at best: a key tile costs 2 x (12 + 8) instructions
+// of 64 cycles, the softmax of a tile about 1000 cycles of its warpgroup.
+#include <math.h>
+
+#include "kda_common.cuh"
+#include "kda_paths.h"
+#include "kda_sm100_ops.cuh"
+#include "kda_tensor_map.h"
+
+namespace kda {
+using namespace sm100;
+
+constexpr int kLpRows = 256;                  // query rows of a CTA
+constexpr int kLpKeys = 128;
+constexpr uint32_t kLpPiece = 16384;
+constexpr int kLpSlots = 8;
+constexpr uint32_t kLpOffRing = 6 * kLpPiece, kLpOffSmall = kLpOffRing + kLpSlots * kLpPiece;
+constexpr uint32_t kLpSmem = kLpOffSmall + 1024 + 256;
+constexpr int kLpThreads = 384;
+constexpr float kLpUnset = -1e30f, kLpSlack = 8.f;
+
+struct LpArgs {
+    int N, H, causal;
+    float scale;
+    int64_t tq, tk;
+    const int32_t *cu_q, *cu_k;
+    __nv_bfloat16* out;
+    float* lse;
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(kLpThreads, 1)
+kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
+                      const LpArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    uint64_t* full = (uint64_t*)(mem + kLpOffSmall);
+    uint64_t *empty = full + kLpSlots, *q_full = empty + kLpSlots, *s_full = q_full + 1, *p_full = s_full + 2,
+             *o_full = p_full + 2;
+    uint32_t* tmem_at = (uint32_t*)(o_full + 2);
+    int* where = (int*)(tmem_at + 1);          // sequence, its tile of rows (-1: none)
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
+    // Which rows: the blocks of a head go from the last tile of the last sequence (which sees most) to the first.
+    if (warp == 0) {
+        int n = 0, tile = -1;
+        if (a.cu_q == nullptr) {
+            const int64_t t = (a.tq + kLpRows - 1) / kLpRows - 1 - blockIdx.x;
+            tile = t >= 0 ? (int)t : -1;
+        } else {
+            int64_t total = 0;
+            for (int pass = 0; pass < 2; ++pass) {
+                const int64_t want = total - 1 - blockIdx.x;           // pass 1: index from the front
+                int64_t before = 0;
+                for (int b = 0; b < a.N; b += 32) {
+                    const int i = b + lane;
+                    const int64_t len = i < a.N ? (int64_t)a.cu_q[i + 1] - a.cu_q[i] : 0;
+                    const int t = len > 0 ? (int)((len + kLpRows - 1) / kLpRows) : 0;
+                    int x = t;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, x, o);
+                        if (lane >= o) x += y;
+                    }
+                    if (pass == 1) {
+                        const uint32_t hit = want < 0 ? 0u : __ballot_sync(0xffffffffu, before + x > want);
+                        if (hit) {
+                            const int l = __ffs(hit) - 1;
+                            n = b + l;
+                            tile = (int)(want - before - (__shfl_sync(0xffffffffu, x, l) - __shfl_sync(0xffffffffu, t, l)));
+                            break;
+                        }
+                    }
+                    before += __shfl_sync(0xffffffffu, x, 31);
+                }
+                if (pass == 0) total = before;
+            }
+        }
+        if (lane == 0) { where[0] = n; where[1] = tile; }
+        tmem_alloc(tmem_at, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (uint64_t* b = full; b < p_full; ++b) mbar_init(b, 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+        fence_mbar_init();
+    }
+    if (blockIdx.x == 0 && head == 0) check_cu_seqlens(a.cu_q, a.cu_k, a.N, a.tq, a.tk, a.status);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
+
+    const int n = where[0], tile = where[1];
+    int64_t q0 = 0, k0 = 0, lq = a.tq, lk = a.tk;
+    if (a.cu_q) {
+        q0 = a.cu_q[n]; lq = (int64_t)a.cu_q[n + 1] - q0;
+        k0 = a.cu_k[n]; lk = (int64_t)a.cu_k[n + 1] - k0;
+        if (k0 < 0 || lk < 0 || k0 + lk > a.tk) lk = 0;                // malformed: reported by block 0
+        if (q0 < 0 || q0 + lq > a.tq) lq = 0;
+    }
+    const int64_t r0 = (int64_t)tile * kLpRows;                        // first row within the sequence
+    // keys that the last row of each tile sees, in tiles
+    int tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t f = r0 + i * 128;
+        const int64_t last = (f + 128 < lq ? f + 128 : lq) - 1;
+        int64_t seen = tile < 0 || f >= lq ? 0 : a.causal ? lk - lq + last + 1 : lk;
+        seen = seen < 0 ? 0 : seen > lk ? lk : seen;
+        tiles[i] = (int)((seen + kLpKeys - 1) / kLpKeys);
+    }
+    const int steps = max(tiles[0], tiles[1]);
+
+    if (warp < 8) {                                                    // ---------------- softmax
+        regs_inc<232>();
+        const int i = warp >> 2, quarter = warp & 3;
+        const int64_t row = r0 + i * 128 + quarter * 32 + lane;        // within the sequence
+        const int64_t seen = a.causal ? lk - lq + row : lk - 1;        // last key it sees
+        const uint32_t ts = tmem_addr(tmem, 32 * quarter, i * 128), to = ts + 256;
+        const float sc = a.scale * 1.4426950408889634f;
+        float ref = kLpUnset, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < tiles[i]; ++j) {
+            ok = mbar_wait_warp(&s_full[i], j & 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            float x[128];
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, *(float(*)[32])(x + c));
+            tmem_wait_ld();
+            tmem_ready(x);
+            const int64_t first = (int64_t)j * kLpKeys;
+            if (first + kLpKeys - 1 > (seen < lk - 1 ? seen : lk - 1)) {
+                const int64_t end = seen < lk - 1 ? seen : lk - 1;
+                const int keep = end < first ? 0 : (int)(end - first + 1);
+#pragma unroll
+                for (int c = 0; c < 128; ++c) x[c] = c < keep ? x[c] : -INFINITY;
+            }
+            float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < 128; c += 4) {
+                m[0] = fmaxf(m[0], x[c]); m[1] = fmaxf(m[1], x[c + 1]);
+                m[2] = fmaxf(m[2], x[c + 2]); m[3] = fmaxf(m[3], x[c + 3]);
+            }
+            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sc;
+            const bool move = top > ref + kLpSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                const float now = move ? top : ref;
+                const float f = ex2(ref - now);
+                ref = now;
+                l *= f;
+                if (j > 0) {                                           // the products before S are complete: O is still
+                    for (int c = 0; c < 128; c += 32) {
+                        float o[32];
+                        tmem_ld32(to + c, o);
+                        tmem_wait_ld();
+                        tmem_ready(o);
+                        uint32_t b[32];
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) b[q] = __float_as_uint(o[q] * f);
+                        tmem_st32(to + c, b);
+                    }
+                }
+            }
+            const f32x2 sc2 = pack2(sc, sc), nref = pack2(-ref, -ref);
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t b[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(x[c + 2 * q], x[c + 2 * q + 1]), sc2, nref), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum[(q & 1) * 2] += p0;
+                    sum[(q & 1) * 2 + 1] += p1;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);    // the product's operand: 8 bits
+                    b[q] = *(const uint32_t*)&h;
+                }
+                tmem_st32(ts + c / 2, b);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            // Weight 0 times what lies behind the last key: make that 0.  Done by the first tile that uses it.
+            if (j + 1 == steps && lk - first < kLpKeys && (i == 0 || j >= tiles[0])) {
+                const int r = quarter * 32 + lane;
+                const uint32_t u = 5 * j + 3 + r / 64;
+                if (r >= lk - first) {
+                    if (!mbar_wait_spin(&full[u % kLpSlots], (u / kLpSlots) & 1)) record_status(a.status, KDA_ERR_TIMEOUT);
+                    uint8_t* at = mem + kLpOffRing + u % kLpSlots * kLpPiece + r % 64 * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        *(uint4*)(at + 16 * q) = make_uint4(0, 0, 0, 0);
+                        *(uint4*)(at + 8192 + 16 * q) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[i]);
+        }
+        if (ok && tiles[i] > 0) {
+            ok = mbar_wait_warp(&o_full[i], 0);
+            tc_fence_after_sync();
+        }
+        if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const bool live = tile >= 0 && row < lq;
+        __nv_bfloat16* dst = a.out + ((q0 + (live ? row : 0)) * a.H + head) * 128;
+        for (int c = 0; c < 128; c += 32) {
+            float o[32];
+            if (tiles[i] > 0) {
+                tmem_ld32(to + c, o);
+                tmem_wait_ld();
+                tmem_ready(o);
+            }
+            if (live) {
+#pragma unroll
+                for (int q = 0; q < 32; q += 8) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        b[e] = tiles[i] > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
+                    *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+            }
+        }
+        if (live && a.lse)
+            a.lse[(q0 + row) * a.H + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+    } else {
+        regs_dec<40>();
+        if (warp == 8) {                                               // ---------------- producer
+            if (lane == 0 && steps > 0) {
+                mbar_arrive_expect_tx(q_full, 6 * kLpPiece);
+                for (int p = 0; p < 6; ++p)
+                    tma_load_3d_at(base + p * kLpPiece, &map_q, p % 3 * 64, head, (int)(q0 + r0) + p / 3 * 128, smem_u32(q_full));
+                bool ok = true;
+                uint32_t u = 0;
+                for (int j = 0; j < steps && ok; ++j) {
+                    const int key = (int)k0 + j * kLpKeys;
+                    for (int p = 0; p < 5; ++p, ++u) {
+                        const uint32_t s = u % kLpSlots, ph = (u / kLpSlots) & 1;
+                        if (u >= kLpSlots && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
+                        const uint32_t at = base + kLpOffRing + s * kLpPiece, bar = smem_u32(&full[s]);
+                        mbar_arrive_expect_tx(&full[s], kLpPiece);
+                        if (p < 2) tma_load_3d_at(at, &map_k, p * 64, head, key, bar);
+                        else if (p == 2) tma_load_2d(at, &map_r, 0, key, bar);
+                        else {
+                            tma_load_3d_at(at, &map_v, 0, head, key + (p - 3) * 64, bar);
+                            tma_load_3d_at(at + 8192, &map_v, 64, head, key + (p - 3) * 64, bar);
+                        }
+                    }
+                }
+                if (!ok) drain_copies();
+            }
+        } else if (warp == 9 && steps > 0) {                           // ---------------- matrix instructions
+            const uint32_t idesc_s = idesc_bf16(128, 128), idesc_o = idesc_bf16(128, 128, 0, 1);
+            bool ok = mbar_wait_warp(q_full, 0);
+            tc_fence_after_sync();
+            auto scores = [&](int i, int j) {                          // S_j(i); the last user of K_j frees it
+                const bool free = i == 1 || j >= tiles[1];
+                for (int p = 0; p < 3 && ok; ++p) {
+                    const uint32_t u = 5 * j + p, s = u % kLpSlots;
+                    if (!(ok = mbar_wait_warp(&full[s], (u / kLpSlots) & 1))) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = sdesc_k_sw128(base + (i * 3 + p) * kLpPiece);
+                    const uint64_t db = sdesc_k_sw128(base + kLpOffRing + s * kLpPiece);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_bf16_ss(tmem + i * 128, da + 2 * k, db + 2 * k, idesc_s, p > 0 || k > 0);
+                        if (free) mma_commit(&empty[s]);
+                        if (p == 2) mma_commit(&s_full[i]);
+                    }
+                    __syncwarp();
+                }
+            };
+            if (ok && tiles[0] > 0) scores(0, 0);
+            if (ok && tiles[1] > 0) scores(1, 0);
+            for (int j = 0; j < steps && ok; ++j) {
+#pragma unroll 1
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (j >= tiles[i]) continue;
+                    const bool free = i == 1 || j >= tiles[1];
+                    if (!(ok = mbar_wait_warp(&p_full[i], j & 1))) break;
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        const uint32_t u = 5 * j + 3 + h, s = u % kLpSlots;
+                        if (!(ok = mbar_wait_warp(&full[s], (u / kLpSlots) & 1))) break;
+                        tc_fence_after_sync();
+                        const uint64_t db = sdesc(base + kLpOffRing + s * kLpPiece, 8192, 1024, 2);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + h * 32 + k * 8, db + k * (2048 / 16),
+                                            idesc_o, j > 0 || h > 0 || k > 0);
+                            if (free) mma_commit(&empty[s]);
+                            if (h == 1 && j + 1 == tiles[i]) mma_commit(&o_full[i]);
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && j + 1 < tiles[i]) scores(i, j + 1);
+                }
+            }
+            if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host
+bool latent_prefill_tc_takes(const LatentPrefillArgs& d) {
+    const int64_t st[7] = {d.q_ts, d.q_hs, d.k_ts, d.k_hs, d.v_ts, d.v_hs, d.r_ts};
+    for (int i = 0; i < 7; ++i)
+        if (st[i] <= 0 || st[i] % 8 || st[i] >= (1ll << 38)) return false;
+    return d.dtype == KDA_BF16 && d.dk == 128 && d.dr == 64 && d.dv == 128 && d.tk > 0 &&
+           (((uintptr_t)d.q | (uintptr_t)d.k | (uintptr_t)d.r | (uintptr_t)d.v | (uintptr_t)d.out) & 15) == 0;
+}
+
+cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& d, cudaStream_t stream) {
+    static bool ready = false;
+    if (!ready) {
+        cudaError_t e = cudaFuncSetAttribute(kda_latent_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpSmem);
+        if (e != cudaSuccess) return e;
+        ready = true;
+    }
+    auto map3 = [&](CUtensorMap* m, const void* p, int width, int64_t tokens, int64_t ts, int64_t hs, int rows) {
+        const uint64_t dims[3] = {(uint64_t)width, (uint64_t)d.H, (uint64_t)tokens};
+        const uint64_t str[2] = {(uint64_t)hs * 2, (uint64_t)ts * 2};
+        const uint32_t box[3] = {64, 1, (uint32_t)rows};
+        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, str, box);
+    };
+    CUtensorMap mq, mk, mr, mv;
+    const uint64_t rd[2] = {64, (uint64_t)d.tk}, rs[1] = {(uint64_t)d.r_ts * 2};
+    const uint32_t rb[2] = {64, kLpKeys};
+    if (!map3(&mq, d.q, 192, d.tq, d.q_ts, d.q_hs, 128) || !map3(&mk, d.k, 128, d.tk, d.k_ts, d.k_hs, kLpKeys) ||
+        !map3(&mv, d.v, 128, d.tk, d.v_ts, d.v_hs, 64) ||
+        !make_map(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.r, rd, rs, rb)) return cudaErrorInvalidValue;
+    LpArgs a;
+    a.N = d.N; a.H = d.H; a.causal = d.causal; a.scale = d.scale; a.tq = d.tq; a.tk = d.tk; a.cu_q = d.cu_q;
+    a.cu_k = d.cu_k; a.out = (__nv_bfloat16*)d.out; a.lse = d.lse; a.status = d.status;
+    // at most this many tiles of rows, whatever the lengths
+    const int64_t blocks = d.cu_q ? d.tq / kLpRows + min64(d.N, d.tq) : (d.tq + kLpRows - 1) / kLpRows;
+    kda_latent_prefill_tc<<<dim3((unsigned)blocks, d.H), kLpThreads, kLpSmem, stream>>>(mq, mk, mr, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -107,6 +107,8 @@ struct LatentPrefillArgs {
     int32_t* status;                 // OK on entry
 };
 cudaError_t latent_prefill_simt_launch(const LatentPrefillArgs& a, cudaStream_t stream);
+bool latent_prefill_tc_takes(const LatentPrefillArgs& a);    // bf16, 128 + 64 / 128 channels, 16-byte rows
+cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& a, cudaStream_t stream);
 
 struct LatentDecodeArgs {
     int dtype, N, H, Lq, dk, dr;
