@@ -57,6 +57,7 @@ def _declare():
 _declare()
 _byref = ctypes.byref
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 
 
@@ -102,11 +103,6 @@ def kda_latent_status(desc: KdaLatentDesc, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ checks
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _tensor(t, name: str, dtype, dim: int, device):
     """A tensor of `dim` dimensions on `device` whose last one is dense."""
     if t.dtype != dtype or t.dim() != dim or t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1):
@@ -121,10 +117,9 @@ def _dense(t, name: str, dtype, shape, device):
 
 
 def _device(t, name: str):
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device: got {d}")
-    return d
+    if not t.is_cuda or t.get_device() != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device: got {t.device}")
+    return t.device
 
 
 def _row_stride(t, width: int) -> int:
@@ -157,12 +152,16 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, normed: bool =
     not asked for is None."""
     dev = _device(x, "x")
     dt = B._DTYPES.get(x.dtype)
-    _need(dt is not None and x.dim() >= 1, f"x must be float32 or bfloat16 rows: got {x.dtype}, {tuple(x.shape)}")
-    _need(normed or quantize or residual is not None, "nothing to compute: normed, quantize or a residual")
+    if dt is None or x.dim() < 1:
+        raise ValueError(f"x must be float32 or bfloat16 rows: got {x.dtype}, {tuple(x.shape)}")
+    if not (normed or quantize or residual is not None):
+        raise ValueError("nothing to compute: normed, quantize or a residual")
     shape, dim = x.shape, x.shape[-1]
-    _need(dim >= 1, "rows must have an element")
+    if dim < 1:
+        raise ValueError("rows must have an element")
     if x.dim() != 2:
-        _need(x.is_contiguous(), "x must be contiguous unless it is 2-D")
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous unless it is 2-D")
         x2 = x.view(-1, dim)
     else:
         _tensor(x, "x", x.dtype, 2, dev)
@@ -172,7 +171,8 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, normed: bool =
     if weight is not None:
         _dense(weight, "weight", x.dtype, (dim,), dev)
     if residual is not None:
-        _need(residual.shape == shape, f"residual must have x's shape {tuple(shape)}: got {tuple(residual.shape)}")
+        if residual.shape != shape:
+            raise ValueError(f"residual must have x's shape {tuple(shape)}: got {tuple(residual.shape)}")
         if residual.dim() == 2:
             _tensor(residual, "residual", x.dtype, 2, dev)
             r_stride = _row_stride(residual, dim)
@@ -184,7 +184,8 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, normed: bool =
         if residual is not None and residual_out is None:
             residual_out = torch.empty(shape, dtype=x.dtype, device=dev)
         elif residual_out is not None:
-            _need(residual is not None, "residual_out without a residual")
+            if residual is None:
+                raise ValueError("residual_out without a residual")
             _dense(residual_out, "residual_out", x.dtype, shape, dev)
         if normed:
             y = torch.empty(shape, dtype=x.dtype, device=dev)
@@ -213,7 +214,8 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out: Optional[torch.Tensor] = None, ou
     _tensor(a, "a", _F8, 2, dev)
     _tensor(b, "b", _F8, 2, dev)
     (m, k), (n, kb_) = a.shape, b.shape
-    _need(kb_ == k and k >= 1, f"a and b must have rows of the same length: got {k} and {kb_}")
+    if kb_ != k or k < 1:
+        raise ValueError(f"a and b must have rows of the same length: got {k} and {kb_}")
     kb = (k + 127) // 128
     _dense(a_scale, "a_scale", _F32, (m, kb), dev)
     _dense(b_scale, "b_scale", _F32, ((n + 127) // 128, kb), dev)
@@ -224,10 +226,12 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out: Optional[torch.Tensor] = None, ou
         ldc = n
     else:
         _tensor(out, "out", out.dtype, 2, dev)
-        _need(out.shape == (m, n), f"out must be {(m, n)}: got {tuple(out.shape)}")
+        if out.shape != (m, n):
+            raise ValueError(f"out must be {(m, n)}: got {tuple(out.shape)}")
         ldc = _row_stride(out, n)
     dt = B._DTYPES.get(out.dtype)
-    _need(dt is not None, f"the output must be float32 or bfloat16: got {out.dtype}")
+    if dt is None:
+        raise ValueError(f"the output must be float32 or bfloat16: got {out.dtype}")
     if m and n:
         rc = lib.kda_matmul_fp8(_byref(KdaMatmulDesc(m, n, k, _row_stride(a, k), _row_stride(b, k), ldc, dt, flags)),
                                 a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
@@ -261,7 +265,8 @@ def latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q=None, cu_seqlens_k=None, *
     ``latent_status``."""
     dev = _device(q, "q")
     dt = B._DTYPES.get(q.dtype)
-    _need(dt is not None, f"q must be float32 or bfloat16: got {q.dtype}")
+    if dt is None:
+        raise ValueError(f"q must be float32 or bfloat16: got {q.dtype}")
     for t, name in ((q, "q"), (k_nope, "k_nope"), (v, "v")):
         _tensor(t, name, q.dtype, 3, dev)
     tq, h, dqk = q.shape
@@ -271,11 +276,13 @@ def latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q=None, cu_seqlens_k=None, *
     if k_rope is not None:
         _tensor(k_rope, "k_rope", q.dtype, 2, dev)
         dr = k_rope.shape[1]
-        _need(k_rope.shape[0] == tk, "k_rope must have k_nope's tokens")
-    _need(hk == h and v.shape[:2] == k_nope.shape[:2] and dk + dr == dqk,
-          f"shapes do not fit: q {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}, v {tuple(v.shape)}, d_rope {dr}")
+        if k_rope.shape[0] != tk:
+            raise ValueError("k_rope must have k_nope's tokens")
+    if hk != h or v.shape[0] != tk or v.shape[1] != h or dk + dr != dqk:
+        raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}, v {tuple(v.shape)}, d_rope {dr}")
     n = 1
-    _need((cu_seqlens_q is None) == (cu_seqlens_k is None), "both cu_seqlens or neither")
+    if (cu_seqlens_q is None) != (cu_seqlens_k is None):
+        raise ValueError("both cu_seqlens or neither")
     if cu_seqlens_q is not None:
         n = cu_seqlens_q.shape[0] - 1
         _dense(cu_seqlens_q, "cu_seqlens_q", _I32, (n + 1,), dev)
@@ -318,7 +325,8 @@ def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional
     rank]``, lse fp32 ``[N, (Lq,) H]``)."""
     dev = _device(q, "q")
     dt = B._DTYPES.get(q.dtype)
-    _need(dt is not None, f"q must be float32 or bfloat16: got {q.dtype}")
+    if dt is None:
+        raise ValueError(f"q must be float32 or bfloat16: got {q.dtype}")
     single = q.dim() == 3
     _tensor(q, "q", q.dtype, 3 if single else 4, dev)
     if single:
@@ -330,13 +338,15 @@ def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional
         if lq == 1:
             q_ts = q.stride(0)
         else:
-            _need(n <= 1 or q.stride(0) == lq * q_ts, "q's sequences and queries must form one strided dimension")
-    _need(cache.dim() == 3 and cache.dtype == q.dtype and cache.device == dev and cache.shape[2] == w and
-          cache.stride(2) == 1 and cache.stride(1) == w,
-          f"cache must be a [pages, page_size, {w}] {q.dtype} tensor on {dev} with dense pages")
+            if n > 1 and q.stride(0) != lq * q_ts:
+                raise ValueError("q's sequences and queries must form one strided dimension")
+    if not (cache.dim() == 3 and cache.dtype == q.dtype and cache.device == dev and cache.shape[2] == w and cache.stride(2) == 1 and cache.stride(1) == w):
+        raise ValueError(f"cache must be a [pages, page_size, {w}] {q.dtype} tensor on {dev} with dense pages")
     rank = w - 64 if rank is None else rank
-    _need(1 <= rank <= w, f"rank must be within 1 .. {w}: got {rank}")
-    _need(page_table.dim() == 2 and page_table.shape[0] == n, f"page_table must be [{n}, max_pages]")
+    if not 1 <= rank <= w:
+        raise ValueError(f"rank must be within 1 .. {w}: got {rank}")
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError(f"page_table must be [{n}, max_pages]")
     _dense(page_table, "page_table", _I32, page_table.shape, dev)
     _dense(lengths, "lengths", _I32, (n,), dev)
     pages, size = cache.shape[0], cache.shape[1]

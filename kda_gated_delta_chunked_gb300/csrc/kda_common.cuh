@@ -54,18 +54,22 @@ __device__ __forceinline__ int chunk_owner(const int32_t* chunk_first, int N, in
     return lo;
 }
 
-// Run by all threads of one block: records KDA_ERR_BAD_SEQLENS unless both
-// arrays (nullptr: one sequence, nothing to check) run 0 = c_0 <= ... <= c_N = total.
+// Run by all threads of one block: writes the status word, KDA_ERR_BAD_SEQLENS
+// unless both arrays (nullptr: one sequence, nothing to check) run 0 = c_0 <=
+// ... <= c_N = total.  The block is of the first ones to run; what others
+// record (a wait that gave up) comes seconds later.
 __device__ __forceinline__ void check_cu_seqlens(const int32_t* cu_q, const int32_t* cu_k, int N, int64_t tq,
                                                  int64_t tk, int32_t* status) {
-    if (!cu_q) return;
-    bool bad = false;
-    for (int n = threadIdx.x; n <= N; n += blockDim.x) {
-        if (n == 0) bad |= cu_q[0] != 0 || cu_k[0] != 0;
-        else bad |= cu_q[n] < cu_q[n - 1] || cu_k[n] < cu_k[n - 1];
-        if (n == N) bad |= cu_q[N] != tq || cu_k[N] != tk;
+    int bad = 0;
+    if (cu_q) {
+        for (int n = threadIdx.x; n <= N; n += blockDim.x) {
+            if (n == 0) bad |= cu_q[0] != 0 || cu_k[0] != 0;
+            else bad |= cu_q[n] < cu_q[n - 1] || cu_k[n] < cu_k[n - 1];
+            if (n == N) bad |= cu_q[N] != tq || cu_k[N] != tk;
+        }
     }
-    if (bad) record_status(status, KDA_ERR_BAD_SEQLENS);
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *status = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
 }
 
 }  // namespace kda

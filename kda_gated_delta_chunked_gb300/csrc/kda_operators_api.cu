@@ -182,9 +182,8 @@ int kda_latent_prefill(const kda_latent_desc* d, const void* q, const void* k_no
     a.q = q; a.k = k_nope; a.r = k_rope; a.v = v; a.cu_q = cu_seqlens_q; a.cu_k = cu_seqlens_k;
     a.out = out; a.lse = lse; a.status = (int32_t*)d->workspace;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t err = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
     const bool tc = (d->flags & KDA_FLAG_CUDA_CORE_PREFILL) == 0 && latent_prefill_tc_takes(a);
-    if (err == cudaSuccess) err = tc ? latent_prefill_tc_launch(a, s) : latent_prefill_simt_launch(a, s);
+    const cudaError_t err = tc ? latent_prefill_tc_launch(a, s) : latent_prefill_simt_launch(a, s);
     return err == cudaSuccess ? KDA_OK : cuda_fail(err);
 }
 

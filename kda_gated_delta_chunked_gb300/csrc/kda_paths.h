@@ -104,7 +104,7 @@ struct LatentPrefillArgs {
     const int32_t *cu_q, *cu_k;      // nullptr: one sequence
     void* out;
     float* lse;
-    int32_t* status;                 // OK on entry
+    int32_t* status;                 // written by the kernels
 };
 cudaError_t latent_prefill_simt_launch(const LatentPrefillArgs& a, cudaStream_t stream);
 bool latent_prefill_tc_takes(const LatentPrefillArgs& a);    // bf16, 128 + 64 / 128 channels, 16-byte rows
@@ -119,7 +119,7 @@ struct LatentDecodeArgs {
     const int32_t *table, *lens;
     void* out;
     float* lse;
-    int32_t* status;                 // OK on entry (CUDA cores), written whole (tensor cores)
+    int32_t* status;                 // OK on entry (CUDA cores), written by the kernels (tensor cores)
     void* scratch;
 };
 cudaError_t latent_decode_simt_launch(const LatentDecodeArgs& a, cudaStream_t stream);
