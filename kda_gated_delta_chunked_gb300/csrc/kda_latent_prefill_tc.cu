@@ -61,7 +61,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     uint32_t* tmem_at = (uint32_t*)(o_full + 2);
     int* where = (int*)(tmem_at + 1);          // sequence, its tile of rows (-1: none)
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, head = blockIdx.y;
     // Which rows: the blocks of a head go from the last tile of the last sequence (which sees most) to the first.
     if (warp == 0) {
         int n = 0, tile = -1;
@@ -112,7 +112,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
 
-    const int n = where[0], tile = where[1];
+    const int n = uniform(where[0]), tile = uniform(where[1]);
     int64_t q0 = 0, k0 = 0, lq = a.tq, lk = a.tk;
     if (a.cu_q) {
         q0 = a.cu_q[n]; lq = (int64_t)a.cu_q[n + 1] - q0;
@@ -129,7 +129,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         const int64_t last = (f + 128 < lq ? f + 128 : lq) - 1;
         int64_t seen = tile < 0 || f >= lq ? 0 : a.causal ? lk - lq + last + 1 : lk;
         seen = seen < 0 ? 0 : seen > lk ? lk : seen;
-        tiles[i] = (int)((seen + kLpKeys - 1) / kLpKeys);
+        tiles[i] = uniform((int)((seen + kLpKeys - 1) / kLpKeys));
     }
     const int steps = max(tiles[0], tiles[1]);
 
