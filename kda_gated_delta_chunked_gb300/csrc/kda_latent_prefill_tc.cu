@@ -55,9 +55,9 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t* mem = raw + (base - smem_u32(raw));
-    uint64_t* full = (uint64_t*)(mem + kLpOffSmall);
-    uint64_t *empty = full + kLpSlots, *q_full = empty + kLpSlots, *s_full = q_full + 1, *p_full = s_full + 2,
-             *o_full = p_full + 2;
+    uint64_t* q_full = (uint64_t*)(mem + kLpOffSmall);
+    uint64_t *kv_full = q_full + 1, *kv_empty = kv_full + 4;   // [2 steps][K, V]
+    uint64_t *s_full = kv_empty + 4, *p_full = s_full + 2, *o_full = p_full + 2;
     uint32_t* tmem_at = (uint32_t*)(o_full + 2);
     int* where = (int*)(tmem_at + 1);          // sequence, its tile of rows (-1: none)
 
@@ -102,8 +102,9 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        for (uint64_t* b = full; b < p_full; ++b) mbar_init(b, 1);
-        for (int i = 0; i < 2; ++i) { mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+        mbar_init(q_full, 1);
+        for (int i = 0; i < 4; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
         fence_mbar_init();
     }
     if (blockIdx.x == 0 && head == 0) check_cu_seqlens(a.cu_q, a.cu_k, a.N, a.tq, a.tk, a.status);
@@ -135,14 +136,14 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
 
     if (warp < 8) {                                                    // ---------------- softmax
         regs_inc<232>();
-        const int i = warp >> 2, quarter = warp & 3;
+        const int i = warp >> 2, quarter = warp & 3, mine = i == 0 ? tiles[0] : tiles[1];
         const int64_t row = r0 + i * 128 + quarter * 32 + lane;        // within the sequence
         const int64_t seen = a.causal ? lk - lq + row : lk - 1;        // last key it sees
         const uint32_t ts = tmem_addr(tmem, 32 * quarter, i * 128), to = ts + 256;
         const float sc = a.scale * 1.4426950408889634f;
         float ref = kLpUnset, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < tiles[i]; ++j) {
+        for (int j = 0; j < mine; ++j) {
             ok = mbar_wait_warp(&s_full[i], j & 1);
             if (!ok) break;
             tc_fence_after_sync();
@@ -209,7 +210,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 const int r = quarter * 32 + lane;
                 const uint32_t u = 5 * j + 3 + r / 64;
                 if (r >= lk - first) {
-                    if (!mbar_wait_spin(&full[u % kLpSlots], (u / kLpSlots) & 1)) record_status(a.status, KDA_ERR_TIMEOUT);
+                    if (!mbar_wait_spin(&kv_full[(j & 1) * 2 + 1], (j >> 1) & 1)) record_status(a.status, KDA_ERR_TIMEOUT);
                     uint8_t* at = mem + kLpOffRing + u % kLpSlots * kLpPiece + r % 64 * 128;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -223,7 +224,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[i]);
         }
-        if (ok && tiles[i] > 0) {
+        if (ok && mine > 0) {
             ok = mbar_wait_warp(&o_full[i], 0);
             tc_fence_after_sync();
         }
@@ -233,7 +234,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         __nv_bfloat16* dst = a.out + ((q0 + (live ? row : 0)) * a.H + head) * 128;
         for (int c = 0; c < 128; c += 32) {
             float o[32];
-            if (tiles[i] > 0) {
+            if (mine > 0) {
                 tmem_ld32(to + c, o);
                 tmem_wait_ld();
                 tmem_ready(o);
@@ -244,7 +245,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     uint32_t b[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        b[e] = tiles[i] > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
+                        b[e] = mine > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
                     *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
             }
@@ -263,10 +264,13 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 for (int j = 0; j < steps && ok; ++j) {
                     const int key = (int)k0 + j * kLpKeys;
                     for (int p = 0; p < 5; ++p, ++u) {
-                        const uint32_t s = u % kLpSlots, ph = (u / kLpSlots) & 1;
-                        if (u >= kLpSlots && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
-                        const uint32_t at = base + kLpOffRing + s * kLpPiece, bar = smem_u32(&full[s]);
-                        mbar_arrive_expect_tx(&full[s], kLpPiece);
+                        if (u >= kLpSlots) {                           // the piece this one takes the place of
+                            const uint32_t o = u - kLpSlots, oj = o / 5, g = (oj & 1) * 2 + (o % 5 >= 3);
+                            if (!(ok = mbar_wait_spin(&kv_empty[g], (oj >> 1) & 1))) break;
+                        }
+                        uint64_t* f = &kv_full[(j & 1) * 2 + (p >= 3)];
+                        const uint32_t at = base + kLpOffRing + u % kLpSlots * kLpPiece, bar = smem_u32(f);
+                        if (p == 0 || p == 3) mbar_arrive_expect_tx(f, (p == 0 ? 3 : 2) * kLpPiece);
                         if (p < 2) tma_load_3d_at(at, &map_k, p * 64, head, key, bar);
                         else if (p == 2) tma_load_2d(at, &map_r, 0, key, bar);
                         else {
@@ -277,51 +281,58 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 if (!ok) drain_copies();
             }
-        } else if (warp == 9 && steps > 0) {                           // ---------------- matrix instructions
+        } else if (warp == 9 && steps > 0) {
+            // Matrix instructions.  One warp for both tiles keeps them in turn; whole products behind one wait
+            // each, since a wait costs about 90 cycles and instruction fetches compete with the softmax's.
             const uint32_t idesc_s = idesc_bf16(128, 128), idesc_o = idesc_bf16(128, 128, 0, 1);
+            const uint64_t dq = sdesc_k_sw128(base), dk = sdesc_k_sw128(base + kLpOffRing);
+            const uint64_t dv = sdesc(base + kLpOffRing, 8192, 1024, 2);
+            const int n0 = tiles[0], n1 = tiles[1];
             bool ok = mbar_wait_warp(q_full, 0);
-            tc_fence_after_sync();
-            auto scores = [&](int i, int j) {                          // S_j(i); the last user of K_j frees it
-                const bool free = i == 1 || j >= tiles[1];
-                for (int p = 0; p < 3 && ok; ++p) {
-                    const uint32_t u = 5 * j + p, s = u % kLpSlots;
-                    if (!(ok = mbar_wait_warp(&full[s], (u / kLpSlots) & 1))) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = sdesc_k_sw128(base + (i * 3 + p) * kLpPiece);
-                    const uint64_t db = sdesc_k_sw128(base + kLpOffRing + s * kLpPiece);
-                    if (elect_one()) {
+            for (int j = -1; j < steps && ok; ++j) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_bf16_ss(tmem + i * 128, da + 2 * k, db + 2 * k, idesc_s, p > 0 || k > 0);
-                        if (free) mma_commit(&empty[s]);
-                        if (p == 2) mma_commit(&s_full[i]);
-                    }
-                    __syncwarp();
-                }
-            };
-            if (ok && tiles[0] > 0) scores(0, 0);
-            if (ok && tiles[1] > 0) scores(1, 0);
-            for (int j = 0; j < steps && ok; ++j) {
-#pragma unroll 1
-                for (int i = 0; i < 2 && ok; ++i) {
-                    if (j >= tiles[i]) continue;
-                    const bool free = i == 1 || j >= tiles[1];
-                    if (!(ok = mbar_wait_warp(&p_full[i], j & 1))) break;
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        const uint32_t u = 5 * j + 3 + h, s = u % kLpSlots;
-                        if (!(ok = mbar_wait_warp(&full[s], (u / kLpSlots) & 1))) break;
+                for (int i = 0; i < 2; ++i) {
+                    const int mine = i == 0 ? n0 : n1;
+                    const uint32_t ts = tmem + i * 128, to = ts + 256;
+                    if (j >= 0 && j < mine) {                          // O += P_j V_j
+                        ok = mbar_wait_warp(&p_full[i], j & 1);
+                        if (ok && (i == 0 || j >= n0)) ok = mbar_wait_warp(&kv_full[(j & 1) * 2 + 1], (j >> 1) & 1);
+                        if (!ok) break;
                         tc_fence_after_sync();
-                        const uint64_t db = sdesc(base + kLpOffRing + s * kLpPiece, 8192, 1024, 2);
                         if (elect_one()) {
+                            const uint32_t u = 5 * j + 3;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + h * 32 + k * 8, db + k * (2048 / 16),
-                                            idesc_o, j > 0 || h > 0 || k > 0);
-                            if (free) mma_commit(&empty[s]);
-                            if (h == 1 && j + 1 == tiles[i]) mma_commit(&o_full[i]);
+                            for (int h = 0; h < 2; ++h) {
+                                const uint64_t db = dv + (u + h) % kLpSlots * (kLpPiece / 16);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16_ts(to, ts + h * 32 + k * 8, db + k * (2048 / 16), idesc_o, j > 0 || h > 0 || k > 0);
+                            }
+                            if (i == 1 || j >= n1) mma_commit(&kv_empty[(j & 1) * 2 + 1]);   // its last user
+                            if (j + 1 == mine) mma_commit(&o_full[i]);
                         }
                         __syncwarp();
                     }
-                    if (ok && j + 1 < tiles[i]) scores(i, j + 1);
+                    const int jn = j + 1;                              // S_{j+1}: behind the product that reads P_j in its place
+                    if (jn < mine) {
+                        if (i == 0 || jn >= n0) ok = mbar_wait_warp(&kv_full[(jn & 1) * 2], (jn >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t u = 5 * jn;
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const uint64_t da = dq + (i * 3 + p) * (kLpPiece / 16);
+                                const uint64_t db = dk + (u + p) % kLpSlots * (kLpPiece / 16);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16_ss(ts, da + 2 * k, db + 2 * k, idesc_s, p > 0 || k > 0);
+                            }
+                            mma_commit(&s_full[i]);
+                            if (i == 1 || jn >= n1) mma_commit(&kv_empty[(jn & 1) * 2]);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
