@@ -75,18 +75,18 @@ __device__ __forceinline__ int ld_len(const LdArgs& a, int n) {
 }
 __device__ __forceinline__ int ld_tiles(const LdArgs& a, int n) { return (ld_len(a, n) + kLdTile - 1) / kLdTile; }
 
-// Position in the tiles of a CTA's range.
+// Position in the tiles of a CTA's range; the same in all lanes of a warp, which call it together.
 struct LdWalk {
     int n, j, tiles, left;
     bool first;                                // first tile of a segment
     int from;                                  // its tile
     __device__ __forceinline__ bool last() const { return j + 1 == tiles || left == 1; }
     __device__ __forceinline__ void settle(const LdArgs& a) {      // on to the next sequence that has tiles
-        while (left > 0 && j >= tiles) { ++n; j = 0; tiles = ld_tiles(a, n); }
+        while (left > 0 && j >= tiles) { ++n; j = 0; tiles = uniform(ld_tiles(a, n)); }
     }
     __device__ __forceinline__ void start(const LdArgs& a, int n0, int j0, int count) {
-        n = n0; j = j0; left = count; first = true; from = j0;
-        tiles = count > 0 ? ld_tiles(a, n0) : 0;
+        n = uniform(n0); j = uniform(j0); left = uniform(count); first = true; from = j;
+        tiles = left > 0 ? uniform(ld_tiles(a, n)) : 0;
     }
     __device__ __forceinline__ void next(const LdArgs& a) {
         first = last();
@@ -137,7 +137,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     int* range = (int*)(tmem_at + 1);                  // first sequence, its first tile, tiles
     int* fault = range + 3;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {

@@ -74,7 +74,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint64_t* tempty = tfull + 4;                  // [2][2] leader: the pair's epilogue warps of that half have read it
     uint32_t* tmem_at = (uint32_t*)(tempty + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
@@ -283,7 +283,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint64_t* tempty = tfull + 2;
     uint32_t* tmem_at = (uint32_t*)(tempty + 2);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int splits = gridDim.x;                                  // = the cluster
     const int rank = blockIdx.x, n0 = blockIdx.y * 128;
     const int64_t m0 = (int64_t)blockIdx.z * BT;
