@@ -2,14 +2,16 @@
 layers (argument marshalling only; see include/kda.h for what each computes)."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 from typing import Optional
 
 import torch
 
 from . import _binding as B
-from ._binding import KDA_ERR_UNSUPPORTED, KDA_OK, KdaError, lib
+from ._binding import KdaError, lib
 
 KDA_FLAG_NO_CAUSAL = 4
 
@@ -56,9 +58,24 @@ def _declare():
 
 _declare()
 _byref = ctypes.byref
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+def _load_native():
+    """The compiled marshalling (csrc/kda_torch.cpp), bound to the entry points of the loaded library."""
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "_kda_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_kda_torch.so not built at {path}: run "
+                          f"`python -c 'import __graft_entry__ as g; g.build()'` first")
+    loader = importlib.machinery.ExtensionFileLoader("_kda_torch", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kda_torch", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes", "kda_latent_decode_workspace_bytes",
+        "kda_latent_prefill", "kda_latent_decode")))
+    return module
+
+
+_native = _load_native()
 
 
 def kda_rms_norm(desc: KdaNormDesc, x, weight, residual, residual_out, normed, quantized, scales, stream=None) -> int:
@@ -102,44 +119,21 @@ def kda_latent_status(desc: KdaLatentDesc, stream=None) -> int:
     return lib.kda_latent_status(_byref(desc), B._stream(stream))
 
 
-# ------------------------------------------------------------------ checks
-def _tensor(t, name: str, dtype, dim: int, device):
-    """A tensor of `dim` dimensions on `device` whose last one is dense."""
-    if t.dtype != dtype or t.dim() != dim or t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be a {dim}-D {dtype} tensor on {device} with a dense last dimension: got "
-                         f"{tuple(t.shape)}, {t.dtype}, {t.device}, strides {t.stride()}")
-
-
-def _dense(t, name: str, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}: got "
-                         f"{tuple(t.shape)}, {t.dtype}, {t.device}, strides {t.stride()}")
-
-
-def _device(t, name: str):
-    if not t.is_cuda or t.get_device() != _current_device():
-        raise ValueError(f"{name} must be on the current CUDA device: got {t.device}")
-    return t.device
-
-
-def _row_stride(t, width: int) -> int:
-    """Elements between rows of a 2-D tensor (a single row may carry any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-_NULL = contextlib.nullcontext()
-
-
-def _on(stream, device):
-    """(raw stream, context in which buffers are allocated so that they belong to it)."""
-    if stream is None:
-        return _current_raw_stream(device.index), _NULL
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return stream.cuda_stream, torch.cuda.stream(stream)
-
-
 # ------------------------------------------------------------------ operators
+def _call(name: str, stream, *args):
+    """The native call on the current stream or on ``stream`` (whose allocations its outputs then are)."""
+    if stream is None:
+        r = getattr(_native, name)(*args)
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            r = getattr(_native, name)(*args)
+    if type(r) is int:
+        raise KdaError(f"kda_{name}", r)
+    return r
+
+
 def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, normed: bool = True, quantize: bool = False,
              residual_out: Optional[torch.Tensor] = None, stream=None):
     """y = h / sqrt(mean(h^2) + eps) * weight over the last dimension, h = x + residual.
@@ -150,57 +144,7 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, normed: bool =
     ``quantize``; h in x's dtype if a residual is given, written to
     ``residual_out`` (which may be x or residual) or to a new tensor.  What is
     not asked for is None."""
-    dev = _device(x, "x")
-    dt = B._DTYPES.get(x.dtype)
-    if dt is None or x.dim() < 1:
-        raise ValueError(f"x must be float32 or bfloat16 rows: got {x.dtype}, {tuple(x.shape)}")
-    if not (normed or quantize or residual is not None):
-        raise ValueError("nothing to compute: normed, quantize or a residual")
-    shape, dim = x.shape, x.shape[-1]
-    if dim < 1:
-        raise ValueError("rows must have an element")
-    if x.dim() != 2:
-        if not x.is_contiguous():
-            raise ValueError("x must be contiguous unless it is 2-D")
-        x2 = x.view(-1, dim)
-    else:
-        _tensor(x, "x", x.dtype, 2, dev)
-        x2 = x
-    rows = x2.shape[0]
-    r_stride = dim
-    if weight is not None:
-        _dense(weight, "weight", x.dtype, (dim,), dev)
-    if residual is not None:
-        if residual.shape != shape:
-            raise ValueError(f"residual must have x's shape {tuple(shape)}: got {tuple(residual.shape)}")
-        if residual.dim() == 2:
-            _tensor(residual, "residual", x.dtype, 2, dev)
-            r_stride = _row_stride(residual, dim)
-        else:
-            _dense(residual, "residual", x.dtype, shape, dev)
-    y = q = s = None
-    raw, where = _on(stream, dev)
-    with where:
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty(shape, dtype=x.dtype, device=dev)
-        elif residual_out is not None:
-            if residual is None:
-                raise ValueError("residual_out without a residual")
-            _dense(residual_out, "residual_out", x.dtype, shape, dev)
-        if normed:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
-        if quantize:
-            q = torch.empty(shape, dtype=_F8, device=dev)
-            s = torch.empty((*shape[:-1], (dim + 127) // 128), dtype=_F32, device=dev)
-    if rows:
-        rc = lib.kda_rms_norm(
-            _byref(KdaNormDesc(rows, dim, dt, _row_stride(x2, dim), r_stride, eps)), x.data_ptr(),
-            None if weight is None else weight.data_ptr(), None if residual is None else residual.data_ptr(),
-            None if residual_out is None else residual_out.data_ptr(), y.data_ptr() if normed else None,
-            q.data_ptr() if quantize else None, s.data_ptr() if quantize else None, raw)
-        if rc != KDA_OK:
-            raise KdaError("kda_rms_norm", rc)
-    return y, q, s, residual_out
+    return _call("rms_norm", stream, x, weight, residual, eps, normed, quantize, residual_out)
 
 
 def matmul_fp8(a, a_scale, b, b_scale, *, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None,
@@ -210,46 +154,9 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out: Optional[torch.Tensor] = None, ou
     a ``[M, K]``, b ``[N, K]`` e4m3 (rows may be strided), a_scale ``[M,
     ceil(K / 128)]``, b_scale ``[ceil(N / 128), ceil(K / 128)]`` fp32.  Returns c
     ``[M, N]`` in ``out_dtype`` (bf16 or fp32), or ``out`` (rows may be strided)."""
-    dev = _device(a, "a")
-    _tensor(a, "a", _F8, 2, dev)
-    _tensor(b, "b", _F8, 2, dev)
-    (m, k), (n, kb_) = a.shape, b.shape
-    if kb_ != k or k < 1:
-        raise ValueError(f"a and b must have rows of the same length: got {k} and {kb_}")
-    kb = (k + 127) // 128
-    _dense(a_scale, "a_scale", _F32, (m, kb), dev)
-    _dense(b_scale, "b_scale", _F32, ((n + 127) // 128, kb), dev)
-    raw, where = _on(stream, dev)
-    if out is None:
-        with where:
-            out = torch.empty((m, n), dtype=out_dtype, device=dev)
-        ldc = n
-    else:
-        _tensor(out, "out", out.dtype, 2, dev)
-        if out.shape != (m, n):
-            raise ValueError(f"out must be {(m, n)}: got {tuple(out.shape)}")
-        ldc = _row_stride(out, n)
-    dt = B._DTYPES.get(out.dtype)
-    if dt is None:
-        raise ValueError(f"the output must be float32 or bfloat16: got {out.dtype}")
-    if m and n:
-        rc = lib.kda_matmul_fp8(_byref(KdaMatmulDesc(m, n, k, _row_stride(a, k), _row_stride(b, k), ldc, dt, flags)),
-                                a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
-                                raw)
-        if rc != KDA_OK:
-            raise KdaError("kda_matmul_fp8", rc)
-    return out
-
-
-def _latent_workspace(desc, bytes_of, name, workspace, dev):
-    if workspace is None:
-        n = bytes_of(_byref(desc))
-        if n == 0:
-            raise KdaError(name, KDA_ERR_UNSUPPORTED)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    desc.workspace = workspace.data_ptr()
-    desc.workspace_bytes = workspace.numel() * workspace.element_size()
-    return workspace
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError(f"the output must be float32 or bfloat16: got {out_dtype}")
+    return _call("matmul_fp8", stream, a, a_scale, b, b_scale, out, out_dtype is torch.bfloat16, flags)
 
 
 def latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q=None, cu_seqlens_k=None, *, scale: float, causal: bool = True,
@@ -263,53 +170,8 @@ def latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q=None, cu_seqlens_k=None, *
     Returns (out ``[Tq, H, d_v]``, lse fp32 ``[Tq, H]``).  A caller that passes
     a ``workspace`` (uint8) can read the call's device status from it with
     ``latent_status``."""
-    dev = _device(q, "q")
-    dt = B._DTYPES.get(q.dtype)
-    if dt is None:
-        raise ValueError(f"q must be float32 or bfloat16: got {q.dtype}")
-    for t, name in ((q, "q"), (k_nope, "k_nope"), (v, "v")):
-        _tensor(t, name, q.dtype, 3, dev)
-    tq, h, dqk = q.shape
-    tk, hk, dk = k_nope.shape
-    dv = v.shape[2]
-    dr = 0
-    if k_rope is not None:
-        _tensor(k_rope, "k_rope", q.dtype, 2, dev)
-        dr = k_rope.shape[1]
-        if k_rope.shape[0] != tk:
-            raise ValueError("k_rope must have k_nope's tokens")
-    if hk != h or v.shape[0] != tk or v.shape[1] != h or dk + dr != dqk:
-        raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}, v {tuple(v.shape)}, d_rope {dr}")
-    n = 1
-    if (cu_seqlens_q is None) != (cu_seqlens_k is None):
-        raise ValueError("both cu_seqlens or neither")
-    if cu_seqlens_q is not None:
-        n = cu_seqlens_q.shape[0] - 1
-        _dense(cu_seqlens_q, "cu_seqlens_q", _I32, (n + 1,), dev)
-        _dense(cu_seqlens_k, "cu_seqlens_k", _I32, (n + 1,), dev)
-    desc = KdaLatentDesc(n, h, dt, flags if causal else flags | KDA_FLAG_NO_CAUSAL, scale, dk, dr, dv, tq, tk,
-                         q.stride(0), q.stride(1), k_nope.stride(0), k_nope.stride(1), v.stride(0), v.stride(1),
-                         k_rope.stride(0) if dr else 0)
-    raw, where = _on(stream, dev)
-    with where:
-        if out is None:
-            out = torch.empty((tq, h, dv), dtype=q.dtype, device=dev)
-        else:
-            _dense(out, "out", q.dtype, (tq, h, dv), dev)
-        if lse is None:
-            lse = torch.empty((tq, h), dtype=_F32, device=dev)
-        else:
-            _dense(lse, "lse", _F32, (tq, h), dev)
-        workspace = _latent_workspace(desc, lib.kda_latent_prefill_workspace_bytes, "kda_latent_prefill", workspace,
-                                      dev)
-    rc = lib.kda_latent_prefill(_byref(desc), q.data_ptr(), k_nope.data_ptr(),
-                                k_rope.data_ptr() if dr else None, v.data_ptr(),
-                                None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(),
-                                None if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), out.data_ptr(),
-                                lse.data_ptr(), raw)
-    if rc != KDA_OK:
-        raise KdaError("kda_latent_prefill", rc)
-    return out, lse
+    return _call("latent_prefill", stream, q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, scale,
+                 flags if causal else flags | KDA_FLAG_NO_CAUSAL, out, lse, workspace)
 
 
 def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional[int] = None, out=None, lse=None,
@@ -323,53 +185,8 @@ def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional
     of each sequence in the cache, its queries' own among them.  ``rank`` is the
     values' width, by default all but the last 64.  Returns (out ``[N, (Lq,) H,
     rank]``, lse fp32 ``[N, (Lq,) H]``)."""
-    dev = _device(q, "q")
-    dt = B._DTYPES.get(q.dtype)
-    if dt is None:
-        raise ValueError(f"q must be float32 or bfloat16: got {q.dtype}")
-    single = q.dim() == 3
-    _tensor(q, "q", q.dtype, 3 if single else 4, dev)
-    if single:
-        n, h, w = q.shape
-        lq, q_ts, q_hs = 1, q.stride(0), q.stride(1)
-    else:
-        n, lq, h, w = q.shape
-        q_ts, q_hs = q.stride(1), q.stride(2)
-        if lq == 1:
-            q_ts = q.stride(0)
-        else:
-            if n > 1 and q.stride(0) != lq * q_ts:
-                raise ValueError("q's sequences and queries must form one strided dimension")
-    if not (cache.dim() == 3 and cache.dtype == q.dtype and cache.device == dev and cache.shape[2] == w and cache.stride(2) == 1 and cache.stride(1) == w):
-        raise ValueError(f"cache must be a [pages, page_size, {w}] {q.dtype} tensor on {dev} with dense pages")
-    rank = w - 64 if rank is None else rank
-    if not 1 <= rank <= w:
-        raise ValueError(f"rank must be within 1 .. {w}: got {rank}")
-    if page_table.dim() != 2 or page_table.shape[0] != n:
-        raise ValueError(f"page_table must be [{n}, max_pages]")
-    _dense(page_table, "page_table", _I32, page_table.shape, dev)
-    _dense(lengths, "lengths", _I32, (n,), dev)
-    pages, size = cache.shape[0], cache.shape[1]
-    desc = KdaLatentDesc(n, h, dt, flags, scale, rank, w - rank, rank, 0, 0, q_ts, q_hs, 0, 0, 0, 0, 0, lq, size,
-                         pages, page_table.shape[1], cache.stride(0) if pages > 1 else size * w)
-    lead = (n, h) if single else (n, lq, h)
-    raw, where = _on(stream, dev)
-    with where:
-        if out is None:
-            out = torch.empty((*lead, rank), dtype=q.dtype, device=dev)
-        else:
-            _dense(out, "out", q.dtype, (*lead, rank), dev)
-        if lse is None:
-            lse = torch.empty(lead, dtype=_F32, device=dev)
-        else:
-            _dense(lse, "lse", _F32, lead, dev)
-        workspace = _latent_workspace(desc, lib.kda_latent_decode_workspace_bytes, "kda_latent_decode", workspace,
-                                      dev)
-    rc = lib.kda_latent_decode(_byref(desc), q.data_ptr(), cache.data_ptr(), page_table.data_ptr(),
-                               lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), raw)
-    if rc != KDA_OK:
-        raise KdaError("kda_latent_decode", rc)
-    return out, lse
+    return _call("latent_decode", stream, q, cache, page_table, lengths, scale, -1 if rank is None else rank, flags, out,
+                 lse, workspace)
 
 
 def latent_status(workspace, stream=None) -> int:

@@ -2,21 +2,26 @@
 
 Each translation unit compiles in parallel into an object file; the shared
 library links them against the CUDA runtime (shared, so that it is the same
-runtime instance PyTorch uses in the process).  Rebuilds only what changed.
+runtime instance PyTorch uses in the process).  ``csrc/kda_torch.cpp``, the
+marshalling of torch tensors for the short operators, becomes a module of its
+own, ``_build/_kda_torch.so``.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
+TORCH_MODULE = os.path.join(BUILD, "_kda_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -60,6 +65,20 @@ def _compile(nvcc: str, src: str, obj: str, extra) -> None:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
 
 
+def _compile_torch_module(nvcc: str, src: str) -> None:
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = TORCH_MODULE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", INCLUDE, "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_MODULE)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every CUDA translation unit for sm_103a and link libkda.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -72,9 +91,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(o)
         if force or _stale(o, [s, *hdrs, __file__]):
             jobs.append((s, o))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    module = os.path.join(CSRC, "kda_torch.cpp")
+    stale_module = force or _stale(TORCH_MODULE, [module, __file__, os.path.join(INCLUDE, "kda.h")])
+    if jobs or stale_module:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = [ex.submit(_compile, nvcc, s, o, list(extra_flags)) for s, o in jobs]
+            if stale_module:
+                futs.append(ex.submit(_compile_torch_module, nvcc, module))
             for f in futs:
                 f.result()
     if force or jobs or _stale(LIB, objs):
