@@ -22,8 +22,11 @@
 // sum) and a second kernel joins them in range order.
 //
 // Bound by HBM: at 6.78 TB/s a tile's 147 KB take an SM 6600 cycles; its
-// products and softmax take about 3700.  Shared memory holds the tile, a fifth
-// pair of 64-channel pieces on its way, the queries and P.
+// products take about 2900 (40 cycles an instruction whatever R up to 32).  A
+// tile does not stay in shared memory between its two products: the second
+// fetches the 512 channels again, out of L2, so that all of the ring (160 KB)
+// is copies in flight; S^T of the next tile is formed before the second product
+// of this one, which hides the softmax.
 #include <math.h>
 
 #include "kda_common.cuh"
@@ -36,7 +39,6 @@ using namespace sm100;
 
 constexpr int kLdTile = 128;                  // tokens of a tile
 constexpr int kLdRank = 512, kLdWidth = 576;
-constexpr int kLdPairs = 5;                   // ring of 128-channel pairs of pieces
 constexpr uint32_t kLdPiece = kLdTile * 128;  // 64 channels of a tile
 constexpr int kLdThreads = 192;               // 4 softmax warps, producer, matrix instructions
 constexpr float kLdUnset = -1e30f;            // reference of a row that has seen no key
@@ -44,16 +46,18 @@ constexpr float kLdSlack = 8.f;               // how far (log2) a score may exce
 
 template <int R>
 struct LdShape {
+    static constexpr int kSlots = R == 64 ? 3 : 5;                 // of two pieces (128 channels; the rotary one alone)
+    static constexpr uint32_t kSlot = 2 * kLdPiece;
     static constexpr uint32_t kQPiece = R * 128, kQ = 9 * kQPiece;
-    static constexpr uint32_t kRow = R * 2, kP = kLdTile * kRow;   // P^T: a token's R values
-    static constexpr uint32_t kOffRope = kLdPairs * 2 * kLdPiece, kOffQ = kOffRope + kLdPiece;
-    static constexpr uint32_t kOffP = kOffQ + kQ, kOffSmall = kOffP + kP;
+    static constexpr uint32_t kRow = R * 2, kP = kLdTile * kRow;   // P^T: a token's R values, double-buffered
+    static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + kQ, kOffSmall = kOffP + 2 * kP;
     static constexpr uint32_t kSmem = kOffSmall + 1024 + (2 * 4 + 3) * R * 4 + 512;
-    static constexpr uint32_t kTmem = R == 16 ? 128 : 256;         // S^T and four blocks of O^T: 5 R columns
-    static constexpr uint64_t kSwz = R == 16 ? 6 : 4;
-    // 16-byte piece c of token row r of P^T (32- or 64-byte swizzle)
+    static constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512;   // two S^T, four blocks of O^T: 6 R columns
+    static constexpr uint64_t kSwz = R == 16 ? 6 : R == 32 ? 4 : 2;
+    // 16-byte piece c of token row r of P^T (32-, 64- or 128-byte swizzle)
     static __device__ __forceinline__ uint32_t p_at(int r, int c) {
-        return R == 16 ? r * 32 + ((c ^ (r >> 2)) & 1) * 16 : r * 64 + ((c ^ (r >> 1)) & 3) * 16;
+        return R == 16 ? r * 32 + ((c ^ (r >> 2)) & 1) * 16
+             : R == 32 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 128 + ((c ^ r) & 7) * 16;
     }
 };
 
@@ -65,6 +69,7 @@ struct LdArgs {
     float* lse;
     int32_t *status, *cta_status;
     float* parts;                              // [groups * G][2][R][kLdPart]
+    int64_t* before;                           // [N + 1] tiles ahead of a sequence (where it has tiles); all tiles
     int G;                                     // CTAs of a group
 };
 constexpr int kLdPart = kLdRank + 4;           // O, ref, sum (rows stay 16-byte aligned)
@@ -96,24 +101,30 @@ struct LdWalk {
     }
 };
 
-// Sums (or maxima) over the warp's lanes of R values a lane: lane l gets those of column ld_column(l).
+// Sums (or maxima) over the warp's lanes of R values a lane, to `to`[0 .. R).
 template <int R, bool kMax>
-__device__ __forceinline__ float ld_columns(float (&v)[R], int lane) {
+__device__ __forceinline__ void ld_columns(const float (&x)[R], float* to, int lane) {
     auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
-    if constexpr (R == 16) {
+    constexpr int W = R < 32 ? R : 32;
 #pragma unroll
-        for (int i = 0; i < R; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-    }
+    for (int h = 0; h < R; h += W) {
+        float v[W];
 #pragma unroll
-    for (int o = R == 16 ? 8 : 16; o > 0; o >>= 1) {
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const bool up = lane & o;
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        for (int i = 0; i < W; ++i) {
+            v[i] = x[h + i];
+            if (W == 16) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
         }
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const bool up = lane & o;
+                const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            }
+        }
+        if (lane < W) to[h + lane] = v[0];                         // lane l has come to hold column l
     }
-    return v[0];
 }
 
 template <int R>
@@ -130,19 +141,21 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     float* across = (float*)(query + R);               // [4][R] one value a warp and row
     float* sums = across + 4 * R;                      // [4][R]
     uint64_t* bars = (uint64_t*)(sums + 4 * R);
-    uint64_t *full = bars, *empty = full + kLdPairs, *rope_full = empty + kLdPairs, *rope_empty = rope_full + 1,
-             *q_full = rope_empty + 1, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_full = s_full + 1,
-             *o_full = p_full + 1;
-    uint32_t* tmem_at = (uint32_t*)(o_full + 1);
+    uint64_t *full = bars, *empty = full + S::kSlots, *q_full = empty + S::kSlots, *q_empty = q_full + 1,
+             *s_full = q_empty + 1, *o_full = s_full + 2,          // [2]: alternate tiles
+             *p_full = o_full + 2, *zeroed = p_full + 2,          // zeroed [4]: a pair of pieces each
+             *bars_end = zeroed + 4;
+    uint32_t* tmem_at = (uint32_t*)bars_end;
     int* range = (int*)(tmem_at + 1);                  // first sequence, its first tile, tiles
     int* fault = range + 3;
+    int64_t* range_at = (int64_t*)(((uintptr_t)(fault + 1) + 7) & ~(uintptr_t)7);   // index of the first tile
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (uint64_t* b = bars; b <= o_full; ++b) mbar_init(b, 1);
-        mbar_init(p_full, 4);
+        for (uint64_t* b = bars; b < p_full; ++b) mbar_init(b, 1);
+        for (uint64_t* b = p_full; b < bars_end; ++b) mbar_init(b, 4);
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc(tmem_at, S::kTmem); tmem_relinquish(); }
@@ -185,7 +198,9 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (lane == 0) {
             range[0] = n0; range[1] = j0; range[2] = (int)(t1 - t0);
+            if (cta == 0 && group == 0) a.before[a.N] = total;
             *fault = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+            *range_at = t0;
         }
     }
     if (threadIdx.x < R) {
@@ -196,107 +211,124 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
-    LdWalk w;
-    w.start(a, range[0], range[1], range[2]);
-
+    // Order of the copies and products: S_0, then for each tile j: S_{j+1}, V_j.
     if (warp == 4) {                                                   // ---------------- producer
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
-        uint32_t unit = 0, tile = 0, seg = 0;
+        uint32_t unit = 0, seg = 0;
         bool ok = true, bad_page = false;
-        for (; w.left > 0 && ok; w.next(a), ++tile) {
-            if (w.first) {
-                if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, S::kQ);
-                    for (int c = 0; c < 9; ++c)
-                        tma_load_3d_at(base + S::kOffQ + c * S::kQPiece, &map_q, c * 64, group * R, w.n, smem_u32(q_full));
-                }
-                ++seg;
-            }
-            // a lane for each box of tokens: its page and row; pages behind the length, and bad ones, read as zeros
-            int page = a.num_pages, row = 0;
-            if (lane < boxes) {
-                const int t = w.j * kLdTile + lane * box;
-                if (t < ld_len(a, w.n)) {
-                    const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
-                    if (p < 0 || p >= a.num_pages) bad_page = true;
-                    else { page = p; row = t % a.page_size; }
-                }
-            }
-            if (tile > 0 && !(ok = mbar_wait_warp(rope_empty, (tile - 1) & 1))) break;
-            if (lane == 0) mbar_arrive_expect_tx(rope_full, kLdPiece);
+        // a unit: one piece at x, or two; a lane for each box of tokens
+        auto fetch = [&](int x, int pieces, int row, int page) {
+            const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
+            if (unit >= S::kSlots && !(ok = mbar_wait_warp(&empty[s], ph ^ 1))) return;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], pieces * kLdPiece);
             __syncwarp();
-            if (lane < boxes)
-                tma_load_3d_at(base + S::kOffRope + lane * box * 128, &map_c, kLdRank, row, page, smem_u32(rope_full));
-            for (int p = 0; p < 4; ++p, ++unit) {
-                const uint32_t s = unit % kLdPairs, ph = (unit / kLdPairs) & 1;
-                if (unit >= kLdPairs && !(ok = mbar_wait_warp(&empty[s], ph ^ 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * kLdPiece);
-                __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t at = base + s * 2 * kLdPiece + lane * box * 128;
-                    tma_load_3d_at(at, &map_c, p * 128, row, page, smem_u32(&full[s]));
-                    tma_load_3d_at(at + kLdPiece, &map_c, p * 128 + 64, row, page, smem_u32(&full[s]));
-                }
+            if (lane < boxes) {
+                const uint32_t at = base + s * S::kSlot + lane * box * 128;
+                tma_load_3d_at(at, &map_c, x, row, page, smem_u32(&full[s]));
+                if (pieces == 2) tma_load_3d_at(at + kLdPiece, &map_c, x + 64, row, page, smem_u32(&full[s]));
             }
+            ++unit;
+        };
+        LdWalk w;
+        w.start(a, range[0], range[1], range[2]);
+        int row_v = 0, page_v = 0;                                     // of the tile before
+        for (bool more = false; ok; more = true) {
+            int row = 0, page = a.num_pages;
+            if (w.left > 0) {
+                if (w.first) {
+                    if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, S::kQ);
+                        for (int c = 0; c < 9; ++c)
+                            tma_load_3d_at(base + S::kOffQ + c * S::kQPiece, &map_q, c * 64, group * R, w.n, smem_u32(q_full));
+                    }
+                    __syncwarp();
+                    ++seg;
+                }
+                // pages behind the length, and bad ones, read as zeros
+                if (lane < boxes) {
+                    const int t = w.j * kLdTile + lane * box;
+                    if (t < ld_len(a, w.n)) {
+                        const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
+                        if (p < 0 || p >= a.num_pages) bad_page = true;
+                        else { page = p; row = t % a.page_size; }
+                    }
+                }
+                fetch(kLdRank, 1, row, page);
+                for (int p = 0; p < 4 && ok; ++p) fetch(p * 128, 2, row, page);
+            }
+            if (more)
+                for (int p = 0; p < 4 && ok; ++p) fetch(p * 128, 2, row_v, page_v);
+            if (w.left <= 0 || !ok) break;
+            row_v = row; page_v = page;
+            w.next(a);
         }
         if (bad_page) atomicMax(fault, KDA_ERR_BAD_PAGE);
         if (!ok) { atomicMax(fault, KDA_ERR_TIMEOUT); drain_copies(); }
     } else if (warp == 5) {                                            // ---------------- matrix instructions
         const uint32_t idesc_s = idesc_bf16(128, R), idesc_o = idesc_bf16(128, R, 1, 1);
-        uint32_t unit = 0, tile = 0, seg = 0;
+        const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
+        uint32_t unit = 0, seg = 0, zero = 0;
         bool ok = true;
-        for (; w.left > 0 && ok; w.next(a), ++tile) {
-            if (w.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
-            if (ok) ok = mbar_wait_warp(rope_full, tile & 1);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
-            if (elect_one()) {
-                const uint64_t da = sdesc_k_sw128(base + S::kOffRope);
+        LdWalk ws, w;
+        ws.start(a, range[0], range[1], range[2]);
+        w = ws;
+        const int count = ws.left;
+        for (int j = -1; j < count && ok; ++j) {
+            const int js = j + 1;
+            if (js < count) {                                          // S^T of the next tile
+                if (ws.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
+                for (int p = -1; p < 4 && ok; ++p, ++unit) {           // rotary channels, then the pairs
+                    const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
+                    if (!(ok = mbar_wait_warp(&full[s], ph))) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = sdesc_k_sw128(base + s * S::kSlot);
+                    const uint64_t db = dq + (p < 0 ? 8 : 2 * p) * (S::kQPiece / 16);
+                    const uint32_t d = tmem + (js & 1) * R;
+                    if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16_ss(tmem, da + 2 * k, dq + 8 * (S::kQPiece / 16) + 2 * k, idesc_s, k > 0);
-            }
-            __syncwarp();
-            for (int p = 0; p < 4 && ok; ++p) {
-                const uint32_t u = unit + p, s = u % kLdPairs, ph = (u / kLdPairs) & 1;
-                if (!(ok = mbar_wait_warp(&full[s], ph))) break;
-                tc_fence_after_sync();
-                const uint64_t da = sdesc_k_sw128(base + s * 2 * kLdPiece);
-                const uint64_t db = dq + 2 * p * (S::kQPiece / 16);
-                if (elect_one()) {
+                        for (int k = 0; k < 4; ++k) mma_bf16_ss(d, da + 2 * k, db + 2 * k, idesc_s, p >= 0 || k > 0);
+                        if (p >= 0) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16_ss(tmem, da + (k / 4) * (kLdPiece / 16) + 2 * (k % 4),
-                                    db + (k / 4) * (S::kQPiece / 16) + 2 * (k % 4), idesc_s, 1);
-                    if (p == 3) {
-                        mma_commit(s_full);
-                        mma_commit(rope_empty);
-                        if (w.last()) mma_commit(q_empty);
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_ss(d, da + kLdPiece / 16 + 2 * k, db + S::kQPiece / 16 + 2 * k, idesc_s, 1);
+                        }
+                        mma_commit(&empty[s]);
+                        if (p == 3) {
+                            mma_commit(&s_full[js & 1]);
+                            if (ws.last()) mma_commit(q_empty);
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
+                ws.next(a);
             }
-            if (ok) ok = mbar_wait_warp(p_full, tile & 1);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t dp = sdesc(base + S::kOffP, 16, 8 * S::kRow, S::kSwz);
-            for (int p = 0; p < 4; ++p, ++unit) {
-                const uint32_t s = unit % kLdPairs;
+            if (j < 0) continue;
+            if (!(ok = mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
+            const uint64_t dp = sdesc(base + S::kOffP + (j & 1) * S::kP, 16, 8 * S::kRow, S::kSwz);
+            const bool ragged = uniform((w.j + 1) * kLdTile > ld_len(a, w.n));
+            for (int p = 0; p < 4; ++p, ++unit) {                      // O^T += V^T P^T
+                const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
+                ok = mbar_wait_warp(&full[s], ph);
+                if (ok && ragged) ok = mbar_wait_warp(&zeroed[p], zero & 1);
+                if (!ok) break;
+                tc_fence_after_sync();
                 // A: 128 channels = two pieces of 64, MN-major; 16 tokens a step
-                const uint64_t da = sdesc(base + s * 2 * kLdPiece, kLdPiece, 1024, 2);
+                const uint64_t da = sdesc(base + s * S::kSlot, kLdPiece, 1024, 2);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_bf16_ss(tmem + (1 + p) * R, da + k * (2048 / 16), dp + k * (16 * S::kRow / 16), idesc_o,
+                        mma_bf16_ss(tmem + (2 + p) * R, da + k * (2048 / 16), dp + k * (16 * S::kRow / 16), idesc_o,
                                     !w.first || k > 0);
                     mma_commit(&empty[s]);
-                    if (p == 3 && w.last()) mma_commit(o_full);
+                    if (p == 3) mma_commit(&o_full[j & 1]);
                 }
                 __syncwarp();
             }
+            zero += ragged;
+            if (ok) w.next(a);
         }
         if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
     } else {                                                           // ---------------- softmax
@@ -306,17 +338,27 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         float l[R];
 #pragma unroll
         for (int c = 0; c < R; ++c) l[c] = 0.f;
-        uint32_t tile = 0, seg = 0;
+        // units of the ring, as the producer orders them
+        uint32_t unit = 5;                                             // behind S_0
         bool ok = true;
-        for (; w.left > 0; w.next(a), ++tile) {
-            ok = bar_and(128, mbar_wait_spin(s_full, tile & 1));
+        LdWalk w;
+        w.start(a, range[0], range[1], range[2]);
+        const int count = w.left;
+        for (int j = 0; j < count; ++j, w.next(a)) {
+            if (w.first && w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+            ok = bar_and(128, mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
+            const uint32_t at_s = lanes + (j & 1) * R;
             const int len = ld_len(a, w.n);
             const int token = w.j * kLdTile + (int)threadIdx.x;
             float x[R];
-            if constexpr (R == 16) tmem_ld16(lanes, x);
-            else tmem_ld32(lanes, x);
+            if constexpr (R == 16) {
+                tmem_ld16(at_s, x);
+            } else {
+#pragma unroll
+                for (int c = 0; c < R; c += 32) tmem_ld32(at_s + c, *(float(*)[32])(x + c));
+            }
             tmem_wait_ld();
             tmem_ready(x);
 #pragma unroll
@@ -334,11 +376,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                         x[c + 3] > m.w + kLdSlack;
             }
             if (!bar_and(128, !over)) {                                // move the references to the maxima
-                float v[R];
-#pragma unroll
-                for (int c = 0; c < R; ++c) v[c] = x[c];
-                const float top = ld_columns<R, true>(v, lane);
-                if (lane < R) across[warp * R + lane] = top;
+                ld_columns<R, true>(x, across + warp * R, lane);
                 asm volatile("bar.sync 2, 128;" ::: "memory");
                 if (threadIdx.x < R) {
                     const int c = threadIdx.x;
@@ -351,8 +389,11 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 asm volatile("bar.sync 2, 128;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < R; ++c) l[c] *= fac[c];
-                if (!w.first) {                                        // O^T: the products before S^T are complete
-                    for (int p = 1; p <= 4; ++p) {
+                if (!w.first) {                                        // O^T, once the products into it are complete
+                    ok = bar_and(128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    for (int p = 2; p <= 5; ++p) {
                         for (int h = 0; h < R; h += 16) {
                             float o[16];
                             tmem_ld16(lanes + p * R + h, o);
@@ -365,6 +406,10 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     }
                     tmem_wait_st();
                 }
+            }
+            if (j >= 2) {                                              // P's buffer: the products that read it are complete
+                ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
+                if (!ok) break;
             }
 #pragma unroll
             for (int c = 0; c < R; c += 8) {
@@ -379,29 +424,37 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);    // the product's operand: 8 bits
                     b[i] = *(const uint32_t*)&h;
                 }
-                *(uint4*)(mem + S::kOffP + S::p_at(threadIdx.x, c / 8)) = make_uint4(b[0], b[1], b[2], b[3]);
-            }
-            if (token >= len) {                                        // weight 0 times what lies behind the length: make it 0
-                for (int p = 0; p < 4; ++p) {
-                    uint8_t* at = mem + (tile * 4 + p) % kLdPairs * 2 * kLdPiece + threadIdx.x * 128;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        *(uint4*)(at + 16 * i) = make_uint4(0, 0, 0, 0);
-                        *(uint4*)(at + kLdPiece + 16 * i) = make_uint4(0, 0, 0, 0);
-                    }
-                }
+                *(uint4*)(mem + S::kOffP + (j & 1) * S::kP + S::p_at(threadIdx.x, c / 8)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) mbar_arrive(&p_full[j & 1]);
+            // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes.
+            if (j + 1 < count) unit += 5;                              // S_{j+1} comes before V_j
+            if ((w.j + 1) * kLdTile > len) {
+                for (int p = 0; p < 4 && ok; ++p) {
+                    const uint32_t u = unit + p, s = u % S::kSlots;
+                    ok = mbar_wait_warp(&full[s], (u / S::kSlots) & 1);
+                    if (token >= len) {
+                        uint8_t* at = mem + s * S::kSlot + threadIdx.x * 128;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            *(uint4*)(at + 16 * i) = make_uint4(0, 0, 0, 0);
+                            *(uint4*)(at + kLdPiece + 16 * i) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&zeroed[p]);
+                }
+            }
+            unit += 4;
             if (!w.last()) continue;
 
             // end of a segment: sums across the tokens' threads, then O^T out
-            const float part = ld_columns<R, false>(l, lane);
-            if (lane < R) sums[warp * R + lane] = part;
-            ok = bar_and(128, mbar_wait_spin(o_full, seg & 1));
-            ++seg;
+            ld_columns<R, false>(l, sums + warp * R, lane);
+            ok = bar_and(128, ok && mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
             const bool whole = w.from == 0 && w.j + 1 == w.tiles;
@@ -424,7 +477,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
                 for (int h = 0; h < R; h += 16) {
                     float o[16];
-                    tmem_ld16(lanes + (1 + p) * R + h, o);
+                    tmem_ld16(lanes + (2 + p) * R + h, o);
                     tmem_wait_ld();
                     tmem_ready(o);
                     if (whole) {
@@ -454,95 +507,100 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 }
 
 // Joins the pieces of sequences that several CTAs shared, gives sequences
-// without tiles their zeros, and collects the CTAs' status.  A warp a row.
+// without tiles their zeros, and collects the CTAs' status.  A block a row, its
+// warps a share of the pieces each.
+constexpr int kLdJoinWarps = 4;
 template <int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kLdJoinWarps)
 kda_latent_decode_join(const LdArgs a, const int groups) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int64_t s_before[8], s_total[8];
-    const int n = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (n == 0 && blockIdx.y == 0) {
-        int st = KDA_OK;
-        for (int i = threadIdx.x; i < a.G * groups; i += 256) st = max(st, a.cta_status[i]);
-        st = __syncthreads_or(st == KDA_ERR_BAD_PAGE) ? KDA_ERR_BAD_PAGE
-             : __syncthreads_or(st == KDA_ERR_BAD_SEQLENS) ? KDA_ERR_BAD_SEQLENS
-             : __syncthreads_or(st == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : KDA_OK;
-        if (threadIdx.x == 0) *a.status = st;
+    const int n = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (n == 0 && row == 0) {
+        int bad_page = 0, bad_len = 0, late = 0;
+        for (int i = threadIdx.x; i < a.G * groups; i += 32 * kLdJoinWarps) {
+            const int st = a.cta_status[i];
+            bad_page |= st == KDA_ERR_BAD_PAGE; bad_len |= st == KDA_ERR_BAD_SEQLENS; late |= st == KDA_ERR_TIMEOUT;
+        }
+        bad_page = __syncthreads_or(bad_page); bad_len = __syncthreads_or(bad_len); late = __syncthreads_or(late);
+        if (threadIdx.x == 0)
+            *a.status = bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : late ? KDA_ERR_TIMEOUT : KDA_OK;
     }
-    int64_t before = 0, total = 0;
-    for (int i = threadIdx.x; i < a.N; i += 256) {
-        const int t = ld_tiles(a, i);
-        total += t;
-        if (i < n) before += t;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    if (lane == 0) { s_before[warp] = before; s_total[warp] = total; }
-    __syncthreads();
-    before = total = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { before += s_before[i]; total += s_total[i]; }
-    const int row = blockIdx.y * 8 + warp;
-    if (row >= a.rows) return;
     const int tiles = ld_tiles(a, n);
-    __nv_bfloat16* to = a.out + ((size_t)n * a.rows + row) * kLdRank;
+    int cf = 0, cl = -1;
+    if (tiles > 0) {
+        const int64_t total = a.before[a.N], before = a.before[n], parts = min64(a.G, total);
+        cf = (int)(((before + 1) * parts - 1) / total);
+        cl = (int)(((before + tiles) * parts - 1) / total);
+        if (cf == cl) return;                          // finished by its CTA
+    }
+    const int group = row / R, c = row % R;
+    auto piece = [&](int i) {
+        return a.parts + (((size_t)(i * groups + group) * 2 + (i == cf)) * R + c) * kLdPart;
+    };
+    __shared__ float sh_top[kLdJoinWarps], sh_sum[kLdJoinWarps];
+    __shared__ __align__(16) float sh_o[kLdJoinWarps][kLdRank];
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
-    float lse = -INFINITY;
-    if (tiles > 0) {
-        const int64_t parts = min64(a.G, total);
-        const int cf = (int)(((before + 1) * parts - 1) / total), cl = (int)(((before + tiles) * parts - 1) / total);
-        if (cf == cl) return;                          // finished by its CTA
-        const int group = row / R, c = row % R;
-        auto piece = [&](int i) {
-            return a.parts + (((size_t)(i * groups + group) * 2 + (i == cf)) * R + c) * kLdPart;
-        };
-        float top = kLdUnset, sum = 0.f;
-        for (int i = cf + lane; i <= cl; i += 32) top = fmaxf(top, piece(i)[kLdRank]);
+    float top = kLdUnset, sum = 0.f;
+    for (int i = cf + threadIdx.x; i <= cl; i += 32 * kLdJoinWarps) top = fmaxf(top, piece(i)[kLdRank]);
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        for (int i = cf; i <= cl; ++i) {
-            const float* p = piece(i);
-            const float wgt = ex2(p[kLdRank] - top);
-            sum += wgt * p[kLdRank + 1];
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    if (lane == 0) sh_top[warp] = top;
+    __syncthreads();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = *(const float4*)(p + q * 128 + lane * 4);
-                o[4 * q] += wgt * v.x; o[4 * q + 1] += wgt * v.y; o[4 * q + 2] += wgt * v.z; o[4 * q + 3] += wgt * v.w;
-            }
+    for (int w = 0; w < kLdJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
+#pragma unroll 4
+    for (int i = cf + warp; i <= cl; i += kLdJoinWarps) {
+        const float* p = piece(i);
+        const float2 ml = *(const float2*)(p + kLdRank);
+        const float wgt = ex2(ml.x - top);
+        sum += wgt * ml.y;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 v = *(const float4*)(p + q * 128 + lane * 4);
+            o[4 * q] += wgt * v.x; o[4 * q + 1] += wgt * v.y; o[4 * q + 2] += wgt * v.z; o[4 * q + 3] += wgt * v.w;
         }
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= inv;
-        if (sum != 0.f) lse = (top + log2f(sum)) * 0.6931471805599453f;
     }
+    if (lane == 0) sh_sum[warp] = sum;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(o[4 * q], o[4 * q + 1]), y = __floats2bfloat162_rn(o[4 * q + 2], o[4 * q + 3]);
-        *(uint2*)(to + q * 128 + lane * 4) = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+    for (int q = 0; q < 4; ++q)
+        *(float4*)(sh_o[warp] + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLdJoinWarps; ++w) sum += sh_sum[w];
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kLdJoinWarps; ++w) {
+        const float4 y = *(const float4*)(sh_o[w] + threadIdx.x * 4);
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
     }
-    if (lane == 0 && a.lse) a.lse[(size_t)n * a.rows + row] = lse;
+    uint2 b;
+    b.x = bf16x2(pack2(x.x * inv, x.y * inv));
+    b.y = bf16x2(pack2(x.z * inv, x.w * inv));
+    *(uint2*)(a.out + ((size_t)n * a.rows + row) * kLdRank + threadIdx.x * 4) = b;
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[(size_t)n * a.rows + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------- host
-struct LdPlan { int R, groups, G; size_t bytes; };
+struct LdPlan { int R, groups, G; size_t before, parts, bytes; };   // offsets behind the CTAs' status
 
 // CTAs and workspace of a call, from its sizes alone.
 static LdPlan ld_plan(int N, int Lq, int H, int page_size, int max_pages) {
     LdPlan p;
     const int64_t rows = (int64_t)Lq * H;
-    p.R = rows <= 16 ? 16 : 32;
+    p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     p.groups = (int)((rows + p.R - 1) / p.R);
     const int64_t tiles = (int64_t)N * (((int64_t)max_pages * page_size + kLdTile - 1) / kLdTile);
     int64_t g = 152 / p.groups;
     g = g < 1 ? 1 : g;
     p.G = (int)(g < tiles ? g : tiles);
-    const size_t status = ((size_t)p.groups * p.G * 4 + 255) / 256 * 256;
-    p.bytes = status + (size_t)p.groups * p.G * 2 * p.R * kLdPart * 4;
+    p.before = ((size_t)p.groups * p.G * 4 + 255) / 256 * 256;
+    p.parts = p.before + ((size_t)(N + 1) * 8 + 255) / 256 * 256;
+    p.bytes = p.parts + (size_t)p.groups * p.G * 2 * p.R * kLdPart * 4;
     return p;
 }
 
@@ -574,7 +632,8 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
     a.max_pages = d.max_pages; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
-    a.parts = (float*)((char*)d.scratch + ((size_t)p.groups * p.G * 4 + 255) / 256 * 256);
+    a.before = (int64_t*)((char*)d.scratch + p.before);
+    a.parts = (float*)((char*)d.scratch + p.parts);
     CUtensorMap mq, mc;
     const uint64_t qd[3] = {kLdWidth, (uint64_t)a.rows, (uint64_t)d.N};
     const uint64_t qs[2] = {(uint64_t)(d.H == 1 ? d.q_ts : d.q_hs) * 2, (uint64_t)d.q_ts * d.Lq * 2};
@@ -588,7 +647,7 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(d.N, (a.rows + 7) / 8); cfg.blockDim = dim3(256); cfg.stream = stream;
+    cfg.gridDim = dim3(d.N, a.rows); cfg.blockDim = dim3(32 * kLdJoinWarps); cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -598,7 +657,7 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
 
 cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {
     const LdPlan p = ld_plan(d.N, d.Lq, d.H, d.page_size, d.max_pages);
-    return p.R == 16 ? ld_launch<16>(d, p, stream) : ld_launch<32>(d, p, stream);
+    return p.R == 16 ? ld_launch<16>(d, p, stream) : p.R == 32 ? ld_launch<32>(d, p, stream) : ld_launch<64>(d, p, stream);
 }
 
 }  // namespace kda
