@@ -40,7 +40,7 @@ using namespace sm100;
 constexpr int kLdTile = 128;                  // tokens of a tile
 constexpr int kLdRank = 512, kLdWidth = 576;
 constexpr uint32_t kLdPiece = kLdTile * 128;  // 64 channels of a tile
-constexpr int kLdThreads = 192;               // 4 softmax warps, producer, matrix instructions
+constexpr int kLdThreads = 224;               // 4 softmax warps, 2 producers, matrix instructions
 constexpr float kLdUnset = -1e30f;            // reference of a row that has seen no key
 constexpr float kLdSlack = 8.f;               // how far (log2) a score may exceed its reference
 
@@ -212,13 +212,16 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
     // Order of the copies and products: S_0, then for each tile j: S_{j+1}, V_j.
-    if (warp == 4) {                                                   // ---------------- producer
+    // Two producer warps take the ring's slots in turn: a copy takes a warp about 90 cycles to issue, and with
+    // pages of 16 tokens there are 136 to a tile.
+    if (warp == 4 || warp == 5) {                                      // ---------------- producers
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
         uint32_t unit = 0, seg = 0;
         bool ok = true, bad_page = false;
         // a unit: one piece at x, or two; a lane for each box of tokens
         auto fetch = [&](int x, int pieces, int row, int page) {
             const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
+            if ((unit & 1) != (uint32_t)(warp & 1)) { ++unit; return; }
             if (unit >= S::kSlots && !(ok = mbar_wait_warp(&empty[s], ph ^ 1))) return;
             if (lane == 0) mbar_arrive_expect_tx(&full[s], pieces * kLdPiece);
             __syncwarp();
@@ -235,7 +238,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (bool more = false; ok; more = true) {
             int row = 0, page = a.num_pages;
             if (w.left > 0) {
-                if (w.first) {
+                if (w.first && warp == 4) {
                     if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
                     if (!ok) break;
                     if (lane == 0) {
@@ -266,7 +269,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (bad_page) atomicMax(fault, KDA_ERR_BAD_PAGE);
         if (!ok) { atomicMax(fault, KDA_ERR_TIMEOUT); drain_copies(); }
-    } else if (warp == 5) {                                            // ---------------- matrix instructions
+    } else if (warp == 6) {                                            // ---------------- matrix instructions
         const uint32_t idesc_s = idesc_bf16(128, R), idesc_o = idesc_bf16(128, R, 1, 1);
         const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
         uint32_t unit = 0, seg = 0, zero = 0;
@@ -508,16 +511,20 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
 // Joins the pieces of sequences that several CTAs shared, gives sequences
 // without tiles their zeros, and collects the CTAs' status.  A block a row, its
-// warps a share of the pieces each.
-constexpr int kLdJoinWarps = 4;
+// warps a share of the pieces each: two of them for many rows (so small that the
+// blocks wait beside the CTAs above instead of after them), eight for few.
 template <int R>
-__global__ void __launch_bounds__(32 * kLdJoinWarps)
+__global__ void __launch_bounds__(256)
 kda_latent_decode_join(const LdArgs a, const int groups) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ __align__(16) float sh[];        // [warps][kLdRank] O, [warps] ref, [warps] sum
     const int n = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = blockDim.x >> 5;
+    float *sh_top = sh + warps * kLdRank, *sh_sum = sh_top + warps;
+    const int tiles = ld_tiles(a, n);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0 && row == 0) {
         int bad_page = 0, bad_len = 0, late = 0;
-        for (int i = threadIdx.x; i < a.G * groups; i += 32 * kLdJoinWarps) {
+        for (int i = threadIdx.x; i < a.G * groups; i += blockDim.x) {
             const int st = a.cta_status[i];
             bad_page |= st == KDA_ERR_BAD_PAGE; bad_len |= st == KDA_ERR_BAD_SEQLENS; late |= st == KDA_ERR_TIMEOUT;
         }
@@ -525,7 +532,6 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
         if (threadIdx.x == 0)
             *a.status = bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : late ? KDA_ERR_TIMEOUT : KDA_OK;
     }
-    const int tiles = ld_tiles(a, n);
     int cf = 0, cl = -1;
     if (tiles > 0) {
         const int64_t total = a.before[a.N], before = a.before[n], parts = min64(a.G, total);
@@ -537,21 +543,18 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     auto piece = [&](int i) {
         return a.parts + (((size_t)(i * groups + group) * 2 + (i == cf)) * R + c) * kLdPart;
     };
-    __shared__ float sh_top[kLdJoinWarps], sh_sum[kLdJoinWarps];
-    __shared__ __align__(16) float sh_o[kLdJoinWarps][kLdRank];
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
     float top = kLdUnset, sum = 0.f;
-    for (int i = cf + threadIdx.x; i <= cl; i += 32 * kLdJoinWarps) top = fmaxf(top, piece(i)[kLdRank]);
+    for (int i = cf + threadIdx.x; i <= cl; i += blockDim.x) top = fmaxf(top, piece(i)[kLdRank]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
     if (lane == 0) sh_top[warp] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kLdJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
+    for (int w = 0; w < warps; ++w) top = fmaxf(top, sh_top[w]);
 #pragma unroll 4
-    for (int i = cf + warp; i <= cl; i += kLdJoinWarps) {
+    for (int i = cf + warp; i <= cl; i += warps) {
         const float* p = piece(i);
         const float2 ml = *(const float2*)(p + kLdRank);
         const float wgt = ex2(ml.x - top);
@@ -565,22 +568,22 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     if (lane == 0) sh_sum[warp] = sum;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        *(float4*)(sh_o[warp] + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        *(float4*)(sh + warp * kLdRank + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
     __syncthreads();
     sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kLdJoinWarps; ++w) sum += sh_sum[w];
+    for (int w = 0; w < warps; ++w) sum += sh_sum[w];
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kLdJoinWarps; ++w) {
-        const float4 y = *(const float4*)(sh_o[w] + threadIdx.x * 4);
-        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+    for (int e = threadIdx.x * 4; e < kLdRank; e += blockDim.x * 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < warps; ++w) {
+            const float4 y = *(const float4*)(sh + w * kLdRank + e);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        uint2 b;
+        b.x = bf16x2(pack2(x.x * inv, x.y * inv));
+        b.y = bf16x2(pack2(x.z * inv, x.w * inv));
+        *(uint2*)(a.out + ((size_t)n * a.rows + row) * kLdRank + e) = b;
     }
-    uint2 b;
-    b.x = bf16x2(pack2(x.x * inv, x.y * inv));
-    b.y = bf16x2(pack2(x.z * inv, x.w * inv));
-    *(uint2*)(a.out + ((size_t)n * a.rows + row) * kLdRank + threadIdx.x * 4) = b;
     if (threadIdx.x == 0 && a.lse)
         a.lse[(size_t)n * a.rows + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
@@ -647,7 +650,9 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(d.N, a.rows); cfg.blockDim = dim3(32 * kLdJoinWarps); cfg.stream = stream;
+    const int warps = (int64_t)d.N * a.rows >= 512 ? 2 : 8;
+    cfg.gridDim = dim3(d.N, a.rows); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
+    cfg.dynamicSmemBytes = warps * (kLdRank + 2) * 4;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
