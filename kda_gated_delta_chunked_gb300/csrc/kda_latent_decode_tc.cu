@@ -24,9 +24,13 @@
 // Bound by HBM: at 6.78 TB/s a tile's 147 KB take an SM 6600 cycles; its
 // products take about 2900 (40 cycles an instruction whatever R up to 32).  A
 // tile does not stay in shared memory between its two products: the second
-// fetches the 512 channels again, out of L2, so that all of the ring (160 KB)
-// is copies in flight; S^T of the next tile is formed before the second product
-// of this one, which hides the softmax.
+// fetches the 512 channels again, out of L2.  So each product has a stream of
+// its own, with a producer warp, a ring and a warp that issues it, and the next
+// tiles' scores go ahead while this one's softmax and second product run.
+//
+// A wait on an mbarrier looks at a parity only, so each waiter stays within one
+// phase of what it waits for: a ring has one producer and one consumer, both in
+// order, and what alternates between tiles has a barrier for odd and even ones.
 #include <math.h>
 
 #include "kda_common.cuh"
@@ -40,17 +44,19 @@ using namespace sm100;
 constexpr int kLdTile = 128;                  // tokens of a tile
 constexpr int kLdRank = 512, kLdWidth = 576;
 constexpr uint32_t kLdPiece = kLdTile * 128;  // 64 channels of a tile
-constexpr int kLdThreads = 224;               // 4 softmax warps, 2 producers, matrix instructions
+constexpr int kLdThreads = 256;               // 4 softmax warps, 2 producers, a warp for each product
 constexpr float kLdUnset = -1e30f;            // reference of a row that has seen no key
 constexpr float kLdSlack = 8.f;               // how far (log2) a score may exceed its reference
 
 template <int R>
 struct LdShape {
-    static constexpr int kSlots = R == 64 ? 3 : 5;                 // of two pieces (128 channels; the rotary one alone)
+    // slots of two pieces (128 channels; the rotary one alone): the first for S^T, the others for O^T
+    static constexpr int kSlotsS = R == 64 ? 2 : 3, kSlotsV = 2, kSlots = kSlotsS + kSlotsV;
+    static constexpr int kBufP = R == 64 ? 1 : 2;
     static constexpr uint32_t kSlot = 2 * kLdPiece;
     static constexpr uint32_t kQPiece = R * 128, kQ = 9 * kQPiece;
-    static constexpr uint32_t kRow = R * 2, kP = kLdTile * kRow;   // P^T: a token's R values, double-buffered
-    static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + kQ, kOffSmall = kOffP + 2 * kP;
+    static constexpr uint32_t kRow = R * 2, kP = kLdTile * kRow;   // P^T: a token's R values
+    static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + kQ, kOffSmall = kOffP + kBufP * kP;
     static constexpr uint32_t kSmem = kOffSmall + 1024 + (2 * 4 + 3) * R * 4 + 512;
     static constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512;   // two S^T, four blocks of O^T: 6 R columns
     static constexpr uint64_t kSwz = R == 16 ? 6 : R == 32 ? 4 : 2;
@@ -141,7 +147,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     float* across = (float*)(query + R);               // [4][R] one value a warp and row
     float* sums = across + 4 * R;                      // [4][R]
     uint64_t* bars = (uint64_t*)(sums + 4 * R);
-    uint64_t *full = bars, *empty = full + S::kSlots, *q_full = empty + S::kSlots, *q_empty = q_full + 1,
+    uint64_t *full = bars, *empty = full + S::kSlots,              // first the slots for S^T, then those for O^T
+             *full_v = full + S::kSlotsS, *empty_v = empty + S::kSlotsS, *q_full = empty + S::kSlots, *q_empty = q_full + 1,
              *s_full = q_empty + 1, *o_full = s_full + 2,          // [2]: alternate tiles
              *p_full = o_full + 2, *zeroed = p_full + 2,          // zeroed [4]: a pair of pieces each
              *bars_end = zeroed + 4;
@@ -153,33 +160,46 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        for (uint64_t* b = bars; b < p_full; ++b) mbar_init(b, 1);
-        for (uint64_t* b = p_full; b < bars_end; ++b) mbar_init(b, 4);
-        fence_mbar_init();
-    }
-    if (warp == 0) { tmem_alloc(tmem_at, S::kTmem); tmem_relinquish(); }
     if (warp == 4) {
-        // this CTA's range of the tiles of all sequences
+        if (lane == 0) {
+            for (uint64_t* b = bars; b < p_full; ++b) mbar_init(b, 1);
+            for (uint64_t* b = p_full; b < bars_end; ++b) mbar_init(b, 4);
+            fence_mbar_init();
+            prefetch_map(&map_c);
+            prefetch_map(&map_q);
+        }
+        // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
+        // warps wait for it at the barrier.
+        const int64_t cap = (int64_t)a.max_pages * a.page_size;
         int64_t total = 0;
         bool bad = false;
+        int first = 0;                                                 // tiles of sequence `lane`
         for (int b = 0; b < a.N; b += 32) {
             const int n = b + lane;
-            if (n < a.N) { const int l = a.lens[n]; bad |= l < 0 || (int64_t)l > (int64_t)a.max_pages * a.page_size; }
-            int t = n < a.N ? ld_tiles(a, n) : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            total += t;
+            const int len = n < a.N ? a.lens[n] : 0;
+            bad |= len < 0 || len > cap;
+            int t = len < 0 || len > cap ? 0 : (len + kLdTile - 1) / kLdTile;
+            if (b == 0) first = t;
+            total += __reduce_add_sync(0xffffffffu, t);
         }
         bad = __any_sync(0xffffffffu, bad);
         const int64_t parts = min64(a.G, total);       // no empty range between two that hold tiles
-        const int64_t t0 = cta < parts ? total * cta / parts : 0, t1 = cta < parts ? total * (cta + 1) / parts : 0;
+        int64_t t0 = 0, t1 = 0;
+        if (cta < parts) {
+            if (total < (1 << 20)) {
+                t0 = (uint32_t)total * cta / (uint32_t)parts;
+                t1 = (uint32_t)total * (cta + 1) / (uint32_t)parts;
+            } else {
+                t0 = total * cta / parts;
+                t1 = total * (cta + 1) / parts;
+            }
+        }
         int64_t before = 0;
         int n0 = 0, j0 = 0;
         if (t1 > t0) {
             for (int b = 0; b < a.N; b += 32) {
                 const int n = b + lane;
-                const int t = n < a.N ? ld_tiles(a, n) : 0;
+                const int t = b == 0 ? first : n < a.N ? ld_tiles(a, n) : 0;
                 int x = t;                                             // inclusive scan
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -202,136 +222,132 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             *fault = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
             *range_at = t0;
         }
+        __syncwarp();
+        asm volatile("bar.arrive 3, %0;" ::"n"(kLdThreads) : "memory");
+    } else {
+        if (warp == 0) { tmem_alloc(tmem_at, S::kTmem); tmem_relinquish(); }
+        if (threadIdx.x < R) {
+            ref[threadIdx.x] = kLdUnset;
+            query[threadIdx.x] = min((group * R + (int)threadIdx.x) / a.H, a.Lq - 1);
+        }
+        tc_fence_before_sync();
+        asm volatile("bar.sync 3, %0;" ::"n"(kLdThreads) : "memory");
+        tc_fence_after_sync();
     }
-    if (threadIdx.x < R) {
-        ref[threadIdx.x] = kLdUnset;
-        query[threadIdx.x] = min((group * R + (int)threadIdx.x) / a.H, a.Lq - 1);
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
-    // Order of the copies and products: S_0, then for each tile j: S_{j+1}, V_j.
-    // Two producer warps take the ring's slots in turn: a copy takes a warp about 90 cycles to issue, and with
-    // pages of 16 tokens there are 136 to a tile.
-    if (warp == 4 || warp == 5) {                                      // ---------------- producers
+    const uint32_t tmem = warp == 4 ? 0 : __shfl_sync(0xffffffffu, *tmem_at, 0);
+    const uint32_t base_v = base + S::kSlotsS * S::kSlot;
+    if (warp == 4 || warp == 5) {                                      // ---------------- producers: for S^T, for O^T
+        const bool scores = warp == 4;
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
-        uint32_t unit = 0, seg = 0;
+        const uint32_t slots = scores ? S::kSlotsS : S::kSlotsV, ring = scores ? base : base_v;
+        uint64_t *fulls = scores ? full : full_v, *empties = scores ? empty : empty_v;
+        uint32_t seg = 0, s = 0, ph = 1;                               // slot and the parity its emptying has (first round: none)
         bool ok = true, bad_page = false;
-        // a unit: one piece at x, or two; a lane for each box of tokens
-        auto fetch = [&](int x, int pieces, int row, int page) {
-            const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
-            if ((unit & 1) != (uint32_t)(warp & 1)) { ++unit; return; }
-            if (unit >= S::kSlots && !(ok = mbar_wait_warp(&empty[s], ph ^ 1))) return;
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], pieces * kLdPiece);
-            __syncwarp();
-            if (lane < boxes) {
-                const uint32_t at = base + s * S::kSlot + lane * box * 128;
-                tma_load_3d_at(at, &map_c, x, row, page, smem_u32(&full[s]));
-                if (pieces == 2) tma_load_3d_at(at + kLdPiece, &map_c, x + 64, row, page, smem_u32(&full[s]));
-            }
-            ++unit;
-        };
         LdWalk w;
         w.start(a, range[0], range[1], range[2]);
-        int row_v = 0, page_v = 0;                                     // of the tile before
-        for (bool more = false; ok; more = true) {
-            int row = 0, page = a.num_pages;
-            if (w.left > 0) {
-                if (w.first && warp == 4) {
-                    if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full, S::kQ);
-                        for (int c = 0; c < 9; ++c)
-                            tma_load_3d_at(base + S::kOffQ + c * S::kQPiece, &map_q, c * 64, group * R, w.n, smem_u32(q_full));
-                    }
-                    __syncwarp();
-                    ++seg;
+        for (; w.left > 0 && ok; w.next(a)) {
+            if (scores && w.first) {
+                if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, S::kQ);
+                    for (int c = 0; c < 9; ++c)
+                        tma_load_3d_at(base + S::kOffQ + c * S::kQPiece, &map_q, c * 64, group * R, w.n, smem_u32(q_full));
                 }
-                // pages behind the length, and bad ones, read as zeros
-                if (lane < boxes) {
-                    const int t = w.j * kLdTile + lane * box;
-                    if (t < ld_len(a, w.n)) {
-                        const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
-                        if (p < 0 || p >= a.num_pages) bad_page = true;
-                        else { page = p; row = t % a.page_size; }
-                    }
-                }
-                fetch(kLdRank, 1, row, page);
-                for (int p = 0; p < 4 && ok; ++p) fetch(p * 128, 2, row, page);
+                __syncwarp();
+                ++seg;
             }
-            if (more)
-                for (int p = 0; p < 4 && ok; ++p) fetch(p * 128, 2, row_v, page_v);
-            if (w.left <= 0 || !ok) break;
-            row_v = row; page_v = page;
-            w.next(a);
+            // A lane for each box of tokens: its page and row.  Pages behind the length, and bad ones, read as zeros.
+            int row = 0, page = a.num_pages;
+            if (lane < boxes) {
+                const int t = w.j * kLdTile + lane * box;
+                if (t < ld_len(a, w.n)) {
+                    const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
+                    if (p < 0 || p >= a.num_pages) bad_page = true;
+                    else { page = p; row = t % a.page_size; }
+                }
+            }
+            for (int p = scores ? -1 : 0; p < 4; ++p) {                // the rotary piece, pairs of the others
+                if (!(ok = mbar_wait_warp(&empties[s], ph))) break;    // (a fresh barrier counts as emptied)
+                const uint32_t bar = smem_u32(&fulls[s]), at = ring + s * S::kSlot + lane * box * 128;
+                if (lane == 0) mbar_arrive_expect_tx(&fulls[s], (p < 0 ? 1 : 2) * kLdPiece);
+                __syncwarp();
+                if (lane < boxes) {
+                    tma_load_3d_at(at, &map_c, p < 0 ? kLdRank : p * 128, row, page, bar);
+                    if (p >= 0) tma_load_3d_at(at + kLdPiece, &map_c, p * 128 + 64, row, page, bar);
+                }
+                __syncwarp();
+                if (++s == slots) { s = 0; ph ^= 1; }
+            }
         }
         if (bad_page) atomicMax(fault, KDA_ERR_BAD_PAGE);
         if (!ok) { atomicMax(fault, KDA_ERR_TIMEOUT); drain_copies(); }
-    } else if (warp == 6) {                                            // ---------------- matrix instructions
-        const uint32_t idesc_s = idesc_bf16(128, R), idesc_o = idesc_bf16(128, R, 1, 1);
+    } else if (warp == 6) {                                            // ---------------- S^T
+        const uint32_t idesc = idesc_bf16(128, R);
         const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
-        uint32_t unit = 0, seg = 0, zero = 0;
+        uint32_t s = 0, ph = 0, seg = 0;
         bool ok = true;
-        LdWalk ws, w;
-        ws.start(a, range[0], range[1], range[2]);
-        w = ws;
-        const int count = ws.left;
-        for (int j = -1; j < count && ok; ++j) {
-            const int js = j + 1;
-            if (js < count) {                                          // S^T of the next tile
-                if (ws.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
-                for (int p = -1; p < 4 && ok; ++p, ++unit) {           // rotary channels, then the pairs
-                    const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
-                    if (!(ok = mbar_wait_warp(&full[s], ph))) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = sdesc_k_sw128(base + s * S::kSlot);
-                    const uint64_t db = dq + (p < 0 ? 8 : 2 * p) * (S::kQPiece / 16);
-                    const uint32_t d = tmem + (js & 1) * R;
-                    if (elect_one()) {
+        LdWalk w;
+        w.start(a, range[0], range[1], range[2]);
+        const int count = w.left;
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
+            if (w.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
+            if (ok && j >= 2) ok = mbar_wait_warp(&p_full[j & 1], ((j - 2) >> 1) & 1);   // S_{j-2} is read
+            const uint32_t d = tmem + (j & 1) * R;
+            for (int p = -1; p < 4 && ok; ++p) {
+                if (!(ok = mbar_wait_warp(&full[s], ph))) break;
+                tc_fence_after_sync();
+                const uint64_t da = sdesc_k_sw128(base + s * S::kSlot);
+                const uint64_t db = dq + (p < 0 ? 8 : 2 * p) * (S::kQPiece / 16);
+                if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_bf16_ss(d, da + 2 * k, db + 2 * k, idesc_s, p >= 0 || k > 0);
-                        if (p >= 0) {
+                    for (int k = 0; k < 4; ++k) mma_bf16_ss(d, da + 2 * k, db + 2 * k, idesc, p >= 0 || k > 0);
+                    if (p >= 0) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16_ss(d, da + kLdPiece / 16 + 2 * k, db + S::kQPiece / 16 + 2 * k, idesc_s, 1);
-                        }
-                        mma_commit(&empty[s]);
-                        if (p == 3) {
-                            mma_commit(&s_full[js & 1]);
-                            if (ws.last()) mma_commit(q_empty);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss(d, da + kLdPiece / 16 + 2 * k, db + S::kQPiece / 16 + 2 * k, idesc, 1);
                     }
-                    __syncwarp();
+                    mma_commit(&empty[s]);
+                    if (p == 3) {
+                        mma_commit(&s_full[j & 1]);
+                        if (w.last()) mma_commit(q_empty);
+                    }
                 }
-                if (!ok) break;
-                ws.next(a);
+                __syncwarp();
+                if (++s == S::kSlotsS) { s = 0; ph ^= 1; }
             }
-            if (j < 0) continue;
+        }
+        if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
+    } else if (warp == 7) {                                            // ---------------- O^T += V^T P^T
+        const uint32_t idesc = idesc_bf16(128, R, 1, 1);
+        uint32_t s = 0, ph = 0, zero = 0;
+        bool ok = true;
+        LdWalk w;
+        w.start(a, range[0], range[1], range[2]);
+        const int count = w.left;
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
             if (!(ok = mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
-            const uint64_t dp = sdesc(base + S::kOffP + (j & 1) * S::kP, 16, 8 * S::kRow, S::kSwz);
+            const uint64_t dp = sdesc(base + S::kOffP + j % S::kBufP * S::kP, 16, 8 * S::kRow, S::kSwz);
             const bool ragged = uniform((w.j + 1) * kLdTile > ld_len(a, w.n));
-            for (int p = 0; p < 4; ++p, ++unit) {                      // O^T += V^T P^T
-                const uint32_t s = unit % S::kSlots, ph = (unit / S::kSlots) & 1;
-                ok = mbar_wait_warp(&full[s], ph);
+            for (int p = 0; p < 4; ++p) {
+                ok = mbar_wait_warp(&full_v[s], ph);
                 if (ok && ragged) ok = mbar_wait_warp(&zeroed[p], zero & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 // A: 128 channels = two pieces of 64, MN-major; 16 tokens a step
-                const uint64_t da = sdesc(base + s * S::kSlot, kLdPiece, 1024, 2);
+                const uint64_t da = sdesc(base_v + s * S::kSlot, kLdPiece, 1024, 2);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_bf16_ss(tmem + (2 + p) * R, da + k * (2048 / 16), dp + k * (16 * S::kRow / 16), idesc_o,
+                        mma_bf16_ss(tmem + (2 + p) * R, da + k * (2048 / 16), dp + k * (16 * S::kRow / 16), idesc,
                                     !w.first || k > 0);
-                    mma_commit(&empty[s]);
+                    mma_commit(&empty_v[s]);
                     if (p == 3) mma_commit(&o_full[j & 1]);
                 }
                 __syncwarp();
+                if (++s == S::kSlotsV) { s = 0; ph ^= 1; }
             }
             zero += ragged;
-            if (ok) w.next(a);
         }
         if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
     } else {                                                           // ---------------- softmax
@@ -341,8 +357,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         float l[R];
 #pragma unroll
         for (int c = 0; c < R; ++c) l[c] = 0.f;
-        // units of the ring, as the producer orders them
-        uint32_t unit = 5;                                             // behind S_0
         bool ok = true;
         LdWalk w;
         w.start(a, range[0], range[1], range[2]);
@@ -410,8 +424,9 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     tmem_wait_st();
                 }
             }
-            if (j >= 2) {                                              // P's buffer: the products that read it are complete
-                ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
+            if (j >= S::kBufP) {                                       // P's buffer: the products that read it are complete
+                const int before = j - S::kBufP;
+                ok = mbar_wait_warp(&o_full[before & 1], (before >> 1) & 1);
                 if (!ok) break;
             }
 #pragma unroll
@@ -427,32 +442,29 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);    // the product's operand: 8 bits
                     b[i] = *(const uint32_t*)&h;
                 }
-                *(uint4*)(mem + S::kOffP + (j & 1) * S::kP + S::p_at(threadIdx.x, c / 8)) = make_uint4(b[0], b[1], b[2], b[3]);
+                *(uint4*)(mem + S::kOffP + j % S::kBufP * S::kP + S::p_at(threadIdx.x, c / 8)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[j & 1]);
-            // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes.
-            if (j + 1 < count) unit += 5;                              // S_{j+1} comes before V_j
+            // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes (once the
+            // products of the tile before are complete, the ring is at this tile's).
             if ((w.j + 1) * kLdTile > len) {
+                if (j > 0) ok = mbar_wait_warp(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
                 for (int p = 0; p < 4 && ok; ++p) {
-                    const uint32_t u = unit + p, s = u % S::kSlots;
-                    ok = mbar_wait_warp(&full[s], (u / S::kSlots) & 1);
-                    if (token >= len) {
-                        uint8_t* at = mem + s * S::kSlot + threadIdx.x * 128;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            *(uint4*)(at + 16 * i) = make_uint4(0, 0, 0, 0);
-                            *(uint4*)(at + kLdPiece + 16 * i) = make_uint4(0, 0, 0, 0);
-                        }
+                    const uint32_t u = 4 * j + p, s = u % S::kSlotsV;
+                    ok = mbar_wait_warp(&full_v[s], (u / S::kSlotsV) & 1);
+                    uint8_t* at = mem + (S::kSlotsS + s) * S::kSlot + threadIdx.x % 8 * 16;
+                    for (int r = len - w.j * kLdTile + (int)threadIdx.x / 8; r < kLdTile; r += 16) {
+                        *(uint4*)(at + r * 128) = make_uint4(0, 0, 0, 0);
+                        *(uint4*)(at + kLdPiece + r * 128) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&zeroed[p]);
                 }
             }
-            unit += 4;
             if (!w.last()) continue;
 
             // end of a segment: sums across the tokens' threads, then O^T out
@@ -512,17 +524,19 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 // Joins the pieces of sequences that several CTAs shared, gives sequences
 // without tiles their zeros, and collects the CTAs' status.  A block a row, its
 // warps a share of the pieces each: two of them for many rows (so small that the
-// blocks wait beside the CTAs above instead of after them), eight for few.
-template <int R>
+// blocks wait beside the CTAs above instead of after them), eight for few, and
+// then a block for each 128 of its channels.
+template <int R, int Q>                                // Q: 128-channel blocks of a block, 4 or 1
 __global__ void __launch_bounds__(256)
 kda_latent_decode_join(const LdArgs a, const int groups) {
-    extern __shared__ __align__(16) float sh[];        // [warps][kLdRank] O, [warps] ref, [warps] sum
+    extern __shared__ __align__(16) float sh[];        // [warps][128 Q] O, [warps] ref, [warps] sum
     const int n = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warps = blockDim.x >> 5;
-    float *sh_top = sh + warps * kLdRank, *sh_sum = sh_top + warps;
+    const int ch0 = blockIdx.z * 128 * Q;
+    float *sh_top = sh + warps * 128 * Q, *sh_sum = sh_top + warps;
     const int tiles = ld_tiles(a, n);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n == 0 && row == 0) {
+    if (n == 0 && row == 0 && blockIdx.z == 0) {
         int bad_page = 0, bad_len = 0, late = 0;
         for (int i = threadIdx.x; i < a.G * groups; i += blockDim.x) {
             const int st = a.cta_status[i];
@@ -543,9 +557,9 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     auto piece = [&](int i) {
         return a.parts + (((size_t)(i * groups + group) * 2 + (i == cf)) * R + c) * kLdPart;
     };
-    float o[16];
+    float o[4 * Q];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    for (int i = 0; i < 4 * Q; ++i) o[i] = 0.f;
     float top = kLdUnset, sum = 0.f;
     for (int i = cf + threadIdx.x; i <= cl; i += blockDim.x) top = fmaxf(top, piece(i)[kLdRank]);
 #pragma unroll
@@ -560,31 +574,31 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
         const float wgt = ex2(ml.x - top);
         sum += wgt * ml.y;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 v = *(const float4*)(p + q * 128 + lane * 4);
+        for (int q = 0; q < Q; ++q) {
+            const float4 v = *(const float4*)(p + ch0 + q * 128 + lane * 4);
             o[4 * q] += wgt * v.x; o[4 * q + 1] += wgt * v.y; o[4 * q + 2] += wgt * v.z; o[4 * q + 3] += wgt * v.w;
         }
     }
     if (lane == 0) sh_sum[warp] = sum;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        *(float4*)(sh + warp * kLdRank + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    for (int q = 0; q < Q; ++q)
+        *(float4*)(sh + warp * 128 * Q + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
     __syncthreads();
     sum = 0.f;
     for (int w = 0; w < warps; ++w) sum += sh_sum[w];
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    for (int e = threadIdx.x * 4; e < kLdRank; e += blockDim.x * 4) {
+    for (int e = threadIdx.x * 4; e < 128 * Q; e += blockDim.x * 4) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < warps; ++w) {
-            const float4 y = *(const float4*)(sh + w * kLdRank + e);
+            const float4 y = *(const float4*)(sh + w * 128 * Q + e);
             x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         }
         uint2 b;
         b.x = bf16x2(pack2(x.x * inv, x.y * inv));
         b.y = bf16x2(pack2(x.z * inv, x.w * inv));
-        *(uint2*)(a.out + ((size_t)n * a.rows + row) * kLdRank + e) = b;
+        *(uint2*)(a.out + ((size_t)n * a.rows + row) * kLdRank + ch0 + e) = b;
     }
-    if (threadIdx.x == 0 && a.lse)
+    if (threadIdx.x == 0 && blockIdx.z == 0 && a.lse)
         a.lse[(size_t)n * a.rows + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
@@ -650,14 +664,16 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int warps = (int64_t)d.N * a.rows >= 512 ? 2 : 8;
-    cfg.gridDim = dim3(d.N, a.rows); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
-    cfg.dynamicSmemBytes = warps * (kLdRank + 2) * 4;
+    const bool many = (int64_t)d.N * a.rows >= 512;
+    const int warps = many ? 2 : 8, per = many ? 4 : 1;
+    cfg.gridDim = dim3(d.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
+    cfg.dynamicSmemBytes = warps * (128 * per + 2) * 4;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at; cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R>, a, p.groups);
+    return many ? cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 4>, a, p.groups)
+                : cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 1>, a, p.groups);
 }
 
 cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {

@@ -275,6 +275,21 @@ def test_prefill_large_scores_and_infinities(kda):
     assert (out[0] == 0).all() and (lse[0] == -float("inf")).all()
 
 
+def test_prefill_nan_behind_a_sequence_stays_there(kda):
+    """Keys and values of the next sequence (here NaN and infinities) never enter a sequence's last tile."""
+    lq, lk = [130, 40, 70], [150, 40, 70]
+    q, kn, kr, v = expanded(sum(lq), sum(lk), 2, seed=8)
+    want, wl = check_prefill(kda, q, kn, kr, v, lq, lk, rows=[0, 129])
+    kn, kr, v = kn.clone(), kr.clone(), v.clone()
+    kn[150:190], kr[150:190], v[150:190] = float("nan"), float("inf"), float("nan")
+    for causal in (True, False):
+        cu = lambda l: torch.tensor([0] + list(torch.tensor(l).cumsum(0)), dtype=torch.int32).cuda()  # noqa: E731
+        good, _ = kda.latent_prefill(*(t.cuda() for t in expanded(sum(lq), sum(lk), 2, seed=8)), cu(lq), cu(lk), scale=192 ** -0.5, causal=causal)
+        out, lse = kda.latent_prefill(q.cuda(), kn.cuda(), kr.cuda(), v.cuda(), cu(lq), cu(lk), scale=192 ** -0.5, causal=causal)
+        assert torch.equal(out[:130], good[:130]) and torch.equal(out[170:], good[170:])
+        assert torch.isnan(out[130:170].float()).all()
+
+
 def test_prefill_reports_bad_lengths(kda):
     q, kn, kr, v = (t.cuda() for t in expanded(100, 100, 2))
     ws = torch.empty(kda.latent_prefill_workspace_bytes(2, 2, BF16), dtype=torch.uint8, device="cuda")
@@ -334,6 +349,44 @@ def test_decode(kda, simt, lens, lq, h, page):
 @pytest.mark.parametrize("lens,lq,h", [([9000], 1, 16), ([5000, 17, 0, 3001], 2, 32), ([40] * 300, 1, 16), ([0] * 5, 1, 16)])
 def test_decode_split_over_the_cache(kda, lens, lq, h):
     check_decode(kda, lens, lq, h, 64, rows=[0, 9, h - 1])
+
+
+@pytest.mark.parametrize("lens,lq,h,page", [([45000], 1, 32, 64), ([1500] * 70, 1, 16, 64), ([2100, 0, 1, 3333] * 14, 1, 32, 16),
+                                            ([1900] * 40, 3, 16, 32), ([2500] * 30, 1, 100, 64)])
+def test_decode_many_tiles_a_block_and_nan_behind_the_lengths(kda, lens, lq, h, page):
+    """Several tiles and sequences a thread block; pages hold NaN and infinities behind each sequence's length."""
+    cache, table, seqs = paged(lens, page, 576, BF16, 31)
+    seqs = [c.clone() for c in seqs]
+    host = cache.cpu()
+    for n, length in enumerate(lens):
+        if length % page:
+            last = int(table[n, length // page])
+            host[last, length % page:] = float("nan")
+            host[last, -1] = float("inf")
+    for spare in set(range(cache.shape[0])) - set(table.flatten().tolist()):
+        host[spare] = float("nan")
+    q = normal(32, len(lens), lq, h, 576, dtype=BF16)
+    L = torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = torch.empty(kda.latent_decode_workspace_bytes(len(lens), lq, h, 512, 64, BF16, page, table.shape[1]), dtype=torch.uint8, device="cuda")
+    out, lse = kda.latent_decode(q.cuda(), host.cuda(), table, L, scale=0.0722, workspace=ws)
+    assert kda.latent_status(ws) == kda.KDA_OK
+    again, lse2 = kda.latent_decode(q.cuda(), host.cuda(), table, L, scale=0.0722)
+    assert torch.equal(out, again) and torch.equal(lse, lse2) and torch.isfinite(out.float()).all()
+    simt, slse = kda.latent_decode(q.cuda(), cache, table, L, scale=0.0722, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL)
+    o, l = out.cpu(), lse.cpu()
+    for n in sorted({0, 1, len(lens) // 2, len(lens) - 1} & set(range(len(lens)))):
+        for i in range(lq):
+            end = max(0, lens[n] - lq + i + 1)
+            for hh in (0, h - 1):
+                want, wl, weight, ds = ref.attend(q[n, i, hh], seqs[n][:end], seqs[n][:end, :512], 0.0722)
+                bo, bl = ref.attention_bounds(want, wl, weight, ds, end, BF16, True)
+                within(o[n, i, hh], want, bo, ("out", n, i, hh))
+                within(l[n, i, hh], torch.tensor(wl), bl, ("lse", n, i, hh))
+    # every row against the CUDA cores' form: both round the output, one its weights
+    off = (out.float() - simt.float()).norm(dim=-1) / simt.float().norm(dim=-1).clamp_min(1e-20)
+    assert float(off.max()) < 3 * 2.0 ** -8, float(off.max())
+    some = torch.isfinite(slse)
+    assert torch.equal(torch.isfinite(lse), some) and float((lse - slse)[some].abs().max()) < 1e-4
 
 
 @pytest.mark.parametrize("rank,rope,dtype,page", [(512, 64, F32, 64), (512, 64, BF16, 48), (256, 32, BF16, 64), (100, 7, F32, 5), (512, 0, BF16, 1)])
