@@ -50,13 +50,15 @@ constexpr float kLdSlack = 8.f;               // how far (log2) a score may exce
 
 template <int R>
 struct LdShape {
-    // slots of two pieces (128 channels; the rotary one alone): the first for S^T, the others for O^T
-    static constexpr int kSlotsS = R == 64 ? 2 : 3, kSlotsV = 2, kSlots = kSlotsS + kSlotsV;
+    // Slots of three pieces (64 channels; with 64 rows two) for S^T, of two for O^T.  A slot is what one copy a
+    // page fills: [8 tokens][piece][token of 8][128 bytes], so that pages of any size make one operand.
+    static constexpr int kPieces = R == 64 ? 2 : 3, kUnits = (9 + kPieces - 1) / kPieces;
+    static constexpr int kSlotsS = 2, kSlotsV = 2, kSlots = kSlotsS + kSlotsV;
     static constexpr int kBufP = R == 64 ? 1 : 2;
-    static constexpr uint32_t kSlot = 2 * kLdPiece;
+    static constexpr uint32_t kSlotS = kPieces * kLdPiece, kSlotV = 2 * kLdPiece, kOffV = kSlotsS * kSlotS;
     static constexpr uint32_t kQPiece = R * 128, kQ = 9 * kQPiece;
     static constexpr uint32_t kRow = R * 2, kP = kLdTile * kRow;   // P^T: a token's R values
-    static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + kQ, kOffSmall = kOffP + kBufP * kP;
+    static constexpr uint32_t kOffQ = kOffV + kSlotsV * kSlotV, kOffP = kOffQ + kQ, kOffSmall = kOffP + kBufP * kP;
     static constexpr uint32_t kSmem = kOffSmall + 1024 + (2 * 4 + 3) * R * 4 + 512;
     static constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512;   // two S^T, four blocks of O^T: 6 R columns
     static constexpr uint64_t kSwz = R == 16 ? 6 : R == 32 ? 4 : 2;
@@ -135,8 +137,8 @@ __device__ __forceinline__ void ld_columns(const float (&x)[R], float* to, int l
 
 template <int R>
 __global__ void __launch_bounds__(kLdThreads, 1)
-kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
-                     const LdArgs a) {
+kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_s,
+                     const __grid_constant__ CUtensorMap map_v, const LdArgs a) {
     using S = LdShape<R>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -165,7 +167,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (uint64_t* b = bars; b < p_full; ++b) mbar_init(b, 1);
             for (uint64_t* b = p_full; b < bars_end; ++b) mbar_init(b, 4);
             fence_mbar_init();
-            prefetch_map(&map_c);
+            prefetch_map(&map_s);
+            prefetch_map(&map_v);
             prefetch_map(&map_q);
         }
         // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
@@ -235,11 +238,14 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         tc_fence_after_sync();
     }
     const uint32_t tmem = warp == 4 ? 0 : __shfl_sync(0xffffffffu, *tmem_at, 0);
-    const uint32_t base_v = base + S::kSlotsS * S::kSlot;
+    const uint32_t base_v = base + S::kOffV;
     if (warp == 4 || warp == 5) {                                      // ---------------- producers: for S^T, for O^T
         const bool scores = warp == 4;
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
         const uint32_t slots = scores ? S::kSlotsS : S::kSlotsV, ring = scores ? base : base_v;
+        const uint32_t slot = scores ? S::kSlotS : S::kSlotV;
+        const int units = scores ? S::kUnits : 4, pieces = scores ? S::kPieces : 2;
+        const CUtensorMap* map = scores ? &map_s : &map_v;
         uint64_t *fulls = scores ? full : full_v, *empties = scores ? empty : empty_v;
         uint32_t seg = 0, s = 0, ph = 1;                               // slot and the parity its emptying has (first round: none)
         bool ok = true, bad_page = false;
@@ -267,15 +273,12 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     else { page = p; row = t % a.page_size; }
                 }
             }
-            for (int p = scores ? -1 : 0; p < 4; ++p) {                // the rotary piece, pairs of the others
+            for (int u = 0; u < units; ++u) {
                 if (!(ok = mbar_wait_warp(&empties[s], ph))) break;    // (a fresh barrier counts as emptied)
-                const uint32_t bar = smem_u32(&fulls[s]), at = ring + s * S::kSlot + lane * box * 128;
-                if (lane == 0) mbar_arrive_expect_tx(&fulls[s], (p < 0 ? 1 : 2) * kLdPiece);
+                if (lane == 0) mbar_arrive_expect_tx(&fulls[s], slot);
                 __syncwarp();
-                if (lane < boxes) {
-                    tma_load_3d_at(at, &map_c, p < 0 ? kLdRank : p * 128, row, page, bar);
-                    if (p >= 0) tma_load_3d_at(at + kLdPiece, &map_c, p * 128 + 64, row, page, bar);
-                }
+                if (lane < boxes)
+                    tma_load_5d(ring + s * slot + lane * (slot / boxes), map, 0, 0, u * pieces, row / 8, page, smem_u32(&fulls[s]));
                 __syncwarp();
                 if (++s == slots) { s = 0; ph ^= 1; }
             }
@@ -294,21 +297,23 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (w.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
             if (ok && j >= 2) ok = mbar_wait_warp(&p_full[j & 1], ((j - 2) >> 1) & 1);   // S_{j-2} is read
             const uint32_t d = tmem + (j & 1) * R;
-            for (int p = -1; p < 4 && ok; ++p) {
-                if (!(ok = mbar_wait_warp(&full[s], ph))) break;
+#pragma unroll
+            for (int u = 0; u < S::kUnits; ++u) {
+                if (ok) ok = mbar_wait_warp(&full[s], ph);
+                if (!ok) break;
                 tc_fence_after_sync();
-                const uint64_t da = sdesc_k_sw128(base + s * S::kSlot);
-                const uint64_t db = dq + (p < 0 ? 8 : 2 * p) * (S::kQPiece / 16);
+                // A: tokens, K-major, 8-token groups a slot's pieces apart
+                const uint64_t da = sdesc(base + s * S::kSlotS, 16, S::kPieces * 1024, 2);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_bf16_ss(d, da + 2 * k, db + 2 * k, idesc, p >= 0 || k > 0);
-                    if (p >= 0) {
+                    for (int p = 0; p < S::kPieces && u * S::kPieces + p < 9; ++p) {
+                        const uint64_t db = dq + (u * S::kPieces + p) * (S::kQPiece / 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss(d, da + kLdPiece / 16 + 2 * k, db + S::kQPiece / 16 + 2 * k, idesc, 1);
+                            mma_bf16_ss(d, da + p * (1024 / 16) + 2 * k, db + 2 * k, idesc, u > 0 || p > 0 || k > 0);
                     }
                     mma_commit(&empty[s]);
-                    if (p == 3) {
+                    if (u == S::kUnits - 1) {
                         mma_commit(&s_full[j & 1]);
                         if (w.last()) mma_commit(q_empty);
                     }
@@ -335,11 +340,11 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (!ok) break;
                 tc_fence_after_sync();
                 // A: 128 channels = two pieces of 64, MN-major; 16 tokens a step
-                const uint64_t da = sdesc(base_v + s * S::kSlot, kLdPiece, 1024, 2);
+                const uint64_t da = sdesc(base_v + s * S::kSlotV, 1024, 2048, 2);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_bf16_ss(tmem + (2 + p) * R, da + k * (2048 / 16), dp + k * (16 * S::kRow / 16), idesc,
+                        mma_bf16_ss(tmem + (2 + p) * R, da + k * (4096 / 16), dp + k * (16 * S::kRow / 16), idesc,
                                     !w.first || k > 0);
                     mma_commit(&empty_v[s]);
                     if (p == 3) mma_commit(&o_full[j & 1]);
@@ -455,10 +460,10 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 for (int p = 0; p < 4 && ok; ++p) {
                     const uint32_t u = 4 * j + p, s = u % S::kSlotsV;
                     ok = mbar_wait_warp(&full_v[s], (u / S::kSlotsV) & 1);
-                    uint8_t* at = mem + (S::kSlotsS + s) * S::kSlot + threadIdx.x % 8 * 16;
+                    uint8_t* at = mem + S::kOffV + s * S::kSlotV + threadIdx.x % 8 * 16;
                     for (int r = len - w.j * kLdTile + (int)threadIdx.x / 8; r < kLdTile; r += 16) {
-                        *(uint4*)(at + r * 128) = make_uint4(0, 0, 0, 0);
-                        *(uint4*)(at + kLdPiece + r * 128) = make_uint4(0, 0, 0, 0);
+                        *(uint4*)(at + r / 8 * 2048 + r % 8 * 128) = make_uint4(0, 0, 0, 0);
+                        *(uint4*)(at + r / 8 * 2048 + 1024 + r % 8 * 128) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -651,16 +656,20 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
     a.before = (int64_t*)((char*)d.scratch + p.before);
     a.parts = (float*)((char*)d.scratch + p.parts);
-    CUtensorMap mq, mc;
+    CUtensorMap mq, ms, mv;
     const uint64_t qd[3] = {kLdWidth, (uint64_t)a.rows, (uint64_t)d.N};
     const uint64_t qs[2] = {(uint64_t)(d.H == 1 ? d.q_ts : d.q_hs) * 2, (uint64_t)d.q_ts * d.Lq * 2};
     const uint32_t qb[3] = {64, R, 1};
-    const uint64_t cd[3] = {kLdWidth, (uint64_t)d.page_size, (uint64_t)d.num_pages};
-    const uint64_t cs[2] = {kLdWidth * 2, (uint64_t)d.page_stride * 2};
-    const uint32_t cb[3] = {64, (uint32_t)(d.page_size < kLdTile ? d.page_size : kLdTile), 1};
-    if (!make_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, d.q, qd, qs, qb) ||
-        !make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, d.cache, cd, cs, cb)) return cudaErrorInvalidValue;
-    kda_latent_decode_tc<R><<<dim3(p.groups, p.G), kLdThreads, S::kSmem, stream>>>(mq, mc, a);
+    // the cache as [page][8 tokens][piece][token of 8][channel of 64], the last three the innermost
+    const uint64_t cd[5] = {64, 8, kLdWidth / 64, (uint64_t)d.page_size / 8, (uint64_t)d.num_pages};
+    const uint64_t cs[4] = {kLdWidth * 2, 128, 8 * kLdWidth * 2, (uint64_t)d.page_stride * 2};
+    uint32_t cb[5] = {64, 8, (uint32_t)S::kPieces, (uint32_t)(d.page_size < kLdTile ? d.page_size : kLdTile) / 8, 1};
+    bool made = make_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, d.q, qd, qs, qb) &&
+                make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, d.cache, cd, cs, cb);
+    cb[2] = 2;
+    made = made && make_map(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, d.cache, cd, cs, cb);
+    if (!made) return cudaErrorInvalidValue;
+    kda_latent_decode_tc<R><<<dim3(p.groups, p.G), kLdThreads, S::kSmem, stream>>>(mq, ms, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
