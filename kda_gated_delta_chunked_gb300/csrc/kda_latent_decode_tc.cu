@@ -163,25 +163,24 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int group = blockIdx.x, cta = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 4) {
+        // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
+        // warps wait for it at the barrier.
+        const int64_t cap = (int64_t)a.max_pages * a.page_size;
+        int len = lane < a.N ? a.lens[lane] : 0;                       // on its way while the barriers are made
+        if (lane < bars_end - bars) mbar_init(bars + lane, lane < p_full - bars ? 1 : 4);
         if (lane == 0) {
-            for (uint64_t* b = bars; b < p_full; ++b) mbar_init(b, 1);
-            for (uint64_t* b = p_full; b < bars_end; ++b) mbar_init(b, 4);
-            fence_mbar_init();
             prefetch_map(&map_s);
             prefetch_map(&map_v);
             prefetch_map(&map_q);
         }
-        // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
-        // warps wait for it at the barrier.
-        const int64_t cap = (int64_t)a.max_pages * a.page_size;
+        fence_mbar_init();
         int64_t total = 0;
         bool bad = false;
         int first = 0;                                                 // tiles of sequence `lane`
         for (int b = 0; b < a.N; b += 32) {
-            const int n = b + lane;
-            const int len = n < a.N ? a.lens[n] : 0;
+            if (b > 0) len = b + lane < a.N ? a.lens[b + lane] : 0;
             bad |= len < 0 || len > cap;
-            int t = len < 0 || len > cap ? 0 : (len + kLdTile - 1) / kLdTile;
+            const int t = len < 0 || len > cap ? 0 : (len + kLdTile - 1) / kLdTile;
             if (b == 0) first = t;
             total += __reduce_add_sync(0xffffffffu, t);
         }
@@ -572,7 +571,7 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     if (lane == 0) sh_top[warp] = top;
     __syncthreads();
     for (int w = 0; w < warps; ++w) top = fmaxf(top, sh_top[w]);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = cf + warp; i <= cl; i += warps) {
         const float* p = piece(i);
         const float2 ml = *(const float2*)(p + kLdRank);

@@ -397,15 +397,28 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         for (int t = 0; t < BT; ++t) sums[t * 128 + r] = acc[t];
     }
     cluster_sync();
-    // each CTA joins and stores its share of the tokens, the splits in rank order
+    // each CTA joins and stores its share of the tokens, the splits in rank order; four rows of b a thread
     const int live = (int)min64(BT, g.m - m0);
-    for (int i = rank * kThinThreads + threadIdx.x; i < live * 128; i += splits * kThinThreads) {
-        const uint32_t at = base + i * 4;
-        float x = 0.f;
-        for (int c = 0; c < splits; ++c) x += ld_cluster_f32(map_cta(at, c));
-        const int64_t m = m0 + i / 128;
-        const int n = n0 + i % 128;
-        if (n < g.n) ((T*)g.c)[m * g.ldc + n] = from_f32<T>(x);
+    for (int i = rank * kThinThreads + threadIdx.x; i < live * 32; i += splits * kThinThreads) {
+        float4 part[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < splits) part[c] = ld_cluster_f32x4(map_cta(base + i * 16, c));
+        float4 x = part[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c)
+            if (c < splits) { x.x += part[c].x; x.y += part[c].y; x.z += part[c].z; x.w += part[c].w; }
+        const int n = n0 + i % 32 * 4;
+        T* to = (T*)g.c + (m0 + i / 32) * g.ldc + n;
+        if (n + 4 <= g.n && ((uintptr_t)to & (4 * sizeof(T) - 1)) == 0) {
+            if constexpr (sizeof(T) == 2) *(uint2*)to = make_uint2(bf16x2(pack2(x.x, x.y)), bf16x2(pack2(x.z, x.w)));
+            else *(float4*)to = x;
+        } else {
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (n + q < g.n) to[q] = from_f32<T>(v[q]);
+        }
     }
     cluster_sync();
 }
