@@ -4,8 +4,7 @@
 //
 // The scales change with every 128 values of k, so each block's product D_j is
 // formed on its own in TMEM (4 instructions of 32 k) and read back, scaled and
-// added to fp32 registers while the next block's runs into the other half of a
-// TMEM double buffer.  Two shapes of the same loop:
+// added to fp32 registers while the next blocks' run into other parts of TMEM.  Two shapes of the same loop:
 //
 //  wide  rows of a along M.  A pair of CTAs (cta_group::2) owns a 256 x BN tile;
 //        each loads its 128 rows of a and half of b's rows, so a byte from L2
@@ -34,29 +33,13 @@ constexpr int kMmEpiWarps = 8;
 template <int BN>
 struct WideShape {
     static constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
-    static constexpr int kStages = BN == 256 ? 5 : 7;
-    static constexpr uint32_t kOut = 128 * BN * 2;                 // a tile's output on its way to c
+    static constexpr int kStages = BN == 256 ? 4 : 8;              // half for even blocks of k, half for odd ones
+    static constexpr int kBufs = 512 / BN;                         // products in TMEM
+    static constexpr int kGroups = BN / 128;                       // of 128 columns, each with its own barriers
+    static constexpr uint32_t kOut = 128 * BN * 2;                 // output on its way to c, half for each warpgroup
     static constexpr uint32_t kSmem = kStages * kStage + kOut + 1024 + 256;
     static constexpr int kThreads = 32 * (kMmEpiWarps + 4);        // whole warpgroups: registers move between them
 };
-
-// 8 or 16 consecutive values of a row at p (32-byte aligned).
-template <typename T>
-__device__ __forceinline__ void store_row32b(T* p, const f32x2* v) {
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if constexpr (sizeof(T) == 2) {
-            w[j] = bf16x2(v[j]);
-        } else {
-            float lo, hi;
-            unpack2(v[j / 2], lo, hi);
-            w[j] = __float_as_uint(j & 1 ? hi : lo);
-        }
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
 
 template <typename T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WideShape<BN>::kThreads, 1)
@@ -70,18 +53,20 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint8_t* after = raw + (base - smem_u32(raw)) + kStages * S::kStage + S::kOut;
     uint64_t* full = (uint64_t*)after;             // leader: both CTAs' pieces of a stage have landed
     uint64_t* empty = full + kStages;              // the MMAs reading a stage are done
-    uint64_t* tfull = empty + kStages;             // [2][2] half of a block's product is in TMEM
-    uint64_t* tempty = tfull + 4;                  // [2][2] leader: the pair's epilogue warps of that half have read it
-    uint32_t* tmem_at = (uint32_t*)(tempty + 4);
+    constexpr int kBufs = S::kBufs;
+    constexpr int kGroups = S::kGroups;
+    uint64_t* tfull = empty + kStages;             // [kBufs][kGroups] a group of a block's product is in TMEM
+    uint64_t* tempty = tfull + kBufs * kGroups;    // [kBufs][kGroups] leader: the pair's epilogue warps have read it
+    uint32_t* tmem_at = (uint32_t*)(tempty + kBufs * kGroups);
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
-        for (int i = 0; i < 4; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], kMmEpiWarps); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 2 * kMmEpiWarps / kGroups); }
         fence_mbar_init();
     }
-    if (warp == 0) { tmem_alloc_pair(tmem_at, 2 * BN); tmem_relinquish_pair(); }
+    if (warp == 0) { tmem_alloc_pair(tmem_at, 512); tmem_relinquish_pair(); }
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();
@@ -95,6 +80,14 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         const int per = 8 * tiles_n, grp = t / per, rows = min(8, tiles_m - grp * 8), r = t - grp * per;
         tm = grp * 8 + r % rows;
         tn = r / rows;
+    };
+
+    // Stage of block `it` (counted over the tiles) and the parity of its round: even and odd blocks have a ring
+    // each, since a warp each consumes them (in order: a wait on a barrier tells two phases apart, no more).
+    auto stage = [&](uint32_t it, uint32_t& ph) {
+        constexpr uint32_t kHalf = kStages / 2;
+        ph = (it >> 1) / kHalf & 1;
+        return (it & 1) * kHalf + (it >> 1) % kHalf;
     };
 
     // 384 threads x 168 registers at launch = 256 x 232 + 128 x 40
@@ -119,12 +112,12 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             for (int j = 0; j < kb; ++j, ++it) {
                 const float s1 = xa * xb;
                 const f32x2 s = pack2(s1, s1);
-                const uint32_t d = (it & 1) * 2 + half, dph = (it >> 1) & 1;
+                const uint32_t d = it % kBufs * kGroups + (kGroups == 2 ? half : 0), dph = it / kBufs & 1;
                 if (ok) ok = mbar_wait_spin(&tfull[d], dph);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t at = tmem_addr(tmem, 32 * quarter, d * kCols);
+                const uint32_t at = tmem_addr(tmem, 32 * quarter, it % kBufs * BN + half * kCols);
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64) {              // two loads in flight
                     float f[32], e[32];
@@ -159,37 +152,60 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 // next tile's products need not wait for them.  Boxes of 64 columns, 128-byte swizzle.
                 const uint32_t own = base + kStages * S::kStage + half * (S::kOut / 2);
                 const int r = quarter * 32 + lane;
-                if (threadIdx.x % 128 == 0) bulk_wait_read_all();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
-                for (int c = 0; c < kCols; c += 8) {
-                    const uint32_t at = own + c / 64 * 16384 + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16;
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(bf16x2(acc[c / 2])),
-                                 "r"(bf16x2(acc[c / 2 + 1])), "r"(bf16x2(acc[c / 2 + 2])), "r"(bf16x2(acc[c / 2 + 3]))
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                if (threadIdx.x % 128 == 0) {
-#pragma unroll
-                    for (int c = 0; c < kCols; c += 64)
-                        if (col + c < g.n) tma_store_2d(&map_c, own + c / 64 * 16384, col + c, tm * 256 + rank * 128);
-                    bulk_commit();
-                }
-            } else if (row < g.m && col < g.n) {
-                T* p = (T*)g.c + row * g.ldc + col;
-                const int n = min(kCols, g.n - col);
-                if (n == kCols && ((uintptr_t)p & 31) == 0) {
-                    constexpr int per = 32 / sizeof(T);
-#pragma unroll
-                    for (int c = 0; c < kCols; c += per) store_row32b(p + c, acc + c / 2);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) {
-                        float lo, hi;
-                        unpack2(acc[i / 2], lo, hi);
-                        if (i < n) p[i] = from_f32<T>(i & 1 ? hi : lo);
+                for (int c0 = 0; c0 < kCols; c0 += 64) {
+                    if (c0 == 0) {
+                        if (threadIdx.x % 128 == 0) bulk_wait_read_all();
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
                     }
+#pragma unroll
+                    for (int c = 0; c < 64; c += 8) {
+                        const f32x2* v = acc + (c0 + c) / 2;
+                        const uint32_t at = own + c0 / 64 * 16384 + r * 128 + ((c / 8) ^ (r & 7)) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(bf16x2(v[0])),
+                                     "r"(bf16x2(v[1])), "r"(bf16x2(v[2])), "r"(bf16x2(v[3])) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                    if (threadIdx.x % 128 == 0 && col + c0 < g.n) {
+                        tma_store_2d(&map_c, own + c0 / 64 * 16384, col + c0, tm * 256 + rank * 128);
+                        bulk_commit();
+                    }
+                }
+            } else {
+                // Transposed in the warp's 4 KB of shared memory, so that a store goes along a row: 32 words
+                // (fp32, or pairs of bf16) of 32 rows at a time.
+                uint32_t* own = (uint32_t*)(raw + (base - smem_u32(raw)) + kStages * S::kStage) + warp * 1024;
+                constexpr int kPer = sizeof(T) == 2 ? 2 : 1;       // values of a word
+#pragma unroll
+                for (int w0 = 0; w0 < kCols / kPer; w0 += 32) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        uint32_t word;
+                        if constexpr (kPer == 2) {
+                            word = bf16x2(acc[w0 + k]);
+                        } else {
+                            float lo, hi;
+                            unpack2(acc[(w0 + k) / 2], lo, hi);
+                            word = __float_as_uint(k & 1 ? hi : lo);
+                        }
+                        own[lane * 32 + (k ^ lane)] = word;
+                    }
+                    __syncwarp();
+                    const int n = col + (w0 + lane) * kPer;
+                    for (int r = 0; r < 32 && row - lane + r < g.m; ++r) {
+                        const uint32_t word = own[r * 32 + (lane ^ r)];
+                        T* to = (T*)g.c + (row - lane + r) * g.ldc + n;
+                        if constexpr (kPer == 1) {
+                            if (n < g.n) *(uint32_t*)to = word;
+                        } else if (n + 1 < g.n && ((uintptr_t)to & 3) == 0) {
+                            *(uint32_t*)to = word;
+                        } else {
+                            if (n < g.n) *(uint16_t*)to = (uint16_t)word;
+                            if (n + 1 < g.n) *((uint16_t*)to + 1) = (uint16_t)(word >> 16);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -204,42 +220,46 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     int tm, tn;
                     place(t, tm, tn);
                     for (int j = 0; j < kb; ++j, ++it) {
-                        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                        uint32_t ph;
+                        const uint32_t s = stage(it, ph);
                         if (it >= kStages && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
                         const uint32_t at = base + s * S::kStage, bar = map_cta(smem_u32(&full[s]), 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
                         tma_load_2d_pair(at, &map_a, j * 128, tm * 256 + (int)rank * 128, bar);
-                        // each half of the tile's columns takes half of its rows of b from either CTA
-                        tma_load_2d_pair(at + S::kA, &map_b, j * 128, tn * BN + (int)rank * (BN / 4), bar);
-                        tma_load_2d_pair(at + S::kA + S::kB / 2, &map_b, j * 128, tn * BN + BN / 2 + (int)rank * (BN / 4), bar);
+#pragma unroll
+                        for (int h = 0; h < kGroups; ++h)          // a group's 128 rows of b: 64 from either CTA
+                            tma_load_2d_pair(at + S::kA + h * 8192, &map_b, j * 128, tn * BN + h * 128 + (int)rank * 64, bar);
                     }
                 }
                 if (!ok) drain_copies();
             }
         } else if (warp <= kMmEpiWarps + 2) {
-            // Matrix instructions, by the leader: a warp for each half of the columns.  One warp needs about
-            // 500 cycles for the waits, 4 instructions and a commit, as long as the instructions of a whole
-            // block take.
+            // Matrix instructions, by the leader: a warp for even blocks and one for odd ones.  One alone needs about
+            // 500 cycles for the waits, 4 instructions and the commits, as long as the instructions take.
             if (rank == 0) {
-                const int h = warp - kMmEpiWarps - 1;
-                const uint32_t idesc = idesc_e4m3(256, BN / 2);
-                uint32_t it = 0;
+                const uint32_t own = warp - kMmEpiWarps - 1;
+                const uint32_t idesc = idesc_e4m3(256, 128);
+                const int mine = (tiles - pair + pairs - 1) / pairs;
+                const uint32_t all = (uint32_t)mine * kb;
                 bool ok = true;
-                for (int t = pair; t < tiles && ok; t += pairs) {
-                    for (int j = 0; j < kb && ok; ++j, ++it) {
-                        const uint32_t s = it % kStages, ph = (it / kStages) & 1, dph = (it >> 1) & 1, d = (it & 1) * 2 + h;
-                        ok = mbar_wait_warp(&full[s], ph);
-                        if (ok && it >= 2) ok = mbar_wait_warp(&tempty[d], dph ^ 1);
+                for (uint32_t it = own; it < all && ok; it += 2) {
+                    uint32_t ph;
+                    const uint32_t s = stage(it, ph), dph = it / kBufs & 1;
+                    const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
+                    const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA);
+                    ok = mbar_wait_warp(&full[s], ph);
+#pragma unroll
+                    for (int h = 0; h < kGroups; ++h) {
+                        const uint32_t d = it % kBufs * kGroups + h;
+                        if (ok && it >= kBufs) ok = mbar_wait_warp(&tempty[d], dph ^ 1);
                         if (!ok) break;
-                        const uint64_t da = sdesc_k_sw128(base + s * S::kStage);
-                        const uint64_t db = sdesc_k_sw128(base + s * S::kStage + S::kA + h * (S::kB / 2));
                         tc_fence_after_sync();
                         if (elect_one()) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                mma_f8_ss_pair(tmem + d * (BN / 2), da + 2 * q, db + 2 * q, idesc, q > 0);
+                                mma_f8_ss_pair(tmem + d * 128, da + 2 * q, db + h * (8192 / 16) + 2 * q, idesc, q > 0);
                             mma_commit_pair(&tfull[d], 3);
-                            mma_commit_pair(&empty[s], 3);
+                            if (h == kGroups - 1) mma_commit_pair(&empty[s], 3);
                         }
                         __syncwarp();
                     }
@@ -250,7 +270,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();                                                // the peer may still read or signal this CTA
-    if (warp == 0) tmem_dealloc_pair(tmem, 2 * BN);
+    if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
 // ------------------------------------------------------------------- thin
@@ -260,7 +280,7 @@ constexpr int kThinThreads = 32 * 6;
 template <int BT>
 struct ThinShape {
     static constexpr uint32_t kA = 128 * 128, kB = BT * 128, kStage = kA + kB;
-    static constexpr int kStages = (int)(160 * 1024 / kStage) > 9 ? 9 : (int)(160 * 1024 / kStage);
+    static constexpr int kStages = (int)(100 * 1024 / kStage);     // two CTAs on an SM
     static constexpr uint32_t kTmem = 2 * BT < 32 ? 32 : 2 * BT;
     static constexpr uint32_t kScales = kStages * kStage;          // then factors [k blocks of the CTA][BT]
     // sums [BT][128] of the cluster's CTAs: over the stages, which are read by then
@@ -268,7 +288,7 @@ struct ThinShape {
 };
 
 template <typename T, int BT>
-__global__ void __launch_bounds__(kThinThreads, 1)
+__global__ void __launch_bounds__(kThinThreads, 2)
 kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const MatmulArgs g, const int blocks_per) {
     using S = ThinShape<BT>;
@@ -446,7 +466,7 @@ static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
         resident = n > 0 ? n : 1;
     }
     CUtensorMap ma, mb;
-    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, BN / 4))
+    if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, 64))
         return cudaErrorInvalidValue;
     // c by TMA where its rows start on 16-byte boundaries
     CUtensorMap mc = ma;
@@ -463,47 +483,65 @@ static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+static void thin_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, dim3 grid, int cluster, uint32_t smem,
+                        cudaStream_t stream) {
+    cfg.gridDim = grid; cfg.blockDim = dim3(kThinThreads); cfg.dynamicSmemBytes = smem; cfg.stream = stream;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    cfg.attrs = at; cfg.numAttrs = 1;
+}
+
 template <typename T, int BT>
 static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
     using S = ThinShape<BT>;
     auto kern = kda_matmul_fp8_thin<T, BT>;
-    const int kb = (a.k + 127) / 128, tn = (a.n + 127) / 128, tm = (int)((a.m + BT - 1) / BT);
-    int splits = 152 / (tn * tm);
-    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
-    splits = splits > kb ? kb : splits;
+    const int kb = (a.k + 127) / 128, tn = (a.n + 127) / 128;
+    const int64_t tm = (a.m + BT - 1) / BT, tiles = tn * tm;
+    // clusters of 1 .. 8 CTAs that run at once, two CTAs on an SM: properties of the device and the kernel
+    static int active[9] = {};
+    if (!active[1]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        for (int c = 8; c >= 1 && e == cudaSuccess; --c) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at[1];
+            thin_config(cfg, at, dim3(c, 1024), c, S::smem(24), 0);
+            e = cudaOccupancyMaxActiveClusters(&active[c], kern, &cfg);
+        }
+        if (e != cudaSuccess) { active[1] = 0; return e; }
+    }
+    // as many splits as run at once, of four blocks of k at least
+    int splits = 1;
+    for (int c = 2; c <= 8; ++c)
+        if (tiles <= active[c] && kb >= 4 * c) splits = c;
     const int per = (kb + splits - 1) / splits;
     splits = (kb + per - 1) / per;
     const uint32_t smem = S::smem(per);
-    static bool ready = false;
-    if (!ready) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e != cudaSuccess) return e;
-        ready = true;
-    }
     if (smem > 227 * 1024) return cudaErrorInvalidValue;
     CUtensorMap ma, mb;
     if (!make_operand(&ma, a.a, a.m, a.k, a.lda, BT) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, 128))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits, tn, tm); cfg.blockDim = dim3(kThinThreads); cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = splits; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
-    cfg.attrs = at; cfg.numAttrs = 1;
+    thin_config(cfg, at, dim3(splits, tn, (unsigned)tm), splits, smem, stream);
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, a, per);
 }
 
 template <typename T>
 static cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t stream) {
-    const int blocks = (a.k + 127) / 128;
-    // the factors of a CTA's k blocks lie in shared memory
-    const bool thin_fits = blocks <= 96;
-    if (a.m <= 16 && thin_fits) return launch_thin<T, 16>(a, stream);
-    if (a.m <= 32 && thin_fits) return launch_thin<T, 32>(a, stream);
-    if (a.m <= 64 && thin_fits) return launch_thin<T, 64>(a, stream);
-    if (a.m <= 128 && thin_fits) return launch_thin<T, 128>(a, stream);
-    if ((a.m + 255) / 256 * ((a.n + 255) / 256) < 64) return launch_wide<T, 128>(a, stream);
+    // Measured on a GB300 (us, thin with 64 rows of a / wide with 128 columns / with 256):
+    //   1 x 4096 x 4096    7 / 13 / 17     64 x 8192 x 8192   19 / 21 / 30    128 x 1024 x 4096   7 / 12 / 17
+    //   512 x 1024 x 1024  6 / 6.4 / 8     128 x 6144 x 4096  16 / 13 / 18    1024 x 1024 x 4096  17 / 12 / 18
+    //   1024 x 4096 x 4096  42 / 21 / 19   2048 x 8192 x 4096  139 / 64 / 62  16384 x 8192 x 4096  1040 / 455 / 395
+    // thin while its tiles are few (its splits then use SMs that tiles of the others would leave idle); of the wide
+    // ones the narrower while all its tiles run at once.
+    const int64_t tn = (a.n + 127) / 128;
+    const bool thin_fits = a.k <= 96 * 128;                // the factors of a CTA's blocks of k lie in shared memory
+    if (thin_fits && (a.m <= 64 || (a.m + 63) / 64 * tn <= 64)) {
+        if (a.m <= 16) return launch_thin<T, 16>(a, stream);
+        if (a.m <= 32) return launch_thin<T, 32>(a, stream);
+        return launch_thin<T, 64>(a, stream);
+    }
+    if ((a.m + 255) / 256 * tn <= 76) return launch_wide<T, 128>(a, stream);
     return launch_wide<T, 256>(a, stream);
 }
 

@@ -146,6 +146,14 @@ def test_matmul(kda, simt, m, n, k):
     check_matmul(kda, a, sa, b, sb, flags=flags)
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 200, 96 * 128 + 16), (90, 4000, 1008), (256, 2000, 2064), (700, 10000, 272), (1500, 1026, 400),
+                                   (2000, 3001, 160)])
+def test_matmul_shapes_on_both_sides_of_the_choices(kda, m, n, k):
+    a, sa, b, sb = operands(m, n, k)
+    check_matmul(kda, a, sa, b, sb, out_dtype=F32)
+    check_matmul(kda, a, sa, b, sb)
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 5, 1), (20, 130, 77), (130, 200, 333)])
 def test_matmul_rows_off_every_boundary(kda, m, n, k):
     a, sa, b, sb = operands(m, n, k)
