@@ -39,27 +39,41 @@ __device__ __forceinline__ int norm_element(int step, int tpr, int t) {
     return kAligned ? (step * tpr + t) * kNormVec : (step * tpr + (t & ~31)) * kNormVec + (t & 31);
 }
 
+// A step's elements as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void vec(const __nv_bfloat16* p) {
+        const uint4 u = *(const uint4*)p;
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    }
+    __device__ __forceinline__ void set(int i, const __nv_bfloat16* p) {
+        const uint32_t b = p ? *(const uint16_t*)p : 0u;
+        w[i / 2] = i % 2 ? w[i / 2] | (b << 16) : b;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+template <> struct Raw8<float> {
+    float f[8];
+    __device__ __forceinline__ void vec(const float* p) {
+        const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(int i, const float* p) { f[i] = p ? *p : 0.f; }
+    __device__ __forceinline__ float get(int i) const { return f[i]; }
+};
+
 template <typename T, bool kAligned>
-__device__ __forceinline__ Vec8 load8(const T* row, int e, int dim) {
-    Vec8 o;
+__device__ __forceinline__ Raw8<T> load8(const T* row, int e, int dim) {
+    Raw8<T> o;
     if (kAligned && e + kNormVec <= dim) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 u = *(const uint4*)(row + e);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o.v[2 * i] = __uint_as_float(w[i] << 16);
-                o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-            const float4 a = ((const float4*)(row + e))[0], b = ((const float4*)(row + e))[1];
-            o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
-            o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
-        }
+        o.vec(row + e);
     } else {
         constexpr int d = kAligned ? 1 : 32;
 #pragma unroll
-        for (int i = 0; i < kNormVec; ++i) o.v[i] = e + i * d < dim ? to_f32(row[e + i * d]) : 0.f;
+        for (int i = 0; i < kNormVec; ++i) o.set(i, e + i * d < dim ? row + e + i * d : nullptr);
     }
     return o;
 }
@@ -90,11 +104,15 @@ __device__ __forceinline__ void store8(T* row, int e, int dim, const Vec8& x) {
 // h of one step: x + r, written out where wanted.
 template <typename T, bool kAligned>
 __device__ __forceinline__ Vec8 norm_sum8(const NormArgs& a, int64_t row, int e, bool write) {
-    Vec8 h = load8<T, kAligned>((const T*)a.x + row * a.x_stride, e, a.dim);
+    const Raw8<T> x = load8<T, kAligned>((const T*)a.x + row * a.x_stride, e, a.dim);
+    Vec8 h;
     if (a.r) {
-        const Vec8 r = load8<T, kAligned>((const T*)a.r + row * a.r_stride, e, a.dim);
+        const Raw8<T> r = load8<T, kAligned>((const T*)a.r + row * a.r_stride, e, a.dim);
 #pragma unroll
-        for (int i = 0; i < kNormVec; ++i) h.v[i] += r.v[i];
+        for (int i = 0; i < kNormVec; ++i) h.v[i] = x.get(i) + r.get(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNormVec; ++i) h.v[i] = x.get(i);
     }
     if (write && a.h) store8<T, kAligned>((T*)a.h + row * a.dim, e, a.dim, h);
     return h;
@@ -103,12 +121,12 @@ __device__ __forceinline__ Vec8 norm_sum8(const NormArgs& a, int64_t row, int e,
 // The outputs of one step.  All lanes of the warp call it (the block maximum
 // crosses lanes); elements behind the row are left out.
 template <typename T, bool kAligned>
-__device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int e, const Vec8& h, float rstd) {
+__device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int e, const Vec8& h, const Raw8<T>& w,
+                                          float rstd) {
     Vec8 y;
     if (a.w) {
-        const Vec8 w = load8<T, kAligned>((const T*)a.w, e, a.dim);
 #pragma unroll
-        for (int i = 0; i < kNormVec; ++i) y.v[i] = h.v[i] * rstd * w.v[i];
+        for (int i = 0; i < kNormVec; ++i) y.v[i] = h.v[i] * rstd * w.get(i);
     } else {
 #pragma unroll
         for (int i = 0; i < kNormVec; ++i) y.v[i] = h.v[i] * rstd;
@@ -132,7 +150,7 @@ __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int e,
         if (writes && first < a.dim) a.s[row * blocks + first / kNormBlock] = amax / 448.f;
         inv[b] = 448.f / amax;
     }
-    uint32_t w[2];
+    uint32_t bytes[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float c = inv[kAligned ? 0 : i];
@@ -140,25 +158,30 @@ __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int e,
                                                      __NV_SATFINITE, __NV_E4M3);
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i + 2] * c, y.v[4 * i + 3] * c),
                                                      __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
+        bytes[i] = lo | (hi << 16);
     }
     uint8_t* q = a.q + row * a.dim + e;
     if (kAligned && e + kNormVec <= a.dim) {
-        *(uint2*)q = make_uint2(w[0], w[1]);
+        *(uint2*)q = make_uint2(bytes[0], bytes[1]);
     } else {
         constexpr int d = kAligned ? 1 : 32;
 #pragma unroll
         for (int i = 0; i < kNormVec; ++i)
-            if (e + i * d < a.dim) q[i * d] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+            if (e + i * d < a.dim) q[i * d] = (uint8_t)(bytes[i >> 2] >> (8 * (i & 3)));
     }
 }
 
+constexpr int norm_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
+
 // TPR threads share a row; each holds STEPS vectors of it (STEPS = 0: the row
-// is too long for registers and is read a second time, out of L2).
+// is too long for registers and is read a second time, out of L2).  Few vectors
+// a thread and 1536 threads an SM keep the most bytes on their way: 65536 x 4096
+// bf16 to all four outputs 361 us (99% of the measured copy rate), 380 without
+// the bound on registers, 406 with the weights read behind the sum.
 template <typename T, bool kAligned, int TPR, int STEPS>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(norm_threads(TPR), sizeof(T) == 2 && (STEPS == 1 || STEPS == 2) ? 1536 / norm_threads(TPR) : 1)
 kda_rms_norm_kernel(NormArgs a) {
-    constexpr int kThreads = TPR < 128 ? 128 : TPR;
+    constexpr int kThreads = norm_threads(TPR);
     constexpr int kRows = kThreads / TPR;
     constexpr int kWarpsPerRow = TPR / 32;
     const int t = threadIdx.x % TPR;
@@ -167,11 +190,15 @@ kda_rms_norm_kernel(NormArgs a) {
     const int64_t row = real ? row_of : a.rows - 1;
 
     Vec8 h[STEPS > 0 ? STEPS : 1];
+    Raw8<T> w[STEPS > 0 ? STEPS : 1];                    // on its way while the row is summed
     float ss = 0.f;
     if constexpr (STEPS > 0) {
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
+        for (int k = 0; k < STEPS; ++k)
             h[k] = norm_sum8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), real);
+        if (a.w) {
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) w[k] = load8<T, kAligned>((const T*)a.w, norm_element<kAligned>(k, TPR, t), a.dim);
         }
 #pragma unroll
         for (int k = 0; k < STEPS; ++k)
@@ -199,12 +226,13 @@ kda_rms_norm_kernel(NormArgs a) {
     const float rstd = 1.f / sqrtf(ss / (float)a.dim + a.eps);
     if constexpr (STEPS > 0) {
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k) norm_out8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), h[k], rstd);
+        for (int k = 0; k < STEPS; ++k) norm_out8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), h[k], w[k], rstd);
     } else {
         // residual_out may be x or residual: each element is read (again) before it is written, by its thread
         for (int k = 0; k * TPR * kNormVec < a.dim; ++k) {
             const int e = norm_element<kAligned>(k, TPR, t);
-            norm_out8<T, kAligned>(a, row, e, norm_sum8<T, kAligned>(a, row, e, true), rstd);
+            if (a.w) w[0] = load8<T, kAligned>((const T*)a.w, e, a.dim);
+            norm_out8<T, kAligned>(a, row, e, norm_sum8<T, kAligned>(a, row, e, true), w[0], rstd);
         }
     }
 }
@@ -214,17 +242,17 @@ static cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
     const int steps = (a.dim + kNormVec - 1) / kNormVec;    // vectors of a row
 #define KDA_NORM(tpr, per)                                                                            \
     do {                                                                                              \
-        constexpr int th = tpr < 128 ? 128 : tpr;                                                     \
+        constexpr int th = norm_threads(tpr);                                                     \
         const int64_t blocks = (a.rows + th / tpr - 1) / (th / tpr);                                  \
         kda_rms_norm_kernel<T, kAligned, tpr, per><<<(unsigned)blocks, th, 0, stream>>>(a);           \
         return cudaGetLastError();                                                                    \
     } while (0)
     if (steps <= 32) KDA_NORM(32, 1);
-    if (steps <= 64) KDA_NORM(32, 2);
-    if (steps <= 128) KDA_NORM(64, 2);
-    if (steps <= 256) KDA_NORM(128, 2);
+    if (steps <= 64) KDA_NORM(64, 1);
+    if (steps <= 128) KDA_NORM(128, 1);
+    if (steps <= 256) KDA_NORM(256, 1);
     if (steps <= 512) KDA_NORM(256, 2);
-    if (steps <= 1024) KDA_NORM(256, 4);
+    if (steps <= 1024) KDA_NORM(512, 2);
     if (steps <= 2048) KDA_NORM(512, 4);
     KDA_NORM(512, 0);
 #undef KDA_NORM
