@@ -491,23 +491,25 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
             }
             asm volatile("bar.sync 2, 128;" ::: "memory");
+            constexpr int W = R < 32 ? R : 32;
+#pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int ch = p * 128 + threadIdx.x;
 #pragma unroll
-                for (int h = 0; h < R; h += 16) {
-                    float o[16];
-                    tmem_ld16(lanes + (2 + p) * R + h, o);
+                for (int h = 0; h < R; h += W) {
+                    float o[W];
+                    if constexpr (W == 16) tmem_ld16(lanes + (2 + p) * R + h, o);
+                    else tmem_ld32(lanes + (2 + p) * R + h, o);
                     tmem_wait_ld();
                     tmem_ready(o);
                     if (whole) {
                         __nv_bfloat16* to = a.out + ((size_t)w.n * a.rows + row0 + h) * kLdRank + ch;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
+                        for (int c = 0; c < W; ++c)
                             if (h + c < live) to[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[h + c]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            if (h + c < live) dst[(h + c) * kLdPart + ch] = o[c];
+                        for (int c = 0; c < W; ++c) dst[(h + c) * kLdPart + ch] = o[c];
                     }
                 }
             }
@@ -527,17 +529,15 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
 // Joins the pieces of sequences that several CTAs shared, gives sequences
 // without tiles their zeros, and collects the CTAs' status.  A block a row, its
-// warps a share of the pieces each: two of them for many rows (so small that the
-// blocks wait beside the CTAs above instead of after them), eight for few, and
-// then a block for each 128 of its channels.
+// warps a share of the pieces each: two of them for many rows, sixteen for few,
+// and then a block for each 128 of its channels.
 template <int R, int Q>                                // Q: 128-channel blocks of a block, 4 or 1
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 kda_latent_decode_join(const LdArgs a, const int groups) {
-    extern __shared__ __align__(16) float sh[];        // [warps][128 Q] O, [warps] ref, [warps] sum
+    extern __shared__ __align__(16) float sh[];        // [warps][128 Q] O
     const int n = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warps = blockDim.x >> 5;
     const int ch0 = blockIdx.z * 128 * Q;
-    float *sh_top = sh + warps * 128 * Q, *sh_sum = sh_top + warps;
     const int tiles = ld_tiles(a, n);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0 && row == 0 && blockIdx.z == 0) {
@@ -553,8 +553,13 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     int cf = 0, cl = -1;
     if (tiles > 0) {
         const int64_t total = a.before[a.N], before = a.before[n], parts = min64(a.G, total);
-        cf = (int)(((before + 1) * parts - 1) / total);
-        cl = (int)(((before + tiles) * parts - 1) / total);
+        if (total < (1 << 20)) {
+            cf = (int)(((uint32_t)(before + 1) * (uint32_t)parts - 1) / (uint32_t)total);
+            cl = (int)(((uint32_t)(before + tiles) * (uint32_t)parts - 1) / (uint32_t)total);
+        } else {
+            cf = (int)(((before + 1) * parts - 1) / total);
+            cl = (int)(((before + tiles) * parts - 1) / total);
+        }
         if (cf == cl) return;                          // finished by its CTA
     }
     const int group = row / R, c = row % R;
@@ -564,32 +569,40 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     float o[4 * Q];
 #pragma unroll
     for (int i = 0; i < 4 * Q; ++i) o[i] = 0.f;
+    // Every warp weighs all pieces (152 at most), a lane each, and adds up its share of them.
+    float2 ml[5];
     float top = kLdUnset, sum = 0.f;
-    for (int i = cf + threadIdx.x; i <= cl; i += blockDim.x) top = fmaxf(top, piece(i)[kLdRank]);
+#pragma unroll
+    for (int g = 0; g < 5; ++g) {
+        const int i = cf + 32 * g + lane;
+        ml[g] = i <= cl ? *(const float2*)(piece(i) + kLdRank) : make_float2(kLdUnset, 0.f);
+    }
+#pragma unroll
+    for (int g = 0; g < 5; ++g) top = fmaxf(top, ml[g].x);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    if (lane == 0) sh_top[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < warps; ++w) top = fmaxf(top, sh_top[w]);
-#pragma unroll 8
-    for (int i = cf + warp; i <= cl; i += warps) {
-        const float* p = piece(i);
-        const float2 ml = *(const float2*)(p + kLdRank);
-        const float wgt = ex2(ml.x - top);
-        sum += wgt * ml.y;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const float4 v = *(const float4*)(p + ch0 + q * 128 + lane * 4);
-            o[4 * q] += wgt * v.x; o[4 * q + 1] += wgt * v.y; o[4 * q + 2] += wgt * v.z; o[4 * q + 3] += wgt * v.w;
+    for (int g = 0; g < 5; ++g) {
+        const float wgt = ex2(ml[g].x - top);
+        sum += wgt * ml[g].y;
+        const int here = min(32, cl - cf - 32 * g + 1);
+#pragma unroll 4
+        for (int k = warp; k < here; k += warps) {
+            const float x = __shfl_sync(0xffffffffu, wgt, k);
+            const float* p = piece(cf + 32 * g + k);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float4 v = *(const float4*)(p + ch0 + q * 128 + lane * 4);
+                o[4 * q] += x * v.x; o[4 * q + 1] += x * v.y; o[4 * q + 2] += x * v.z; o[4 * q + 3] += x * v.w;
+            }
         }
     }
-    if (lane == 0) sh_sum[warp] = sum;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         *(float4*)(sh + warp * 128 * Q + q * 128 + lane * 4) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
     __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < warps; ++w) sum += sh_sum[w];
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     for (int e = threadIdx.x * 4; e < 128 * Q; e += blockDim.x * 4) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -673,13 +686,14 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     const bool many = (int64_t)d.N * a.rows >= 512;
-    const int warps = many ? 2 : 8, per = many ? 4 : 1;
+    const int warps = many ? 2 : 16, per = many ? 4 : 1;
     cfg.gridDim = dim3(d.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
-    cfg.dynamicSmemBytes = warps * (128 * per + 2) * 4;
+    cfg.dynamicSmemBytes = warps * 128 * per * 4;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at; cfg.numAttrs = 1;
+    // started early, few blocks gain 0.5 us; many would take from the kernel before (2 us more)
+    cfg.attrs = at; cfg.numAttrs = many ? 0 : 1;
     return many ? cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 4>, a, p.groups)
                 : cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 1>, a, p.groups);
 }
