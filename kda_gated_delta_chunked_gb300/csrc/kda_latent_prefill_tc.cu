@@ -17,8 +17,16 @@
 // 16 KB pieces, in the order of their use; with the queries' 96 KB that fills
 // shared memory.
 //
-// Bound by the tensor pipe at best: a key tile costs 2 x (12 + 8) instructions
-// of 64 cycles, the softmax of a tile about 1000 cycles of its warpgroup.
+// Few rows (a chunk of a long prompt, few heads) leave SMs idle and the longest
+// row alone decides: then the 2 or 4 CTAs of a cluster share the rows' key tiles,
+// and their parts of O are joined, in rank order, in distributed shared memory
+// (256 rows of 8192 keys, 16 heads: 123 -> 48 us with 4).
+//
+// A key tile of both row tiles is 2 x (12 + 8) instructions of 64 cycles, 2560 of
+// the tensor pipe; it takes 3400, the turn of product, commit, softmax (about
+// 1000 cycles of its warpgroup) and wait.  8192 tokens, 32 heads, causal: 445 us,
+// 1.54 PFLOP/s.  Short sequences pay about 9 us for a CTA's start, queries and
+// end, one CTA to an SM.
 #include <math.h>
 
 #include "kda_common.cuh"
@@ -34,13 +42,15 @@ constexpr int kLpKeys = 128;
 constexpr uint32_t kLpPiece = 16384;
 constexpr int kLpSlots = 8;
 constexpr uint32_t kLpOffRing = 6 * kLpPiece, kLpOffSmall = kLpOffRing + kLpSlots * kLpPiece;
-constexpr uint32_t kLpSmem = kLpOffSmall + 1024 + 256;
+constexpr uint32_t kLpRow = 512;              // bytes of an fp32 row of O, where a cluster joins
+constexpr int kLpSplits = 4;                  // CTAs that share the keys of a tile of rows at most
+constexpr uint32_t kLpOffLse = kLpOffSmall + 256, kLpSmem = kLpOffLse + kLpRows * 4 + 1024;
 constexpr int kLpThreads = 384;
 constexpr int kLpHeads = 8;                   // heads of a group
 constexpr float kLpUnset = -1e30f, kLpSlack = 8.f;
 
 struct LpArgs {
-    int N, H, causal, blocks;                  // blocks: tiles of rows of a head at most
+    int N, H, causal, blocks, splits;          // blocks: tiles of rows of a head at most; splits: CTAs that share them
     float scale;
     int64_t tq, tk;
     const int32_t *cu_q, *cu_k;
@@ -49,6 +59,7 @@ struct LpArgs {
     int32_t* status;
 };
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kLpThreads, 1)
 kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
@@ -59,14 +70,16 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     uint64_t* q_full = (uint64_t*)(mem + kLpOffSmall);
     uint64_t *kv_full = q_full + 1, *kv_empty = kv_full + 4;   // [2 steps][K, V]
     uint64_t *s_full = kv_empty + 4, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint32_t* tmem_at = (uint32_t*)(o_full + 2);
+    uint64_t* rows_full = o_full + 2;
+    uint32_t* tmem_at = (uint32_t*)(rows_full + 1);
     int* where = (int*)(tmem_at + 1);          // sequence, its tile of rows (-1: none)
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     // Which rows: in groups of heads (whose keys and values then stay in L2), a sequence's last tile, which sees most
     // keys, first, so that what runs last is short (8192 tokens, 32 heads: 488 us a head at a time, 445 in groups).
-    const int per = a.blocks * kLpHeads, grp = blockIdx.x / per;
-    const int heads = min(kLpHeads, a.H - grp * kLpHeads), in_grp = blockIdx.x - grp * per;
+    const int splits = SHARED ? a.splits : 1, rank = SHARED ? (int)blockIdx.x % splits : 0;   // of the rows' keys
+    const int per = a.blocks * kLpHeads, index = (int)blockIdx.x / splits, grp = index / per;
+    const int heads = min(kLpHeads, a.H - grp * kLpHeads), in_grp = index - grp * per;
     const int head = grp * kLpHeads + in_grp % heads, block = in_grp / heads;
     if (threadIdx.x == 32) { prefetch_map(&map_q); prefetch_map(&map_k); prefetch_map(&map_r); prefetch_map(&map_v); }
     if (warp == 0) {
@@ -102,6 +115,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     }
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(rows_full, 1);
         for (int i = 0; i < 4; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
         fence_mbar_init();
@@ -131,7 +145,11 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         seen = seen < 0 ? 0 : seen > lk ? lk : seen;
         tiles[i] = uniform((int)((seen + kLpKeys - 1) / kLpKeys));
     }
-    const int steps = max(tiles[0], tiles[1]);
+    // this CTA's share of the key tiles
+    const int steps_all = max(tiles[0], tiles[1]);
+    const int start = steps_all * rank / splits, steps = steps_all * (rank + 1) / splits - start;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tiles[i] = min(max(tiles[i] - start, 0), steps);
 
     if (warp < 8) {                                                    // ---------------- softmax
         regs_inc<232>();
@@ -151,7 +169,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, *(float(*)[32])(x + c));
             tmem_wait_ld();
             tmem_ready(x);
-            const int64_t first = (int64_t)j * kLpKeys;
+            const int64_t first = (int64_t)(start + j) * kLpKeys;
             if (first + kLpKeys - 1 > (seen < lk - 1 ? seen : lk - 1)) {
                 const int64_t end = seen < lk - 1 ? seen : lk - 1;
                 const int keep = end < first ? 0 : (int)(end - first + 1);
@@ -205,7 +223,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             // Weight 0 times what lies behind the last key: make that 0.  Done by the first tile that uses it.
-            if (j + 1 == steps && lk - first < kLpKeys && (i == 0 || j >= tiles[0])) {
+            if (start + j + 1 == steps_all && lk - first < kLpKeys && (i == 0 || j >= tiles[0])) {
                 const int r = quarter * 32 + lane;
                 const uint32_t u = 5 * j + 3 + r / 64;
                 if (r >= lk - first) {
@@ -229,28 +247,52 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         }
         if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const bool live = tile >= 0 && row < lq;
-        __nv_bfloat16* dst = a.out + ((q0 + (live ? row : 0)) * a.H + head) * 128;
-        for (int c = 0; c < 128; c += 32) {
-            float o[32];
-            if (mine > 0) {
-                tmem_ld32(to + c, o);
-                tmem_wait_ld();
-                tmem_ready(o);
+        if (SHARED) {
+            // This CTA's part to shared memory, once neither tile's products read there: [row][128] fp32 in 16-byte
+            // pieces turned by the row, and log2 of the rows' sums.
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int r = i * 128 + quarter * 32 + lane;
+            float4* part = (float4*)(mem + r * kLpRow);
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                if (mine > 0) {
+                    tmem_ld32(to + c, o);
+                    tmem_wait_ld();
+                    tmem_ready(o);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    part[(c / 4 + q) ^ lane] = mine > 0 ? make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv,
+                                                                      o[4 * q + 3] * inv)
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (live) {
+            ((float*)(mem + kLpOffLse))[r] = l == 0.f ? -INFINITY : ref + log2f(l);
+            fence_proxy_async_smem();                                  // read by copies
+        } else {
+            const bool live = tile >= 0 && row < lq;
+            __nv_bfloat16* dst = a.out + ((q0 + (live ? row : 0)) * a.H + head) * 128;
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                if (mine > 0) {
+                    tmem_ld32(to + c, o);
+                    tmem_wait_ld();
+                    tmem_ready(o);
+                }
+                if (live) {
 #pragma unroll
-                for (int q = 0; q < 32; q += 8) {
-                    uint32_t b[4];
+                    for (int q = 0; q < 32; q += 8) {
+                        uint32_t b[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        b[e] = mine > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
-                    *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
+                        for (int e = 0; e < 4; ++e)
+                            b[e] = mine > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
+                        *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
                 }
             }
+            if (live && a.lse)
+                a.lse[(q0 + row) * a.H + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
         }
-        if (live && a.lse)
-            a.lse[(q0 + row) * a.H + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
     } else {
         regs_dec<40>();
         if (warp == 8) {                                               // ---------------- producer
@@ -261,7 +303,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 bool ok = true;
                 uint32_t u = 0;
                 for (int j = 0; j < steps && ok; ++j) {
-                    const int key = (int)k0 + j * kLpKeys;
+                    const int key = (int)k0 + (start + j) * kLpKeys;
                     for (int p = 0; p < 5; ++p, ++u) {
                         if (u >= kLpSlots) {                           // the piece this one takes the place of
                             const uint32_t o = u - kLpSlots, oj = o / 5, g = (oj & 1) * 2 + (o % 5 >= 3);
@@ -337,6 +379,62 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
         }
     }
+    if (SHARED) {
+        // Each CTA joins a share of the rows: the others copy their parts of those behind its own, 64 KB in 3300
+        // cycles with two CTAs.
+        const int share = kLpRows / splits;
+        auto rows_of = [&](int c) {
+            const int64_t left = lq - r0 - c * share;
+            return tile < 0 || left < 0 ? 0 : (int)min64(left, share);
+        };
+        const int rows = rows_of(rank);
+        if (threadIdx.x == 0 && rows) mbar_arrive_expect_tx(rows_full, (splits - 1) * rows * kLpRow);
+        __syncwarp();
+        cluster_sync();
+        if (threadIdx.x < splits && (int)threadIdx.x != rank) {
+            const int to = threadIdx.x, slot = rank < to ? rank : rank - 1, count = rows_of(to);
+            if (count)
+                copy_to_cta(map_cta(base + (kLpRows + slot * share) * kLpRow, to), base + to * share * kLpRow, count * kLpRow,
+                            map_cta(smem_u32(rows_full), to));
+        }
+        __syncwarp();
+        if (warp < 8 && rows) {
+            // the parts' weights, a lane a row of the warp; then the rows
+            const int own = share / 8, first = rank * share + warp * own, count = min(own, rows - warp * own);
+            float w[kLpSplits], top = kLpUnset, sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kLpSplits; ++c)
+                w[c] = c < splits && lane < count ? ld_cluster_f32(map_cta(base + kLpOffLse + (first + lane) * 4, c)) : -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kLpSplits; ++c) top = fmaxf(top, w[c]);
+#pragma unroll
+            for (int c = 0; c < kLpSplits; ++c) sum += w[c] = ex2(w[c] - top);
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+            const int64_t row = (q0 + r0 + first) * a.H + head;
+            if (a.lse && lane < count)
+                a.lse[row + lane * a.H] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            const bool ok = mbar_wait_warp(rows_full, 0);
+            if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
+#pragma unroll 4
+            for (int r = 0; r < count; ++r) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < kLpSplits; ++c) {
+                    if (c >= splits) break;
+                    const int at = c == rank ? first + r : kLpRows + (c < rank ? c : c - 1) * share + warp * own + r;
+                    const float4 o = *(const float4*)(mem + at * kLpRow + (lane ^ ((first + r) & 31)) * 16);
+                    const float v = __shfl_sync(0xffffffffu, w[c] * inv, r);
+                    x.x += v * o.x; x.y += v * o.y; x.z += v * o.z; x.w += v * o.w;
+                }
+                uint2 b;
+                b.x = bf16x2(pack2(x.x, x.y));
+                b.y = bf16x2(pack2(x.z, x.w));
+                *(uint2*)(a.out + (row + (int64_t)r * a.H) * 128 + lane * 4) = b;
+            }
+        }
+        __syncwarp();
+        cluster_sync();                                                // the others may still read this CTA's rows
+    }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
@@ -351,10 +449,32 @@ bool latent_prefill_tc_takes(const LatentPrefillArgs& d) {
            (((uintptr_t)d.q | (uintptr_t)d.k | (uintptr_t)d.r | (uintptr_t)d.v | (uintptr_t)d.out) & 15) == 0;
 }
 
+// CTAs that share the keys of a tile of rows.  In units of a key tile's time (1.8
+// us) a CTA costs its tiles and 5, or 8 and 10 where 2 and 4 share the keys; the
+// longest CTA decides, or all of them on 152 SMs.  The lengths of the sequences
+// are on the device: taken as even, the longest half as long again.  Measured, us
+// (causal, rows x keys x heads; 1, 2 and 4 CTAs):
+//   256 x 8192 x 16   123  72  48      2048 x 2048 x 4     42   31   27
+//   256 x 8192 x 32   126  74  60      2048 x 2048 x 16    44   44   74
+//   256 x 32768 x 8   459 234 130      8192 x 8192 x 4    126   74  111
+//   512 x 512 x 16     21  21  25      8192 x 8192 x 16   234  275  408
+//   128 x 128 x 16     13  17  18    32768 x 32768 x 1    455  240  246
+static int lp_splits(const LatentPrefillArgs& d) {
+    const double n = d.cu_q ? d.N : 1, lq = d.tq / n, lk = d.tk / n;
+    const double longest = lk / kLpKeys * (n > 1 ? 1.5 : 1);
+    const double mean = (!d.causal ? lk : lk > lq ? lk - lq / 2 : lk / 2) / kLpKeys;
+    const double ctas = (d.tq / (double)kLpRows + n / 2) * d.H;
+    auto time = [&](int s, double fixed) { return fmax(longest / s + fixed, ctas * s / 152 * (mean / s + fixed)); };
+    const double one = 0.9 * time(1, 5), two = time(2, 8), four = time(kLpSplits, 10);
+    return one <= fmin(two, four) ? 1 : two <= four ? 2 : kLpSplits;
+}
+
 cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& d, cudaStream_t stream) {
     static bool ready = false;
     if (!ready) {
-        cudaError_t e = cudaFuncSetAttribute(kda_latent_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLpSmem);
+        const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaError_t e = cudaFuncSetAttribute(kda_latent_prefill_tc<false>, at, (int)kLpSmem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_latent_prefill_tc<true>, at, (int)kLpSmem);
         if (e != cudaSuccess) return e;
         ready = true;
     }
@@ -375,10 +495,17 @@ cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& d, cudaStream_t st
     a.cu_k = d.cu_k; a.out = (__nv_bfloat16*)d.out; a.lse = d.lse; a.status = d.status;
     // at most this many tiles of rows, whatever the lengths
     const int64_t blocks = d.cu_q ? d.tq / kLpRows + min64(d.N, d.tq) : (d.tq + kLpRows - 1) / kLpRows;
-    if (blocks * d.H > 0x7fffffffLL) return cudaErrorInvalidValue;
     a.blocks = (int)blocks;
-    kda_latent_prefill_tc<<<(unsigned)(blocks * d.H), kLpThreads, kLpSmem, stream>>>(mq, mk, mr, mv, a);
-    return cudaGetLastError();
+    a.splits = lp_splits(d);
+    if (blocks * d.H * a.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * d.H * a.splits)); cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = kLpSmem; cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.splits; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    cfg.attrs = at; cfg.numAttrs = a.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, a.splits > 1 ? kda_latent_prefill_tc<true> : kda_latent_prefill_tc<false>, mq, mk, mr, mv, a);
 }
 
 }  // namespace kda

@@ -244,6 +244,18 @@ def test_prefill_long_rows(kda):
     check_prefill(kda, *expanded(300, 2222, 2), rows=[0, 1, 255, 256, 299])
 
 
+@pytest.mark.parametrize("lq,lk,h", [([256], [5000], 2), ([256], [5000], 33), ([1], [2000], 2), ([300], [1999], 1), ([129, 0, 40], [2100, 500, 1900], 2),
+                                     ([1500], [1100], 1), ([7000], [6999], 1), ([200], [130], 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_rows_of_many_keys(kda, lq, lk, h, causal):
+    """Where several blocks share the keys of the same rows, some of them without a key that the rows see."""
+    x = expanded(sum(lq) + 3, sum(lk) + 9, h, seed=11)
+    q, kn, kr, v = x[0][:sum(lq)], x[1], x[2], x[3]
+    kn, kr, v = kn.clone(), kr.clone(), v.clone()
+    kn[sum(lk):], kr[sum(lk):], v[sum(lk):] = float("nan"), float("nan"), float("inf")
+    check_prefill(kda, q, kn[:sum(lk)], kr[:sum(lk)], v[:sum(lk)], lq, lk, causal, rows=[0, 63, 64, 128, 255, 256, 399, 400, 1499, 6999])
+
+
 @pytest.mark.parametrize("dk,dr,dv,dtype", [(128, 64, 128, F32), (96, 32, 64, BF16), (40, 0, 33, BF16), (192, 64, 256, F32)])
 def test_prefill_other_sizes_and_types(kda, dk, dr, dv, dtype):
     check_prefill(kda, *expanded(50, 70, 3, dk, dr, dv, dtype), simt=True)
