@@ -5,7 +5,7 @@
 //
 // A CTA owns 256 query rows of one head as two tiles of 128 and walks the key
 // tiles of 128 that they see.  While the softmax of one tile runs on its own
-// warpgroup (a thread a row), the tensor core works on the other:
+// eight warps (two threads a row), the tensor core works on the other:
 //
 //     PV_j(0)  S_{j+1}(0)  PV_j(1)  S_{j+1}(1)  PV_{j+1}(0) ...
 //
@@ -13,9 +13,13 @@
 // read from there, so only V passes through shared memory for the second
 // product.  The reference of a row moves only when a score exceeds it by 2^8
 // (then the row of O is rescaled), which is rare after the first tiles.
-// K (three pieces of 64 channels) and V (two of 64 keys) share one ring of eight
-// 16 KB pieces, in the order of their use; with the queries' 96 KB that fills
-// shared memory.
+// With the queries' 96 KB, rings of five 16 KB pieces for K (64 channels each)
+// and three for V (64 keys) fill shared memory.  A piece is freed by the last
+// product that reads it, and K and V have a producer each: what bounds a step is
+// the time from there to the next piece's arrival.
+//
+// A CTA that is done takes over the rows of a block that has not started yet, and
+// fetches their queries and keys while the last values of its own are weighed.
 //
 // Few rows (a chunk of a long prompt, few heads) leave SMs idle and the longest
 // row alone decides: then the 2 or 4 CTAs of a cluster share the rows' key tiles,
@@ -23,10 +27,10 @@
 // (256 rows of 8192 keys, 16 heads: 123 -> 48 us with 4).
 //
 // A key tile of both row tiles is 2 x (12 + 8) instructions of 64 cycles, 2560 of
-// the tensor pipe; it takes 3400, the turn of product, commit, softmax (about
-// 1000 cycles of its warpgroup) and wait.  8192 tokens, 32 heads, causal: 445 us,
-// 1.54 PFLOP/s.  Short sequences pay about 9 us for a CTA's start, queries and
-// end, one CTA to an SM.
+// the tensor pipe; it takes about 3300.  8192 tokens, 32 heads, causal: 429 us,
+// 1.60 PFLOP/s.  What it took there (us): a thread a row 461; one ring of eight
+// pieces freed a step at a time 439, then two rings so 470; blocks that run one
+// tile of rows each 445 (and 100 prompts of 60 tokens 99 instead of 54).
 #include <math.h>
 
 #include "kda_common.cuh"
@@ -40,12 +44,13 @@ using namespace sm100;
 constexpr int kLpRows = 256;                  // query rows of a CTA
 constexpr int kLpKeys = 128;
 constexpr uint32_t kLpPiece = 16384;
-constexpr int kLpSlots = 8;
-constexpr uint32_t kLpOffRing = 6 * kLpPiece, kLpOffSmall = kLpOffRing + kLpSlots * kLpPiece;
+constexpr int kLpSlotsK = 5, kLpSlotsV = 3;
+constexpr uint32_t kLpOffK = 6 * kLpPiece, kLpOffV = kLpOffK + kLpSlotsK * kLpPiece, kLpOffSmall = kLpOffV + kLpSlotsV * kLpPiece;
 constexpr uint32_t kLpRow = 512;              // bytes of an fp32 row of O, where a cluster joins
 constexpr int kLpSplits = 4;                  // CTAs that share the keys of a tile of rows at most
-constexpr uint32_t kLpOffLse = kLpOffSmall + 256, kLpSmem = kLpOffLse + kLpRows * 4 + 1024;
-constexpr int kLpThreads = 384;
+constexpr uint32_t kLpOffLse = kLpOffSmall + 384, kLpSmem = kLpOffLse + kLpRows * 4 + 1024;
+constexpr int kLpSoftmax = 16;                // warps: two for 32 rows, half of the keys each
+constexpr int kLpThreads = 32 * (kLpSoftmax + 4);
 constexpr int kLpHeads = 8;                   // heads of a group
 constexpr float kLpUnset = -1e30f, kLpSlack = 8.f;
 
@@ -59,6 +64,35 @@ struct LpArgs {
     int32_t* status;
 };
 
+// 128 + 128 query rows of a head: what every warp needs to know of them.
+struct alignas(16) LpItem {
+    int q0, lq, k0, lk;                        // their sequence: first row and rows, first key and keys
+    int r0, head;                              // first row within the sequence; -1: no more work
+    int start, tiles[2];                       // key tiles: first, and how many for each half
+};
+
+// A ring of N slots that starts anew with every rows' first piece, so that a piece's slot depends on its place among
+// these rows' alone and stays in uniform registers (counted over all rows it does not: 6% of the whole).  A bit for each
+// slot keeps the parity of its barriers.
+template <int N>
+struct LpRing {
+    uint32_t bits = 0;
+    __device__ __forceinline__ uint32_t parity(int piece) const { return (bits >> piece % N ^ piece / N) & 1; }
+    __device__ __forceinline__ void add(int pieces) {
+#pragma unroll
+        for (int s = 0; s < N; ++s) bits ^= ((pieces - s + N - 1) / N & 1) << s;
+    }
+};
+
+// Among the 256 threads of a tile's softmax.
+__device__ __forceinline__ void tile_sync(int i) { asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory"); }
+__device__ __forceinline__ bool tile_and(int i, bool v) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.and.pred p, %2, 256, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + i) : "memory");
+    return r;
+}
+
 template <bool SHARED>
 __global__ void __launch_bounds__(kLpThreads, 1)
 kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -67,314 +101,445 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t* mem = raw + (base - smem_u32(raw));
-    uint64_t* q_full = (uint64_t*)(mem + kLpOffSmall);
-    uint64_t *kv_full = q_full + 1, *kv_empty = kv_full + 4;   // [2 steps][K, V]
-    uint64_t *s_full = kv_empty + 4, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint64_t* rows_full = o_full + 2;
+    LpItem* items = (LpItem*)(mem + kLpOffSmall);              // [2]
+    uint4* answer = (uint4*)(items + 2);
+    uint64_t* q_full = (uint64_t*)(answer + 1);
+    uint64_t *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + kLpSlotsK;
+    uint64_t *v_full = k_empty + kLpSlotsK, *v_empty = v_full + kLpSlotsV;
+    uint64_t *s_full = v_empty + kLpSlotsV, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *item_full = o_full + 2, *item_empty = item_full + 2, *next = item_empty + 2, *answered = next + 1;
+    uint64_t* rows_full = answered + 1;
     uint32_t* tmem_at = (uint32_t*)(rows_full + 1);
-    int* where = (int*)(tmem_at + 1);          // sequence, its tile of rows (-1: none)
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    // Which rows: in groups of heads (whose keys and values then stay in L2), a sequence's last tile, which sees most
-    // keys, first, so that what runs last is short (8192 tokens, 32 heads: 488 us a head at a time, 445 in groups).
     const int splits = SHARED ? a.splits : 1, rank = SHARED ? (int)blockIdx.x % splits : 0;   // of the rows' keys
-    const int per = a.blocks * kLpHeads, index = (int)blockIdx.x / splits, grp = index / per;
-    const int heads = min(kLpHeads, a.H - grp * kLpHeads), in_grp = index - grp * per;
-    const int head = grp * kLpHeads + in_grp % heads, block = in_grp / heads;
     if (threadIdx.x == 32) { prefetch_map(&map_q); prefetch_map(&map_k); prefetch_map(&map_r); prefetch_map(&map_v); }
     if (warp == 0) {
-        int n = 0, tile = -1;
-        if (a.cu_q == nullptr) {
-            const int64_t t = (a.tq + kLpRows - 1) / kLpRows - 1 - block;
-            tile = t >= 0 ? (int)t : -1;
-        } else {
-            int before = 0;
-            for (int b = 0; b < a.N; b += 32) {
-                const int i = b + lane;
-                const int len = i < a.N ? a.cu_q[i + 1] - a.cu_q[i] : 0;
-                const int t = len > 0 ? (len + kLpRows - 1) / kLpRows : 0;
-                int x = t;                                             // inclusive scan
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const uint32_t hit = __ballot_sync(0xffffffffu, before + x > block);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    n = b + l;
-                    tile = before + __shfl_sync(0xffffffffu, x, l) - 1 - block;
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, x, 31);
-            }
-        }
-        if (lane == 0) { where[0] = n; where[1] = tile; }
         tmem_alloc(tmem_at, 512);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(rows_full, 1);
-        for (int i = 0; i < 4; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+        mbar_init(next, 1);
+        mbar_init(answered, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2 * (kLpSlotsK + kLpSlotsV); ++i) mbar_init(k_full + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], kLpSoftmax / 2); mbar_init(&o_full[i], 1);
+            mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], kLpSoftmax + 3);
+        }
         fence_mbar_init();
     }
-    if (blockIdx.x == 0) check_cu_seqlens(a.cu_q, a.cu_k, a.N, a.tq, a.tk, a.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
 
-    const int n = uniform(where[0]), tile = uniform(where[1]);
-    int64_t q0 = 0, k0 = 0, lq = a.tq, lk = a.tk;
-    if (a.cu_q) {
-        q0 = a.cu_q[n]; lq = (int64_t)a.cu_q[n + 1] - q0;
-        k0 = a.cu_k[n]; lk = (int64_t)a.cu_k[n + 1] - k0;
-        if (k0 < 0 || lk < 0 || k0 + lk > a.tk) lk = 0;                // malformed: reported by block 0
-        if (q0 < 0 || q0 + lq > a.tq) lq = 0;
-    }
-    const int64_t r0 = (int64_t)tile * kLpRows;                        // first row within the sequence
-    // keys that the last row of each tile sees, in tiles
-    int tiles[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t f = r0 + i * 128;
-        const int64_t last = (f + 128 < lq ? f + 128 : lq) - 1;
-        int64_t seen = tile < 0 || f >= lq ? 0 : a.causal ? lk - lq + last + 1 : lk;
-        seen = seen < 0 ? 0 : seen > lk ? lk : seen;
-        tiles[i] = uniform((int)((seen + kLpKeys - 1) / kLpKeys));
-    }
-    // this CTA's share of the key tiles
-    const int steps_all = max(tiles[0], tiles[1]);
-    const int start = steps_all * rank / splits, steps = steps_all * (rank + 1) / splits - start;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) tiles[i] = min(max(tiles[i] - start, 0), steps);
-
-    if (warp < 8) {                                                    // ---------------- softmax
-        regs_inc<232>();
-        const int i = warp >> 2, quarter = warp & 3, mine = i == 0 ? tiles[0] : tiles[1];
-        const int64_t row = r0 + i * 128 + quarter * 32 + lane;        // within the sequence
-        const int64_t seen = a.causal ? lk - lq + row : lk - 1;        // last key it sees
-        const uint32_t ts = tmem_addr(tmem, 32 * quarter, i * 128), to = ts + 256;
+    if (warp < kLpSoftmax) {                                           // ---------------- softmax
+        regs_inc<112>();
+        // Two threads a row, half of the keys (and of O's channels) each.  They share the row's reference, by way of
+        // shared memory when it moves.
+        const int i = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t ts = tmem_addr(tmem, 32 * quarter, i * 128), to = ts + 256 + half * 64;
+        float* shared = (float*)(mem + kLpOffLse) + i * 128 + r;
         const float sc = a.scale * 1.4426950408889634f;
-        float ref = kLpUnset, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < mine; ++j) {
-            ok = mbar_wait_warp(&s_full[i], j & 1);
+        LpRing<kLpSlotsV> v_ring;
+        uint32_t tile0 = 0, outs = 0;                                  // this tile's steps and results so far
+        for (uint32_t it = 0; ok; ++it) {
+            ok = mbar_wait_warp(&item_full[it & 1], it >> 1 & 1);
             if (!ok) break;
+            const LpItem& item = items[it & 1];
+            if (item.r0 < 0) break;
+            const int mine = uniform(item.tiles[i]);
+            const int64_t row = (int64_t)item.r0 + i * 128 + r;        // within the sequence
+            int end = item.lk - 1;                                     // last key it sees
+            if (a.causal) end = (int)min64(end, (int64_t)item.lk - item.lq + row);
+            const int seen = end - item.start * kLpKeys + 1 - half * 64;   // of this thread's
+            const int ragged = item.lk % kLpKeys ? item.lk / kLpKeys - item.start : -1;   // step whose tile is not full
+            float ref = kLpUnset, l = 0.f;
+            for (int j = 0; j < mine; ++j) {
+                ok = tile_and(i, ok && mbar_wait_spin(&s_full[i], (tile0 + j) & 1));
+                if (!ok) break;
+                tc_fence_after_sync();
+                float x[64];
+                tmem_ld32(ts + half * 64, *(float(*)[32])x);
+                tmem_ld32(ts + half * 64 + 32, *(float(*)[32])(x + 32));
+                tmem_wait_ld();
+                tmem_ready(x);
+                const int keep = seen - j * kLpKeys;
+                if (keep < 64) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = c < keep ? x[c] : -INFINITY;
+                }
+                float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < 64; c += 4) {
+                    m[0] = fmaxf(m[0], x[c]); m[1] = fmaxf(m[1], x[c + 1]);
+                    m[2] = fmaxf(m[2], x[c + 2]); m[3] = fmaxf(m[3], x[c + 3]);
+                }
+                float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sc;
+                // (behind this both halves of S are read, and P may take their place)
+                if (!tile_and(i, !(top > ref + kLpSlack))) {
+                    if (half) *shared = top;
+                    tile_sync(i);
+                    float now = ref;
+                    if (!half) {
+                        top = fmaxf(top, *shared);
+                        if (top > ref + kLpSlack) now = top;
+                        *shared = now;
+                    }
+                    tile_sync(i);
+                    if (half) now = *shared;
+                    const float f = ex2(ref - now);
+                    ref = now;
+                    l *= f;
+                    if (j > 0) {                                       // the products before S are complete: O is still
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 16) {
+                            float o[16];
+                            tmem_ld16(to + c, o);
+                            tmem_wait_ld();
+                            tmem_ready(o);
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) o[q] *= f;
+                            tmem_st16(to + c, o);
+                        }
+                    }
+                }
+                const f32x2 sc2 = pack2(sc, sc), nref = pack2(-ref, -ref);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float b[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        float p0, p1;
+                        unpack2(fma2(pack2(x[c + 2 * q], x[c + 2 * q + 1]), sc2, nref), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[(q & 1) * 2] += p0;
+                        sum[(q & 1) * 2 + 1] += p1;
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);    // the product's operand: 8 bits
+                        b[q] = __uint_as_float(*(const uint32_t*)&h);
+                    }
+                    tmem_st16(ts + half * 32 + c / 2, b);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                // Weight 0 times what lies behind the last key: make that 0.  Done by the first tile that uses it.
+                if (j == ragged && (i == 0 || j >= item.tiles[0])) {
+                    const int piece = 2 * j + r / 64;
+                    if (r >= item.lk % kLpKeys) {
+                        if (!mbar_wait_spin(&v_full[piece % kLpSlotsV], v_ring.parity(piece))) record_status(a.status, KDA_ERR_TIMEOUT);
+                        uint8_t* at = mem + kLpOffV + piece % kLpSlotsV * kLpPiece + half * 8192 + r % 64 * 128;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) *(uint4*)(at + 16 * q) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[i]);
+            }
+            // the row's sum, and O once its products are complete
+            if (half) *shared = l;
+            tile_sync(i);
+            if (!half) {
+                l += *shared;
+                *shared = l;
+            }
+            ok = tile_and(i, ok && (mine == 0 || mbar_wait_spin(&o_full[i], outs & 1)));
+            if (half) l = *shared;
             tc_fence_after_sync();
-            float x[128];
+            v_ring.add(2 * max(item.tiles[0], item.tiles[1]));
+            tile0 += mine;
+            outs += mine > 0;
+            if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            if (SHARED) {
+                // This CTA's part to shared memory, once neither tile's products read there: [row][128] fp32 in 16-byte
+                // pieces turned by the row, and log2 of the rows' sums.
+                asm volatile("bar.sync 3, %0;" ::"n"(32 * kLpSoftmax) : "memory");
+                float4* part = (float4*)(mem + (i * 128 + r) * kLpRow);
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, *(float(*)[32])(x + c));
-            tmem_wait_ld();
-            tmem_ready(x);
-            const int64_t first = (int64_t)(start + j) * kLpKeys;
-            if (first + kLpKeys - 1 > (seen < lk - 1 ? seen : lk - 1)) {
-                const int64_t end = seen < lk - 1 ? seen : lk - 1;
-                const int keep = end < first ? 0 : (int)(end - first + 1);
-#pragma unroll
-                for (int c = 0; c < 128; ++c) x[c] = c < keep ? x[c] : -INFINITY;
-            }
-            float m[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int c = 4; c < 128; c += 4) {
-                m[0] = fmaxf(m[0], x[c]); m[1] = fmaxf(m[1], x[c + 1]);
-                m[2] = fmaxf(m[2], x[c + 2]); m[3] = fmaxf(m[3], x[c + 3]);
-            }
-            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sc;
-            const bool move = top > ref + kLpSlack;
-            if (__any_sync(0xffffffffu, move)) {
-                const float now = move ? top : ref;
-                const float f = ex2(ref - now);
-                ref = now;
-                l *= f;
-                if (j > 0) {                                           // the products before S are complete: O is still
-                    for (int c = 0; c < 128; c += 32) {
-                        float o[32];
+                for (int c = 0; c < 64; c += 32) {
+                    float o[32];
+                    if (mine > 0) {
                         tmem_ld32(to + c, o);
                         tmem_wait_ld();
                         tmem_ready(o);
-                        uint32_t b[32];
+                    }
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) b[q] = __float_as_uint(o[q] * f);
-                        tmem_st32(to + c, b);
+                    for (int q = 0; q < 8; ++q)
+                        part[(half * 16 + c / 4 + q) ^ lane] =
+                            mine > 0 ? make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                if (half) *shared = l == 0.f ? -INFINITY : ref + log2f(l);
+                fence_proxy_async_smem();                              // read by copies
+            } else {
+                const bool live = row < item.lq;
+                const int64_t at = (item.q0 + (live ? row : 0)) * a.H + item.head;
+                __nv_bfloat16* dst = a.out + at * 128 + half * 64;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float o[32];
+                    if (mine > 0) {
+                        tmem_ld32(to + c, o);
+                        tmem_wait_ld();
+                        tmem_ready(o);
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 8) {
+                            uint32_t b[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                b[e] = mine > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
+                            *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
+                        }
                     }
                 }
+                if (live && half && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
             }
-            const f32x2 sc2 = pack2(sc, sc), nref = pack2(-ref, -ref);
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t b[32];
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    float p0, p1;
-                    unpack2(fma2(pack2(x[c + 2 * q], x[c + 2 * q + 1]), sc2, nref), p0, p1);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    sum[(q & 1) * 2] += p0;
-                    sum[(q & 1) * 2 + 1] += p1;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);    // the product's operand: 8 bits
-                    b[q] = *(const uint32_t*)&h;
-                }
-                tmem_st32(ts + c / 2, b);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            // Weight 0 times what lies behind the last key: make that 0.  Done by the first tile that uses it.
-            if (start + j + 1 == steps_all && lk - first < kLpKeys && (i == 0 || j >= tiles[0])) {
-                const int r = quarter * 32 + lane;
-                const uint32_t u = 5 * j + 3 + r / 64;
-                if (r >= lk - first) {
-                    if (!mbar_wait_spin(&kv_full[(j & 1) * 2 + 1], (j >> 1) & 1)) record_status(a.status, KDA_ERR_TIMEOUT);
-                    uint8_t* at = mem + kLpOffRing + u % kLpSlots * kLpPiece + r % 64 * 128;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        *(uint4*)(at + 16 * q) = make_uint4(0, 0, 0, 0);
-                        *(uint4*)(at + 8192 + 16 * q) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-            }
-            tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[i]);
-        }
-        if (ok && mine > 0) {
-            ok = mbar_wait_warp(&o_full[i], 0);
-            tc_fence_after_sync();
-        }
-        if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        if (SHARED) {
-            // This CTA's part to shared memory, once neither tile's products read there: [row][128] fp32 in 16-byte
-            // pieces turned by the row, and log2 of the rows' sums.
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            const int r = i * 128 + quarter * 32 + lane;
-            float4* part = (float4*)(mem + r * kLpRow);
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                if (mine > 0) {
-                    tmem_ld32(to + c, o);
-                    tmem_wait_ld();
-                    tmem_ready(o);
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    part[(c / 4 + q) ^ lane] = mine > 0 ? make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv,
-                                                                      o[4 * q + 3] * inv)
-                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            ((float*)(mem + kLpOffLse))[r] = l == 0.f ? -INFINITY : ref + log2f(l);
-            fence_proxy_async_smem();                                  // read by copies
-        } else {
-            const bool live = tile >= 0 && row < lq;
-            __nv_bfloat16* dst = a.out + ((q0 + (live ? row : 0)) * a.H + head) * 128;
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                if (mine > 0) {
-                    tmem_ld32(to + c, o);
-                    tmem_wait_ld();
-                    tmem_ready(o);
-                }
-                if (live) {
-#pragma unroll
-                    for (int q = 0; q < 32; q += 8) {
-                        uint32_t b[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            b[e] = mine > 0 ? bf16x2(pack2(o[q + 2 * e] * inv, o[q + 2 * e + 1] * inv)) : 0u;
-                        *(uint4*)(dst + c + q) = make_uint4(b[0], b[1], b[2], b[3]);
-                    }
-                }
-            }
-            if (live && a.lse)
-                a.lse[(q0 + row) * a.H + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+            if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         }
     } else {
-        regs_dec<40>();
-        if (warp == 8) {                                               // ---------------- producer
-            if (lane == 0 && steps > 0) {
-                mbar_arrive_expect_tx(q_full, 6 * kLpPiece);
-                for (int p = 0; p < 6; ++p)
-                    tma_load_3d_at(base + p * kLpPiece, &map_q, p % 3 * 64, head, (int)(q0 + r0) + p / 3 * 128, smem_u32(q_full));
+        regs_dec<32>();
+        if (warp == kLpSoftmax || warp == kLpSoftmax + 3) {                                 // ---------------- producers: queries and keys, values
+            // Each its own ring and warp: values wait for room longer than the keys behind them.
+            if (lane == 0) {
                 bool ok = true;
-                uint32_t u = 0;
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int key = (int)k0 + (start + j) * kLpKeys;
-                    for (int p = 0; p < 5; ++p, ++u) {
-                        if (u >= kLpSlots) {                           // the piece this one takes the place of
-                            const uint32_t o = u - kLpSlots, oj = o / 5, g = (oj & 1) * 2 + (o % 5 >= 3);
-                            if (!(ok = mbar_wait_spin(&kv_empty[g], (oj >> 1) & 1))) break;
+                LpRing<kLpSlotsK> k_ring;
+                LpRing<kLpSlotsV> v_ring;
+                uint32_t loaded = 0;
+                for (uint32_t it = 0; ok; ++it) {
+                    if (!(ok = mbar_wait_spin(&item_full[it & 1], it >> 1 & 1))) break;
+                    const LpItem x = items[it & 1];
+                    mbar_arrive(&item_empty[it & 1]);
+                    if (x.r0 < 0) break;
+                    const int steps = max(x.tiles[0], x.tiles[1]), ask = max(steps - 2, 0);
+                    int key = x.k0 + x.start * kLpKeys;
+                    if (warp == kLpSoftmax) {
+                        if (steps == 0) mbar_arrive(next);
+                        for (int j = 0; j < steps && ok; ++j, key += kLpKeys) {
+                            if (j == ask) mbar_arrive(next);           // the next rows will be wanted soon
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const int piece = 3 * j + p, slot = piece % kLpSlotsK;
+                                if (!(ok = mbar_wait_spin(&k_empty[slot], k_ring.parity(piece) ^ 1))) break;
+                                const uint32_t at = base + kLpOffK + slot * kLpPiece, bar = smem_u32(&k_full[slot]);
+                                mbar_arrive_expect_tx(&k_full[slot], kLpPiece);
+                                if (p < 2) tma_load_3d_at(at, &map_k, p * 64, x.head, key, bar);
+                                else tma_load_2d(at, &map_r, 0, key, bar);
+                            }
+                            if (j == 0 && ok) {
+                                if (loaded > 0 && !(ok = mbar_wait_spin(q_empty, (loaded - 1) & 1))) break;
+                                ++loaded;
+                                mbar_arrive_expect_tx(q_full, 6 * kLpPiece);
+                                for (int c = 0; c < 6; ++c)
+                                    tma_load_3d_at(base + c * kLpPiece, &map_q, c % 3 * 64, x.head,
+                                                   x.q0 + x.r0 + c / 3 * 128, smem_u32(q_full));
+                            }
                         }
-                        uint64_t* f = &kv_full[(j & 1) * 2 + (p >= 3)];
-                        const uint32_t at = base + kLpOffRing + u % kLpSlots * kLpPiece, bar = smem_u32(f);
-                        if (p == 0 || p == 3) mbar_arrive_expect_tx(f, (p == 0 ? 3 : 2) * kLpPiece);
-                        if (p < 2) tma_load_3d_at(at, &map_k, p * 64, head, key, bar);
-                        else if (p == 2) tma_load_2d(at, &map_r, 0, key, bar);
-                        else {
-                            tma_load_3d_at(at, &map_v, 0, head, key + (p - 3) * 64, bar);
-                            tma_load_3d_at(at + 8192, &map_v, 64, head, key + (p - 3) * 64, bar);
+                        k_ring.add(3 * steps);
+                    } else {
+                        for (int j = 0; j < steps && ok; ++j, key += kLpKeys) {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                const int piece = 2 * j + p, slot = piece % kLpSlotsV;
+                                if (!(ok = mbar_wait_spin(&v_empty[slot], v_ring.parity(piece) ^ 1))) break;
+                                const uint32_t at = base + kLpOffV + slot * kLpPiece, bar = smem_u32(&v_full[slot]);
+                                mbar_arrive_expect_tx(&v_full[slot], kLpPiece);
+                                tma_load_3d_at(at, &map_v, 0, x.head, key + p * 64, bar);
+                                tma_load_3d_at(at + 8192, &map_v, 64, x.head, key + p * 64, bar);
+                            }
                         }
+                        v_ring.add(2 * steps);
                     }
                 }
                 if (!ok) drain_copies();
             }
-        } else if (warp == 9 && steps > 0) {
+        } else if (warp == kLpSoftmax + 1) {
             // Matrix instructions.  One warp for both tiles keeps them in turn; whole products behind one wait
             // each, since a wait costs about 90 cycles and instruction fetches compete with the softmax's.
             const uint32_t idesc_s = idesc_bf16(128, 128), idesc_o = idesc_bf16(128, 128, 0, 1);
-            const uint64_t dq = sdesc_k_sw128(base), dk = sdesc_k_sw128(base + kLpOffRing);
-            const uint64_t dv = sdesc(base + kLpOffRing, 8192, 1024, 2);
-            const int n0 = tiles[0], n1 = tiles[1];
-            bool ok = mbar_wait_warp(q_full, 0);
-            for (int j = -1; j < steps && ok; ++j) {
+            const uint64_t dq = sdesc_k_sw128(base), dk = sdesc_k_sw128(base + kLpOffK);
+            const uint64_t dv = sdesc(base + kLpOffV, 8192, 1024, 2);
+            LpRing<kLpSlotsK> k_ring;
+            LpRing<kLpSlotsV> v_ring;
+            uint32_t tile0[2] = {0, 0}, loaded = 0;
+            bool ok = true;
+            for (uint32_t it = 0; ok; ++it) {
+                if (!(ok = mbar_wait_warp(&item_full[it & 1], it >> 1 & 1))) break;
+                const int n0 = uniform(items[it & 1].tiles[0]), n1 = uniform(items[it & 1].tiles[1]);
+                const int r0 = uniform(items[it & 1].r0), steps = max(n0, n1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+                if (r0 < 0) break;
+                if (steps == 0) continue;
+                ok = mbar_wait_warp(q_full, loaded & 1);
+                ++loaded;
+                for (int j = -1; j < steps && ok; ++j) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int mine = i == 0 ? n0 : n1;
-                    const uint32_t ts = tmem + i * 128, to = ts + 256;
-                    if (j >= 0 && j < mine) {                          // O += P_j V_j
-                        ok = mbar_wait_warp(&p_full[i], j & 1);
-                        if (ok && (i == 0 || j >= n0)) ok = mbar_wait_warp(&kv_full[(j & 1) * 2 + 1], (j >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        if (elect_one()) {
-                            const uint32_t u = 5 * j + 3;
+                    for (int i = 0; i < 2; ++i) {
+                        const int mine = i == 0 ? n0 : n1;
+                        const uint32_t ts = tmem + i * 128, to = ts + 256;
+                        const int jn = j + 1;
+                        const bool pv = j >= 0 && j < mine, scores = jn < mine;
+                        if (pv) {                                      // O += P_j V_j
+                            const bool first = i == 0 || j >= n0, last = i == 1 || j >= n1;   // of V's users
+                            if (first) ok = mbar_wait_warp(&v_full[2 * j % kLpSlotsV], v_ring.parity(2 * j));
+                            if (ok) ok = mbar_wait_warp(&p_full[i], (tile0[i] + j) & 1);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint64_t db = dv + (u + h) % kLpSlots * (kLpPiece / 16);
+                                const int piece = 2 * j + h, slot = piece % kLpSlotsV;
+                                if (h > 0 && first && ok) ok = mbar_wait_warp(&v_full[slot], v_ring.parity(piece));
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                if (elect_one()) {
+                                    const uint64_t db = dv + slot * (kLpPiece / 16);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_bf16_ts(to, ts + h * 32 + k * 8, db + k * (2048 / 16), idesc_o, j > 0 || h > 0 || k > 0);
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_bf16_ts(to, ts + h * 32 + k * 8, db + k * (2048 / 16), idesc_o, j > 0 || h > 0 || k > 0);
+                                    if (last) mma_commit(&v_empty[slot]);
+                                    if (h == 1 && j + 1 == mine) mma_commit(&o_full[i]);
+                                }
+                                __syncwarp();
                             }
-                            if (i == 1 || j >= n1) mma_commit(&kv_empty[(j & 1) * 2 + 1]);   // its last user
-                            if (j + 1 == mine) mma_commit(&o_full[i]);
                         }
-                        __syncwarp();
-                    }
-                    const int jn = j + 1;                              // S_{j+1}: behind the product that reads P_j in its place
-                    if (jn < mine) {
-                        if (i == 0 || jn >= n0) ok = mbar_wait_warp(&kv_full[(jn & 1) * 2], (jn >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        if (elect_one()) {
-                            const uint32_t u = 5 * jn;
+                        if (ok && scores) {                            // S_{j+1}: behind the product that reads P_j in its place
+                            const bool first = i == 0 || jn >= n0, last = i == 1 || jn >= n1;
 #pragma unroll
                             for (int p = 0; p < 3; ++p) {
-                                const uint64_t da = dq + (i * 3 + p) * (kLpPiece / 16);
-                                const uint64_t db = dk + (u + p) % kLpSlots * (kLpPiece / 16);
+                                const int piece = 3 * jn + p, slot = piece % kLpSlotsK;
+                                if (first) ok = mbar_wait_warp(&k_full[slot], k_ring.parity(piece));
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                if (elect_one()) {
+                                    const uint64_t da = dq + (i * 3 + p) * (kLpPiece / 16), db = dk + slot * (kLpPiece / 16);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_bf16_ss(ts, da + 2 * k, db + 2 * k, idesc_s, p > 0 || k > 0);
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_bf16_ss(ts, da + 2 * k, db + 2 * k, idesc_s, p > 0 || k > 0);
+                                    if (last) mma_commit(&k_empty[slot]);
+                                    if (p == 2) {
+                                        mma_commit(&s_full[i]);
+                                        if (last && jn + 1 == steps) mma_commit(q_empty);
+                                    }
+                                }
+                                __syncwarp();
                             }
-                            mma_commit(&s_full[i]);
-                            if (i == 1 || jn >= n1) mma_commit(&kv_empty[(jn & 1) * 2]);
                         }
-                        __syncwarp();
+                        if (!ok) break;
                     }
                 }
+                k_ring.add(3 * steps);
+                v_ring.add(2 * steps);
+                tile0[0] += n0;
+                tile0[1] += n1;
+            }
+            if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
+        } else if (warp == kLpSoftmax + 2) {                                       // ---------------- which rows
+            // In groups of heads (whose keys and values then stay in L2), a sequence's last rows, which see most keys,
+            // first, so that what runs last is short (8192 tokens, 32 heads: a tenth less than a head at a time).
+            // A CTA that is done with its own takes over those of a block that has not started yet.
+            bool ok = true;
+            uint32_t it = 0, asked = 0;
+            int index = (int)blockIdx.x / splits;
+            for (;;) {
+                const int per = a.blocks * kLpHeads, grp = index / per;
+                const int heads = min(kLpHeads, a.H - grp * kLpHeads), in_grp = index - grp * per;
+                const int block = in_grp / heads;
+                int n = 0, tile = -1;
+                if (a.cu_q == nullptr) {
+                    tile = (int)((a.tq + kLpRows - 1) / kLpRows) - 1 - block;
+                } else {
+                    int before = 0;
+                    for (int b = 0; b < a.N; b += 32) {
+                        const int s = b + lane;
+                        const int len = s < a.N ? a.cu_q[s + 1] - a.cu_q[s] : 0;
+                        const int t = len > 0 ? (len + kLpRows - 1) / kLpRows : 0;
+                        int x = t;                                     // inclusive scan
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int y = __shfl_up_sync(0xffffffffu, x, o);
+                            if (lane >= o) x += y;
+                        }
+                        const uint32_t hit = __ballot_sync(0xffffffffu, before + x > block);
+                        if (hit) {
+                            const int l = __ffs(hit) - 1;
+                            n = b + l;
+                            tile = before + __shfl_sync(0xffffffffu, x, l) - 1 - block;
+                            break;
+                        }
+                        before += __shfl_sync(0xffffffffu, x, 31);
+                    }
+                }
+                if (tile >= 0) {
+                    LpItem x;
+                    x.head = grp * kLpHeads + in_grp % heads;
+                    x.q0 = 0; x.k0 = 0; x.lq = (int)a.tq; x.lk = (int)a.tk; x.r0 = tile * kLpRows;
+                    if (a.cu_q) {
+                        x.q0 = a.cu_q[n]; x.lq = a.cu_q[n + 1] - x.q0;
+                        x.k0 = a.cu_k[n]; x.lk = a.cu_k[n + 1] - x.k0;
+                        if (x.k0 < 0 || x.lk < 0 || x.k0 > a.tk - x.lk) x.lk = 0;        // malformed: reported
+                        if (x.q0 < 0 || x.q0 > a.tq - x.lq) x.lq = 0;
+                    }
+                    // keys that the last row of each half sees, in tiles
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int64_t f = (int64_t)x.r0 + i * 128;
+                        const int64_t last = min64(f + 128, x.lq) - 1;
+                        int64_t seen = f >= x.lq ? 0 : a.causal ? (int64_t)x.lk - x.lq + last + 1 : x.lk;
+                        seen = seen < 0 ? 0 : min64(seen, x.lk);
+                        x.tiles[i] = (int)((seen + kLpKeys - 1) / kLpKeys);
+                    }
+                    // this CTA's share of them
+                    const int64_t all = max(x.tiles[0], x.tiles[1]);
+                    x.start = (int)(all * rank / splits);
+                    const int steps = (int)(all * (rank + 1) / splits) - x.start;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x.tiles[i] = min(max(x.tiles[i] - x.start, 0), steps);
+                    if (it >= 2 && !(ok = mbar_wait_warp(&item_empty[it & 1], ((it >> 1) - 1) & 1))) break;
+                    if (lane == 0) {
+                        items[it & 1] = x;
+                        mbar_arrive(&item_full[it & 1]);
+                    }
+                    ++it;
+                }
+                if (index == 0 && rank == 0) {
+                    bool bad = false;
+                    for (int s = lane; a.cu_q && s <= a.N; s += 32) {
+                        if (s == 0) bad |= a.cu_q[0] != 0 || a.cu_k[0] != 0;
+                        else bad |= a.cu_q[s] < a.cu_q[s - 1] || a.cu_k[s] < a.cu_k[s - 1];
+                        if (s == a.N) bad |= a.cu_q[s] != a.tq || a.cu_k[s] != a.tk;
+                    }
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (lane == 0) *a.status = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+                }
+                if (SHARED) break;
+                if (tile >= 0) {                                       // as long as the rows take: for all keys that fit
+                    if (!(ok = mbar_wait_idle(next, (it - 1) & 1))) break;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    fence_proxy_async_smem();                          // the answer before this one is read
+                    mbar_arrive_expect_tx(answered, 16);
+                    take_block(answer, answered);
+                }
+                __syncwarp();
+                if (!(ok = mbar_wait_warp(answered, asked & 1))) break;
+                ++asked;
+                if (!taken_block(answer, index)) break;
+                index = uniform(index);
+            }
+            if (ok && it >= 2) ok = mbar_wait_warp(&item_empty[it & 1], ((it >> 1) - 1) & 1);
+            if (ok && lane == 0) {
+                items[it & 1].r0 = -1;
+                mbar_arrive(&item_full[it & 1]);
             }
             if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
         }
@@ -382,10 +547,11 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     if (SHARED) {
         // Each CTA joins a share of the rows: the others copy their parts of those behind its own, 64 KB in 3300
         // cycles with two CTAs.
-        const int share = kLpRows / splits;
+        const int share = kLpRows / splits, head = items[0].head;
+        const int64_t q0 = items[0].q0, r0 = items[0].r0, lq = items[0].lq;
         auto rows_of = [&](int c) {
             const int64_t left = lq - r0 - c * share;
-            return tile < 0 || left < 0 ? 0 : (int)min64(left, share);
+            return r0 < 0 || left < 0 ? 0 : (int)min64(left, share);
         };
         const int rows = rows_of(rank);
         if (threadIdx.x == 0 && rows) mbar_arrive_expect_tx(rows_full, (splits - 1) * rows * kLpRow);
@@ -398,9 +564,9 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                             map_cta(smem_u32(rows_full), to));
         }
         __syncwarp();
-        if (warp < 8 && rows) {
+        if (warp < kLpSoftmax && rows) {
             // the parts' weights, a lane a row of the warp; then the rows
-            const int own = share / 8, first = rank * share + warp * own, count = min(own, rows - warp * own);
+            const int own = share / kLpSoftmax, first = rank * share + warp * own, count = min(own, rows - warp * own);
             float w[kLpSplits], top = kLpUnset, sum = 0.f;
 #pragma unroll
             for (int c = 0; c < kLpSplits; ++c)

@@ -42,6 +42,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
 }
 
+// For waits of many microseconds beside working warps: looks twice a microsecond, ten times as long.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    for (uint64_t t0 = globaltimer_ns(); !ok && globaltimer_ns() - t0 < 10 * kOpWaitNs; ok = mbar_try_wait(bar, parity))
+        __nanosleep(500);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -93,6 +101,29 @@ template <int N> __device__ __forceinline__ void regs_inc() {
 }
 template <int N> __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---------------------------------------------------------------- blocks that have not started
+// Asks for one of the grid's blocks that have not started, which then never
+// does; the answer (16 bytes, counted on `bar`) says which, or that none is
+// left, after which nothing more is asked.
+__device__ __forceinline__ void take_block(void* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool taken_block(const void* answer, int& x) {
+    uint32_t got, at;
+    asm volatile("{\n"
+                 ".reg .b128 a;\n"
+                 ".reg .pred p;\n"
+                 "mov.u32 %1, 0;\n"
+                 "ld.shared.b128 a, [%2];\n"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+                 "selp.u32 %0, 1, 0, p;\n"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n"
+                 "}" : "=&r"(got), "=&r"(at) : "r"(smem_u32(answer)) : "memory");
+    x = (int)at;
+    return got;
 }
 
 // ---------------------------------------------------------------- TMA
