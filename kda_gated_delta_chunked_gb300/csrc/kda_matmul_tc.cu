@@ -212,27 +212,28 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         if (sizeof(T) == 2 && use_map_c && threadIdx.x % 128 == 0) bulk_wait_all();
     } else {
         regs_dec<40>();
-        if (warp == kMmEpiWarps) {                                 // producer
-            if (lane == 0) {
-                uint32_t it = 0;
-                bool ok = true;
-                for (int t = pair; t < tiles && ok; t += pairs) {
-                    int tm, tn;
-                    place(t, tm, tn);
-                    for (int j = 0; j < kb; ++j, ++it) {
-                        uint32_t ph;
-                        const uint32_t s = stage(it, ph);
-                        if (it >= kStages && !(ok = mbar_wait_spin(&empty[s], ph ^ 1))) break;
-                        const uint32_t at = base + s * S::kStage, bar = map_cta(smem_u32(&full[s]), 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
-                        tma_load_2d_pair(at, &map_a, j * 128, tm * 256 + (int)rank * 128, bar);
+        if (warp == kMmEpiWarps || warp == kMmEpiWarps + 3) {      // producers: of even blocks, of odd ones
+            const uint32_t own = warp == kMmEpiWarps ? 0 : 1;
+            const uint32_t all = (uint32_t)((tiles - pair + pairs - 1) / pairs) * kb;
+            int t = pair, j = own, tm, tn;
+            place(t, tm, tn);
+            bool ok = true;
+            for (uint32_t it = own; it < all; it += 2, j += 2) {
+                while (j >= kb) { j -= kb; t += pairs; place(t, tm, tn); }
+                uint32_t ph;
+                const uint32_t s = stage(it, ph);
+                if (it >= kStages && !(ok = mbar_wait_warp(&empty[s], ph ^ 1))) break;
+                if (elect_one()) {
+                    const uint32_t at = base + s * S::kStage, bar = map_cta(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+                    tma_load_2d_pair(at, &map_a, j * 128, tm * 256 + (int)rank * 128, bar);
 #pragma unroll
-                        for (int h = 0; h < kGroups; ++h)          // a group's 128 rows of b: 64 from either CTA
-                            tma_load_2d_pair(at + S::kA + h * 8192, &map_b, j * 128, tn * BN + h * 128 + (int)rank * 64, bar);
-                    }
+                    for (int h = 0; h < kGroups; ++h)              // a group's 128 rows of b: 64 from either CTA
+                        tma_load_2d_pair(at + S::kA + h * 8192, &map_b, j * 128, tn * BN + h * 128 + (int)rank * 64, bar);
                 }
-                if (!ok) drain_copies();
+                __syncwarp();
             }
+            if (!ok) drain_copies();
         } else if (warp <= kMmEpiWarps + 2) {
             // Matrix instructions, by the leader: a warp for even blocks and one for odd ones.  One alone needs about
             // 500 cycles for the waits, 4 instructions and the commits, as long as the instructions take.
