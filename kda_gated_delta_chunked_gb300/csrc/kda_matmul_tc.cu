@@ -63,7 +63,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 2 * kMmEpiWarps / kGroups); }
+        for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], kMmEpiWarps); }
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc_pair(tmem_at, 512); tmem_relinquish_pair(); }
@@ -93,7 +93,11 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     // 384 threads x 168 registers at launch = 256 x 232 + 128 x 40
     if (warp < kMmEpiWarps) {                                      // scale, add, store
         regs_inc<232>();
-        constexpr int kCols = BN / 2;                              // columns of a thread
+        // A thread sums 128 columns of its row.  Of 256, a warpgroup has a half each; 128 they take in turns, one the even
+        // blocks of k and the other the odd ones, and join their sums at the end: a block's wait, reads and sums take a
+        // warp about 450 cycles, its products 256 (256 x 6144 x 4096: 11.3 us so, 12.0 with both on every block).
+        constexpr bool kTurns = BN == 128;
+        constexpr int kCols = 128, kOutCols = BN / 2, kStep = kTurns ? 2 : 1;
         const int quarter = warp & 3, half = warp >> 2;
         const int nb_all = (g.n + 127) / 128;
         uint32_t it = 0;
@@ -102,14 +106,17 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             int tm, tn;
             place(t, tm, tn);
             const int64_t row = (int64_t)tm * 256 + rank * 128 + quarter * 32 + lane;
-            const int col = tn * BN + half * kCols;
+            const int col = tn * BN + half * kOutCols;             // of those it stores
             const float* sa = g.sa + (row < g.m ? row : 0) * kb;
-            const float* sb = g.sb + (int64_t)min(col / 128, nb_all - 1) * kb;
+            const float* sb = g.sb + (int64_t)min(kTurns ? tn : col / 128, nb_all - 1) * kb;
             f32x2 acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
-            float xa = sa[0], xb = sb[0];                          // loaded a block ahead
-            for (int j = 0; j < kb; ++j, ++it) {
+            const uint32_t end = it + kb;
+            int j = kTurns ? (it + half) & 1 : 0;                  // the turns are counted over the tiles, as the buffers are
+            it += j;
+            float xa = j < kb ? sa[j] : 0.f, xb = j < kb ? sb[j] : 0.f;   // loaded a block ahead
+            for (; j < kb; j += kStep, it += kStep) {
                 const float s1 = xa * xb;
                 const f32x2 s = pack2(s1, s1);
                 const uint32_t d = it % kBufs * kGroups + (kGroups == 2 ? half : 0), dph = it / kBufs & 1;
@@ -117,14 +124,14 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t at = tmem_addr(tmem, 32 * quarter, it % kBufs * BN + half * kCols);
+                const uint32_t at = tmem_addr(tmem, 32 * quarter, it % kBufs * BN + (kTurns ? 0 : half * kCols));
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64) {              // two loads in flight
                     float f[32], e[32];
                     tmem_ld32(at + c, f);
                     tmem_ld32(at + c + 32, e);
                     if (c == 0) {
-                        const int jn = j + 1 < kb ? j + 1 : j;
+                        const int jn = j + kStep < kb ? j + kStep : j;
                         xa = sa[jn];
                         xb = sb[jn];
                     }
@@ -143,9 +150,30 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         acc[c / 2 + 16 + i] = fma2(pack2(e[2 * i], e[2 * i + 1]), s, acc[c / 2 + 16 + i]);
                 }
             }
+            it = end;
             if (!ok) {
 #pragma unroll
                 for (int i = 0; i < kCols / 2; ++i) acc[i] = pack2(NAN, NAN);
+            }
+            if constexpr (kTurns) {
+                // The first warpgroup's columns 0 .. 63, then the second's 64 .. 127, each in 32 KB that lie there for
+                // the output too: pairs of columns, a row's threads beside each other.
+                f32x2* turn = (f32x2*)(raw + (base - smem_u32(raw)) + kStages * S::kStage) + quarter * 32 + lane;
+                if (sizeof(T) == 2 && use_map_c && threadIdx.x % 128 == 0) bulk_wait_read_all();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    asm volatile("bar.sync 3, 256;" ::: "memory");
+                    if (half != h) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) turn[i * 128] = acc[h * 32 + i];
+                    }
+                    asm volatile("bar.sync 3, 256;" ::: "memory");
+                    if (half == h) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[i] = h == 0 ? add2(acc[i], turn[i * 128]) : add2(turn[i * 128], acc[32 + i]);
+                    }
+                }
+                asm volatile("bar.sync 3, 256;" ::: "memory");
             }
             if (sizeof(T) == 2 && use_map_c) {
                 // Through shared memory and out by TMA: the stores of all SMs' tiles come at once, and the
@@ -153,7 +181,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 const uint32_t own = base + kStages * S::kStage + half * (S::kOut / 2);
                 const int r = quarter * 32 + lane;
 #pragma unroll
-                for (int c0 = 0; c0 < kCols; c0 += 64) {
+                for (int c0 = 0; c0 < kOutCols; c0 += 64) {
                     if (c0 == 0) {
                         if (threadIdx.x % 128 == 0) bulk_wait_read_all();
                         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
@@ -178,7 +206,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 uint32_t* own = (uint32_t*)(raw + (base - smem_u32(raw)) + kStages * S::kStage) + warp * 1024;
                 constexpr int kPer = sizeof(T) == 2 ? 2 : 1;       // values of a word
 #pragma unroll
-                for (int w0 = 0; w0 < kCols / kPer; w0 += 32) {
+                for (int w0 = 0; w0 < kOutCols / kPer; w0 += 32) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         uint32_t word;
@@ -530,9 +558,9 @@ static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
 template <typename T>
 static cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t stream) {
     // Measured on a GB300 (us, thin with 64 rows of a / wide with 128 columns / with 256):
-    //   1 x 4096 x 4096    7 / 13 / 17     64 x 8192 x 8192   19 / 21 / 30    128 x 1024 x 4096   7 / 12 / 17
-    //   512 x 1024 x 1024  6 / 6.4 / 8     128 x 6144 x 4096  16 / 13 / 18    1024 x 1024 x 4096  17 / 12 / 18
-    //   1024 x 4096 x 4096  42 / 21 / 19   2048 x 8192 x 4096  139 / 64 / 62  16384 x 8192 x 4096  1040 / 455 / 395
+    //   1 x 4096 x 4096  6.4 / 12.5 / 16.8     64 x 8192 x 8192  16.8 / 17.4 / 29.6    128 x 2048 x 4096  7.2 / 11.1 / 17.4
+    //   512 x 1024 x 1024  6.2 / 6.8 / 8.2     128 x 6144 x 4096  16.5 / 11.4 / 17.5   1024 x 1024 x 4096  16.9 / 11.5 / 17.5
+    //   1024 x 4096 x 4096  42 / 19.6 / 18.3   2048 x 8192 x 4096  140 / 59.7 / 60.0   16384 x 8192 x 4096  1049 / 435 / 386
     // thin while its tiles are few (its splits then use SMs that tiles of the others would leave idle); of the wide
     // ones the narrower while all its tiles run at once.
     const int64_t tn = (a.n + 127) / 128;
