@@ -392,14 +392,17 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         const bool pv = j >= 0 && j < mine, scores = jn < mine;
                         if (pv) {                                      // O += P_j V_j
                             const bool first = i == 0 || j >= n0, last = i == 1 || j >= n1;   // of V's users
-                            if (first) ok = mbar_wait_warp(&v_full[2 * j % kLpSlotsV], v_ring.parity(2 * j));
-                            if (ok) ok = mbar_wait_warp(&p_full[i], (tile0[i] + j) & 1);
+                            uint64_t* const p_at = &p_full[i];
+                            const uint32_t p_parity = (tile0[i] + j) & 1;
+                            if (first)
+                                ok = mbar_wait_all<3>({p_at, &v_full[2 * j % kLpSlotsV], &v_full[(2 * j + 1) % kLpSlotsV]},
+                                                      {p_parity, v_ring.parity(2 * j), v_ring.parity(2 * j + 1)});
+                            else ok = mbar_wait_all<1>({p_at}, {p_parity});
+                            if (!ok) break;
+                            tc_fence_after_sync();
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int piece = 2 * j + h, slot = piece % kLpSlotsV;
-                                if (h > 0 && first && ok) ok = mbar_wait_warp(&v_full[slot], v_ring.parity(piece));
-                                if (!ok) break;
-                                tc_fence_after_sync();
                                 if (elect_one()) {
                                     const uint64_t db = dv + slot * (kLpPiece / 16);
 #pragma unroll
@@ -413,12 +416,15 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         }
                         if (ok && scores) {                            // S_{j+1}: behind the product that reads P_j in its place
                             const bool first = i == 0 || jn >= n0, last = i == 1 || jn >= n1;
+                            if (first)
+                                ok = mbar_wait_all<3>({&k_full[3 * jn % kLpSlotsK], &k_full[(3 * jn + 1) % kLpSlotsK],
+                                                       &k_full[(3 * jn + 2) % kLpSlotsK]},
+                                                      {k_ring.parity(3 * jn), k_ring.parity(3 * jn + 1), k_ring.parity(3 * jn + 2)});
+                            if (!ok) break;
+                            tc_fence_after_sync();
 #pragma unroll
                             for (int p = 0; p < 3; ++p) {
                                 const int piece = 3 * jn + p, slot = piece % kLpSlotsK;
-                                if (first) ok = mbar_wait_warp(&k_full[slot], k_ring.parity(piece));
-                                if (!ok) break;
-                                tc_fence_after_sync();
                                 if (elect_one()) {
                                     const uint64_t da = dq + (i * 3 + p) * (kLpPiece / 16), db = dk + slot * (kLpPiece / 16);
 #pragma unroll

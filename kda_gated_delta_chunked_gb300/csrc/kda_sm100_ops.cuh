@@ -37,9 +37,32 @@ __device__ __forceinline__ bool elect_one() {
 // The same value in every lane, known to the compiler as such: loops and
 // descriptors that hang on values from memory stay uniform only through this.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 // mbar_wait_spin by a whole warp, with one answer.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
+}
+
+// All of several barriers, by a whole warp: what is there already costs one look (about 90 cycles), not one each.
+template <int N>
+__device__ __forceinline__ bool mbar_wait_all(uint64_t* const (&bars)[N], const uint32_t (&parities)[N]) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        bool done = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k) done &= mbar_test_wait(bars[k], parities[k]);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((i & 15) == 0) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (__any_sync(0xffffffffu, t - t0 > kOpWaitNs)) return false;
+        }
+    }
 }
 
 // For waits of many microseconds beside working warps: looks twice a microsecond, ten times as long.
