@@ -256,6 +256,20 @@ def test_prefill_few_rows_of_many_keys(kda, lq, lk, h, causal):
     check_prefill(kda, q, kn[:sum(lk)], kr[:sum(lk)], v[:sum(lk)], lq, lk, causal, rows=[0, 63, 64, 128, 255, 256, 399, 400, 1499, 6999])
 
 
+@pytest.mark.parametrize("lq,lk,h", [([37 * i % 301 for i in range(70)], [53 * i % 407 for i in range(70)], 9), ([0] * 200 + [5], [3] * 201, 2),
+                                     ([600] * 12, [700] * 12, 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_more_rows_than_the_gpu_holds(kda, lq, lk, h, causal):
+    """Blocks take over the rows of others: every row once, whoever computes it, and the same bits each time."""
+    q, kn, kr, v = (t.cuda() for t in expanded(sum(lq), sum(lk), h, seed=21))
+    o, l = check_prefill(kda, q, kn, kr, v, lq, lk, causal, rows=[0, 127, 128, 300, 599])
+    cu = lambda x: torch.tensor([0] + list(torch.tensor(x).cumsum(0)), dtype=torch.int32).cuda()  # noqa: E731
+    for _ in range(3):
+        out = torch.full_like(o, 7.0)
+        o2, l2 = kda.latent_prefill(q, kn, kr, v, cu(lq), cu(lk), scale=1 / math.sqrt(192), causal=causal, out=out)
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
 @pytest.mark.parametrize("dk,dr,dv,dtype", [(128, 64, 128, F32), (96, 32, 64, BF16), (40, 0, 33, BF16), (192, 64, 256, F32)])
 def test_prefill_other_sizes_and_types(kda, dk, dr, dv, dtype):
     check_prefill(kda, *expanded(50, 70, 3, dk, dr, dv, dtype), simt=True)
