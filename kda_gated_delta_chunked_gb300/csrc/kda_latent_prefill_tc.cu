@@ -27,10 +27,14 @@
 // (256 rows of 8192 keys, 16 heads: 123 -> 48 us with 4).
 //
 // A key tile of both row tiles is 2 x (12 + 8) instructions of 64 cycles, 2560 of
-// the tensor pipe; it takes about 3300.  8192 tokens, 32 heads, causal: 429 us,
-// 1.60 PFLOP/s.  What it took there (us): a thread a row 461; one ring of eight
-// pieces freed a step at a time 439, then two rings so 470; blocks that run one
-// tile of rows each 445 (and 100 prompts of 60 tokens 99 instead of 54).
+// the tensor pipe; it takes 3360.  The pipe starts an instruction about when it is
+// issued, and the issuing warp's waits between products are the difference; loads,
+// exponentials and maxima are hidden (without them the time is the same).  8192
+// tokens, 32 heads, causal: 420 us, 1.63 PFLOP/s.  What else was measured there
+// (us): a thread a row 461 (two: 429); a wait for each of a product's barriers 429;
+// one ring of eight pieces freed a step at a time 439; a warp for each tile's
+// instructions, in turns 474; blocks that run one tile of rows each 445 (and 100
+// prompts of 60 tokens 99 instead of 54).
 #include <math.h>
 
 #include "kda_common.cuh"
