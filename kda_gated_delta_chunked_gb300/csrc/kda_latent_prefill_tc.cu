@@ -15,8 +15,8 @@
 // (then the row of O is rescaled), which is rare after the first tiles.
 // With the queries' 96 KB, rings of five 16 KB pieces for K (64 channels each)
 // and three for V (64 keys) fill shared memory.  A piece is freed by the last
-// product that reads it, and K and V have a producer each: what bounds a step is
-// the time from there to the next piece's arrival.
+// product that reads it, and K and V have a producer each, since V waits for room
+// longer than the K behind it.
 //
 // A CTA that is done takes over the rows of a block that has not started yet, and
 // fetches their queries and keys while the last values of its own are weighed.
@@ -31,9 +31,9 @@
 // issued, and the issuing warp's waits between products are the difference; loads,
 // exponentials and maxima are hidden (without them the time is the same).  8192
 // tokens, 32 heads, causal: 420 us, 1.63 PFLOP/s.  What else was measured there
-// (us): a thread a row 461 (two: 429); a wait for each of a product's barriers 429;
-// one ring of eight pieces freed a step at a time 439; a warp for each tile's
-// instructions, in turns 474; blocks that run one tile of rows each 445 (and 100
+// (us): a wait for each of a product's barriers 429, and a thread a row then 461;
+// the rings freed a step at a time 470; a warp for each tile's instructions, in
+// turns 474; blocks of one tile of rows, one ring, a thread a row 445 (and 100
 // prompts of 60 tokens 99 instead of 54).
 #include <math.h>
 
@@ -141,7 +141,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
 
     if (warp < kLpSoftmax) {                                           // ---------------- softmax
-        regs_inc<112>();
+        regs_inc<112>();                                               // 640 x 96 at launch = 512 x 112 + 128 x 32
         // Two threads a row, half of the keys (and of O's channels) each.  They share the row's reference, by way of
         // shared memory when it moves.
         const int i = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, r = quarter * 32 + lane;
