@@ -103,19 +103,17 @@ __device__ __forceinline__ void store8(T* row, int e, int dim, const Vec8& x) {
 
 // h of one step: x + r, written out where wanted.
 template <typename T, bool kAligned>
-__device__ __forceinline__ Vec8 norm_sum8(const NormArgs& a, int64_t row, int e, bool write) {
-    const Raw8<T> x = load8<T, kAligned>((const T*)a.x + row * a.x_stride, e, a.dim);
+__device__ __forceinline__ Vec8 norm_add8(const NormArgs& a, int64_t row, int e, bool write, const Raw8<T>& x, const Raw8<T>& r) {
     Vec8 h;
-    if (a.r) {
-        const Raw8<T> r = load8<T, kAligned>((const T*)a.r + row * a.r_stride, e, a.dim);
 #pragma unroll
-        for (int i = 0; i < kNormVec; ++i) h.v[i] = x.get(i) + r.get(i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kNormVec; ++i) h.v[i] = x.get(i);
-    }
+    for (int i = 0; i < kNormVec; ++i) h.v[i] = a.r ? x.get(i) + r.get(i) : x.get(i);
     if (write && a.h) store8<T, kAligned>((T*)a.h + row * a.dim, e, a.dim, h);
     return h;
+}
+template <typename T, bool kAligned>
+__device__ __forceinline__ void norm_load8(const NormArgs& a, int64_t row, int e, Raw8<T>& x, Raw8<T>& r) {
+    x = load8<T, kAligned>((const T*)a.x + row * a.x_stride, e, a.dim);
+    if (a.r) r = load8<T, kAligned>((const T*)a.r + row * a.r_stride, e, a.dim);
 }
 
 // The outputs of one step.  All lanes of the warp call it (the block maximum
@@ -171,91 +169,130 @@ __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int e,
     }
 }
 
-constexpr int norm_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
-
-// TPR threads share a row; each holds STEPS vectors of it (STEPS = 0: the row
-// is too long for registers and is read a second time, out of L2).  Few vectors
-// a thread and 1536 threads an SM keep the most bytes on their way: 65536 x 4096
-// bf16 to all four outputs 361 us (99% of the measured copy rate), 380 without
-// the bound on registers, 406 with the weights read behind the sum.
-template <typename T, bool kAligned, int TPR, int STEPS>
-__global__ void __launch_bounds__(norm_threads(TPR), sizeof(T) == 2 && (STEPS == 1 || STEPS == 2) ? 1536 / norm_threads(TPR) : 1)
+// TPR threads share a row (0: the block's, as many warps as the row needs; up to 64
+// have other rows beside them); each holds STEPS vectors of it (STEPS = 0: the row
+// is too long for registers and is read a second time, out of L2).  Few vectors a
+// thread and 1536 threads an SM keep the most bytes on their way: 65536 x 4096 bf16
+// to all four outputs 346 us (the copy rate), 380 without the bound on registers,
+// 406 with the weights read behind the sum; 16384 x 5120 115 us, 169 with threads
+// in powers of two.  Rows of four vectors a thread leave an SM one block, which
+// goes on to other rows (LOOP) with their loads on the way while it works on the
+// one before: 8192 x 12288 to one output 84 us, 127 a block for each row; with two
+// vectors the registers for that cost more than it gives (65536 x 4096: 386).
+constexpr int norm_blocks(int esz, int steps) {   // of 512 threads an SM, at least
+    return steps == 0 || steps > 2 ? 1 : esz == 2 ? 3 : 2;
+}
+template <typename T, bool kAligned, int TPR, int STEPS, bool LOOP>
+__global__ void __launch_bounds__(512, norm_blocks(sizeof(T), STEPS))
 kda_rms_norm_kernel(NormArgs a) {
-    constexpr int kThreads = norm_threads(TPR);
-    constexpr int kRows = kThreads / TPR;
-    constexpr int kWarpsPerRow = TPR / 32;
-    const int t = threadIdx.x % TPR;
-    const int64_t row_of = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool real = row_of < a.rows;                   // whole warps, since TPR >= 32
-    const int64_t row = real ? row_of : a.rows - 1;
+    constexpr int ROWS = TPR && TPR < 128 ? 128 / TPR : 1;
+    constexpr int kWarps = TPR ? TPR / 32 : STEPS == 1 ? 8 : 16;     // of a row at most
+    const int tpr = TPR ? TPR : blockDim.x, t = ROWS > 1 ? threadIdx.x % tpr : threadIdx.x, warps = tpr / 32;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t row_of = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / tpr : 0);
+    __shared__ float part[2][16];
+    constexpr int kHeld = STEPS > 0 ? STEPS : 1;
+    Raw8<T> w[kHeld], x[kHeld], r[kHeld];
+    if constexpr (STEPS > 0) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+            norm_load8<T, kAligned>(a, row_of < a.rows ? row_of : a.rows - 1, norm_element<kAligned>(k, tpr, t), x[k], r[k]);
+        if (a.w) {                                       // on their way while the row is summed
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) w[k] = load8<T, kAligned>((const T*)a.w, norm_element<kAligned>(k, tpr, t), a.dim);
+        }
+    }
+    // whole warps have a row or none; all of a block's go round together
+    for (int64_t first = (int64_t)blockIdx.x * ROWS, turn = 0; first < a.rows; first += step, row_of += step, turn ^= 1) {
+        const bool real = row_of < a.rows;
+        const int64_t row = real ? row_of : a.rows - 1;
+        Vec8 h[kHeld];
+        float ss = 0.f;
+        if constexpr (STEPS > 0) {
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k)
+                h[k] = norm_add8<T, kAligned>(a, row, norm_element<kAligned>(k, tpr, t), real, x[k], r[k]);
+            if (LOOP && row_of + step < a.rows) {
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k)
+                    norm_load8<T, kAligned>(a, row_of + step, norm_element<kAligned>(k, tpr, t), x[k], r[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+                for (int i = 0; i < kNormVec; ++i) ss += h[k].v[i] * h[k].v[i];
+        } else {
+            for (int k = 0; k * tpr * kNormVec < a.dim; ++k) {
+                const int e = norm_element<kAligned>(k, tpr, t);
+                norm_load8<T, kAligned>(a, row, e, x[0], r[0]);
+                const Vec8 y = norm_add8<T, kAligned>(a, row, e, false, x[0], r[0]);
+#pragma unroll
+                for (int i = 0; i < kNormVec; ++i) ss += y.v[i] * y.v[i];
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if constexpr (kWarps > 1) {                      // (two rounds' sums: nobody is further ahead)
+            if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = ss;
+            __syncthreads();
+            const int w0 = ROWS > 1 ? threadIdx.x / tpr * kWarps : 0;
+            ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float p = part[turn][w0 + i];
+                ss += TPR || i < warps ? p : 0.f;
+            }
+        }
+        if (real) {
+            const float rstd = 1.f / sqrtf(ss / (float)a.dim + a.eps);
+            if constexpr (STEPS > 0) {
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k)
+                    norm_out8<T, kAligned>(a, row, norm_element<kAligned>(k, tpr, t), h[k], w[k], rstd);
+            } else {
+                // residual_out may be x or residual: each element is read (again) before it is written, by its thread
+                for (int k = 0; k * tpr * kNormVec < a.dim; ++k) {
+                    const int e = norm_element<kAligned>(k, tpr, t);
+                    if (a.w) w[0] = load8<T, kAligned>((const T*)a.w, e, a.dim);
+                    norm_load8<T, kAligned>(a, row, e, x[0], r[0]);
+                    norm_out8<T, kAligned>(a, row, e, norm_add8<T, kAligned>(a, row, e, true, x[0], r[0]), w[0], rstd);
+                }
+            }
+        }
+        if (!LOOP) break;
+    }
+}
 
-    Vec8 h[STEPS > 0 ? STEPS : 1];
-    Raw8<T> w[STEPS > 0 ? STEPS : 1];                    // on its way while the row is summed
-    float ss = 0.f;
-    if constexpr (STEPS > 0) {
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-            h[k] = norm_sum8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), real);
-        if (a.w) {
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) w[k] = load8<T, kAligned>((const T*)a.w, norm_element<kAligned>(k, TPR, t), a.dim);
+template <typename T, bool kAligned, int TPR, int STEPS, bool LOOP>
+static cudaError_t launch_rows(const NormArgs& a, int threads, cudaStream_t stream) {
+    auto kern = kda_rms_norm_kernel<T, kAligned, TPR, STEPS, LOOP>;
+    constexpr int rows = TPR && TPR < 128 ? 128 / TPR : 1;
+    int64_t blocks = (a.rows + rows - 1) / rows;
+    if (LOOP) {
+        static int resident[17] = {};                    // blocks of so many warps on an SM: a property of device and kernel
+        int& n = resident[threads / 32];
+        if (!n) {
+            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0);
+            if (e != cudaSuccess) { n = 0; return e; }
         }
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-            for (int i = 0; i < kNormVec; ++i) ss += h[k].v[i] * h[k].v[i];
-    } else {
-        for (int k = 0; k * TPR * kNormVec < a.dim; ++k) {
-            const Vec8 x = norm_sum8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), false);
-#pragma unroll
-            for (int i = 0; i < kNormVec; ++i) ss += x.v[i] * x.v[i];
-        }
+        blocks = min64(blocks, (int64_t)n * 152);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if constexpr (kWarpsPerRow > 1) {
-        __shared__ float part[kThreads / 32];
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        const int w0 = threadIdx.x / TPR * kWarpsPerRow;
-        ss = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarpsPerRow; ++w) ss += part[w0 + w];
-    }
-    if (!real) return;
-    const float rstd = 1.f / sqrtf(ss / (float)a.dim + a.eps);
-    if constexpr (STEPS > 0) {
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) norm_out8<T, kAligned>(a, row, norm_element<kAligned>(k, TPR, t), h[k], w[k], rstd);
-    } else {
-        // residual_out may be x or residual: each element is read (again) before it is written, by its thread
-        for (int k = 0; k * TPR * kNormVec < a.dim; ++k) {
-            const int e = norm_element<kAligned>(k, TPR, t);
-            if (a.w) w[0] = load8<T, kAligned>((const T*)a.w, e, a.dim);
-            norm_out8<T, kAligned>(a, row, e, norm_sum8<T, kAligned>(a, row, e, true), w[0], rstd);
-        }
-    }
+    kern<<<(unsigned)blocks, threads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T, bool kAligned>
 static cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
     const int steps = (a.dim + kNormVec - 1) / kNormVec;    // vectors of a row
-#define KDA_NORM(tpr, per)                                                                            \
-    do {                                                                                              \
-        constexpr int th = norm_threads(tpr);                                                     \
-        const int64_t blocks = (a.rows + th / tpr - 1) / (th / tpr);                                  \
-        kda_rms_norm_kernel<T, kAligned, tpr, per><<<(unsigned)blocks, th, 0, stream>>>(a);           \
-        return cudaGetLastError();                                                                    \
-    } while (0)
-    if (steps <= 32) KDA_NORM(32, 1);
-    if (steps <= 64) KDA_NORM(64, 1);
-    if (steps <= 128) KDA_NORM(128, 1);
-    if (steps <= 256) KDA_NORM(256, 1);
-    if (steps <= 512) KDA_NORM(256, 2);
-    if (steps <= 1024) KDA_NORM(512, 2);
-    if (steps <= 2048) KDA_NORM(512, 4);
-    KDA_NORM(512, 0);
-#undef KDA_NORM
+    if (steps <= 32) return launch_rows<T, kAligned, 32, 1, false>(a, 128, stream);
+    if (steps <= 64) return launch_rows<T, kAligned, 64, 1, false>(a, 128, stream);
+    const int warps1 = (steps + 31) / 32, warps2 = (steps + 63) / 64, warps4 = (steps + 127) / 128;
+    if (warps1 == 4) return launch_rows<T, kAligned, 128, 1, false>(a, 128, stream);
+    if (warps1 == 8) return launch_rows<T, kAligned, 256, 1, false>(a, 256, stream);
+    if (warps1 < 8) return launch_rows<T, kAligned, 0, 1, false>(a, 32 * warps1, stream);
+    if (warps2 <= 16) return launch_rows<T, kAligned, 0, 2, false>(a, 32 * warps2, stream);
+    if (warps4 <= 16) return launch_rows<T, kAligned, 0, 4, true>(a, 32 * warps4, stream);
+    return launch_rows<T, kAligned, 0, 0, false>(a, 512, stream);
 }
 
 cudaError_t rms_norm_launch(const kda_norm_desc& d, const void* x, const void* weight, const void* residual,
