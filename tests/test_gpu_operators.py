@@ -75,6 +75,19 @@ def test_norm(kda, dtype, tokens, dim):
     check_norm(kda, x, w, None, True, False)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,dim", [(40, 1100), (40, 2560), (17, 4305), (21, 6592), (500, 8200), (700, 9001), (500, 16384)])
+def test_norm_of_rows_between_powers_of_two_and_blocks_with_several_rows(kda, dtype, tokens, dim):
+    x = normal(31, tokens, dim, dtype=dtype).cuda()
+    r = normal(32, tokens, dim, dtype=dtype, scale=3).cuda()
+    w = (1 + normal(33, dim, scale=0.2)).to(dtype).cuda()
+    y, q, s, h = check_norm(kda, x, w, r, True, True)
+    check_norm(kda, x, None, None, False, True)
+    again = kda.rms_norm(x, w, r, quantize=True, residual_out=x)          # in place of its own input
+    assert torch.equal(again[0], y) and torch.equal(again[1].view(torch.uint8), q.view(torch.uint8))
+    assert torch.equal(again[2], s) and torch.equal(x, h)
+
+
 def test_norm_shapes_strides_and_updates_in_place(kda):
     wide = normal(4, 9, 1000, dtype=BF16).cuda()
     x, r = wide[:, 8:520], wide[:, 488:1000]              # 16-byte rows that are not dense
