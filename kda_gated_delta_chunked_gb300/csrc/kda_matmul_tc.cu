@@ -159,7 +159,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 // The first warpgroup's columns 0 .. 63, then the second's 64 .. 127, each in 32 KB that lie there for
                 // the output too: pairs of columns, a row's threads beside each other.
                 f32x2* turn = (f32x2*)(raw + (base - smem_u32(raw)) + kStages * S::kStage) + quarter * 32 + lane;
-                if (sizeof(T) == 2 && use_map_c && threadIdx.x % 128 == 0) bulk_wait_read_all();
+                if (use_map_c && threadIdx.x % 128 == 0) bulk_wait_read_all();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     asm volatile("bar.sync 3, 256;" ::: "memory");
@@ -175,28 +175,43 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
                 asm volatile("bar.sync 3, 256;" ::: "memory");
             }
-            if (sizeof(T) == 2 && use_map_c) {
+            if (use_map_c) {
                 // Through shared memory and out by TMA: the stores of all SMs' tiles come at once, and the
-                // next tile's products need not wait for them.  Boxes of 64 columns, 128-byte swizzle.
+                // next tile's products need not wait for them.  Boxes of 128 bytes by 128 rows, 128-byte swizzle.
                 const uint32_t own = base + kStages * S::kStage + half * (S::kOut / 2);
                 const int r = quarter * 32 + lane;
+                constexpr int kBox = 128 / sizeof(T), kBoxes = S::kOut / 2 / 16384;   // columns; boxes at a time
 #pragma unroll
-                for (int c0 = 0; c0 < kOutCols; c0 += 64) {
-                    if (c0 == 0) {
+                for (int c0 = 0; c0 < kOutCols; c0 += kBox) {
+                    const uint32_t box = own + c0 / kBox % kBoxes * 16384;
+                    if (c0 / kBox % kBoxes == 0) {
                         if (threadIdx.x % 128 == 0) bulk_wait_read_all();
                         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
                     }
 #pragma unroll
-                    for (int c = 0; c < 64; c += 8) {
+                    for (int c = 0; c < kBox; c += 16 / sizeof(T)) {
                         const f32x2* v = acc + (c0 + c) / 2;
-                        const uint32_t at = own + c0 / 64 * 16384 + r * 128 + ((c / 8) ^ (r & 7)) * 16;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(bf16x2(v[0])),
-                                     "r"(bf16x2(v[1])), "r"(bf16x2(v[2])), "r"(bf16x2(v[3])) : "memory");
+                        const uint32_t at = box + r * 128 + (c * (int)sizeof(T) / 16 ^ (r & 7)) * 16;
+                        uint32_t w[4];
+                        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = bf16x2(v[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float lo, hi;
+                                unpack2(v[i], lo, hi);
+                                w[2 * i] = __float_as_uint(lo);
+                                w[2 * i + 1] = __float_as_uint(hi);
+                            }
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                                     "r"(w[3]) : "memory");
                     }
                     fence_proxy_async_smem();
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
                     if (threadIdx.x % 128 == 0 && col + c0 < g.n) {
-                        tma_store_2d(&map_c, own + c0 / 64 * 16384, col + c0, tm * 256 + rank * 128);
+                        tma_store_2d(&map_c, box, col + c0, tm * 256 + rank * 128);
                         bulk_commit();
                     }
                 }
@@ -237,7 +252,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
             }
         }
-        if (sizeof(T) == 2 && use_map_c && threadIdx.x % 128 == 0) bulk_wait_all();
+        if (use_map_c && threadIdx.x % 128 == 0) bulk_wait_all();
     } else {
         regs_dec<40>();
         if (warp == kMmEpiWarps || warp == kMmEpiWarps + 3) {      // producers: of even blocks, of odd ones
@@ -499,11 +514,12 @@ static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     // c by TMA where its rows start on 16-byte boundaries
     CUtensorMap mc = ma;
-    const bool use_mc = sizeof(T) == 2 && (((uintptr_t)a.c | (uintptr_t)(a.ldc * 2)) & 15) == 0 && a.ldc < (1ll << 38);
+    const bool use_mc = (((uintptr_t)a.c | (uintptr_t)(a.ldc * sizeof(T))) & 15) == 0 && a.ldc < (1ll << 37);
     if (use_mc) {
-        const uint64_t dims[2] = {(uint64_t)a.n, (uint64_t)a.m}, strides[1] = {(uint64_t)a.ldc * 2};
-        const uint32_t box[2] = {64, 128};
-        if (!make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims, strides, box)) return cudaErrorInvalidValue;
+        const uint64_t dims[2] = {(uint64_t)a.n, (uint64_t)a.m}, strides[1] = {(uint64_t)a.ldc * sizeof(T)};
+        const uint32_t box[2] = {128 / sizeof(T), 128};
+        if (!make_map(&mc, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.c, dims,
+                      strides, box)) return cudaErrorInvalidValue;
     }
     const int tm = (int)((a.m + 255) / 256), tn = (a.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)tm * tn;
