@@ -236,9 +236,11 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     }
                     __syncwarp();
                     const int n = col + (w0 + lane) * kPer;
-                    for (int r = 0; r < 32 && row - lane + r < g.m; ++r) {
+                    const int rows = (int)min64(32, g.m - (row - lane));
+                    T* to = (T*)g.c + (row - lane) * g.ldc + n;
+#pragma unroll 4
+                    for (int r = 0; r < rows; ++r, to += g.ldc) {
                         const uint32_t word = own[r * 32 + (lane ^ r)];
-                        T* to = (T*)g.c + (row - lane + r) * g.ldc + n;
                         if constexpr (kPer == 1) {
                             if (n < g.n) *(uint32_t*)to = word;
                         } else if (n + 1 < g.n && ((uintptr_t)to & 3) == 0) {
