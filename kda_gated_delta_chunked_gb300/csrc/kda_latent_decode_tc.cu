@@ -80,7 +80,6 @@ struct LdArgs {
     float* parts;                              // [groups * G][2][R][kLdPart]
     int64_t* before;                           // [N + 1] tiles ahead of a sequence (where it has tiles); all tiles
     int G;                                     // CTAs of a group
-    int early;                                 // whether the joining kernel starts with this one or behind it
 };
 constexpr int kLdPart = kLdRank + 4;           // O, ref, sum (rows stay 16-byte aligned)
 
@@ -164,7 +163,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
-    if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 4) {
         // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
         // warps wait for it at the barrier.
@@ -541,7 +539,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (!a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) tmem_dealloc(tmem, S::kTmem);
     if (threadIdx.x == 0) a.cta_status[cta * gridDim.x + group] = *fault;
 }
@@ -682,8 +680,6 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
         ready = true;
     }
     LdArgs a;
-    const bool many = (int64_t)d.N * d.Lq * d.H >= 512;
-    a.early = !many;
     a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
     a.max_pages = d.max_pages; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
@@ -706,14 +702,17 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
+    // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many; 16 x 2048, 16 heads:
+    // 21 us, 17 as for many).
+    const bool many = (int64_t)d.N * a.rows >= 256;
     const int warps = many ? 2 : 16, per = many ? 4 : 1;
     cfg.gridDim = dim3(d.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
     cfg.dynamicSmemBytes = warps * 128 * per * 4;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    // Few blocks start with the kernel before (0.5 us less); many would take from it, and start as its last CTAs end
-    // (128 x 1024 tokens, 16 heads: 56 us behind it, 52 so).
+    // It starts as the last CTAs of the kernel before end (128 x 1024 tokens, 16 heads: 56 us behind them, 52 so);
+    // started with them, its waiting blocks take from it (4 queries x 30000 tokens, 16 heads: 29 us, 26 so).
     cfg.attrs = at; cfg.numAttrs = 1;
     return many ? cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 4>, a, p.groups)
                 : cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 1>, a, p.groups);
