@@ -153,8 +153,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     uint64_t *full = bars, *empty = full + S::kSlots,              // first the slots for S^T, then those for O^T
              *full_v = full + S::kSlotsS, *empty_v = empty + S::kSlotsS, *q_full = empty + S::kSlots, *q_empty = q_full + 1,
              *s_full = q_empty + 1, *o_full = s_full + 2,          // [2]: alternate tiles
-             *begun = o_full + 2,                                  // the first tile's scores, once
-             *p_full = begun + 1, *zeroed = p_full + 2,            // zeroed [4]: a pair of pieces each
+             *p_full = o_full + 2, *zeroed = p_full + 2,            // zeroed [4]: a pair of pieces each
              *bars_end = zeroed + 4;
     uint32_t* tmem_at = (uint32_t*)bars_end;
     int* range = (int*)(tmem_at + 1);                  // first sequence, its first tile, tiles
@@ -255,8 +254,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         bool ok = true, bad_page = false;
         LdWalk w;
         w.start(a, range[0], range[1], range[2]);
-        // At the start all SMs ask at once: the first tile's scores go first, then the same channels come from L2.
-        if (!scores && w.left > 0) ok = mbar_wait_warp(begun, 0);
         for (; w.left > 0 && ok; w.next(a)) {
             if (scores && w.first) {
                 if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
@@ -324,7 +321,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     mma_commit(&empty[s]);
                     if (u == S::kUnits - 1) {
                         mma_commit(&s_full[j & 1]);
-                        if (j == 0) mma_commit(begun);
                         if (w.last()) mma_commit(q_empty);
                     }
                 }
