@@ -26,9 +26,10 @@ __device__ __forceinline__ float warp_sum(float x) {
 template <int VC>
 __device__ __forceinline__ void online_step(float s, float& m, float& l, float (&o)[VC], const float (&v)[VC]) {
     const float mn = fmaxf(m, s);
-    // a row of -infinity so far keeps weight 0 instead of exp(-inf + inf)
+    // -infinity hides a key, also before the first finite score, where m is -infinity too (exp(-inf + inf)); a score
+    // that is no number, which the maximum leaves out, makes the row one that is none
     const float keep = m == mn ? 1.f : expf(m - mn);
-    const float p = mn == -INFINITY ? 0.f : expf(s - mn);
+    const float p = s == -INFINITY ? 0.f : expf(s - mn);
     m = mn;
     l = l * keep + p;
 #pragma unroll

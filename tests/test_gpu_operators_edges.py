@@ -1,0 +1,85 @@
+"""Norm, scaled 8-bit product and latent attention where a call is unusual: values
+that are no numbers, waits that run out, calls without work, other contexts and
+streams."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_operators import BF16, F32, expanded, kda, normal, paged  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def lengths(*l):
+    return torch.tensor(l, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ values that are no numbers
+# Nothing here is a question of rounding: a row with a score that is no number has no numbers in it, every other row
+# keeps its bits.
+FORMS = [(BF16, False), (BF16, True), (F32, True)]          # tensor cores, CUDA cores, CUDA cores
+
+
+@pytest.mark.parametrize("dtype,simt", FORMS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("at", [0, 1, 5, 63, 99])
+def test_prefill_nan_scores_reach_the_rows_that_see_them(kda, dtype, simt, causal, at):  # noqa: F811
+    n, flags = 100, kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0
+    q, kn, kr, v = (t.cuda() for t in expanded(n, n, 2, dtype=dtype, seed=41))
+    go = lambda: kda.latent_prefill(q, kn, kr, v, scale=192 ** -0.5, causal=causal, flags=flags)  # noqa: E731
+    out, lse = go()
+    keep = kn.clone()
+    kn = kn.clone()
+    kn[at, 1] = NAN                                          # a key of one head
+    o, l = go()
+    seen = torch.arange(n, device="cuda") >= (at if causal else 0)
+    assert torch.isnan(o[seen, 1]).all() and torch.isnan(l[seen, 1]).all()
+    assert torch.equal(o[~seen], out[~seen]) and torch.equal(l[~seen], lse[~seen])
+    assert torch.equal(o[:, 0], out[:, 0]) and torch.equal(l[:, 0], lse[:, 0])
+    kn, q = keep, q.clone()
+    q[at, 0, 3] = NAN                                        # a query: all its scores
+    o, l = go()
+    assert torch.isnan(o[at, 0]).all() and torch.isnan(l[at, 0])
+    o[at, 0], l[at, 0] = out[at, 0], lse[at, 0]
+    assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("dtype,simt", FORMS)
+@pytest.mark.parametrize("length,at", [(1, 0), (300, 0), (300, 1), (300, 2), (300, 3), (300, 130), (300, 299)])
+def test_decode_nan_scores_reach_the_rows_that_see_them(kda, dtype, simt, length, at):  # noqa: F811
+    flags = kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0
+    cache, table, _ = paged([length, 70], 64, 576, dtype, 43)
+    q = normal(44, 2, 1, 16, 576, dtype=dtype).cuda()
+    go = lambda: kda.latent_decode(q, cache, table, lengths(length, 70), scale=192 ** -0.5, flags=flags)  # noqa: E731
+    out, lse = go()
+    keep = cache.clone()
+    cache[int(table[0, at // 64]), at % 64, 570] = NAN       # a rotary channel: no value has it
+    o, l = go()
+    assert torch.isnan(o[0]).all() and torch.isnan(l[0]).all()
+    assert torch.equal(o[1], out[1]) and torch.equal(l[1], lse[1])
+    cache, q = keep, q.clone()
+    q[0, 0, 7, 0] = NAN
+    o, l = go()
+    assert torch.isnan(o[0, 0, 7]).all() and torch.isnan(l[0, 0, 7])
+    o[0, 0, 7], l[0, 0, 7] = out[0, 0, 7], lse[0, 0, 7]
+    assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("dtype,simt", FORMS)
+def test_scores_of_minus_infinity_hide_and_of_plus_infinity_spoil(kda, dtype, simt):  # noqa: F811
+    flags = kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0
+    q, kn, kr, v = (t.cuda() for t in expanded(40, 40, 1, dtype=dtype, seed=45))
+    q, kr = q.abs() + 0.01, torch.zeros_like(kr)
+    kn = torch.zeros_like(kn)
+    kn[:3] = -INF
+    out, lse = kda.latent_prefill(q, kn, kr, v, scale=0.1, flags=flags)
+    assert (out[:3] == 0).all() and (lse[:3] == -INF).all() and torch.isfinite(out[3:].float()).all()
+    # the scores behind are zeros: equal weights, and the log of their number to fp32's rounding of one logarithm
+    want = torch.log(torch.arange(1, 38, device="cuda", dtype=torch.float64))
+    assert float((lse[3:, 0].double() - want).abs().max()) < 2.0 ** -20
+    kn[10] = INF
+    out, lse = kda.latent_prefill(q, kn, kr, v, scale=0.1, flags=flags)
+    assert (out[:3] == 0).all() and torch.isfinite(out[3:10].float()).all() and torch.isnan(out[10:].float()).all()
