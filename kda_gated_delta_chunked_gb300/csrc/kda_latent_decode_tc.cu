@@ -330,6 +330,24 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
     } else if (warp == 7) {                                            // ---------------- O^T += V^T P^T
+        if (group == 0) {
+            // Where the sequences that start in this range lie among all tiles.  The join takes its pieces by it, so it is
+            // written before anything that may give up.
+            const int64_t begin = *range_at, end = begin + range[2];
+            int64_t at = begin - range[1];
+            for (int b = range[0]; at < end && b < a.N; b += 32) {
+                const int t = b + lane < a.N ? ld_tiles(a, b + lane) : 0;
+                int x = t;                                             // inclusive scan
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                const int64_t first = at + x - t;
+                if (t > 0 && first >= begin && first < end) a.before[b + lane] = first;
+                at += __shfl_sync(0xffffffffu, x, 31);
+            }
+        }
         const uint32_t idesc = idesc_bf16(128, R, 1, 1);
         uint32_t s = 0, ph = 0, zero = 0;
         bool ok = true;
@@ -373,7 +391,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         w.start(a, range[0], range[1], range[2]);
         const int count = w.left;
         for (int j = 0; j < count; ++j, w.next(a)) {
-            if (w.first && w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
             ok = bar_and(128, mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
@@ -574,6 +591,8 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
             cl = (int)(((before + tiles) * parts - 1) / total);
         }
         if (cf == cl) return;                          // finished by its CTA
+        cf = max(cf, 0);                               // (no piece is looked for outside, also if the lengths changed meanwhile)
+        cl = min(cl, a.G - 1);
     }
     const int group = row / R, c = row % R;
     auto piece = [&](int i) {

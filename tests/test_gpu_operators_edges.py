@@ -83,3 +83,21 @@ def test_scores_of_minus_infinity_hide_and_of_plus_infinity_spoil(kda, dtype, si
     kn[10] = INF
     out, lse = kda.latent_prefill(q, kn, kr, v, scale=0.1, flags=flags)
     assert (out[:3] == 0).all() and torch.isfinite(out[3:10].float()).all() and torch.isnan(out[10:].float()).all()
+
+
+# ------------------------------------------------------------------ what a workspace held, waits that run out
+@pytest.mark.parametrize("lens,lq,h", [([5000], 1, 16), ([0, 0, 9000, 0, 1, 20000, 0], 2, 16), ([n % 3 * 70 for n in range(3001)], 1, 16),
+                                       ([0] * 500 + [40000] + [0] * 500 + [1], 1, 32), ([0] * 70, 1, 16), ([3000, 129, 5000], 1, 100)])
+def test_decode_does_not_depend_on_what_its_workspace_held(kda, lens, lq, h):  # noqa: F811
+    cache, table, _ = paged(lens, 64, 576, BF16, 61)
+    q = normal(62, len(lens), lq, h, 576, dtype=BF16).cuda()
+    n = kda.latent_decode_workspace_bytes(len(lens), lq, h, 512, 64, BF16, 64, table.shape[1])
+    go = lambda fill: kda.latent_decode(q, cache, table, lengths(*lens), scale=0.07,  # noqa: E731
+                                        workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+    out, lse = go(0)
+    for fill in (0x7F, 0xFF):
+        o, l = go(fill)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    simt, slse = kda.latent_decode(q, cache, table, lengths(*lens), scale=0.07, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL)
+    some = torch.isfinite(slse)
+    assert torch.equal(torch.isfinite(lse), some) and (not some.any() or float((lse - slse)[some].abs().max()) < 1e-4)
