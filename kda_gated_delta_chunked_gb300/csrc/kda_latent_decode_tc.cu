@@ -391,7 +391,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         w.start(a, range[0], range[1], range[2]);
         const int count = w.left;
         for (int j = 0; j < count; ++j, w.next(a)) {
-            ok = bar_and(128, mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
+            // (a wait of one warp that gave up ends the loop here, for all four: they meet at barriers)
+            ok = bar_and(128, ok && mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t at_s = lanes + (j & 1) * R;
@@ -455,7 +456,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (j >= S::kBufP) {                                       // P's buffer: the products that read it are complete
                 const int before = j - S::kBufP;
                 ok = mbar_wait_warp(&o_full[before & 1], (before >> 1) & 1);
-                if (!ok) break;
             }
 #pragma unroll
             for (int c = 0; c < R; c += 8) {
@@ -475,14 +475,14 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[j & 1]);
+            if (ok && lane == 0) mbar_arrive(&p_full[j & 1]);      // (nobody is told of P after a wait that gave up)
             // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes (once the
             // products of the tile before are complete, the ring is at this tile's).
-            if ((w.j + 1) * kLdTile > len) {
+            if (ok && (w.j + 1) * kLdTile > len) {
                 if (j > 0) ok = mbar_wait_warp(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
                 for (int p = 0; p < 4 && ok; ++p) {
                     const uint32_t u = 4 * j + p, s = u % S::kSlotsV;
-                    ok = mbar_wait_warp(&full_v[s], (u / S::kSlotsV) & 1);
+                    if (!(ok = mbar_wait_warp(&full_v[s], (u / S::kSlotsV) & 1))) break;
                     uint8_t* at = mem + S::kOffV + s * S::kSlotV + threadIdx.x % 8 * 16;
                     for (int r = len - w.j * kLdTile + (int)threadIdx.x / 8; r < kLdTile; r += 16) {
                         *(uint4*)(at + r / 8 * 2048 + r % 8 * 128) = make_uint4(0, 0, 0, 0);
