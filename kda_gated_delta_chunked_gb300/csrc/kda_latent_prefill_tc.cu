@@ -90,12 +90,13 @@ struct LpRing {
 
 // Among the 256 threads of a tile's softmax.
 __device__ __forceinline__ void tile_sync(int i) { asm volatile("bar.sync %0, 256;" ::"r"(1 + i) : "memory"); }
-__device__ __forceinline__ bool tile_and(int i, bool v) {
+__device__ __forceinline__ bool barrier_and(int id, int threads, bool v) {
     uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.and.pred p, %2, 256, q;\n selp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + i) : "memory");
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.and.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r) : "r"((uint32_t)v), "r"(id), "r"(threads) : "memory");
     return r;
 }
+__device__ __forceinline__ bool tile_and(int i, bool v) { return barrier_and(1 + i, 256, v); }
 
 template <bool SHARED>
 __global__ void __launch_bounds__(kLpThreads, 1)
@@ -152,8 +153,14 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         LpRing<kLpSlotsV> v_ring;
         uint32_t tile0 = 0, outs = 0;                                  // this tile's steps and results so far
         for (uint32_t it = 0; ok; ++it) {
+            // All who meet at barriers further down leave here together, if one of them gave up: a tile's warps, and where
+            // parts are joined both tiles'.
             ok = mbar_wait_warp(&item_full[it & 1], it >> 1 & 1);
-            if (!ok) break;
+            ok = SHARED ? barrier_and(3, 32 * kLpSoftmax, ok) : tile_and(i, ok);
+            if (!ok) {
+                record_status(a.status, KDA_ERR_TIMEOUT);
+                break;
+            }
             const LpItem& item = items[it & 1];
             if (item.r0 < 0) break;
             const int mine = uniform(item.tiles[i]);
