@@ -48,6 +48,7 @@ constexpr uint32_t kLdPiece = kLdTile * 128;  // 64 channels of a tile
 constexpr int kLdThreads = 256;               // 4 softmax warps, 2 producers, a warp for each product
 constexpr float kLdUnset = -1e30f;            // reference of a row that has seen no key
 constexpr float kLdSlack = 8.f;               // how far (log2) a score may exceed its reference
+constexpr int kLdLate = 1, kLdBadLen = 2, kLdBadPage = 4;   // bits of a CTA's status
 
 template <int R>
 struct LdShape {
@@ -221,7 +222,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (lane == 0) {
             range[0] = n0; range[1] = j0; range[2] = (int)(t1 - t0);
             if (cta == 0 && group == 0) a.before[a.N] = total;
-            *fault = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+            *fault = bad ? kLdBadLen : 0;
             *range_at = t0;
         }
         __syncwarp();
@@ -289,8 +290,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (++s == slots) { s = 0; ph ^= 1; }
             }
         }
-        if (bad_page) atomicMax(fault, KDA_ERR_BAD_PAGE);
-        if (!ok) { atomicMax(fault, KDA_ERR_TIMEOUT); drain_copies(); }
+        if (bad_page) atomicOr(fault, kLdBadPage);
+        if (!ok) { atomicOr(fault, kLdLate); drain_copies(); }
     } else if (warp == 6) {                                            // ---------------- S^T
         const uint32_t idesc = idesc_bf16(128, R);
         const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
@@ -328,7 +329,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (++s == S::kSlotsS) { s = 0; ph ^= 1; }
             }
         }
-        if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
+        if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 7) {                                            // ---------------- O^T += V^T P^T
         if (group == 0) {
             // Where the sequences that start in this range lie among all tiles.  The join takes its pieces by it, so it is
@@ -378,7 +379,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
             zero += ragged;
         }
-        if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
+        if (!ok) atomicOr(fault, kLdLate);
     } else {                                                           // ---------------- softmax
         const uint32_t lanes = tmem_addr(tmem, 32 * warp, 0);
         const float sc = a.scale * 1.4426950408889634f;
@@ -548,7 +549,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int c = 0; c < R; ++c) l[c] = 0.f;
             asm volatile("bar.sync 2, 128;" ::: "memory");
         }
-        if (!ok) atomicMax(fault, KDA_ERR_TIMEOUT);
+        if (!ok) atomicOr(fault, kLdLate);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -571,14 +572,12 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     const int tiles = ld_tiles(a, n);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0 && row == 0 && blockIdx.z == 0) {
-        int bad_page = 0, bad_len = 0, late = 0;
-        for (int i = threadIdx.x; i < a.G * groups; i += blockDim.x) {
-            const int st = a.cta_status[i];
-            bad_page |= st == KDA_ERR_BAD_PAGE; bad_len |= st == KDA_ERR_BAD_SEQLENS; late |= st == KDA_ERR_TIMEOUT;
-        }
-        bad_page = __syncthreads_or(bad_page); bad_len = __syncthreads_or(bad_len); late = __syncthreads_or(late);
+        int st = 0;
+        for (int i = threadIdx.x; i < a.G * groups; i += blockDim.x) st |= a.cta_status[i];
+        const bool late = __syncthreads_or(st & kLdLate);          // leaves any output unspecified; the others their sequences'
+        const bool bad_page = __syncthreads_or(st & kLdBadPage), bad_len = __syncthreads_or(st & kLdBadLen);
         if (threadIdx.x == 0)
-            *a.status = bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : late ? KDA_ERR_TIMEOUT : KDA_OK;
+            *a.status = late ? KDA_ERR_TIMEOUT : bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : KDA_OK;
     }
     int cf = 0, cl = -1;
     if (tiles > 0) {

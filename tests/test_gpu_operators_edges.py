@@ -101,3 +101,19 @@ def test_decode_does_not_depend_on_what_its_workspace_held(kda, lens, lq, h):  #
     simt, slse = kda.latent_decode(q, cache, table, lengths(*lens), scale=0.07, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL)
     some = torch.isfinite(slse)
     assert torch.equal(torch.isfinite(lse), some) and (not some.any() or float((lse - slse)[some].abs().max()) < 1e-4)
+
+
+@pytest.mark.parametrize("simt", [False, True])
+def test_decode_reports_one_of_several_faults(kda, simt):  # noqa: F811
+    """A bad page and a bad length in one call: one of the two, and the sequences without a fault keep their bits."""
+    cache, table, _ = paged([300, 200, 70], 64, 576, BF16, 63)
+    q = normal(64, 3, 1, 16, 576, dtype=BF16).cuda()
+    ws = torch.zeros(kda.latent_decode_workspace_bytes(3, 1, 16, 512, 64, BF16, 64, table.shape[1]), dtype=torch.uint8, device="cuda")
+    go = lambda t, l: kda.latent_decode(q, cache, t, l, scale=0.07, workspace=ws, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0)[0]  # noqa: E731
+    want = go(table, lengths(300, 200, 70))
+    bad = table.clone()
+    bad[0, 1] = cache.shape[0]
+    out = go(bad, lengths(300, -5, 70))
+    assert kda.latent_status(ws) in (kda.KDA_ERR_BAD_PAGE, kda.KDA_ERR_BAD_SEQLENS)
+    assert torch.equal(out[2], want[2])
+    assert torch.equal(go(table, lengths(300, 200, 70)), want) and kda.latent_status(ws) == kda.KDA_OK
