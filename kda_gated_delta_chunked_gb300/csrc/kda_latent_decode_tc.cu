@@ -291,7 +291,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
-        if (!ok) { atomicOr(fault, kLdLate); drain_copies(); }
+        if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 6) {                                            // ---------------- S^T
         const uint32_t idesc = idesc_bf16(128, R);
         const uint64_t dq = sdesc_k_sw128(base + S::kOffQ);
@@ -552,7 +552,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (!ok) atomicOr(fault, kLdLate);
     }
     tc_fence_before_sync();
-    __syncthreads();
+    meet_at_end(fault);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) tmem_dealloc(tmem, S::kTmem);
     if (threadIdx.x == 0) a.cta_status[cta * gridDim.x + group] = *fault;

@@ -115,6 +115,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     uint64_t *item_full = o_full + 2, *item_empty = item_full + 2, *next = item_empty + 2, *answered = next + 1;
     uint64_t* rows_full = answered + 1;
     uint32_t* tmem_at = (uint32_t*)(rows_full + 1);
+    int* late = (int*)(tmem_at + 1);                           // a wait gave up
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int splits = SHARED ? a.splits : 1, rank = SHARED ? (int)blockIdx.x % splits : 0;   // of the rows' keys
@@ -124,6 +125,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
+        *late = 0;
         mbar_init(q_full, 1);
         mbar_init(rows_full, 1);
         mbar_init(next, 1);
@@ -243,7 +245,10 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 if (j == ragged && (i == 0 || j >= item.tiles[0])) {
                     const int piece = 2 * j + r / 64;
                     if (r >= item.lk % kLpKeys) {
-                        if (!mbar_wait_spin(&v_full[piece % kLpSlotsV], v_ring.parity(piece))) record_status(a.status, KDA_ERR_TIMEOUT);
+                        if (!mbar_wait_spin(&v_full[piece % kLpSlotsV], v_ring.parity(piece))) {
+                            record_status(a.status, KDA_ERR_TIMEOUT);
+                            *late = 1;
+                        }
                         uint8_t* at = mem + kLpOffV + piece % kLpSlotsV * kLpPiece + half * 8192 + r % 64 * 128;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) *(uint4*)(at + 16 * q) = make_uint4(0, 0, 0, 0);
@@ -318,6 +323,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         }
+        if (!ok) *late = 1;
     } else {
         regs_dec<32>();
         if (warp == kLpSoftmax || warp == kLpSoftmax + 3) {                                 // ---------------- producers: queries and keys, values
@@ -372,7 +378,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         v_ring.add(2 * steps);
                     }
                 }
-                if (!ok) drain_copies();
+                if (!ok) *late = 1;
             }
         } else if (warp == kLpSoftmax + 1) {
             // Matrix instructions.  One warp for both tiles keeps them in turn; whole products behind one wait
@@ -459,6 +465,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 tile0[1] += n1;
             }
             if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
+            if (!ok) *late = 1;
         } else if (warp == kLpSoftmax + 2) {                                       // ---------------- which rows
             // In groups of heads (whose keys and values then stay in L2), a sequence's last rows, which see most keys,
             // first, so that what runs last is short (8192 tokens, 32 heads: a tenth less than a head at a time).
@@ -559,8 +566,11 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 mbar_arrive(&item_full[it & 1]);
             }
             if (!ok && lane == 0) record_status(a.status, KDA_ERR_TIMEOUT);
+            if (!ok) *late = 1;
         }
     }
+    tc_fence_before_sync();
+    meet_at_end(late);
     if (SHARED) {
         // Each CTA joins a share of the rows: the others copy their parts of those behind its own, 64 KB in 3300
         // cycles with two CTAs.
@@ -618,8 +628,6 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
         __syncwarp();
         cluster_sync();                                                // the others may still read this CTA's rows
     }
-    tc_fence_before_sync();
-    __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

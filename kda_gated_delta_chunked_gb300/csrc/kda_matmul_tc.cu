@@ -58,10 +58,12 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint64_t* tfull = empty + kStages;             // [kBufs][kGroups] a group of a block's product is in TMEM
     uint64_t* tempty = tfull + kBufs * kGroups;    // [kBufs][kGroups] leader: the pair's epilogue warps have read it
     uint32_t* tmem_at = (uint32_t*)(tempty + kBufs * kGroups);
+    int* late = (int*)(tmem_at + 1);               // a wait gave up
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
+        *late = 0;
         for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], kMmEpiWarps); }
         fence_mbar_init();
@@ -255,6 +257,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             }
         }
         if (use_map_c && threadIdx.x % 128 == 0) bulk_wait_all();
+        if (!ok) *late = 1;
     } else {
         regs_dec<40>();
         if (warp == kMmEpiWarps || warp == kMmEpiWarps + 3) {      // producers: of even blocks, of odd ones
@@ -278,7 +281,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
                 __syncwarp();
             }
-            if (!ok) drain_copies();
+            if (!ok) *late = 1;
         } else if (warp <= kMmEpiWarps + 2) {
             // Matrix instructions, by the leader: a warp for even blocks and one for odd ones.  One alone needs about
             // 500 cycles for the waits, 4 instructions and the commits, as long as the instructions take.
@@ -310,11 +313,12 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         __syncwarp();
                     }
                 }
+                if (!ok) *late = 1;
             }
         }
     }
     tc_fence_before_sync();
-    __syncthreads();
+    meet_at_end(late);
     cluster_sync();                                                // the peer may still read or signal this CTA
     if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
@@ -348,6 +352,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint32_t* tmem_at = (uint32_t*)(tempty + 2);
+    int* late = (int*)(tmem_at + 1);                               // a wait gave up
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int splits = gridDim.x;                                  // = the cluster
@@ -356,6 +361,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const int kb = (g.k + 127) / 128;
     const int j0 = rank * blocks_per, count = max(0, min(kb, j0 + blocks_per) - j0);
     if (threadIdx.x == 0) {
+        *late = 0;
         for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 4); }
         fence_mbar_init();
@@ -381,7 +387,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 tma_load_2d(at, &map_b, (j0 + i) * 128, n0, bar);
                 tma_load_2d(at + S::kA, &map_a, (j0 + i) * 128, (int)m0, bar);
             }
-            if (!ok) drain_copies();
+            if (!ok) *late = 1;
         }
     } else if (warp == 5) {
         const uint32_t idesc = idesc_e4m3(128, BT);
@@ -402,6 +408,7 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             }
             __syncwarp();
         }
+        if (!ok) *late = 1;
     } else {
         // factors of the CTA's blocks: sa of every token times sb of the 128 rows of b
         const float* sb = g.sb + (int64_t)blockIdx.y * kb + j0;
@@ -443,10 +450,11 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 #pragma unroll
             for (int i = 0; i < BT; ++i) acc[i] = NAN;
         }
+        if (!ok) *late = 1;
     }
     // All copies have landed and all MMAs are done (their products were waited for): the stages become sums[t][r].
     tc_fence_before_sync();
-    __syncthreads();
+    meet_at_end(late);
     if (warp == 0) tmem_dealloc(tmem, S::kTmem);
     const int r = threadIdx.x;                                     // row of b within the tile
     if (splits == 1) {

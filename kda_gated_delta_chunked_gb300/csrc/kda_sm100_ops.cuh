@@ -111,10 +111,16 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
-// Waits a millisecond: after a wait that gave up, the block's own copies land.
-__device__ __forceinline__ void drain_copies() {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 1000000ull) {}
+// The block's threads meet, before it gives back what copies and matrix
+// instructions use.  Were all waits kept, none is under way any more; if one
+// gave up (bit 0 of `late`, in shared memory), they get a millisecond to end.
+__device__ __forceinline__ void meet_at_end(const int* late) {
+    __syncthreads();
+    if (*(const volatile int*)late & 1) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {}
+        __syncthreads();
+    }
 }
 
 // Registers of the calling warpgroup's threads (all its warps call it).  The
