@@ -267,6 +267,8 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 *shared = l;
             }
             ok = tile_and(i, ok && (mine == 0 || mbar_wait_spin(&o_full[i], outs & 1)));
+            // (where parts are joined the tiles stay together: neither goes on alone to the vote on the next rows)
+            if (SHARED) ok = barrier_and(3, 32 * kLpSoftmax, ok);
             if (half) l = *shared;
             tc_fence_after_sync();
             v_ring.add(2 * max(item.tiles[0], item.tiles[1]));
@@ -275,9 +277,8 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
             if (!ok) record_status(a.status, KDA_ERR_TIMEOUT);
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             if (SHARED) {
-                // This CTA's part to shared memory, once neither tile's products read there: [row][128] fp32 in 16-byte
+                // This CTA's part to shared memory, since neither tile's products read there now: [row][128] fp32 in 16-byte
                 // pieces turned by the row, and log2 of the rows' sums.
-                asm volatile("bar.sync 3, %0;" ::"n"(32 * kLpSoftmax) : "memory");
                 float4* part = (float4*)(mem + (i * 128 + r) * kLpRow);
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
