@@ -437,6 +437,14 @@ KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const 
  * unspecified. */
 KDA_API int kda_latent_status(const kda_latent_desc *desc, kda_stream_t stream);
 
+/* A test of the limits of waits: later calls of the process on the tensor cores
+ * wait for something that never comes, so their waits give up (2 s each, up to
+ * some seconds a call) and KDA_ERR_TIMEOUT is recorded, or NaN written
+ * (kda_matmul_fp8).  which: 1 the copies, 2 the first products, 3 the second
+ * ones, 4 the softmax weights, 5 what a block is to work on (the zeros behind a
+ * length, kda_latent_decode); 0 ends it.  kda_matmul_fp8 has 1 and 2. */
+KDA_API int kda_selftest_drop_arrival(int32_t which);
+
 /* Static, human-readable name of a status code. */
 KDA_API const char *kda_status_string(int status);
 

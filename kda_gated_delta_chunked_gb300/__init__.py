@@ -19,7 +19,7 @@ from ._binding import (  # noqa: F401
 )
 from ._operators import (  # noqa: F401
     KDA_FLAG_NO_CAUSAL, KdaNormDesc, KdaMatmulDesc, KdaLatentDesc,
-    kda_rms_norm, kda_matmul_fp8, kda_latent_prefill, kda_latent_decode, kda_latent_status,
+    kda_rms_norm, kda_matmul_fp8, kda_latent_prefill, kda_latent_decode, kda_latent_status, kda_selftest_drop_arrival,
     kda_latent_prefill_workspace_bytes, kda_latent_decode_workspace_bytes,
     rms_norm, matmul_fp8, latent_prefill, latent_decode, latent_status,
     latent_prefill_workspace_bytes, latent_decode_workspace_bytes,

@@ -21,7 +21,8 @@ EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step", "kda
            "kda_status_string", "kda_last_cuda_error", "kda_version", "kda_prefill_noalloc",
            "kda_selftest_wait_timeout", "kda_prefill_snapshots", "kda_backward_workspace_bytes",
            "kda_prefill_backward", "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes",
-           "kda_latent_decode_workspace_bytes", "kda_latent_prefill", "kda_latent_decode", "kda_latent_status")
+           "kda_latent_decode_workspace_bytes", "kda_latent_prefill", "kda_latent_decode", "kda_latent_status",
+           "kda_selftest_drop_arrival")
 KDA_PREFILL_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 

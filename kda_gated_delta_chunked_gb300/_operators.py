@@ -51,7 +51,8 @@ def _declare():
             ("kda_latent_decode_workspace_bytes", [ref(KdaLatentDesc)], ctypes.c_size_t),
             ("kda_latent_prefill", [ref(KdaLatentDesc)] + [vp] * 9, ctypes.c_int),
             ("kda_latent_decode", [ref(KdaLatentDesc)] + [vp] * 7, ctypes.c_int),
-            ("kda_latent_status", [ref(KdaLatentDesc), vp], ctypes.c_int)):
+            ("kda_latent_status", [ref(KdaLatentDesc), vp], ctypes.c_int),
+            ("kda_selftest_drop_arrival", [ctypes.c_int32], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 
@@ -117,6 +118,11 @@ def kda_latent_decode(desc: KdaLatentDesc, q, cache, page_table, lengths, out, l
 def kda_latent_status(desc: KdaLatentDesc, stream=None) -> int:
     """Device status word of the last latent call on the desc's workspace (synchronises the stream)."""
     return lib.kda_latent_status(_byref(desc), B._stream(stream))
+
+
+def kda_selftest_drop_arrival(which: int) -> int:
+    """Lets waits of later calls run out (1 .. 5, see include/kda.h); 0 ends it."""
+    return lib.kda_selftest_drop_arrival(which)
 
 
 # ------------------------------------------------------------------ operators

@@ -72,7 +72,7 @@ struct LdShape {
 };
 
 struct LdArgs {
-    int N, H, Lq, rows, page_size, num_pages, max_pages;
+    int N, H, Lq, rows, page_size, num_pages, max_pages, drop;
     float scale;
     const int32_t *table, *lens;
     __nv_bfloat16* out;
@@ -168,7 +168,12 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // warps wait for it at the barrier.
         const int64_t cap = (int64_t)a.max_pages * a.page_size;
         int len = lane < a.N ? a.lens[lane] : 0;                       // on its way while the barriers are made
-        if (lane < bars_end - bars) mbar_init(bars + lane, lane < p_full - bars ? 1 : 4);
+        if (lane < bars_end - bars) {
+            uint64_t* const bar = bars + lane;
+            const int of = bar < empty || bar == q_full ? kDropCopies : bar < s_full ? kDropNone : bar < o_full ? kDropProducts
+                         : bar < p_full ? kDropSecondProducts : bar < zeroed ? kDropWeights : kDropRows;
+            mbar_init(bar, (bar < p_full ? 1 : 4) + (a.drop != kDropNone && a.drop == of));
+        }
         if (lane == 0) {
             prefetch_map(&map_s);
             prefetch_map(&map_v);
@@ -695,7 +700,7 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     }
     LdArgs a;
     a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
-    a.max_pages = d.max_pages; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
+    a.max_pages = d.max_pages; a.drop = d.drop; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
     a.before = (int64_t*)((char*)d.scratch + p.before);
     a.parts = (float*)((char*)d.scratch + p.parts);

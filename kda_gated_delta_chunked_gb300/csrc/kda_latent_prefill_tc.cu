@@ -59,7 +59,7 @@ constexpr int kLpHeads = 8;                   // heads of a group
 constexpr float kLpUnset = -1e30f, kLpSlack = 8.f;
 
 struct LpArgs {
-    int N, H, causal, blocks, splits;          // blocks: tiles of rows of a head at most; splits: CTAs that share them
+    int N, H, causal, blocks, splits, drop;    // blocks: tiles of rows of a head at most; splits: CTAs that share them
     float scale;
     int64_t tq, tk;
     const int32_t *cu_q, *cu_k;
@@ -126,15 +126,19 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
     }
     if (threadIdx.x == 0) {
         *late = 0;
-        mbar_init(q_full, 1);
+        const int more = a.drop == kDropCopies;
+        mbar_init(q_full, 1 + more);
         mbar_init(rows_full, 1);
         mbar_init(next, 1);
         mbar_init(answered, 1);
         mbar_init(q_empty, 1);
-        for (int i = 0; i < 2 * (kLpSlotsK + kLpSlotsV); ++i) mbar_init(k_full + i, 1);
+        for (int i = 0; i < kLpSlotsK; ++i) { mbar_init(&k_full[i], 1 + more); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < kLpSlotsV; ++i) { mbar_init(&v_full[i], 1 + more); mbar_init(&v_empty[i], 1); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], kLpSoftmax / 2); mbar_init(&o_full[i], 1);
-            mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], kLpSoftmax + 3);
+            mbar_init(&s_full[i], 1 + (a.drop == kDropProducts));
+            mbar_init(&p_full[i], kLpSoftmax / 2 + (a.drop == kDropWeights));
+            mbar_init(&o_full[i], 1 + (a.drop == kDropSecondProducts));
+            mbar_init(&item_full[i], 1 + (a.drop == kDropRows)); mbar_init(&item_empty[i], kLpSoftmax + 3);
         }
         fence_mbar_init();
     }
@@ -547,7 +551,7 @@ kda_latent_prefill_tc(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 if (SHARED) break;
                 if (tile >= 0) {                                       // as long as the rows take: for all keys that fit
-                    if (!(ok = mbar_wait_idle(next, (it - 1) & 1))) break;
+                    if (!(ok = mbar_wait_idle(next, (it - 1) & 1, late))) break;
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -689,6 +693,7 @@ cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& d, cudaStream_t st
     const int64_t blocks = d.cu_q ? d.tq / kLpRows + min64(d.N, d.tq) : (d.tq + kLpRows - 1) / kLpRows;
     a.blocks = (int)blocks;
     a.splits = lp_splits(d);
+    a.drop = d.drop;
     if (blocks * d.H * a.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * d.H * a.splits)); cfg.blockDim = dim3(kLpThreads);

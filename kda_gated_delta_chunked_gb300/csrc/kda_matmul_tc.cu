@@ -64,8 +64,8 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         *late = 0;
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], kMmEpiWarps); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1 + (g.drop == kDropCopies)); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kBufs * kGroups; ++i) { mbar_init(&tfull[i], 1 + (g.drop == kDropProducts)); mbar_init(&tempty[i], kMmEpiWarps); }
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc_pair(tmem_at, 512); tmem_relinquish_pair(); }
@@ -362,8 +362,8 @@ kda_matmul_fp8_thin(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const int j0 = rank * blocks_per, count = max(0, min(kb, j0 + blocks_per) - j0);
     if (threadIdx.x == 0) {
         *late = 0;
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 4); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1 + (g.drop == kDropCopies)); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1 + (g.drop == kDropProducts)); mbar_init(&tempty[i], 4); }
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc(tmem_at, S::kTmem); tmem_relinquish(); }

@@ -1,6 +1,8 @@
 // kda_operators_api.cu -- C entries of the operators around the recurrent
 // layers: argument checks, choice of path, workspaces.
 #include <math.h>
+
+#include <atomic>
 #include <stdint.h>
 #include <string.h>
 
@@ -38,6 +40,8 @@ static bool any_overlap(const Range* outs, int no, const Range* ins, int ni) {
 }
 
 constexpr size_t kStatusBytes = sizeof(DeviceHeader);
+
+static std::atomic<int> g_drop{kDropNone};              // kda_selftest_drop_arrival
 
 static int latent_common(const kda_latent_desc* d) {
     if (!d || d->num_seqs < 0 || d->num_heads < 1 || !dtype_ok(d->dtype)) return KDA_ERR_INVALID_ARGUMENT;
@@ -130,7 +134,7 @@ int kda_matmul_fp8(const kda_matmul_desc* d, const uint8_t* a, const float* a_sc
     if (any_overlap(&out, 1, ins, 4)) return KDA_ERR_INVALID_ARGUMENT;
     MatmulArgs m;
     m.m = d->m; m.lda = d->a_stride; m.ldb = d->b_stride; m.ldc = d->c_stride;
-    m.n = d->n; m.k = d->k; m.dtype = d->dtype;
+    m.n = d->n; m.k = d->k; m.dtype = d->dtype; m.drop = g_drop.load(std::memory_order_relaxed);
     m.a = a; m.b = b; m.sa = a_scale; m.sb = b_scale; m.c = c;
     const bool tc = (d->flags & KDA_FLAG_CUDA_CORE_PREFILL) == 0 && matmul_tc_takes(m);
     const cudaError_t err = tc ? matmul_tc_launch(m, (cudaStream_t)stream) : matmul_simt_launch(m, (cudaStream_t)stream);
@@ -176,7 +180,7 @@ int kda_latent_prefill(const kda_latent_desc* d, const void* q, const void* k_no
     if (workspace_fault(d, kStatusBytes)) return KDA_ERR_WORKSPACE;
     LatentPrefillArgs a;
     a.dtype = d->dtype; a.N = d->num_seqs; a.H = d->num_heads; a.dk = d->d_k; a.dr = d->d_rope; a.dv = d->d_v;
-    a.causal = (d->flags & KDA_FLAG_NO_CAUSAL) == 0; a.scale = d->scale; a.tq = tq; a.tk = tk;
+    a.causal = (d->flags & KDA_FLAG_NO_CAUSAL) == 0; a.drop = g_drop.load(std::memory_order_relaxed); a.scale = d->scale; a.tq = tq; a.tk = tk;
     a.q_ts = d->q_token_stride; a.q_hs = d->q_head_stride; a.k_ts = d->k_token_stride; a.k_hs = d->k_head_stride;
     a.v_ts = d->v_token_stride; a.v_hs = d->v_head_stride; a.r_ts = d->rope_token_stride;
     a.q = q; a.k = k_nope; a.r = k_rope; a.v = v; a.cu_q = cu_seqlens_q; a.cu_k = cu_seqlens_k;
@@ -205,6 +209,7 @@ int kda_latent_decode(const kda_latent_desc* d, const void* q, const void* cache
     if (workspace_fault(d, kda_latent_decode_workspace_bytes(d))) return KDA_ERR_WORKSPACE;
     LatentDecodeArgs a;
     a.dtype = d->dtype; a.N = d->num_seqs; a.H = d->num_heads; a.Lq = d->num_queries; a.dk = d->d_k; a.dr = d->d_rope;
+    a.drop = g_drop.load(std::memory_order_relaxed);
     a.scale = d->scale; a.q_ts = d->q_token_stride; a.q_hs = d->q_head_stride; a.page_stride = d->page_stride;
     a.page_size = d->page_size; a.num_pages = d->num_pages; a.max_pages = d->max_pages;
     a.q = q; a.cache = cache; a.table = page_table; a.lens = lengths; a.out = out; a.lse = lse;
@@ -218,6 +223,12 @@ int kda_latent_decode(const kda_latent_desc* d, const void* q, const void* cache
         if (err == cudaSuccess) err = latent_decode_simt_launch(a, s);
     }
     return err == cudaSuccess ? KDA_OK : cuda_fail(err);
+}
+
+int kda_selftest_drop_arrival(int32_t which) {
+    if (which < kDropNone || which > kDropRows) return KDA_ERR_INVALID_ARGUMENT;
+    g_drop.store(which, std::memory_order_relaxed);
+    return KDA_OK;
 }
 
 int kda_latent_status(const kda_latent_desc* d, kda_stream_t stream) {

@@ -84,9 +84,12 @@ cudaError_t backward_tc_launch(const BackwardArgs& a, int64_t chunks_ub, void* r
 cudaError_t rms_norm_launch(const kda_norm_desc& d, const void* x, const void* weight, const void* residual,
                             void* residual_out, void* normed, uint8_t* quantized, float* scales, cudaStream_t stream);
 
+// The barriers of which kda_selftest_drop_arrival lets one arrival go missing.
+enum Dropped { kDropNone = 0, kDropCopies = 1, kDropProducts = 2, kDropSecondProducts = 3, kDropWeights = 4, kDropRows = 5 };
+
 struct MatmulArgs {
     int64_t m, lda, ldb, ldc;
-    int n, k, dtype;
+    int n, k, dtype, drop;           // drop: Dropped (tensor cores)
     const uint8_t *a, *b;
     const float *sa, *sb;
     void* c;
@@ -96,7 +99,7 @@ bool matmul_tc_takes(const MatmulArgs& a);          // rows of a and b start on 
 cudaError_t matmul_tc_launch(const MatmulArgs& a, cudaStream_t stream);
 
 struct LatentPrefillArgs {
-    int dtype, N, H, dk, dr, dv, causal;
+    int dtype, N, H, dk, dr, dv, causal, drop;
     float scale;
     int64_t tq, tk;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, r_ts;
@@ -111,7 +114,7 @@ bool latent_prefill_tc_takes(const LatentPrefillArgs& a);    // bf16, 128 + 64 /
 cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& a, cudaStream_t stream);
 
 struct LatentDecodeArgs {
-    int dtype, N, H, Lq, dk, dr;
+    int dtype, N, H, Lq, dk, dr, drop;
     float scale;
     int64_t q_ts, q_hs, page_stride;
     int page_size, num_pages, max_pages;

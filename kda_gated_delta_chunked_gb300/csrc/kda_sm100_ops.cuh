@@ -65,10 +65,12 @@ __device__ __forceinline__ bool mbar_wait_all(uint64_t* const (&bars)[N], const 
     }
 }
 
-// For waits of many microseconds beside working warps: looks twice a microsecond, ten times as long.
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity) {
+// For waits of many microseconds beside working warps: looks twice a microsecond, ten times as long, but not on when
+// one of those gave up (bit 0 of `late`, in shared memory).
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, const int* late) {
     bool ok = mbar_try_wait(bar, parity);
-    for (uint64_t t0 = globaltimer_ns(); !ok && globaltimer_ns() - t0 < 10 * kOpWaitNs; ok = mbar_try_wait(bar, parity))
+    for (uint64_t t0 = globaltimer_ns();
+         !ok && !(*(const volatile int*)late & 1) && globaltimer_ns() - t0 < 10 * kOpWaitNs; ok = mbar_try_wait(bar, parity))
         __nanosleep(500);
     return __all_sync(0xffffffffu, ok);
 }

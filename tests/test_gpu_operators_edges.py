@@ -1,12 +1,12 @@
 """Norm, scaled 8-bit product and latent attention where a call is unusual: values
 that are no numbers, waits that run out, calls without work, other contexts and
 streams."""
-import math
+import time
 
 import pytest
 import torch
 
-from test_gpu_operators import BF16, F32, expanded, kda, normal, paged  # noqa: F401
+from test_gpu_operators import BF16, F32, expanded, kda, normal, operands, paged  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,66 @@ def test_decode_reports_one_of_several_faults(kda, simt):  # noqa: F811
     assert kda.latent_status(ws) in (kda.KDA_ERR_BAD_PAGE, kda.KDA_ERR_BAD_SEQLENS)
     assert torch.equal(out[2], want[2])
     assert torch.equal(go(table, lengths(300, 200, 70)), want) and kda.latent_status(ws) == kda.KDA_OK
+
+
+# Each wait of the kernels runs out after 2 s; a call's follow one another a few times at most.
+COPIES, PRODUCTS, SECOND, WEIGHTS, ROWS = 1, 2, 3, 4, 5
+
+
+@pytest.fixture
+def dropped(kda):  # noqa: F811
+    yield kda.kda_selftest_drop_arrival
+    torch.cuda.synchronize()
+    assert kda.kda_selftest_drop_arrival(0) == kda.KDA_OK
+
+
+def runs_out(dropped, which, call):
+    """`call` with an arrival missing ends by itself; after it the same call gives what it gave before."""
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    assert dropped(which) == 0
+    t = time.perf_counter()
+    late = call()
+    torch.cuda.synchronize()
+    assert 1.5 < time.perf_counter() - t < 30
+    yield late
+    assert dropped(0) == 0
+    got = call()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    yield got
+
+
+def test_dropped_arrivals_have_numbers(kda, dropped):  # noqa: F811
+    assert [dropped(w) for w in (-1, 6, 100)] == [kda.KDA_ERR_INVALID_ARGUMENT] * 3 and dropped(5) == kda.KDA_OK
+
+
+@pytest.mark.parametrize("m,n,k,which", [(3, 700, 1024, COPIES), (3, 700, 1024, PRODUCTS), (300, 500, 2000, COPIES), (300, 500, 2000, PRODUCTS),
+                                         (2000, 3001, 1040, COPIES), (2000, 3001, 1040, PRODUCTS)])
+def test_matmul_waits_that_run_out_give_nan(kda, dropped, m, n, k, which):  # noqa: F811
+    a, sa, b, sb = operands(m, n, k, 71)
+    late = [bool(torch.isnan(c).all()) for c, in runs_out(dropped, which, lambda: (kda.matmul_fp8(a, sa, b, sb, out_dtype=F32),))]
+    assert late == [True, False]
+
+
+@pytest.mark.parametrize("tq,tk,h,which", [(300, 2000, 2, COPIES), (300, 2000, 2, SECOND), (300, 2000, 2, ROWS), (2000, 2000, 16, PRODUCTS),
+                                           (2000, 2000, 16, WEIGHTS), (2000, 2000, 16, ROWS)])
+def test_prefill_waits_that_run_out_are_reported(kda, dropped, tq, tk, h, which):  # noqa: F811
+    q, kn, kr, v = (t.cuda() for t in expanded(tq, tk, h, seed=72))
+    ws = torch.zeros(kda.latent_prefill_workspace_bytes(1, h, BF16), dtype=torch.uint8, device="cuda")
+    states = [kda.latent_status(ws) for _ in runs_out(dropped, which, lambda: kda.latent_prefill(q, kn, kr, v, scale=0.07, workspace=ws))]
+    assert states == [kda.KDA_ERR_TIMEOUT, kda.KDA_OK]
+
+
+@pytest.mark.parametrize("lens,h,which", [([5000, 700] * 20 + [1], 16, COPIES), ([5000, 700] * 20 + [1], 16, SECOND), ([700, 1300], 32, PRODUCTS),
+                                          ([700, 1300], 64, WEIGHTS), ([700, 1300], 64, SECOND), ([700, 1300], 100, ROWS)])
+def test_decode_waits_that_run_out_are_reported(kda, dropped, lens, h, which):  # noqa: F811
+    """With a workspace of bytes that make no sense as indices: what the join reads was all written."""
+    cache, table, _ = paged(lens, 64, 576, BF16, 73)
+    q = normal(74, len(lens), 1, h, 576, dtype=BF16).cuda()
+    ws = torch.full((kda.latent_decode_workspace_bytes(len(lens), 1, h, 512, 64, BF16, 64, table.shape[1]),), 0x7F, dtype=torch.uint8, device="cuda")
+
+    def go():
+        ws.fill_(0x7F)
+        return kda.latent_decode(q, cache, table, lengths(*lens), scale=0.07, workspace=ws)
+    states = [kda.latent_status(ws) for _ in runs_out(dropped, which, go)]
+    assert states == [kda.KDA_ERR_TIMEOUT, kda.KDA_OK]
