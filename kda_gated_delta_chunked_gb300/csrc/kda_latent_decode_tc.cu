@@ -36,6 +36,7 @@
 
 #include "kda_common.cuh"
 #include "kda_paths.h"
+#include "kda_per_device.h"
 #include "kda_sm100_ops.cuh"
 #include "kda_tensor_map.h"
 
@@ -692,12 +693,14 @@ bool latent_decode_tc_aligned(const LatentDecodeArgs& d) {
 template <int R>
 static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStream_t stream) {
     using S = LdShape<R>;
-    static bool ready = false;
-    if (!ready) {
-        cudaError_t e = cudaFuncSetAttribute(kda_latent_decode_tc<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-        if (e != cudaSuccess) return e;
-        ready = true;
-    }
+    static PerDevice memory_set;
+    int device = 0, set = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = memory_set.get(device, set, [](int& done) {
+        done = 1;
+        return cudaFuncSetAttribute(kda_latent_decode_tc<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    });
+    if (err != cudaSuccess) return err;
     LdArgs a;
     a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
     a.max_pages = d.max_pages; a.drop = d.drop; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
@@ -718,8 +721,8 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     made = made && make_map(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, d.cache, cd, cs, cb);
     if (!made) return cudaErrorInvalidValue;
     kda_latent_decode_tc<R><<<dim3(p.groups, p.G), kLdThreads, S::kSmem, stream>>>(mq, ms, mv, a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many; 16 x 2048, 16 heads:
     // 21 us, 17 as for many).

@@ -39,6 +39,7 @@
 
 #include "kda_common.cuh"
 #include "kda_paths.h"
+#include "kda_per_device.h"
 #include "kda_sm100_ops.cuh"
 #include "kda_tensor_map.h"
 
@@ -666,14 +667,16 @@ static int lp_splits(const LatentPrefillArgs& d) {
 }
 
 cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& d, cudaStream_t stream) {
-    static bool ready = false;
-    if (!ready) {
+    static PerDevice memory_set;
+    int device = 0, set = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = memory_set.get(device, set, [](int& done) {
+        done = 1;
         const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        cudaError_t e = cudaFuncSetAttribute(kda_latent_prefill_tc<false>, at, (int)kLpSmem);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kda_latent_prefill_tc<true>, at, (int)kLpSmem);
-        if (e != cudaSuccess) return e;
-        ready = true;
-    }
+        const cudaError_t e = cudaFuncSetAttribute(kda_latent_prefill_tc<false>, at, (int)kLpSmem);
+        return e == cudaSuccess ? cudaFuncSetAttribute(kda_latent_prefill_tc<true>, at, (int)kLpSmem) : e;
+    });
+    if (err != cudaSuccess) return err;
     auto map3 = [&](CUtensorMap* m, const void* p, int width, int64_t tokens, int64_t ts, int64_t hs, int rows) {
         const uint64_t dims[3] = {(uint64_t)width, (uint64_t)d.H, (uint64_t)tokens};
         const uint64_t str[2] = {(uint64_t)hs * 2, (uint64_t)ts * 2};

@@ -21,6 +21,7 @@
 
 #include "kda_common.cuh"
 #include "kda_paths.h"
+#include "kda_per_device.h"
 #include "kda_sm100_ops.cuh"
 #include "kda_tensor_map.h"
 
@@ -508,17 +509,19 @@ template <typename T, int BN>
 static cudaError_t launch_wide(const MatmulArgs& a, cudaStream_t stream) {
     using S = WideShape<BN>;
     auto kern = kda_matmul_fp8_wide<T, BN>;
-    static int resident = 0;                       // pairs that run at once: a property of the device and the kernel
-    if (!resident) {
+    static PerDevice pairs_at_once;
+    int device = 0, resident = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = pairs_at_once.get(device, resident, [&](int& n) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * 1024); cfg.blockDim = dim3(S::kThreads); cfg.dynamicSmemBytes = S::kSmem;
-        int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-        if (e != cudaSuccess) return e;
-        resident = n > 0 ? n : 1;
-    }
+        n = n > 0 ? n : 1;
+        return e;
+    });
+    if (err != cudaSuccess) return err;
     CUtensorMap ma, mb;
     if (!make_operand(&ma, a.a, a.m, a.k, a.lda, 128) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, 64))
         return cudaErrorInvalidValue;
@@ -552,22 +555,26 @@ static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
     auto kern = kda_matmul_fp8_thin<T, BT>;
     const int kb = (a.k + 127) / 128, tn = (a.n + 127) / 128;
     const int64_t tm = (a.m + BT - 1) / BT, tiles = tn * tm;
-    // clusters of 1 .. 8 CTAs that run at once, two CTAs on an SM: properties of the device and the kernel
-    static int active[9] = {};
-    if (!active[1]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        for (int c = 8; c >= 1 && e == cudaSuccess; --c) {
+    static PerDevice memory_set, clusters_at_once[9];
+    int device = 0, set = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = memory_set.get(device, set, [&](int& done) {
+        done = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    });
+    // as many splits as run at once, two CTAs on an SM, of four blocks of k at least
+    int splits = 1;
+    for (int c = 2; c <= 8 && kb >= 4 * c && err == cudaSuccess; ++c) {
+        int active = 0;
+        err = clusters_at_once[c].get(device, active, [&](int& n) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute at[1];
             thin_config(cfg, at, dim3(c, 1024), c, S::smem(24), 0);
-            e = cudaOccupancyMaxActiveClusters(&active[c], kern, &cfg);
-        }
-        if (e != cudaSuccess) { active[1] = 0; return e; }
+            return cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        });
+        if (tiles <= active) splits = c;
     }
-    // as many splits as run at once, of four blocks of k at least
-    int splits = 1;
-    for (int c = 2; c <= 8; ++c)
-        if (tiles <= active[c] && kb >= 4 * c) splits = c;
+    if (err != cudaSuccess) return err;
     const int per = (kb + splits - 1) / splits;
     splits = (kb + per - 1) / per;
     const uint32_t smem = S::smem(per);

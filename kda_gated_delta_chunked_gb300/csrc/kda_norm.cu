@@ -11,6 +11,7 @@
 
 #include "kda_common.cuh"
 #include "kda_paths.h"
+#include "kda_per_device.h"
 
 namespace kda {
 
@@ -269,12 +270,13 @@ static cudaError_t launch_rows(const NormArgs& a, int threads, cudaStream_t stre
     constexpr int rows = TPR && TPR < 128 ? 128 / TPR : 1;
     int64_t blocks = (a.rows + rows - 1) / rows;
     if (LOOP) {
-        static int resident[17] = {};                    // blocks of so many warps on an SM: a property of device and kernel
-        int& n = resident[threads / 32];
-        if (!n) {
-            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0);
-            if (e != cudaSuccess) { n = 0; return e; }
-        }
+        static PerDevice resident[17];                   // blocks of so many warps on an SM
+        int device = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e == cudaSuccess) e = resident[threads / 32].get(device, n, [&](int& found) {
+            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kern, threads, 0);
+        });
+        if (e != cudaSuccess) return e;
         blocks = min64(blocks, (int64_t)n * 152);
     }
     kern<<<(unsigned)blocks, threads, 0, stream>>>(a);

@@ -1,6 +1,9 @@
 """Norm, scaled 8-bit product and latent attention where a call is unusual: values
 that are no numbers, waits that run out, calls without work, other contexts and
 streams."""
+import os
+import subprocess
+import sys
 import time
 
 import pytest
@@ -10,6 +13,7 @@ from test_gpu_operators import BF16, F32, expanded, kda, normal, operands, paged
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 NAN, INF = float("nan"), float("inf")
 
 
@@ -180,3 +184,68 @@ def test_decode_waits_that_run_out_are_reported(kda, dropped, lens, h, which):  
         return kda.latent_decode(q, cache, table, lengths(*lens), scale=0.07, workspace=ws)
     states = [kda.latent_status(ws) for _ in runs_out(dropped, which, go)]
     assert states == [kda.KDA_ERR_TIMEOUT, kda.KDA_OK]
+
+
+# ------------------------------------------------------------------ contexts
+CONTEXTS = '''
+import ctypes, re, sys
+sys.path.insert(0, sys.argv[1])
+import kda_gated_delta_chunked_gb300 as kda                 # (torch is imported, and makes no context)
+rt = ctypes.CDLL(re.search(r"\\S*libcudart\\.so\\S*", open("/proc/self/maps").read()).group(0))
+
+class Ptr:
+    def __init__(self, n, words=None):
+        p = ctypes.c_void_p()
+        assert rt.cudaMalloc(ctypes.byref(p), ctypes.c_size_t(n)) == 0
+        assert rt.cudaMemset(p, 0, ctypes.c_size_t(n)) == 0
+        if words is not None:
+            a = (ctypes.c_int32 * len(words))(*words)
+            assert rt.cudaMemcpy(p, a, ctypes.c_size_t(4 * len(words)), 1) == 0
+        self.p = p.value
+    def data_ptr(self):
+        return self.p
+
+def all_calls():
+    x, y = Ptr(1 << 24), [Ptr(1 << 24) for _ in range(8)]
+    sc = Ptr(1 << 20)
+    rc = [kda.kda_rms_norm(kda.KdaNormDesc(4, 16384, kda.KDA_BF16, 16384, 16384, 1e-6), x, None, None, None, y[0], None, None, 0)]
+    for m, n in ((1, 128), (20, 128), (60, 128), (300, 512), (3000, 2000)):
+        for dt in (kda.KDA_BF16, kda.KDA_F32):
+            rc.append(kda.kda_matmul_fp8(kda.KdaMatmulDesc(m, n, 256, 256, 256, n, dt, 0), x, sc, y[0], sc, y[1 + (dt == 0)], 0))
+    def latent(h, rows, **kw):
+        d = kda.KdaLatentDesc(1, h, kda.KDA_BF16, 0, 0.1)
+        for k, v in kw.items():
+            setattr(d, k, v)
+        d.workspace, d.workspace_bytes = y[7].p, 1 << 24
+        return d
+    for h, t in ((2, 100), (8, 300)):                        # keys shared by a cluster, and not
+        d = latent(h, t, d_k=128, d_rope=64, d_v=128, total_q=t, total_k=t * 4, q_token_stride=h * 192, q_head_stride=192,
+                   k_token_stride=h * 128, k_head_stride=128, v_token_stride=h * 128, v_head_stride=128, rope_token_stride=64)
+        rc += [kda.kda_latent_prefill(d, x, y[0], y[1], y[2], None, None, y[3], y[4], 0), kda.kda_latent_status(d, 0)]
+    table, lens = Ptr(1 << 12, list(range(16))), Ptr(1 << 12, [700])
+    for h in (16, 32, 64):
+        d = latent(h, 1, d_k=512, d_rope=64, d_v=512, q_token_stride=h * 576, q_head_stride=576, num_queries=1, page_size=64,
+                   num_pages=16, max_pages=16, page_stride=64 * 576)
+        rc += [kda.kda_latent_decode(d, x, y[0], table, lens, y[3], y[4], 0), kda.kda_latent_status(d, 0)]
+    return rc + [rt.cudaDeviceSynchronize()]
+
+def check(what):
+    rc = all_calls()
+    print(what, rc, kda.lib.kda_last_cuda_error())
+    assert not any(rc)
+
+check("first")
+check("again")
+cu, context = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+assert cu.cuCtxCreate_v2(ctypes.byref(context), 0, 0) == 0   # current from here on
+check("another context of the device")
+assert cu.cuCtxDestroy_v2(context) == 0
+assert rt.cudaDeviceReset() == 0
+check("after a reset")
+'''
+
+
+def test_a_new_context_of_the_device_is_as_good_as_the_first(kda):  # noqa: F811
+    """What was set for kernels in one context (more shared memory than they have by default) is not taken for set in the next."""
+    r = subprocess.run([sys.executable, "-c", CONTEXTS, ROOT], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-1500:] + r.stderr[-1500:]

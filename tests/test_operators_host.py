@@ -131,3 +131,60 @@ def test_python_refusals():
                  lambda: kda.latent_decode(x, x, x, x, scale=1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+PER_DEVICE = r'''
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include "kda_per_device.h"
+
+enum Error { kGood = 0, kBad = 2 };
+
+int main() {
+    static kda::PerDevice one;
+    int out = 0;
+    std::atomic<int> asked{0};
+    auto is = [&](int n) { return [&asked, n](int& x) { ++asked; x = n; return kGood; }; };
+    if (one.get(0, out, [](int& x) { x = 9; return kBad; }) != kBad) return 1;           // an error is not kept
+    if (one.get(0, out, is(5)) != kGood || out != 5 || asked != 1) return 2;
+    if (one.get(0, out, is(6)) != kGood || out != 5 || asked != 1) return 3;             // found before
+    if (one.get(1, out, is(7)) != kGood || out != 7 || asked != 2) return 4;             // another device
+    if (one.get(0, out, is(8)) != kGood || out != 5) return 5;
+    if (one.get(100, out, is(3)) != kGood || out != 3 || one.get(100, out, is(4)) != kGood || out != 4) return 6;   // beyond those kept
+    static kda::PerDevice two;
+    std::vector<std::thread> all;
+    std::atomic<int> wrong{0};
+    for (int t = 0; t < 16; ++t)
+        all.emplace_back([&, t] {
+            for (int i = 0; i < 2000; ++i) {
+                int x = 0;
+                if (two.get(i % 64, x, [i](int& n) { n = 1 + i % 64; return kGood; }) != kGood || x != 1 + i % 64) ++wrong;
+            }
+        });
+    for (auto& t : all) t.join();
+    return wrong ? 7 : 0;
+}
+'''
+
+
+def test_what_is_found_for_a_device_is_kept_for_it_alone(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    (tmp_path / "d.cpp").write_text(PER_DEVICE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", os.path.join(root, "kda_gated_delta_chunked_gb300", "csrc"),
+                    str(tmp_path / "d.cpp"), "-o", str(tmp_path / "d")], check=True)
+    assert subprocess.run([str(tmp_path / "d")]).returncode == 0
+
+
+def test_nothing_of_a_device_is_kept_for_the_process():
+    """Functions' plain statics would be the first device's: attributes of kernels, blocks that run at once."""
+    import glob
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for name in ("kda_norm.cu", "kda_matmul_tc.cu", "kda_latent_prefill_tc.cu", "kda_latent_decode_tc.cu"):
+        path, = glob.glob(os.path.join(root, "kda_gated_delta_chunked_gb300", "csrc", name))
+        found = re.findall(r"^ {4,}static (?!constexpr|__device__)(\w+)", open(path).read(), re.M)
+        assert set(found) <= {"PerDevice", "uint32_t"}, (name, found)     # (uint32_t: a member function)
