@@ -432,7 +432,8 @@ KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const 
                               kda_stream_t stream);
 
 /* Synchronises `stream`, then returns the status word that the last
- * kda_latent_* call on this workspace recorded.  KDA_ERR_TIMEOUT, of a wait on
+ * kda_latent_* call on this workspace recorded, be it one without queries or
+ * sequences (which may do without a workspace).  KDA_ERR_TIMEOUT, of a wait on
  * the device that gave up, comes before the others and leaves every output
  * unspecified. */
 KDA_API int kda_latent_status(const kda_latent_desc *desc, kda_stream_t stream);

@@ -94,6 +94,18 @@ cudaError_t latent_prefill_simt_launch(const LatentPrefillArgs& a, cudaStream_t 
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------- calls without queries or sequences
+__global__ void kda_latent_status_of_lengths(const int32_t* cu_q, const int32_t* cu_k, int N, int64_t tq, int64_t tk,
+                                             int32_t* status) {
+    check_cu_seqlens(cu_q, cu_k, N, tq, tk, status);
+}
+
+cudaError_t latent_status_launch(const int32_t* cu_q, const int32_t* cu_k, int N, int64_t tq, int64_t tk, int32_t* status,
+                                 cudaStream_t stream) {
+    kda_latent_status_of_lengths<<<1, 256, 0, stream>>>(cu_q, cu_k, N, tq, tk, status);
+    return cudaGetLastError();
+}
+
 // ------------------------------------------------------------- absorbed form
 template <typename T, int KC, int VC>
 __global__ void __launch_bounds__(32 * kSimtWarps)

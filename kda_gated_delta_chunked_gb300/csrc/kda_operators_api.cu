@@ -82,6 +82,20 @@ static int workspace_fault(const kda_latent_desc* d, size_t need) {
     return !d->workspace || d->workspace_bytes < need || misaligned(d->workspace, 256);
 }
 
+// Status of a call that computes nothing.  It needs no workspace; one that is not device memory is left alone.
+static int nothing_to_compute(const kda_latent_desc* d, const int32_t* cu_q, const int32_t* cu_k, kda_stream_t stream) {
+    if (workspace_fault(d, kStatusBytes) || misaligned(cu_q, 4) || misaligned(cu_k, 4)) return KDA_OK;
+    cudaPointerAttributes at = {};
+    if (cudaPointerGetAttributes(&at, d->workspace) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_OK;
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return KDA_OK;
+    const cudaError_t err = latent_status_launch(cu_q, cu_k, d->num_seqs, d->total_q, d->total_k, (int32_t*)d->workspace,
+                                                 (cudaStream_t)stream);
+    return err == cudaSuccess ? KDA_OK : cuda_fail(err);
+}
+
 }  // namespace kda
 
 using namespace kda;
@@ -157,7 +171,7 @@ int kda_latent_prefill(const kda_latent_desc* d, const void* q, const void* k_no
     if (int rc = prefill_desc(d)) return rc;
     if ((cu_seqlens_q == nullptr) != (cu_seqlens_k == nullptr)) return KDA_ERR_INVALID_ARGUMENT;
     if (!cu_seqlens_q && d->num_seqs != 1) return KDA_ERR_INVALID_ARGUMENT;
-    if (d->num_seqs == 0 || d->total_q == 0) return KDA_OK;
+    if (d->num_seqs == 0 || d->total_q == 0) return nothing_to_compute(d, cu_seqlens_q, cu_seqlens_k, stream);
     if (!q || !out) return KDA_ERR_INVALID_ARGUMENT;
     if (d->total_k > 0 && (!k_nope || !v || (d->d_rope > 0) != (k_rope != nullptr))) return KDA_ERR_INVALID_ARGUMENT;
     const size_t e = esize(d->dtype);
@@ -194,7 +208,7 @@ int kda_latent_prefill(const kda_latent_desc* d, const void* q, const void* k_no
 int kda_latent_decode(const kda_latent_desc* d, const void* q, const void* cache, const int32_t* page_table,
                       const int32_t* lengths, void* out, float* lse, kda_stream_t stream) {
     if (int rc = decode_desc(d)) return rc;
-    if (d->num_seqs == 0) return KDA_OK;
+    if (d->num_seqs == 0) return nothing_to_compute(d, nullptr, nullptr, stream);
     if (!q || !out || !page_table || !lengths || (d->num_pages > 0 && !cache)) return KDA_ERR_INVALID_ARGUMENT;
     const size_t e = esize(d->dtype);
     if (misaligned(q, e) || misaligned(cache, e) || misaligned(out, e) || misaligned(lse, 4) ||

@@ -113,6 +113,10 @@ cudaError_t latent_prefill_simt_launch(const LatentPrefillArgs& a, cudaStream_t 
 bool latent_prefill_tc_takes(const LatentPrefillArgs& a);    // bf16, 128 + 64 / 128 channels, 16-byte rows
 cudaError_t latent_prefill_tc_launch(const LatentPrefillArgs& a, cudaStream_t stream);
 
+// Writes the status of a call that computes nothing (nullptr lengths: KDA_OK).
+cudaError_t latent_status_launch(const int32_t* cu_q, const int32_t* cu_k, int N, int64_t tq, int64_t tk, int32_t* status,
+                                 cudaStream_t stream);
+
 struct LatentDecodeArgs {
     int dtype, N, H, Lq, dk, dr, drop;
     float scale;

@@ -248,6 +248,7 @@ PyObject* latent_prefill(PyObject* const* p) {
         dense(*cq, "cu_seqlens_q", at::kInt, cq->sizes(), dev);
         dense(*ck, "cu_seqlens_k", at::kInt, cq->sizes(), dev);
         d.num_seqs = narrow(cq->size(0) - 1, "the number of sequences");
+        if (d.num_seqs == 0 && (tq || tk)) refuse("no sequences for ", tq, " queries and ", tk, " keys");
     }
     d.num_heads = narrow(h, "the number of heads");
     d.scale = (float)number(p[6], "scale");

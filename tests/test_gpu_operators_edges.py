@@ -249,3 +249,52 @@ def test_a_new_context_of_the_device_is_as_good_as_the_first(kda):  # noqa: F811
     """What was set for kernels in one context (more shared memory than they have by default) is not taken for set in the next."""
     r = subprocess.run([sys.executable, "-c", CONTEXTS, ROOT], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stdout[-1500:] + r.stderr[-1500:]
+
+
+# ------------------------------------------------------------------ calls without work
+def test_status_of_calls_without_work(kda):  # noqa: F811
+    """They leave a status as others do, whatever the workspace held."""
+    stale = lambda: torch.full((1 << 20,), 5, dtype=torch.uint8, device="cuda")  # noqa: E731
+    q, kn, kr, v = (t.cuda() for t in expanded(5, 5, 2))
+    for flags in (0, kda.KDA_FLAG_CUDA_CORE_PREFILL):
+        def prefill(tq, cq, ck):
+            ws = stale()
+            o, l = kda.latent_prefill(q[:tq], kn, kr, v, cq, ck, scale=0.1, workspace=ws, flags=flags)
+            assert o.shape == (tq, 2, 128) and l.shape == (tq, 2)
+            return kda.latent_status(ws)
+        assert prefill(0, None, None) == kda.KDA_OK
+        assert prefill(0, lengths(0, 0, 0), lengths(0, 2, 5)) == kda.KDA_OK
+        assert prefill(0, lengths(0, 0, 0), lengths(0, 6, 5)) == kda.KDA_ERR_BAD_SEQLENS
+        assert prefill(0, lengths(0, 3, 0), lengths(0, 2, 5)) == kda.KDA_ERR_BAD_SEQLENS
+        assert prefill(0, lengths(0, 0), lengths(1, 5)) == kda.KDA_ERR_BAD_SEQLENS
+        assert prefill(5, lengths(0, 5), lengths(0, 5)) == kda.KDA_OK
+        cache, table, _ = paged([70], 64, 576, BF16, 3)
+        ws = stale()
+        o, l = kda.latent_decode(normal(1, 0, 1, 16, 576, dtype=BF16).cuda(), cache, table[:0], lengths(), scale=0.1, workspace=ws, flags=flags)
+        assert o.shape == (0, 1, 16, 512) and kda.latent_status(ws) == kda.KDA_OK
+    empty = [t[:0].contiguous() for t in (q, kn, kr, v)]
+    ws = stale()
+    kda.latent_prefill(*empty, lengths(0), lengths(0), scale=0.1, workspace=ws)
+    assert kda.latent_status(ws) == kda.KDA_OK
+    kda.latent_prefill(*empty, lengths(3), lengths(0), scale=0.1, workspace=ws)
+    assert kda.latent_status(ws) == kda.KDA_ERR_BAD_SEQLENS
+
+
+def test_rows_without_a_sequence_are_refused(kda):  # noqa: F811
+    q, kn, kr, v = (t.cuda() for t in expanded(5, 5, 2))
+    for args in ((q, kn, kr, v), (q[:0], kn, kr, v), (q, kn[:0].contiguous(), kr[:0].contiguous(), v[:0].contiguous())):
+        with pytest.raises(ValueError):
+            kda.latent_prefill(*args, lengths(0), lengths(0), scale=0.1)
+
+
+def test_calls_without_work_are_captured(kda):  # noqa: F811
+    q, kn, kr, v = (t.cuda() for t in expanded(5, 5, 2))
+    good, bad = lengths(0, 0), lengths(0, 4)
+    ws = torch.full((512,), 5, dtype=torch.uint8, device="cuda")
+    for lk, want in ((lengths(0, 5), kda.KDA_OK), (bad, kda.KDA_ERR_BAD_SEQLENS)):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kda.latent_prefill(q[:0], kn, kr, v, good, lk, scale=0.1, workspace=ws)
+        g.replay()
+        assert kda.latent_status(ws) == want
