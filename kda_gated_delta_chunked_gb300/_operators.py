@@ -6,12 +6,13 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import threading
 from typing import Optional
 
 import torch
 
 from . import _binding as B
-from ._binding import KdaError, lib
+from ._binding import KdaError, lib, library_path
 
 KDA_FLAG_NO_CAUSAL = 4
 
@@ -61,22 +62,32 @@ _declare()
 _byref = ctypes.byref
 
 
+_native = None
+_native_lock = threading.Lock()
+
+
 def _load_native():
-    """The compiled marshalling (csrc/kda_torch.cpp), bound to the entry points of the loaded library."""
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "_kda_torch.so")
-    if not os.path.exists(path):
-        raise ImportError(f"_kda_torch.so not built at {path}: run "
-                          f"`python -c 'import __graft_entry__ as g; g.build()'` first")
-    loader = importlib.machinery.ExtensionFileLoader("_kda_torch", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kda_torch", loader))
-    loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-        "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes", "kda_latent_decode_workspace_bytes",
-        "kda_latent_prefill", "kda_latent_decode")))
-    return module
-
-
-_native = _load_native()
+    """The compiled marshalling (csrc/kda_torch.cpp), bound to the entry points of the loaded library; from beside that
+    library, or from this package.  It is loaded by the first operator that is called: it belongs to one Python and one
+    torch, which the other calls of the package do not need."""
+    global _native
+    with _native_lock:
+        if _native is not None:
+            return _native
+        places = [os.path.dirname(os.path.abspath(library_path())), os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build")]
+        paths = [os.path.join(p, "_kda_torch.so") for p in places]
+        path = next((p for p in paths if os.path.exists(p)), None)
+        if path is None:
+            raise ImportError(f"_kda_torch.so not built at {paths[-1]}: run "
+                              f"`python -c 'import __graft_entry__ as g; g.build()'` first")
+        loader = importlib.machinery.ExtensionFileLoader("_kda_torch", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kda_torch", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes", "kda_latent_decode_workspace_bytes",
+            "kda_latent_prefill", "kda_latent_decode")))
+        _native = module
+        return module
 
 
 def kda_rms_norm(desc: KdaNormDesc, x, weight, residual, residual_out, normed, quantized, scales, stream=None) -> int:
@@ -128,13 +139,14 @@ def kda_selftest_drop_arrival(which: int) -> int:
 # ------------------------------------------------------------------ operators
 def _call(name: str, stream, *args):
     """The native call on the current stream or on ``stream`` (whose allocations its outputs then are)."""
+    native = _native or _load_native()
     if stream is None:
-        r = getattr(_native, name)(*args)
+        r = getattr(native, name)(*args)
     else:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(stream):
-            r = getattr(_native, name)(*args)
+            r = getattr(native, name)(*args)
     if type(r) is int:
         raise KdaError(f"kda_{name}", r)
     return r

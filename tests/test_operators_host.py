@@ -188,3 +188,54 @@ def test_nothing_of_a_device_is_kept_for_the_process():
         path, = glob.glob(os.path.join(root, "kda_gated_delta_chunked_gb300", "csrc", name))
         found = re.findall(r"^ {4,}static (?!constexpr|__device__)(\w+)", open(path).read(), re.M)
         assert set(found) <= {"PerDevice", "uint32_t"}, (name, found)     # (uint32_t: a member function)
+
+
+IMPORT = '''
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import kda_gated_delta_chunked_gb300 as kda
+assert kda.kda_status_string(kda.KDA_OK) == "KDA_OK" and kda.prefill and kda.decode_step
+d = kda.make_desc(1, 1, 128, 128, 64, torch.bfloat16, None)
+assert kda.kda_prefill_workspace_bytes(d) > 0
+x = torch.zeros(4, 256)
+for call in (lambda: kda.rms_norm(x), lambda: kda.matmul_fp8(x, x, x, x)):
+    try:
+        call()
+    except (ImportError, ValueError) as e:
+        print(type(e).__name__)
+'''
+
+
+def test_the_other_calls_do_without_the_module_for_torch_tensors(tmp_path):
+    """Without it, or with one that this Python cannot load, the package imports, its other calls work, and the operators
+    say what is missing.  KDA_LIBRARY leads to the module beside that library, if there is one."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    package, built = "kda_gated_delta_chunked_gb300", kda.library_path()
+    other = tmp_path / "other"
+    (tmp_path / package / "_build").mkdir(parents=True)
+    other.mkdir()
+    for f in os.listdir(os.path.join(root, package)):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(root, package, f), tmp_path / package / f)
+    for to in (tmp_path / package / "_build", other):
+        shutil.copy(built, to / "libkda.so")
+
+    def names(**env):
+        r = subprocess.run([sys.executable, "-c", IMPORT, str(tmp_path)], capture_output=True, text=True, timeout=300,
+                           env={**{k: v for k, v in os.environ.items() if k != "KDA_LIBRARY"}, **env})
+        assert r.returncode == 0, r.stderr[-1500:]
+        return r.stdout.split()
+    module = os.path.join(root, package, "_build", "_kda_torch.so")
+    assert names() == ["ImportError"] * 2
+    (tmp_path / package / "_build" / "_kda_torch.so").write_bytes(b"not a module")
+    assert names() == ["ImportError"] * 2
+    shutil.copy(module, other / "_kda_torch.so")
+    assert names(KDA_LIBRARY=str(other / "libkda.so")) == ["ValueError"] * 2          # loaded: the tensors are not on a GPU
+    shutil.copy(module, tmp_path / package / "_build" / "_kda_torch.so")
+    (other / "_kda_torch.so").unlink()
+    assert names(KDA_LIBRARY=str(other / "libkda.so")) == ["ValueError"] * 2 and names() == ["ValueError"] * 2
