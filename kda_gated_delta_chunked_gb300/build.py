@@ -4,7 +4,8 @@ Each translation unit compiles in parallel into an object file; the shared
 library links them against the CUDA runtime (shared, so that it is the same
 runtime instance PyTorch uses in the process).  ``csrc/kda_torch.cpp``, the
 marshalling of torch tensors for the short operators, becomes a module of its
-own, ``_build/_kda_torch.so``.  Rebuilds only what changed.
+own, ``_build/_kda_torch.so``, for the Python and the torch that build it.
+Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -65,8 +66,28 @@ def _compile(nvcc: str, src: str, obj: str, extra) -> None:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
 
 
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _torch_module_for() -> str:
+    """What the module for torch tensors belongs to: this Python, and the torch that it finds."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sys.version}\n{sysconfig.get_config_var('EXT_SUFFIX')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _torch_module_stale(src: str) -> bool:
+    if _stale(TORCH_MODULE, [src, __file__, os.path.join(INCLUDE, "kda.h")]):
+        return True
+    try:
+        with open(TORCH_MODULE + ".for") as f:
+            return f.read() != _torch_module_for()
+    except OSError:
+        return True
+
+
 def _compile_torch_module(nvcc: str, src: str) -> None:
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
     tmp = TORCH_MODULE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -77,6 +98,8 @@ def _compile_torch_module(nvcc: str, src: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, TORCH_MODULE)
+    with open(TORCH_MODULE + ".for", "w") as f:
+        f.write(_torch_module_for())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -92,7 +115,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s, *hdrs, __file__]):
             jobs.append((s, o))
     module = os.path.join(CSRC, "kda_torch.cpp")
-    stale_module = force or _stale(TORCH_MODULE, [module, __file__, os.path.join(INCLUDE, "kda.h")])
+    stale_module = force or _torch_module_stale(module)
     if jobs or stale_module:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = [ex.submit(_compile, nvcc, s, o, list(extra_flags)) for s, o in jobs]

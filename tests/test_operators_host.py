@@ -239,3 +239,26 @@ def test_the_other_calls_do_without_the_module_for_torch_tensors(tmp_path):
     shutil.copy(module, tmp_path / package / "_build" / "_kda_torch.so")
     (other / "_kda_torch.so").unlink()
     assert names(KDA_LIBRARY=str(other / "libkda.so")) == ["ValueError"] * 2 and names() == ["ValueError"] * 2
+
+
+def test_the_module_for_torch_tensors_is_built_anew_for_another_python_or_torch(tmp_path, monkeypatch):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(kda.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("_kda_build_test", path)
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    src = os.path.join(build.CSRC, "kda_torch.cpp")
+    assert not build._torch_module_stale(src)                       # as the package was built
+    with open(build.TORCH_MODULE + ".for") as f:
+        mark = f.read()
+    monkeypatch.setattr(build, "TORCH_MODULE", str(tmp_path / "m.so"))
+    assert build._torch_module_stale(src)                           # none
+    (tmp_path / "m.so").write_bytes(b"")
+    assert build._torch_module_stale(src)                           # one that does not say what it is for
+    (tmp_path / "m.so.for").write_text(mark)
+    assert not build._torch_module_stale(src)
+    for other in (mark.replace(torch.__version__, "2.0.0"), "another Python\n" + mark):
+        assert other != mark
+        (tmp_path / "m.so.for").write_text(other)
+        assert build._torch_module_stale(src)
