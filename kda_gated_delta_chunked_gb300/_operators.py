@@ -1,5 +1,11 @@
 """Norm, 8-bit products and latent attention: the operators around the recurrent
-layers (argument marshalling only; see include/kda.h for what each computes)."""
+layers (argument marshalling only; see include/kda.h for what each computes).
+
+Work goes to the current stream, or to a given ``stream`` (a torch stream or a
+handle), where it is ordered behind that stream's work alone: the caller lets
+that stream wait for whatever wrote the inputs, and the reader of the outputs
+wait for it.  The memory of the inputs is kept until the stream has read them,
+also if the caller drops them at once; the outputs are allocated on it."""
 from __future__ import annotations
 
 import ctypes
@@ -138,7 +144,7 @@ def kda_selftest_drop_arrival(which: int) -> int:
 
 # ------------------------------------------------------------------ operators
 def _call(name: str, stream, *args):
-    """The native call on the current stream or on ``stream`` (whose allocations its outputs then are)."""
+    """The native call on the current stream or on ``stream``, see above."""
     native = _native or _load_native()
     if stream is None:
         r = getattr(native, name)(*args)
@@ -147,6 +153,9 @@ def _call(name: str, stream, *args):
             stream = torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(stream):
             r = getattr(native, name)(*args)
+        for t in args:                                    # the allocator gives none of them away before the stream is there
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
     if type(r) is int:
         raise KdaError(f"kda_{name}", r)
     return r

@@ -298,3 +298,27 @@ def test_calls_without_work_are_captured(kda):  # noqa: F811
             kda.latent_prefill(q[:0], kn, kr, v, good, lk, scale=0.1, workspace=ws)
         g.replay()
         assert kda.latent_status(ws) == want
+
+
+# ------------------------------------------------------------------ streams
+def test_inputs_of_another_stream_live_until_it_has_read_them(kda):  # noqa: F811
+    """A caller may drop its inputs once a call has returned, also a call on a stream that is not the current one."""
+    other = torch.cuda.Stream()
+    x = normal(51, 64, 512, dtype=BF16).cuda()
+    want = kda.rms_norm(x)[0].clone()
+    raw = torch.cuda.Stream().cuda_stream
+    for stream in (other, raw):
+        torch.cuda.synchronize()
+        s = stream if stream is other else torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(400_000_000)                     # some 0.2 s before the call's kernel starts
+        copy = x.clone()
+        torch.cuda.current_stream().synchronize()
+        at = copy.data_ptr()
+        y = kda.rms_norm(copy, stream=stream)[0]
+        del copy
+        others = [torch.zeros_like(x) for _ in range(8)]
+        assert not s.query()                                   # still asleep: the input must be there
+        assert at not in [t.data_ptr() for t in others]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
