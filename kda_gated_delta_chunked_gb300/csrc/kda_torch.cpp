@@ -106,9 +106,15 @@ double number(PyObject* o, const char* name) {
     return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) { PyErr_Clear(); refuse(name, " must be true or false"); }
+    return v;
+}
+
 // Descriptors hold some sizes in 32 bits.
 int32_t narrow(int64_t x, const char* what) {
-    if (x > 0x7fffffffLL) refuse(what, " is too large: ", x);
+    if (x > 0x7fffffffLL || x < -0x80000000LL) refuse(what, " is too large: ", x);
     return (int32_t)x;
 }
 
@@ -117,7 +123,7 @@ int32_t narrow(int64_t x, const char* what) {
 PyObject* rms_norm(PyObject* const* a) {
     const at::Tensor& x = tensor(a[0], "x");
     const at::Tensor *weight = maybe(a[1], "weight"), *residual = maybe(a[2], "residual"), *given = maybe(a[6], "residual_out");
-    const bool normed = PyObject_IsTrue(a[4]), quantize = PyObject_IsTrue(a[5]);
+    const bool normed = truth(a[4], "normed"), quantize = truth(a[5], "quantize");
     const c10::Device dev = device_of(x, "x");
     const at::ScalarType type = x.scalar_type();
     kda_norm_desc d = {};
@@ -187,12 +193,12 @@ PyObject* matmul_fp8(PyObject* const* p) {
         c = *given;
         d.c_stride = row_stride(c, n);
     } else {
-        c = fresh({m, n}, PyObject_IsTrue(p[5]) ? at::kBFloat16 : at::kFloat, dev);
+        c = fresh({m, n}, truth(p[5], "out_dtype") ? at::kBFloat16 : at::kFloat, dev);
     }
     d.m = m; d.n = narrow(n, "b's rows"); d.k = narrow(k, "the rows' length");
     d.a_stride = row_stride(a, k); d.b_stride = row_stride(b, k);
     d.dtype = dtype_of(c, "out");
-    d.flags = (int32_t)integer(p[6]);
+    d.flags = narrow(integer(p[6]), "flags");
     if (m && n) {
         const int rc = api.matmul_fp8(&d, (const uint8_t*)a.data_ptr(), (const float*)sa.data_ptr(), (const uint8_t*)b.data_ptr(),
                                       (const float*)sb.data_ptr(), c.data_ptr(), stream_of(dev));
@@ -252,7 +258,7 @@ PyObject* latent_prefill(PyObject* const* p) {
     }
     d.num_heads = narrow(h, "the number of heads");
     d.scale = (float)number(p[6], "scale");
-    d.flags = (int32_t)integer(p[7]);
+    d.flags = narrow(integer(p[7]), "flags");
     d.d_k = narrow(k.size(2), "d_k");
     d.d_v = narrow(v.size(2), "d_v");
     d.total_q = tq; d.total_k = tk;
@@ -294,7 +300,7 @@ PyObject* latent_decode(PyObject* const* p) {
     d.num_seqs = narrow(n, "the number of sequences"); d.num_heads = narrow(h, "the number of heads");
     d.num_queries = narrow(lq, "the number of queries");
     d.scale = (float)number(p[4], "scale");
-    d.flags = (int32_t)integer(p[6]);
+    d.flags = narrow(integer(p[6]), "flags");
     d.d_k = d.d_v = narrow(rank, "rank");
     d.d_rope = narrow(width - rank, "d_rope");
     d.page_size = narrow(c.size(1), "the page size"); d.num_pages = narrow(c.size(0), "the number of pages");

@@ -322,3 +322,13 @@ def test_inputs_of_another_stream_live_until_it_has_read_them(kda):  # noqa: F81
         assert at not in [t.data_ptr() for t in others]
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_arguments_that_are_no_truth_value_or_too_large_are_refused(kda):  # noqa: F811
+    x = normal(52, 4, 128, dtype=BF16).cuda()
+    for kw in (dict(normed=torch.ones(2)), dict(quantize=torch.ones(2))):
+        with pytest.raises(ValueError):
+            kda.rms_norm(x, **kw)
+    with pytest.raises(ValueError):
+        kda.matmul_fp8(x.to(torch.float8_e4m3fn), torch.ones(4, 1, device="cuda"), x.to(torch.float8_e4m3fn), torch.ones(1, 1, device="cuda"),
+                       flags=1 << 32)
