@@ -550,7 +550,7 @@ static void thin_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, dim3 g
 }
 
 template <typename T, int BT>
-static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
+static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream, bool& fits) {
     using S = ThinShape<BT>;
     auto kern = kda_matmul_fp8_thin<T, BT>;
     const int kb = (a.k + 127) / 128, tn = (a.n + 127) / 128;
@@ -578,7 +578,8 @@ static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream) {
     const int per = (kb + splits - 1) / splits;
     splits = (kb + per - 1) / per;
     const uint32_t smem = S::smem(per);
-    if (smem > 227 * 1024) return cudaErrorInvalidValue;
+    fits = smem <= 227 * 1024;
+    if (!fits) return cudaSuccess;
     CUtensorMap ma, mb;
     if (!make_operand(&ma, a.a, a.m, a.k, a.lda, BT) || !make_operand(&mb, a.b, a.n, a.k, a.ldb, 128))
         return cudaErrorInvalidValue;
@@ -594,14 +595,16 @@ static cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t stream) {
     //   1 x 4096 x 4096  6.4 / 12.5 / 16.8     64 x 8192 x 8192  16.8 / 17.4 / 29.6    128 x 2048 x 4096  7.2 / 11.1 / 17.4
     //   512 x 1024 x 1024  6.2 / 6.8 / 8.2     128 x 6144 x 4096  16.5 / 11.4 / 17.5   1024 x 1024 x 4096  16.9 / 11.5 / 17.5
     //   1024 x 4096 x 4096  42 / 19.6 / 18.3   2048 x 8192 x 4096  140 / 59.7 / 60.0   16384 x 8192 x 4096  1049 / 435 / 386
+    // and, with L2 flushed before each, thin against the better of the wide ones
+    //   1 x 4096 x 18432  26.8 / 49     64 x 4096 x 18432  31.9 / 42     200 x 1024 x 18432  23.7 / 40     64 x 16384 x 32768  132 / 130
     // thin while its tiles are few (its splits then use SMs that tiles of the others would leave idle); of the wide
     // ones the narrower while all its tiles run at once.
     const int64_t tn = (a.n + 127) / 128;
-    const bool thin_fits = a.k <= 96 * 128;                // the factors of a CTA's blocks of k lie in shared memory
-    if (thin_fits && (a.m <= 64 || (a.m + 63) / 64 * tn <= 64)) {
-        if (a.m <= 16) return launch_thin<T, 16>(a, stream);
-        if (a.m <= 32) return launch_thin<T, 32>(a, stream);
-        return launch_thin<T, 64>(a, stream);
+    if (a.m <= 64 || (a.m + 63) / 64 * tn <= 64) {
+        bool fits = true;                                  // the factors of a CTA's blocks of k lie in shared memory
+        const cudaError_t e = a.m <= 16 ? launch_thin<T, 16>(a, stream, fits) : a.m <= 32 ? launch_thin<T, 32>(a, stream, fits)
+                                        : launch_thin<T, 64>(a, stream, fits);
+        if (fits || e != cudaSuccess) return e;
     }
     if ((a.m + 255) / 256 * tn <= 76) return launch_wide<T, 128>(a, stream);
     return launch_wide<T, 256>(a, stream);

@@ -9,7 +9,7 @@ import time
 import pytest
 import torch
 
-from test_gpu_operators import BF16, F32, expanded, kda, normal, operands, paged  # noqa: F401
+from test_gpu_operators import BF16, F32, check_matmul, expanded, kda, normal, operands, paged  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -332,3 +332,13 @@ def test_arguments_that_are_no_truth_value_or_too_large_are_refused(kda):  # noq
     with pytest.raises(ValueError):
         kda.matmul_fp8(x.to(torch.float8_e4m3fn), torch.ones(4, 1, device="cuda"), x.to(torch.float8_e4m3fn), torch.ones(1, 1, device="cuda"),
                        flags=1 << 32)
+
+
+# ------------------------------------------------------------------ long sums
+@pytest.mark.parametrize("m,n,k", [(1, 300, 12304), (16, 129, 18432), (33, 256, 14352), (64, 128, 20000), (200, 500, 18448), (1, 16, 2300000),
+                                   (64, 8, 540000), (300, 200, 100000)])
+def test_matmul_of_few_rows_and_long_sums(kda, m, n, k):  # noqa: F811
+    """Rows whose blocks' scales lie in shared memory, one CTA's share of them, and rows too long for that."""
+    a, sa, b, sb = operands(m, n, k, 81)
+    check_matmul(kda, a, sa, b, sb, out_dtype=F32)
+    check_matmul(kda, a, sa, b, sb)
