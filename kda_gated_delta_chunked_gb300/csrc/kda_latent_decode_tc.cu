@@ -255,9 +255,11 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         uint64_t *fulls = scores ? full : full_v, *empties = scores ? empty : empty_v;
         uint32_t seg = 0, s = 0, ph = 1;                               // slot and the parity its emptying has (first round: none)
         // With 32 rows the second fetch, a little later than with 16, may come when L2 has given the lines up, depending
-        // on what was in it before: 64 x 16384 tokens 190 to 303 us.  With the first fetch's lines to be kept and the
-        // second's to go: 195 to 209.  With 16 rows the hints cost 2% (199, 203), with 64 they change nothing.
-        const uint64_t policy = scores ? l2_keep() : l2_drop();
+        // on what was in it before: 64 sequences of up to 16384 tokens 107 us by themselves, 132 to 147 between products of
+        // 25 to 100 MB of weights.  With the second fetch's lines marked to go first 111 and 113 to 119.  (The first one's
+        // marked to stay as well: 109 and 111 to 113, but they stay for whatever follows: four products by the same 64 MB
+        // of weights 79 us behind it instead of 72.)  With 16 rows the mark costs 2%, with 64 it changes nothing.
+        const uint64_t last_use = l2_drop();
         bool ok = true, bad_page = false;
         LdWalk w;
         w.start(a, range[0], range[1], range[2]);
@@ -289,8 +291,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 __syncwarp();
                 if (lane < boxes) {
                     const uint32_t at = ring + s * slot + lane * (slot / boxes);
-                    if (R != 32) tma_load_5d(at, map, 0, 0, u * pieces, row / 8, page, smem_u32(&fulls[s]));
-                    else tma_load_5d(at, map, 0, 0, u * pieces, row / 8, page, smem_u32(&fulls[s]), policy);
+                    if (R != 32 || scores) tma_load_5d(at, map, 0, 0, u * pieces, row / 8, page, smem_u32(&fulls[s]));
+                    else tma_load_5d(at, map, 0, 0, u * pieces, row / 8, page, smem_u32(&fulls[s]), last_use);
                 }
                 __syncwarp();
                 if (++s == slots) { s = 0; ph ^= 1; }
