@@ -73,7 +73,8 @@ struct LdShape {
 };
 
 struct LdArgs {
-    int N, H, Lq, rows, page_size, num_pages, max_pages, drop;
+    int N, H, Lq, rows, page_size, num_pages, max_pages;
+    uint32_t drop;                             // barriers, a bit each, that miss an arrival
     float scale;
     const int32_t *table, *lens;
     __nv_bfloat16* out;
@@ -169,12 +170,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // warps wait for it at the barrier.
         const int64_t cap = (int64_t)a.max_pages * a.page_size;
         int len = lane < a.N ? a.lens[lane] : 0;                       // on its way while the barriers are made
-        if (lane < bars_end - bars) {
-            uint64_t* const bar = bars + lane;
-            const int of = bar < empty || bar == q_full ? kDropCopies : bar < s_full ? kDropNone : bar < o_full ? kDropProducts
-                         : bar < p_full ? kDropSecondProducts : bar < zeroed ? kDropWeights : kDropRows;
-            mbar_init(bar, (bar < p_full ? 1 : 4) + (a.drop != kDropNone && a.drop == of));
-        }
+        if (lane < bars_end - bars) mbar_init(bars + lane, (lane < p_full - bars ? 1 : 4) + (a.drop >> lane & 1));
         if (lane == 0) {
             prefetch_map(&map_s);
             prefetch_map(&map_v);
@@ -339,24 +335,6 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 7) {                                            // ---------------- O^T += V^T P^T
-        if (group == 0) {
-            // Where the sequences that start in this range lie among all tiles.  The join takes its pieces by it, so it is
-            // written before anything that may give up.
-            const int64_t begin = *range_at, end = begin + range[2];
-            int64_t at = begin - range[1];
-            for (int b = range[0]; at < end && b < a.N; b += 32) {
-                const int t = b + lane < a.N ? ld_tiles(a, b + lane) : 0;
-                int x = t;                                             // inclusive scan
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const int64_t first = at + x - t;
-                if (t > 0 && first >= begin && first < end) a.before[b + lane] = first;
-                at += __shfl_sync(0xffffffffu, x, 31);
-            }
-        }
         const uint32_t idesc = idesc_bf16(128, R, 1, 1);
         uint32_t s = 0, ph = 0, zero = 0;
         bool ok = true;
@@ -400,8 +378,8 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         w.start(a, range[0], range[1], range[2]);
         const int count = w.left;
         for (int j = 0; j < count; ++j, w.next(a)) {
-            // (a wait of one warp that gave up ends the loop here, for all four: they meet at barriers)
-            ok = bar_and(128, ok && mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
+            if (w.first && w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+            ok = bar_and(128, mbar_wait_spin(&s_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t at_s = lanes + (j & 1) * R;
@@ -465,6 +443,10 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (j >= S::kBufP) {                                       // P's buffer: the products that read it are complete
                 const int before = j - S::kBufP;
                 ok = mbar_wait_warp(&o_full[before & 1], (before >> 1) & 1);
+                if (!ok) {                                             // the other warps leave at their next vote, with this one
+                    bar_and(128, false);
+                    break;
+                }
             }
 #pragma unroll
             for (int c = 0; c < R; c += 8) {
@@ -484,10 +466,10 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&p_full[j & 1]);      // (nobody is told of P after a wait that gave up)
+            if (lane == 0) mbar_arrive(&p_full[j & 1]);
             // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes (once the
             // products of the tile before are complete, the ring is at this tile's).
-            if (ok && (w.j + 1) * kLdTile > len) {
+            if ((w.j + 1) * kLdTile > len) {
                 if (j > 0) ok = mbar_wait_warp(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
                 for (int p = 0; p < 4 && ok; ++p) {
                     const uint32_t u = 4 * j + p, s = u % S::kSlotsV;
@@ -557,7 +539,13 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int c = 0; c < R; ++c) l[c] = 0.f;
             asm volatile("bar.sync 2, 128;" ::: "memory");
         }
-        if (!ok) atomicOr(fault, kLdLate);
+        if (!ok) {
+            // The join finds the pieces by where the sequences start, those of the tiles that were left among them.
+            w.start(a, range[0], range[1], range[2]);
+            for (int j = 0; j < count; ++j, w.next(a))
+                if (w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+            atomicOr(fault, kLdLate);
+        }
     }
     tc_fence_before_sync();
     meet_at_end(fault);
@@ -705,10 +693,14 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     if (err != cudaSuccess) return err;
     LdArgs a;
     a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
-    a.max_pages = d.max_pages; a.drop = d.drop; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
+    a.max_pages = d.max_pages; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
     a.before = (int64_t*)((char*)d.scratch + p.before);
     a.parts = (float*)((char*)d.scratch + p.parts);
+    constexpr uint32_t kS = S::kSlots;                 // the barriers' order: full, empty, q_full, q_empty, s, o, p, zeroed
+    constexpr uint32_t kDrops[6] = {0, ((1u << kS) - 1) | 1u << 2 * kS, 3u << (2 * kS + 2), 3u << (2 * kS + 4), 3u << (2 * kS + 6),
+                                    15u << (2 * kS + 8)};
+    a.drop = kDrops[d.drop];
     CUtensorMap mq, ms, mv;
     const uint64_t qd[3] = {kLdWidth, (uint64_t)a.rows, (uint64_t)d.N};
     const uint64_t qs[2] = {(uint64_t)(d.H == 1 ? d.q_ts : d.q_hs) * 2, (uint64_t)d.q_ts * d.Lq * 2};
