@@ -342,3 +342,32 @@ def test_matmul_of_few_rows_and_long_sums(kda, m, n, k):  # noqa: F811
     a, sa, b, sb = operands(m, n, k, 81)
     check_matmul(kda, a, sa, b, sb, out_dtype=F32)
     check_matmul(kda, a, sa, b, sb)
+
+
+# ------------------------------------------------------------------ what lies beside the outputs
+@pytest.mark.parametrize("rows,dim", [(1, 1), (3, 7), (5, 128), (130, 2051), (33, 4096), (7, 200), (3, 16384), (700, 9001), (2, 40000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_norm_writes_nothing_outside_its_outputs(kda, rows, dim, dtype, shift):  # noqa: F811
+    """Outputs that start on 16 bytes, and outputs that start an element (of 8 bits: a byte) behind."""
+    esz = torch.empty((), dtype=dtype).element_size()
+
+    def guarded(n, width):
+        whole = torch.full((n * width + 512 + width,), 0xA5, dtype=torch.uint8, device="cuda")
+        return whole, 256 + shift * width, n * width
+    x, r = normal(91, rows, dim, dtype=dtype).cuda(), normal(92, rows, dim, dtype=dtype).cuda()
+    w = (1 + normal(93, dim, scale=0.2)).to(dtype).cuda()
+    y, q, s, h = kda.rms_norm(x, w, r, quantize=True)
+    outs = [guarded(rows * dim, esz), guarded(rows * dim, esz), guarded(rows * dim, 1), guarded(s.numel(), 4)]
+    d = kda.KdaNormDesc(rows, dim, kda.KDA_BF16 if dtype == BF16 else kda.KDA_F32, dim, dim, 1e-6)
+    ho, yo, qo, so = (t[at:at + n] for t, at, n in outs)
+    assert kda.kda_rms_norm(d, x, w, r, ho, yo, qo, so) == kda.KDA_OK
+    torch.cuda.synchronize()
+    for t, at, n in outs:
+        assert (t[:at] == 0xA5).all() and (t[at + n:] == 0xA5).all()
+    assert torch.equal(ho, h.view(torch.uint8).flatten())      # one addition and its rounding, whoever does it
+    if not shift:
+        assert torch.equal(yo, y.view(torch.uint8).flatten()) and torch.equal(qo, q.view(torch.uint8).flatten())
+        assert torch.equal(so, s.view(torch.uint8).flatten())
+    else:                                                      # sums in another order: 72 roundings of 2^-24 on either side
+        assert torch.allclose(so.clone().view(F32), s.flatten(), rtol=2 * 72 * 2.0 ** -24, atol=0)
