@@ -196,7 +196,8 @@ def latent_prefill(q, k_nope, k_rope, v, cu_seqlens_q=None, cu_seqlens_k=None, *
     Query i of a sequence sees keys 0 .. Lk - Lq + i, all without ``causal``.
     Returns (out ``[Tq, H, d_v]``, lse fp32 ``[Tq, H]``).  A caller that passes
     a ``workspace`` (uint8) can read the call's device status from it with
-    ``latent_status``."""
+    ``latent_status``.  In bf16 the softmax weights are rounded to bf16 before
+    they meet the values, fp32 inputs keep them in fp32 (include/kda.h)."""
     return _call("latent_prefill", stream, q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, scale,
                  flags if causal else flags | KDA_FLAG_NO_CAUSAL, out, lse, workspace)
 
@@ -211,7 +212,8 @@ def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional
     strided), page_table int32 ``[N, max_pages]``, lengths int32 ``[N]``: tokens
     of each sequence in the cache, its queries' own among them.  ``rank`` is the
     values' width, by default all but the last 64.  Returns (out ``[N, (Lq,) H,
-    rank]``, lse fp32 ``[N, (Lq,) H]``)."""
+    rank]``, lse fp32 ``[N, (Lq,) H]``).  The softmax weights are held as in
+    ``latent_prefill``."""
     return _call("latent_decode", stream, q, cache, page_table, lengths, scale, -1 if rank is None else rank, flags, out,
                  lse, workspace)
 
