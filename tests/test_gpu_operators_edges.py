@@ -371,3 +371,62 @@ def test_norm_writes_nothing_outside_its_outputs(kda, rows, dim, dtype, shift): 
         assert torch.equal(so, s.view(torch.uint8).flatten())
     else:                                                      # sums in another order: 72 roundings of 2^-24 on either side
         assert torch.allclose(so.clone().view(F32), s.flatten(), rtol=2 * 72 * 2.0 ** -24, atol=0)
+
+
+# ------------------------------------------------------------------ offsets above 32 bits
+FAR = 1 << 24                                                # elements between rows: 300 of them span 5e9
+
+
+def far(t, lead=0):
+    """The same values in rows FAR elements apart."""
+    wide = torch.empty(t.shape[0] * FAR, dtype=t.dtype, device="cuda")
+    view = wide.as_strided(t.shape, (FAR, *t.contiguous().stride()[1:]), lead)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("simt", [False, True])
+def test_decode_from_pages_at_the_end_of_a_large_pool(kda, simt):  # noqa: F811
+    cache, table, _ = paged([300, 1, 700], 64, 576, BF16, 95)
+    q = normal(96, 3, 1, 16, 576, dtype=BF16).cuda()
+    go = lambda c, t: kda.latent_decode(q, c, t, lengths(300, 1, 700), scale=0.07, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0)  # noqa: E731
+    want = go(cache, table)
+    pool = torch.empty(120_000, 64, 576, dtype=BF16, device="cuda")
+    first = pool.shape[0] - cache.shape[0]
+    pool[first:] = cache
+    got = go(pool, torch.where(table < cache.shape[0], table + first, table))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("simt", [False, True])
+def test_prefill_of_rows_far_apart(kda, simt):  # noqa: F811
+    q, kn, kr, v = (t.cuda() for t in expanded(300, 300, 2, seed=97))
+    go = lambda *x: kda.latent_prefill(*x, scale=0.07, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0)  # noqa: E731
+    want = go(q, kn, kr, v)
+    for i in range(4):
+        x = [q, kn, kr, v]
+        x[i] = far(x[i])
+        got = go(*x)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("simt,m", [(False, 300), (True, 300), (False, 40)])
+def test_matmul_of_rows_far_apart(kda, simt, m):  # noqa: F811
+    a, sa, b, sb = operands(m, 300, 400, 98)
+    flags = kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0
+    want = kda.matmul_fp8(a, sa, b, sb, flags=flags)
+    bytes_ = lambda t: far(t.view(torch.uint8)).view(t.dtype)  # noqa: E731
+    assert torch.equal(kda.matmul_fp8(bytes_(a), sa, b, sb, flags=flags), want)
+    assert torch.equal(kda.matmul_fp8(a, sa, bytes_(b), sb, flags=flags), want)
+    for lead in (0, 1):
+        out = far(torch.zeros_like(want), lead)
+        assert torch.equal(kda.matmul_fp8(a, sa, b, sb, out=out, flags=flags), want)
+
+
+@pytest.mark.parametrize("dim", [512, 515, 16384])
+def test_norm_of_rows_far_apart(kda, dim):  # noqa: F811
+    x, r = normal(99, 300, dim, dtype=BF16).cuda(), normal(100, 300, dim, dtype=BF16).cuda()
+    want = kda.rms_norm(x, None, r, quantize=True)
+    for y, s in ((far(x), r), (x, far(r))):
+        got = kda.rms_norm(y, None, s, quantize=True)
+        assert all(torch.equal(g.view(torch.uint8), w.view(torch.uint8)) for g, w in zip(got, want))
