@@ -430,3 +430,29 @@ def test_norm_of_rows_far_apart(kda, dim):  # noqa: F811
     for y, s in ((far(x), r), (x, far(r))):
         got = kda.rms_norm(y, None, s, quantize=True)
         assert all(torch.equal(g.view(torch.uint8), w.view(torch.uint8)) for g, w in zip(got, want))
+
+
+def test_calls_on_several_streams_at_once_give_the_same_bits(kda):  # noqa: F811
+    """Kernels of all operators beside one another, each with its own workspace."""
+    a, sa, b, sb = operands(700, 1300, 1024, 101)
+    x = normal(102, 900, 4096, dtype=BF16).cuda()
+    few = [t.cuda() for t in expanded(300, 2500, 2, seed=103)]
+    many = [t.cuda() for t in expanded(1500, 1500, 8, seed=104)]
+    cache, table, _ = paged([5000, 60, 0, 900] * 6, 64, 576, BF16, 105)
+    L = lengths(*([5000, 60, 0, 900] * 6))
+    q16, q48 = normal(106, 24, 1, 16, 576, dtype=BF16).cuda(), normal(107, 24, 3, 16, 576, dtype=BF16).cuda()
+    calls = [lambda s: kda.rms_norm(x, quantize=True, stream=s)[:3], lambda s: [kda.matmul_fp8(a, sa, b, sb, stream=s)],
+             lambda s: [kda.matmul_fp8(a[:9], sa[:9].contiguous(), b, sb, stream=s)],
+             lambda s: kda.latent_prefill(*few, scale=0.07, stream=s), lambda s: kda.latent_prefill(*many, scale=0.07, stream=s),
+             lambda s: kda.latent_decode(q16, cache, table, L, scale=0.07, stream=s),
+             lambda s: kda.latent_decode(q48, cache, table, L, scale=0.07, stream=s)]
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for turn in range(12):
+        for i in range(len(calls)):
+            got.append((i, calls[i](streams[(i + turn) % len(streams)])))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        assert all(torch.equal(o.view(torch.uint8), w.view(torch.uint8)) for o, w in zip(outs, want[i])), i
