@@ -2,9 +2,13 @@
 // tensor cores (bf16, rank 512 + 64 rotary channels).
 //
 // All Lq * H query rows of a sequence read the same 576-channel latents, so a
-// tile of 128 cached tokens is fetched once (1152 bytes a token) and used for
-// all of them.  Both products keep the tokens' side at full height and put the
-// few query rows along N, where an instruction's time follows them down:
+// tile of 128 cached tokens is used for R of them at once (16, 32 or 64; more
+// rows go in groups of 64 to CTAs of their own).  Each group fetches it twice,
+// 1152 bytes a token for the first product and 1024 for the second; memory gives
+// it once, L2 the other times (64 x 4096 tokens: 311 MB of DRAM reads with 64
+// heads, 319 MB with 128, for 302 MB of cache).  Both products keep the tokens'
+// side at full height and put the few query rows along N, where an instruction's
+// time follows them down:
 //
 //     S^T [128 tokens, R rows]       = C Q^T          36 instructions (576 / 16)
 //     P^T                            = exp2(S^T - ref)
@@ -27,7 +31,11 @@
 // fetches the 512 channels again, out of L2.  So each product has a stream of
 // its own, with a producer warp, a ring and a warp that issues it, and the next
 // tiles' scores go ahead while this one's softmax and second product run.
-// Measured: 64 sequences of 16384 tokens, 16 heads: 199 us, 6.1 TB/s.
+// Measured, us in a graph of ten / one behind a flush of L2 (the join included):
+//   64 x 16384 tokens, 16 heads  197 (6.1 TB/s) / 214       64 x 4096, 64 heads   81 / 93
+//   64 x 16384, 32 heads         208 / 222                  64 x 4096, 128 heads  122 / 132
+//   128 x 1024, 16 heads         39 / 52                    3 x 8192, 128 heads   25 / 37
+//   1 x 30000, 32 heads          19 / 30                    1 x 700, 32 heads     12 / 19
 //
 // A wait on an mbarrier looks at a parity only, so each waiter stays within one
 // phase of what it waits for: a ring has one producer and one consumer, both in
@@ -718,8 +726,8 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many; 16 x 2048, 16 heads:
-    // 21 us, 17 as for many).
+    // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many).  From 256 rows on as
+    // for many (16 x 2048, 16 heads: 17 us, 21 as for few).
     const bool many = (int64_t)d.N * a.rows >= 256;
     const int warps = many ? 2 : 16, per = many ? 4 : 1;
     cfg.gridDim = dim3(d.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;

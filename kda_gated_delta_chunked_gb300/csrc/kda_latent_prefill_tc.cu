@@ -30,8 +30,9 @@
 // the tensor pipe; it takes 3360.  The pipe starts an instruction about when it is
 // issued, and the issuing warp's waits between products are the difference; loads,
 // exponentials and maxima are hidden (without them the time is the same).  8192
-// tokens, 32 heads, causal: 420 us, 1.63 PFLOP/s.  What else was measured there
-// (us): a wait for each of a product's barriers 429, and a thread a row then 461;
+// tokens, 32 heads, causal: 420 to 425 us by itself, 1.62 PFLOP/s; 438 to 446 in
+// a stream of calls, where power bounds the clocks; all keys 812 and 847.  What
+// else was measured there (us, by itself): a wait for each of a product's barriers 429, and a thread a row then 461;
 // the rings freed a step at a time 470; a warp for each tile's instructions, in
 // turns 474; blocks of one tile of rows, one ring, a thread a row 445 (and 100
 // prompts of 60 tokens 99 instead of 54).

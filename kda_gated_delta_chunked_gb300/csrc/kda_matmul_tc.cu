@@ -98,7 +98,7 @@ kda_matmul_fp8_wide(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         regs_inc<232>();
         // A thread sums 128 columns of its row.  Of 256, a warpgroup has a half each; 128 they take in turns, one the even
         // blocks of k and the other the odd ones, and join their sums at the end: a block's wait, reads and sums take a
-        // warp about 450 cycles, its products 256 (256 x 6144 x 4096: 11.3 us so, 12.0 with both on every block).
+        // warp about 450 cycles, its products 256 (256 x 6144 x 4096 in a graph: 11.3 us so, 12.0 with both on every block).
         constexpr bool kTurns = BN == 128;
         constexpr int kCols = 128, kOutCols = BN / 2, kStep = kTurns ? 2 : 1;
         const int quarter = warp & 3, half = warp >> 2;
@@ -591,7 +591,8 @@ static cudaError_t launch_thin(const MatmulArgs& a, cudaStream_t stream, bool& f
 
 template <typename T>
 static cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t stream) {
-    // Measured on a GB300 (us, thin with 64 rows of a / wide with 128 columns / with 256):
+    // Measured on a GB300 (us, each of the three the same way, the largest by itself: 430 in a stream of calls; thin with 64
+    // rows of a / wide with 128 columns / with 256):
     //   1 x 4096 x 4096  6.4 / 12.5 / 16.8     64 x 8192 x 8192  16.8 / 17.4 / 29.6    128 x 2048 x 4096  7.2 / 11.1 / 17.4
     //   512 x 1024 x 1024  6.2 / 6.8 / 8.2     128 x 6144 x 4096  16.5 / 11.4 / 17.5   1024 x 1024 x 4096  16.9 / 11.5 / 17.5
     //   1024 x 4096 x 4096  42 / 19.6 / 18.3   2048 x 8192 x 4096  140 / 59.7 / 60.0   16384 x 8192 x 4096  1049 / 435 / 386
