@@ -456,3 +456,21 @@ def test_calls_on_several_streams_at_once_give_the_same_bits(kda):  # noqa: F811
     torch.cuda.synchronize()
     for i, outs in got:
         assert all(torch.equal(o.view(torch.uint8), w.view(torch.uint8)) for o, w in zip(outs, want[i])), i
+
+
+def test_calls_on_a_given_stream_are_captured(kda):  # noqa: F811
+    """The stream that is captured named in the call, with inputs from outside and from inside the capture."""
+    x, w = normal(111, 64, 512, dtype=BF16).cuda(), normal(112, 512, dtype=BF16).cuda()
+    a, sa, b, sb = operands(64, 300, 512, 113)
+    want = [kda.rms_norm(x * 2, w)[0], kda.matmul_fp8(a, sa, b, sb)]
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        inside = x * 2
+        got = [kda.rms_norm(inside, w, stream=s)[0], kda.matmul_fp8(a, sa, b, sb, stream=s)]
+        del inside
+        torch.zeros(64, 512, dtype=BF16, device="cuda")
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
