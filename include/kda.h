@@ -356,7 +356,10 @@ KDA_API int kda_matmul_fp8(const kda_matmul_desc *desc, const uint8_t *a, const 
 /* kda_latent_desc.flags bits, beside KDA_FLAG_CUDA_CORE_PREFILL. */
 enum {
     /* kda_latent_prefill: every key of its sequence is visible to a query. */
-    KDA_FLAG_NO_CAUSAL = 4
+    KDA_FLAG_NO_CAUSAL = 4,
+    /* kda_latent_decode: the cache is one that kda_latent_cache_write fills (8-bit codes, see there); page_stride is in
+       bytes, cache and page_stride are multiples of 16. */
+    KDA_FLAG_CACHE_8 = 64
 };
 
 /* Attention whose keys and values come from one latent vector c_s and one
@@ -400,7 +403,8 @@ typedef struct kda_latent_desc {
     int32_t page_size;       /* tokens of a page, >= 1 */
     int32_t num_pages;       /* pages of the cache */
     int32_t max_pages;       /* row length of the page table, >= 1 */
-    int64_t page_stride;     /* elements between pages; tokens of a page are dense, d_k + d_rope apart */
+    int64_t page_stride;     /* elements between pages; tokens of a page are dense, d_k + d_rope apart (KDA_FLAG_CACHE_8:
+                                bytes between pages) */
     void *workspace;         /* 256-byte aligned device scratch */
     size_t workspace_bytes;
 } kda_latent_desc;
@@ -440,10 +444,132 @@ KDA_API int kda_latent_prefill(const kda_latent_desc *desc, const void *q, const
  *
  * A page number outside the cache (KDA_ERR_BAD_PAGE) or a length outside its
  * range (KDA_ERR_BAD_SEQLENS) is recorded in the device status word and never
- * dereferenced; the outputs of that sequence are then unspecified. */
+ * dereferenced; the outputs of that sequence are then unspecified.
+ *
+ * With KDA_FLAG_CACHE_8, keys are [2^e code | rope] and values 2^e code of the
+ * quantised cache below, each exactly.  bf16 queries, rank 512 and d_rope 64 run
+ * on the tensor cores, on the codes themselves; there a query is the sum of two
+ * e4m3 values under one power of two for its row (exact down to 2^-22 of its
+ * largest channel) and a softmax weight the sum of an e4m3 and an e5m2 value (off
+ * by 2^-7 of it at most, 2^-9.6 on average); sums are fp32.  Everything else, and
+ * fp32 queries, run on CUDA cores in fp32. */
 KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const void *cache,
                               const int32_t *page_table, const int32_t *lengths, void *out, float *lse,
                               kda_stream_t stream);
+
+/* The quantised cache of latents.  A page holds page_size rows of rank e4m3
+ * codes and d_rope bf16 rotary channels, then a byte e + 127 for each of its
+ * tokens, and is padded to 128 bytes:
+ *
+ *     byte t * (rank + 2 d_rope) + c             code c of the page's token t
+ *     byte t * (rank + 2 d_rope) + rank + 2 c    its rotary channel c
+ *     byte page_size * (rank + 2 d_rope) + t     its scale, e + 127
+ *
+ * A latent channel is worth 2^e code.  e is the smallest integer with
+ * max |latent| <= 448 2^e, within -100 .. 120 (448: e4m3's largest value; the
+ * maximum is over the token's finite channels), so that no code saturates and the
+ * values are exact in bf16.  One scale a token does: behind a channel's own
+ * exponent of four bits, scales of shorter groups would change only values below
+ * 2^-14 of the token's largest.  Channels that are infinite or NaN become NaN. */
+typedef struct kda_latent_cache_desc {
+    int32_t num_seqs;        /* N >= 0 */
+    int32_t dtype;           /* kda_dtype of latents and rope */
+    int64_t total_tokens;    /* T >= 0 rows of latents and rope */
+    int32_t rank;            /* a multiple of 16, 16 .. 512 */
+    int32_t d_rope;          /* a multiple of 8, 0 .. 128 */
+    int32_t page_size;       /* tokens of a page, >= 1 */
+    int32_t num_pages;       /* pages of the cache */
+    int32_t max_pages;       /* row length of the page table, >= 1 */
+    int32_t flags;           /* 0 */
+    int64_t page_stride;     /* bytes between pages, a multiple of 16, >= kda_latent_cache_page_bytes */
+    int64_t latent_stride;   /* elements between rows of latents, >= rank */
+    int64_t rope_stride;     /* elements between rows of rope, >= d_rope */
+    void *workspace;         /* 256-byte aligned device memory for the status word, or NULL: none is recorded */
+    size_t workspace_bytes;  /* >= 256 with a workspace */
+} kda_latent_cache_desc;
+
+/* Bytes of a page (0 for sizes that are not supported). */
+KDA_API size_t kda_latent_cache_page_bytes(int32_t page_size, int32_t rank, int32_t d_rope);
+
+/* Quantises the last tokens of each sequence into its pages, and reads tokens
+ * back as rows.
+ *
+ *   latents    [T, rank], rope [T, d_rope] (NULL iff d_rope = 0): rows of the
+ *              sequences, packed; read by _write, written by _read
+ *   cu_seqlens int32 [N+1], device: rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 are
+ *              sequence n's; NULL: T / N rows each (N divides T).  cu_seqlens[N]
+ *              may be less than T: rows behind it are not read, or left as they were
+ *   page_table int32 [N, max_pages], lengths int32 [N] as for kda_latent_decode:
+ *              row i of the L rows of sequence n is its cached token
+ *              lengths[n] - L + i (lengths count the new tokens).  Rows whose
+ *              place is negative are left out (a sequence padded into a batch has
+ *              length 0)
+ *   cache      [num_pages] pages, 16-byte aligned
+ *
+ * A malformed cu_seqlens or a length outside 0 .. max_pages * page_size
+ * (KDA_ERR_BAD_SEQLENS) and page numbers outside the cache (KDA_ERR_BAD_PAGE)
+ * are recorded in the status word (kda_latent_status), if there is one; the rows
+ * concerned are left out, never dereferenced.  Two rows of one call in the same
+ * place of the cache leave that place unspecified. */
+KDA_API int kda_latent_cache_write(const kda_latent_cache_desc *desc, const void *latents, const void *rope,
+                                   const int32_t *cu_seqlens, const int32_t *page_table, const int32_t *lengths,
+                                   uint8_t *cache, kda_stream_t stream);
+KDA_API int kda_latent_cache_read(const kda_latent_cache_desc *desc, const uint8_t *cache, const int32_t *page_table,
+                                  const int32_t *lengths, const int32_t *cu_seqlens, void *latents, void *rope,
+                                  kda_stream_t stream);
+
+/* Rotary positions.  Of each row (token and head) of `width` channels, `dim`
+ * from `offset` on are pairs (a_i, b_i), i < dim / 2: channels i and i + dim / 2
+ * of them, or 2 i and 2 i + 1 with KDA_FLAG_INTERLEAVED.  With
+ * theta = positions[t] * frequencies[i],
+ *
+ *     a_i' = scale (a_i cos theta - b_i sin theta)
+ *     b_i' = scale (b_i cos theta + a_i sin theta)
+ *
+ * and the other channels as they are.  KDA_FLAG_INVERSE turns by -theta, which
+ * makes the gradient of the inputs from that of the outputs.  theta is taken
+ * modulo a turn in 64 bits, whatever the position; the rest is fp32, rounded once. */
+enum {
+    KDA_FLAG_INTERLEAVED = 8,
+    KDA_FLAG_INVERSE = 16,
+    KDA_FLAG_POSITIONS_64 = 32   /* positions are int64, else int32 */
+};
+typedef struct kda_rotary_part {
+    int32_t heads;               /* >= 1, <= 65535 */
+    int32_t width;               /* channels of a row, <= 4096 */
+    int32_t offset;              /* the first one that is turned, offset + dim <= width */
+    int32_t reserved;            /* 0 */
+    int64_t token_stride, head_stride;           /* elements, of the input */
+    int64_t out_token_stride, out_head_stride;   /* of the output, whose rows do not overlap */
+} kda_rotary_part;
+typedef struct kda_rotary_desc {
+    int64_t tokens;              /* >= 0 */
+    int32_t dim;                 /* even, 2 .. 1024 */
+    int32_t dtype;               /* kda_dtype of x, key and the outputs */
+    int32_t flags;
+    float scale;                 /* finite */
+    kda_rotary_part x, key;      /* key is not looked at without one */
+} kda_rotary_desc;
+
+/* x, and key or NULL (the keys of the same tokens, in the same launch), to out
+ * and key_out.  An output may be its own input, with the same strides, and
+ * overlaps nothing else (rows of both inside one wider row, like queries and keys
+ * of one projection, do not overlap).  positions int32 or int64 [tokens],
+ * frequencies fp64 [dim / 2] (radians a position), device. */
+KDA_API int kda_rotary(const kda_rotary_desc *desc, const void *x, const void *key, const void *positions,
+                       const double *frequencies, void *out, void *key_out, kda_stream_t stream);
+
+/* Frequencies base^(-2 i / dim), and their scalings for contexts `factor` times
+ * as long as `original_length`, the trained one.  HOST memory, no CUDA work. */
+typedef enum {
+    KDA_ROTARY_PLAIN = 0,
+    KDA_ROTARY_LINEAR = 1,       /* all divided by factor */
+    KDA_ROTARY_BASE = 2,         /* with base * factor^(dim / (dim - 2)): the slowest divided by factor, the fastest kept */
+    KDA_ROTARY_BY_PARTS = 3      /* f (w + (1 - w) / factor), w = (turns - slow) / (fast - slow) within 0 .. 1, of the
+                                    turns original_length f / (2 pi) that a pair made in training */
+} kda_rotary_method;
+KDA_API int kda_rotary_frequencies(int32_t dim, double base, int32_t method, double factor, double original_length,
+                                   double slow, double fast, double *frequencies);
 
 /* Synchronises `stream`, then returns the status word that the last
  * kda_latent_* call on this workspace recorded, be it one without queries or

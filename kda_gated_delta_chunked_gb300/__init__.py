@@ -18,9 +18,13 @@ from ._binding import (  # noqa: F401
     kda_backward_workspace_bytes, kda_prefill_backward, prefill_backward,
 )
 from ._operators import (  # noqa: F401
-    KDA_FLAG_NO_CAUSAL, KdaNormDesc, KdaMatmulDesc, KdaLatentDesc,
+    KDA_FLAG_NO_CAUSAL, KDA_FLAG_INTERLEAVED, KDA_FLAG_INVERSE, KDA_FLAG_POSITIONS_64, KDA_FLAG_CACHE_8, KDA_ROTARY_PLAIN,
+    KDA_ROTARY_LINEAR, KDA_ROTARY_BASE, KDA_ROTARY_BY_PARTS, KdaNormDesc, KdaMatmulDesc, KdaLatentDesc, KdaLatentCacheDesc,
+    KdaRotaryPart, KdaRotaryDesc,
     kda_rms_norm, kda_matmul_fp8, kda_latent_prefill, kda_latent_decode, kda_latent_status, kda_selftest_drop_arrival,
-    kda_latent_prefill_workspace_bytes, kda_latent_decode_workspace_bytes,
-    rms_norm, matmul_fp8, latent_prefill, latent_decode, latent_status,
+    kda_latent_prefill_workspace_bytes, kda_latent_decode_workspace_bytes, kda_latent_cache_page_bytes,
+    kda_latent_cache_write, kda_latent_cache_read, kda_rotary, kda_rotary_frequencies,
+    rms_norm, matmul_fp8, latent_prefill, latent_decode, latent_status, latent_cache_page_bytes, latent_cache_write,
+    latent_cache_read, rotary, rotary_frequencies,
     latent_prefill_workspace_bytes, latent_decode_workspace_bytes,
 )

@@ -22,7 +22,8 @@ EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step", "kda
            "kda_selftest_wait_timeout", "kda_prefill_snapshots", "kda_backward_workspace_bytes",
            "kda_prefill_backward", "kda_rms_norm", "kda_matmul_fp8", "kda_latent_prefill_workspace_bytes",
            "kda_latent_decode_workspace_bytes", "kda_latent_prefill", "kda_latent_decode", "kda_latent_status",
-           "kda_selftest_drop_arrival")
+           "kda_selftest_drop_arrival", "kda_latent_cache_page_bytes", "kda_latent_cache_write", "kda_latent_cache_read",
+           "kda_rotary", "kda_rotary_frequencies")
 KDA_PREFILL_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 

@@ -1,0 +1,267 @@
+// kda_latent_cache.cu -- latents quantised into the pages of a cache, and read
+// back as rows (layout and rounding: kda.h).
+//
+//     e = min { e : max |c| <= 448 2^e },   code = e4m3(c / 2^e)
+//
+// A warp owns a token, a lane 16 of its channels: the maximum is one reduction,
+// a lane's codes are one 16-byte access.  Division by a power of two is exact, so
+// the code is the latent rounded once.  Bound by HBM bytes (1152 and 641 of them
+// a token in bf16 at rank 512); a warp takes kTokens neighbouring tokens, whose
+// rows it loads before it looks for their places (write), or whose places it
+// finds before it loads any (read).
+//
+// Errors in lengths and pages are found by a block of its own, if there is a
+// status word: it alone writes it.  The others leave out what is wrong.
+#include <cuda_fp8.h>
+#include <string.h>
+
+#include "kda_common.cuh"
+#include "kda_latent_cache.cuh"
+#include "kda_paths.h"
+
+namespace kda {
+
+constexpr int kLcWarps = 8;
+
+// 16 channels of a row, as they lie in memory.
+template <typename T> struct Lc16 { uint4 v[sizeof(T)]; };
+
+template <typename T, bool kWide>
+__device__ __forceinline__ void lc_load(Lc16<T>& x, const T* p) {
+    if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) x.v[i] = ((const uint4*)p)[i];
+    } else {
+        T e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = p[i];
+        memcpy(&x, e, sizeof(x));
+    }
+}
+template <typename T, bool kWide>
+__device__ __forceinline__ void lc_store(const Lc16<T>& x, T* p) {
+    if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) ((uint4*)p)[i] = x.v[i];
+    } else {
+        T e[16];
+        memcpy(e, &x, sizeof(x));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = e[i];
+    }
+}
+
+// Rows [from, to) of a sequence and the place of its first one.
+struct LcSequence { int n; int64_t from, to, place; };
+
+// The sequence of row t, by a whole warp; from == to: there is none, or its lengths are no lengths.
+__device__ __forceinline__ LcSequence lc_sequence(const LatentCacheArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    LcSequence s = {0, 0, 0, 0};
+    if (!a.cu) {
+        s.n = (int)(t / a.rows_each);
+        s.from = s.n * a.rows_each;
+        s.to = s.from + a.rows_each;
+    } else {
+        int lo = 0, hi = a.N;                                      // the last n with cu[n] <= t, 32 of them a look
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+            const uint32_t b = __ballot_sync(0xffffffffu, i < hi && a.cu[i] <= t);
+            const int k = b ? 31 - __clz(b) : 0;
+            lo += k * step;
+            hi = min(lo + step, hi);
+        }
+        s.n = lo;
+        s.from = a.cu[lo];
+        s.to = a.cu[lo + 1];
+        if (t < s.from || t >= s.to) s.to = s.from;
+    }
+    const int64_t len = a.lens[s.n];
+    if (len < 0 || len > (int64_t)a.max_pages * a.page_size) s.to = s.from;
+    s.place = len - (s.to - s.from);
+    return s;
+}
+
+// Page and row of it of tokens t .. t + kTokens - 1 (lane i: token t + i), page -1 where there is none.
+template <int kTokens>
+__device__ __forceinline__ void lc_places(const LatentCacheArgs& a, int64_t t, int& page, int& row) {
+    const int lane = threadIdx.x & 31;
+    page = -1;
+    row = 0;
+    int64_t place = -1;
+    int n = 0;
+#pragma unroll 1
+    for (int i = 0; i < kTokens && t + i < a.T;) {
+        const LcSequence s = lc_sequence(a, t + i);
+        const int64_t end = s.to > s.from ? s.to : t + i + 1;
+        if (lane >= i && lane < kTokens && t + lane < s.to && s.to > s.from) {
+            place = s.place + (t + lane - s.from);
+            n = s.n;
+        }
+        i = (int)min64(kTokens, end - t);
+    }
+    if (lane < kTokens && t + lane < a.T && place >= 0) {
+        const int p = a.table[(int64_t)n * a.max_pages + place / a.page_size];
+        if (p >= 0 && p < a.num_pages) {
+            page = p;
+            row = (int)(place % a.page_size);
+        }
+    }
+}
+
+// The status word, by one block: lengths, and the pages that the call's tokens lie in.
+__device__ __forceinline__ void lc_check(const LatentCacheArgs& a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool bad_len = false, bad_page = false;
+    for (int n = warp; n < a.N; n += kLcWarps) {
+        const int64_t from = a.cu ? a.cu[n] : n * a.rows_each, to = a.cu ? a.cu[n + 1] : from + a.rows_each;
+        const int64_t len = a.lens[n];
+        const bool off = from < 0 || to < from || to > a.T || (n == 0 && from != 0) || len < 0 ||
+                         len > (int64_t)a.max_pages * a.page_size;
+        bad_len |= off;
+        if (off || to == from) continue;
+        const int64_t first = len - (to - from) < 0 ? 0 : len - (to - from);
+        for (int64_t p = first / a.page_size + lane; p * a.page_size < len; p += 32) {
+            const int x = a.table[(int64_t)n * a.max_pages + p];
+            bad_page |= x < 0 || x >= a.num_pages;
+        }
+    }
+    bad_len = __syncthreads_or(bad_len);
+    bad_page = __syncthreads_or(bad_page);
+    if (threadIdx.x == 0) *a.status = bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+}
+
+template <typename T, bool kWide, int kTokens>
+__global__ void __launch_bounds__(32 * kLcWarps)
+kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
+    if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = ((int64_t)blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * kTokens;
+    if (t0 >= a.T) return;
+    const bool codes = lane * 16 < a.rank;
+    Lc16<T> x[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        x[i] = {};
+        if (codes && t0 + i < a.T) lc_load<T, kWide>(x[i], (const T*)a.latents + (t0 + i) * a.latent_stride + lane * 16);
+    }
+    int page, row;
+    lc_places<kTokens>(a, t0, page, row);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
+        if (p < 0) continue;
+        T v[16];
+        memcpy(v, &x[i], sizeof(x[i]));
+        float c[16];
+        uint32_t top = 0;                                          // |c| as bits: ordered like the values
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            c[k] = to_f32(v[k]);
+            const uint32_t b = __float_as_uint(c[k]) & 0x7fffffffu;
+            if (b < 0x7f800000u) top = max(top, b);
+            else c[k] = __uint_as_float(0x7fc00000u);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        // max = 1.f 2^(E - 127), 448 = 1.75 2^8
+        int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u);
+        e = min(max(e, kScaleLow), kScaleHigh);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint8_t* base = a.cache + p * a.page_stride;
+        const int width = latent_row_bytes(a.rank, a.d_rope);
+        uint8_t* to = base + (int64_t)r * width;
+        if (codes) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * k] * inv, c[4 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * k + 2] * inv, c[4 * k + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+                w[k] = lo | hi << 16;
+            }
+            *(uint4*)(to + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        const T* rope = (const T*)a.rope + (t0 + i) * a.rope_stride;
+        for (int k = 2 * lane; k < a.d_rope; k += 64) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(to_f32(rope[k]), to_f32(rope[k + 1]));
+            *(uint32_t*)(to + a.rank + 2 * k) = *(const uint32_t*)&h;
+        }
+        if (lane == 0) base[(int64_t)a.page_size * width + r] = (uint8_t)(e + kScaleBias);
+    }
+}
+
+template <typename T, bool kWide, int kTokens>
+__global__ void __launch_bounds__(32 * kLcWarps)
+kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
+    if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = ((int64_t)blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * kTokens;
+    if (t0 >= a.T) return;
+    int page, row;
+    lc_places<kTokens>(a, t0, page, row);
+    const bool codes = lane * 16 < a.rank;
+    const int width = latent_row_bytes(a.rank, a.d_rope);
+    uint4 w[kTokens];
+    uint32_t rope[kTokens][2], e[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
+        if (p < 0) continue;
+        const uint8_t* base = a.cache + p * a.page_stride;
+        const uint8_t* from = base + (int64_t)r * width;
+        if (codes) w[i] = *(const uint4*)(from + lane * 16);
+        e[i] = base[(int64_t)a.page_size * width + r];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * lane + 64 * k < a.d_rope) rope[i][k] = *(const uint32_t*)(from + a.rank + 4 * lane + 128 * k);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (__shfl_sync(0xffffffffu, page, i) < 0) continue;
+        const float s = __uint_as_float(e[i] << 23);               // 2^e
+        if (codes) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            T v[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[k / 2] >> 16 * (k % 2)), __NV_E4M3));
+                const float2 f = __half22float2(h);
+                v[2 * k] = from_f32<T>(f.x * s);
+                v[2 * k + 1] = from_f32<T>(f.y * s);
+            }
+            Lc16<T> x;
+            memcpy(&x, v, sizeof(x));
+            lc_store<T, kWide>(x, (T*)a.latents + (t0 + i) * a.latent_stride + lane * 16);
+        }
+        T* to = (T*)a.rope + (t0 + i) * a.rope_stride;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = 2 * lane + 64 * k;
+            if (c >= a.d_rope) continue;
+            to[c] = from_f32<T>(__uint_as_float(rope[i][k] << 16));
+            to[c + 1] = from_f32<T>(__uint_as_float(rope[i][k] & 0xffff0000u));
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host
+template <typename T, bool kWide, int kTokens>
+static cudaError_t lc_launch_as(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
+    const int64_t blocks = (a.T + kLcWarps * kTokens - 1) / (kLcWarps * kTokens) + (a.status != nullptr);
+    if (write) kda_latent_cache_write_kernel<T, kWide, kTokens><<<(unsigned)blocks, 32 * kLcWarps, 0, stream>>>(a);
+    else kda_latent_cache_read_kernel<T, kWide, kTokens><<<(unsigned)blocks, 32 * kLcWarps, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t lc_launch(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
+    const bool wide = (((uintptr_t)a.latents | (uintptr_t)(a.latent_stride * (int64_t)sizeof(T))) & 15) == 0;
+    // One token a warp until every SM has eight warps, four behind that
+    if (a.T <= 152 * 32) return wide ? lc_launch_as<T, true, 1>(a, write, stream) : lc_launch_as<T, false, 1>(a, write, stream);
+    return wide ? lc_launch_as<T, true, 4>(a, write, stream) : lc_launch_as<T, false, 4>(a, write, stream);
+}
+
+cudaError_t latent_cache_launch(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
+    return a.dtype == KDA_BF16 ? lc_launch<__nv_bfloat16>(a, write, stream) : lc_launch<float>(a, write, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,17 @@
+// kda_latent_cache.cuh -- layout of the quantised cache of latents (kda.h): in a
+// page, rows of rank codes and d_rope bf16 channels, then a scale byte a token.
+#pragma once
+
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int kScaleBias = 127;                 // a token's byte is e + 127, also the exponent bits of 2^e
+constexpr int kScaleLow = -100, kScaleHigh = 120;
+
+__host__ __device__ inline int latent_row_bytes(int rank, int d_rope) { return rank + 2 * d_rope; }
+__host__ __device__ inline int64_t latent_page_bytes(int page_size, int rank, int d_rope) {
+    return ((int64_t)page_size * (latent_row_bytes(rank, d_rope) + 1) + 127) / 128 * 128;
+}
+
+}  // namespace kda

@@ -9,7 +9,10 @@
 //
 // A warp owns a row, its lanes the channels (lane, lane + 32, ...), so a score
 // is one warp reduction.  Bound by that reduction's latency, not by memory.
+#include <cuda_fp8.h>
+
 #include "kda_common.cuh"
+#include "kda_latent_cache.cuh"
 #include "kda_paths.h"
 
 namespace kda {
@@ -107,7 +110,8 @@ cudaError_t latent_status_launch(const int32_t* cu_q, const int32_t* cu_k, int N
 }
 
 // ------------------------------------------------------------- absorbed form
-template <typename T, int KC, int VC>
+// kCodes: the cache is the quantised one (kda_latent_cache.cuh).
+template <typename T, int KC, int VC, bool kCodes>
 __global__ void __launch_bounds__(32 * kSimtWarps)
 kda_latent_decode_simt(LatentDecodeArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -135,10 +139,21 @@ kda_latent_decode_simt(LatentDecodeArgs a) {
             continue;
         }
         const T* kp = (const T*)a.cache + page * a.page_stride + (j % a.page_size) * dqk;
+        const uint8_t* base = (const uint8_t*)a.cache + page * a.page_stride;
+        const int width = latent_row_bytes(a.dk, a.dr);
+        const uint8_t* cp = base + (j % a.page_size) * width;
+        const float worth = kCodes ? __uint_as_float((uint32_t)base[(int64_t)a.page_size * width + j % a.page_size] << 23) : 1.f;
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            const float x = lane + 32 * c < dqk ? to_f32(kp[lane + 32 * c]) : 0.f;
+            const int e = lane + 32 * c;
+            float x = 0.f;
+            if constexpr (kCodes) {
+                if (e < a.dk) x = __half2float(__half(__nv_cvt_fp8_to_halfraw(cp[e], __NV_E4M3))) * worth;
+                else if (e < dqk) x = to_f32(((const __nv_bfloat16*)(cp + a.dk))[e - a.dk]);
+            } else if (e < dqk) {
+                x = to_f32(kp[e]);
+            }
             s += q[c] * x;
             if (c < VC) v[c] = lane + 32 * c < a.dk ? x : 0.f;
         }
@@ -171,10 +186,14 @@ kda_latent_decode_simt(LatentDecodeArgs a) {
 
 cudaError_t latent_decode_simt_launch(const LatentDecodeArgs& a, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.N * a.Lq), (unsigned)a.H);
-    if (a.dtype == KDA_BF16)
-        kda_latent_decode_simt<__nv_bfloat16, 20, 16><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
-    else
-        kda_latent_decode_simt<float, 20, 16><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
+    const bool bf16 = a.dtype == KDA_BF16;
+    if (a.codes) {
+        if (bf16) kda_latent_decode_simt<__nv_bfloat16, 20, 16, true><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
+        else kda_latent_decode_simt<float, 20, 16, true><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
+    } else {
+        if (bf16) kda_latent_decode_simt<__nv_bfloat16, 20, 16, false><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
+        else kda_latent_decode_simt<float, 20, 16, false><<<grid, 32 * kSimtWarps, 0, stream>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -119,6 +119,7 @@ cudaError_t latent_status_launch(const int32_t* cu_q, const int32_t* cu_k, int N
 
 struct LatentDecodeArgs {
     int dtype, N, H, Lq, dk, dr, drop;
+    bool codes;                      // the cache holds codes; page_stride in bytes
     float scale;
     int64_t q_ts, q_hs, page_stride;
     int page_size, num_pages, max_pages;
@@ -135,5 +136,20 @@ bool latent_decode_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_s
 bool latent_decode_tc_aligned(const LatentDecodeArgs& a);
 size_t latent_decode_tc_bytes(int N, int Lq, int H, int page_size, int max_pages);
 cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& a, cudaStream_t stream);
+
+// The quantised cache: rows into pages (write) and out of them.
+struct LatentCacheArgs {
+    int dtype, N, rank, d_rope, page_size, num_pages, max_pages;
+    int64_t T, rows_each;            // rows_each: of a sequence, without cu
+    int64_t page_stride, latent_stride, rope_stride;
+    void *latents, *rope;
+    const int32_t *cu, *table, *lens;
+    uint8_t* cache;
+    int32_t* status;                 // written by the kernel, or nullptr
+};
+cudaError_t latent_cache_launch(const LatentCacheArgs& a, bool write, cudaStream_t stream);
+
+cudaError_t rotary_launch(const kda_rotary_desc& d, const void* x, const void* key, const void* positions,
+                          const double* frequencies, void* out, void* key_out, cudaStream_t stream);
 
 }  // namespace kda

@@ -31,6 +31,10 @@ struct Api {
     decltype(&kda_latent_decode_workspace_bytes) decode_bytes;
     decltype(&kda_latent_prefill) prefill;
     decltype(&kda_latent_decode) decode;
+    decltype(&kda_latent_cache_page_bytes) page_bytes;
+    decltype(&kda_latent_cache_write) cache_write;
+    decltype(&kda_latent_cache_read) cache_read;
+    decltype(&kda_rotary) rotary;
 } api = {};
 
 template <typename... A>
@@ -274,7 +278,24 @@ PyObject* latent_prefill(PyObject* const* p) {
     return pack<2>({o, l});
 }
 
-// latent_decode(q, cache, page_table, lengths, scale, rank (-1: all but 64), flags, out, lse, workspace)
+// The quantised cache: pages of bytes, dense each; page_size, num_pages and the bytes between pages.
+void pages_of(const at::Tensor& c, PyObject* page_size, int64_t rank, int64_t rope, c10::Device dev, int32_t& size, int32_t& pages,
+              int64_t& stride) {
+    if (page_size == Py_None) refuse("a quantised cache needs page_size");
+    size = narrow(integer(page_size), "page_size");
+    if (rank < 1 || rope < 0) refuse("rank and d_rope must be 1 and 0 at least: got ", rank, " and ", rope);
+    const int64_t bytes = api.page_bytes(size, narrow(rank, "rank"), narrow(rope, "d_rope"));
+    if (bytes == 0)
+        refuse("a quantised cache has pages of at least one token, ranks that are multiples of 16 up to 512 and d_rope of 8 up to 128: got ",
+               size, ", ", rank, ", ", rope);
+    if (c.dim() != 2 || c.scalar_type() != at::kByte || c.device() != dev || c.size(1) != bytes || c.stride(1) != 1)
+        refuse("cache must be a [pages, ", bytes, "] Byte tensor on ", dev, " with dense pages: got ", c.sizes(), ", ",
+               c.scalar_type(), ", ", c.device(), ", strides ", c.strides());
+    pages = narrow(c.size(0), "the number of pages");
+    stride = c.size(0) > 1 ? c.stride(0) : bytes;
+}
+
+// latent_decode(q, cache, page_table, lengths, scale, rank (-1: all but 64), flags, out, lse, workspace, page_size)
 PyObject* latent_decode(PyObject* const* p) {
     const at::Tensor &q = tensor(p[0], "q"), &c = tensor(p[1], "cache"), &table = tensor(p[2], "page_table"), &lens = tensor(p[3], "lengths");
     const c10::Device dev = device_of(q, "q");
@@ -287,8 +308,9 @@ PyObject* latent_decode(PyObject* const* p) {
     d.q_head_stride = q.stride(-2);
     d.q_token_stride = lq == 1 ? q.stride(0) : q.stride(1);
     if (lq > 1 && n > 1 && q.stride(0) != lq * d.q_token_stride) refuse("q's sequences and queries must form one strided dimension");
-    if (c.dim() != 3 || c.scalar_type() != type || c.device() != dev || c.size(2) != width || (width > 1 && c.stride(2) != 1) ||
-        (c.size(1) > 1 && c.stride(1) != width))
+    const bool codes = c.scalar_type() == at::kByte;
+    if (!codes && (c.dim() != 3 || c.scalar_type() != type || c.device() != dev || c.size(2) != width ||
+                   (width > 1 && c.stride(2) != 1) || (c.size(1) > 1 && c.stride(1) != width)))
         refuse("cache must be a [pages, page_size, ", width, "] ", type, " tensor on ", dev, " with dense pages: got ", c.sizes(),
                ", ", c.scalar_type(), ", ", c.device(), ", strides ", c.strides());
     int64_t rank = integer(p[5]);
@@ -303,9 +325,16 @@ PyObject* latent_decode(PyObject* const* p) {
     d.flags = narrow(integer(p[6]), "flags");
     d.d_k = d.d_v = narrow(rank, "rank");
     d.d_rope = narrow(width - rank, "d_rope");
-    d.page_size = narrow(c.size(1), "the page size"); d.num_pages = narrow(c.size(0), "the number of pages");
     d.max_pages = narrow(table.size(1), "max_pages");
-    d.page_stride = c.size(0) > 1 ? c.stride(0) : c.size(1) * width;
+    if (codes) {
+        pages_of(c, p[10], rank, width - rank, dev, d.page_size, d.num_pages, d.page_stride);
+        d.flags |= KDA_FLAG_CACHE_8;
+    } else {
+        d.page_size = narrow(c.size(1), "the page size"); d.num_pages = narrow(c.size(0), "the number of pages");
+        d.page_stride = c.size(0) > 1 ? c.stride(0) : c.size(1) * width;
+        if (d.flags & KDA_FLAG_CACHE_8) refuse("flags say a quantised cache, which is a Byte tensor: got ", c.scalar_type());
+        if (p[10] != Py_None && integer(p[10]) != c.size(1)) refuse("page_size is not the cache's: ", c.sizes());
+    }
     const int64_t four[4] = {n, lq, h, rank}, three[3] = {n, h, rank};
     at::Tensor o, l, w;
     if (!latent_buffers(d, api.decode_bytes(&d), maybe(p[7], "out"), maybe(p[8], "lse"), maybe(p[9], "workspace"),
@@ -315,6 +344,139 @@ PyObject* latent_decode(PyObject* const* p) {
                               o.data_ptr(), (float*)l.data_ptr(), stream_of(dev));
     if (rc != KDA_OK) return PyLong_FromLong(rc);
     return pack<2>({o, l});
+}
+
+// Sequences, pages and workspace of a call on the quantised cache.
+void cache_desc(kda_latent_cache_desc& d, const at::Tensor& c, const at::Tensor& table, const at::Tensor& lens, const at::Tensor* cu,
+                PyObject* page_size, const at::Tensor* work, int64_t rank, int64_t rope, c10::Device dev) {
+    d.rank = narrow(rank, "rank");
+    d.d_rope = narrow(rope, "d_rope");
+    pages_of(c, page_size, rank, rope, dev, d.page_size, d.num_pages, d.page_stride);
+    if (table.dim() != 2) refuse("page_table must be [sequences, max_pages]: got ", table.sizes());
+    const int64_t n = table.size(0);
+    dense(table, "page_table", at::kInt, table.sizes(), dev);
+    dense(lens, "lengths", at::kInt, {n}, dev);
+    d.num_seqs = narrow(n, "the number of sequences");
+    d.max_pages = narrow(table.size(1), "max_pages");
+    if (cu) dense(*cu, "cu_seqlens", at::kInt, {n + 1}, dev);
+    else if (d.total_tokens && (n == 0 || d.total_tokens % n)) refuse(d.total_tokens, " rows are not as many for each of ", n, " sequences: cu_seqlens");
+    if (work) {
+        if (!work->is_cuda() || work->device() != dev || !work->is_contiguous()) refuse("workspace must be a contiguous tensor on ", dev);
+        d.workspace = work->data_ptr();
+        d.workspace_bytes = work->nbytes();
+    }
+}
+
+// latent_cache_write(latents, rope, cache, page_table, lengths, cu_seqlens, page_size, workspace)
+PyObject* latent_cache_write(PyObject* const* p) {
+    const at::Tensor &x = tensor(p[0], "latents"), &c = tensor(p[2], "cache"), &table = tensor(p[3], "page_table"), &lens = tensor(p[4], "lengths");
+    const at::Tensor *r = maybe(p[1], "rope"), *cu = maybe(p[5], "cu_seqlens"), *work = maybe(p[7], "workspace");
+    const c10::Device dev = device_of(x, "latents");
+    kda_latent_cache_desc d = {};
+    d.dtype = dtype_of(x, "latents");
+    rows(x, "latents", x.scalar_type(), 2, dev);
+    d.total_tokens = x.size(0);
+    d.latent_stride = row_stride(x, x.size(1));
+    if (r) {
+        rows(*r, "rope", x.scalar_type(), 2, dev);
+        if (r->size(0) != x.size(0)) refuse("rope must have the latents' rows: got ", r->sizes());
+        d.rope_stride = row_stride(*r, r->size(1));
+    }
+    cache_desc(d, c, table, lens, cu, p[6], work, x.size(1), r ? r->size(1) : 0, dev);
+    const int rc = api.cache_write(&d, x.data_ptr(), data<const void>(r), data<const int32_t>(cu), (const int32_t*)table.data_ptr(),
+                                   (const int32_t*)lens.data_ptr(), (uint8_t*)c.data_ptr(), stream_of(dev));
+    if (rc != KDA_OK) return PyLong_FromLong(rc);
+    Py_RETURN_NONE;
+}
+
+// latent_cache_read(cache, page_table, lengths, cu_seqlens, total_tokens, page_size, rank, d_rope, out is bf16, latents, rope, workspace)
+PyObject* latent_cache_read(PyObject* const* p) {
+    const at::Tensor &c = tensor(p[0], "cache"), &table = tensor(p[1], "page_table"), &lens = tensor(p[2], "lengths");
+    const at::Tensor *cu = maybe(p[3], "cu_seqlens"), *given = maybe(p[9], "latents"), *given_rope = maybe(p[10], "rope"),
+                     *work = maybe(p[11], "workspace");
+    const c10::Device dev = device_of(c, "cache");
+    const int64_t t = integer(p[4]), rank = integer(p[6]), rope = integer(p[7]);
+    if (t < 0) refuse("total_tokens must not be negative: got ", t);
+    kda_latent_cache_desc d = {};
+    d.total_tokens = t;
+    const at::ScalarType type = given ? given->scalar_type() : given_rope ? given_rope->scalar_type() : truth(p[8], "dtype") ? at::kBFloat16 : at::kFloat;
+    cache_desc(d, c, table, lens, cu, p[5], work, rank, rope, dev);
+    at::Tensor x, r;
+    if (given) {
+        rows(*given, "latents", type, 2, dev);
+        if (given->size(0) != t || given->size(1) != rank) refuse("latents must be [", t, ", ", rank, "]: got ", given->sizes());
+        x = *given;
+    } else {
+        x = fresh({t, rank}, type, dev);
+    }
+    if (given_rope) {
+        rows(*given_rope, "rope", type, 2, dev);
+        if (rope == 0 || given_rope->size(0) != t || given_rope->size(1) != rope) refuse("rope must be [", t, ", ", rope, "]: got ", given_rope->sizes());
+        r = *given_rope;
+    } else if (rope) {
+        r = fresh({t, rope}, type, dev);
+    }
+    d.dtype = dtype_of(x, "latents");
+    d.latent_stride = row_stride(x, rank);
+    d.rope_stride = rope ? row_stride(r, rope) : 0;
+    const int rc = api.cache_read(&d, (const uint8_t*)c.data_ptr(), (const int32_t*)table.data_ptr(), (const int32_t*)lens.data_ptr(),
+                                  data<const int32_t>(cu), x.data_ptr(), rope ? r.data_ptr() : nullptr, stream_of(dev));
+    if (rc != KDA_OK) return PyLong_FromLong(rc);
+    return pack<2>({x, r});
+}
+
+// One tensor of a rotary call, [tokens, heads, width] or [tokens, width], and its output.
+at::Tensor rotary_one(const at::Tensor& x, const char* name, const at::Tensor* out, const char* out_name, PyObject* offset, int64_t tokens,
+                      int64_t dim, at::ScalarType type, c10::Device dev, kda_rotary_part& d) {
+    if (x.dim() != 2 && x.dim() != 3) refuse(name, " must be [tokens, heads, channels] or [tokens, channels]: got ", x.sizes());
+    rows(x, name, type, x.dim(), dev);
+    if (x.size(0) != tokens) refuse(name, " must have a row for each of ", tokens, " positions: got ", x.sizes());
+    const int64_t width = x.size(-1), heads = x.dim() == 3 ? x.size(1) : 1;
+    const int64_t at = offset == Py_None ? width - dim : integer(offset);
+    if (dim > width || at < 0 || at > width - dim) refuse(dim, " channels from ", at, " on are not within ", name, "'s ", width);
+    if (heads < 1) refuse(name, " must have heads: got ", x.sizes());
+    if (out) {
+        rows(*out, out_name, type, x.dim(), dev);
+        if (out->sizes() != x.sizes()) refuse(out_name, " must have the shape ", x.sizes(), ": got ", out->sizes());
+    }
+    const at::Tensor y = out ? *out : fresh(x.sizes(), type, dev);
+    d.heads = narrow(heads, "the number of heads");
+    d.width = narrow(width, "the channels of a head");
+    d.offset = narrow(at, "offset");
+    // (sizes of one may carry any stride)
+    d.token_stride = tokens > 1 ? x.stride(0) : heads * width;
+    d.out_token_stride = tokens > 1 ? y.stride(0) : heads * width;
+    d.head_stride = heads > 1 ? x.stride(1) : width;
+    d.out_head_stride = heads > 1 ? y.stride(1) : width;
+    return y;
+}
+
+// rotary(x, positions, frequencies, key, offset, key_offset, scale, flags, out, key_out)
+PyObject* rotary(PyObject* const* p) {
+    const at::Tensor &x = tensor(p[0], "x"), &pos = tensor(p[1], "positions"), &f = tensor(p[2], "frequencies");
+    const at::Tensor *key = maybe(p[3], "key"), *out = maybe(p[8], "out"), *key_out = maybe(p[9], "key_out");
+    const c10::Device dev = device_of(x, "x");
+    kda_rotary_desc d = {};
+    d.dtype = dtype_of(x, "x");
+    if (pos.dim() != 1 || (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong)) refuse("positions must be [tokens] int32 or int64: got ", pos.sizes(), ", ", pos.scalar_type());
+    dense(pos, "positions", pos.scalar_type(), pos.sizes(), dev);
+    if (f.dim() != 1 || f.size(0) < 1) refuse("frequencies must be [channels / 2]: got ", f.sizes());
+    dense(f, "frequencies", at::kDouble, f.sizes(), dev);
+    const int64_t tokens = pos.size(0), dim = 2 * f.size(0);
+    d.tokens = tokens;
+    d.dim = narrow(dim, "the channels turned");
+    d.scale = (float)number(p[6], "scale");
+    d.flags = narrow(integer(p[7]), "flags") | (pos.scalar_type() == at::kLong ? KDA_FLAG_POSITIONS_64 : 0);
+    if (key_out && !key) refuse("key_out without a key");
+    const at::Tensor y = rotary_one(x, "x", out, "out", p[4], tokens, dim, x.scalar_type(), dev, d.x);
+    at::Tensor ky;
+    if (key) ky = rotary_one(*key, "key", key_out, "key_out", p[5], tokens, dim, x.scalar_type(), dev, d.key);
+    if (tokens) {
+        const int rc = api.rotary(&d, x.data_ptr(), data<const void>(key), pos.data_ptr(), (const double*)f.data_ptr(), y.data_ptr(),
+                                  key ? ky.data_ptr() : nullptr, stream_of(dev));
+        if (rc != KDA_OK) return PyLong_FromLong(rc);
+    }
+    return pack<2>({y, ky});
 }
 
 // bind(addresses of the C entry points, in Api's order)
@@ -346,8 +508,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 #define KDA_METHOD(f, n) {#f, (PyCFunction)(void*)(&entry<f, n>), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {KDA_METHOD(bind, 6), KDA_METHOD(rms_norm, 7), KDA_METHOD(matmul_fp8, 7), KDA_METHOD(latent_prefill, 11),
-                         KDA_METHOD(latent_decode, 10), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {KDA_METHOD(bind, 10), KDA_METHOD(rms_norm, 7), KDA_METHOD(matmul_fp8, 7), KDA_METHOD(latent_prefill, 11),
+                         KDA_METHOD(latent_decode, 11), KDA_METHOD(latent_cache_write, 8), KDA_METHOD(latent_cache_read, 12),
+                         KDA_METHOD(rotary, 10), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
