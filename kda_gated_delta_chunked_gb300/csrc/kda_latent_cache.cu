@@ -163,9 +163,7 @@ kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
             else c[k] = __uint_as_float(0x7fc00000u);
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        // max = 1.f 2^(E - 127), 448 = 1.75 2^8
-        int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u);
-        e = min(max(e, kScaleLow), kScaleHigh);
+        const int e = latent_exponent(top);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t* base = a.cache + p * a.page_stride;
         const int width = latent_row_bytes(a.rank, a.d_rope);

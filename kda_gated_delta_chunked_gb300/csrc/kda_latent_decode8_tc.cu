@@ -1,0 +1,560 @@
+// kda_latent_decode8_tc.cu -- absorbed latent attention over the quantised cache on
+// the tensor cores (bf16 queries, rank 512 + 64 rotary channels): the matrix
+// instructions take the cache's e4m3 codes as they are.
+//
+// Token t's latent is 2^e_t c_t with codes c_t, so
+//
+//     s_tr = 2^e_t (c_t . q_r) + rope_t . q_r,    o_r = sum_t (p_tr 2^e_t) c_t / sum_t p_tr
+//
+// The other operand has to be of 8 bits too, so it is split into several values
+// that add up to it:
+//   - a query's channel is 2^x (q1 + q2 / 16) with e4m3 q1, q2 and one x a row: the
+//     8 bits of a bf16 exactly, down to 2^-14 of steps where the row's largest is
+//     224 to 448 (e4m3's subnormals).  q1 and q2 are columns of one product.
+//   - a weight P = p 2^e is p1 + p2 / 8 + p3 / 64 in e5m2, each the rest of the one
+//     before: three bits each, off by 2^-8.7 (bf16: 2^-8), for weights down to 2^-21
+//     of the largest and 2^-30 of that below.  e5m2 for its range: the tokens behind
+//     a dominant one are many and small, and would be lost in e4m3's.
+//
+//     S^T [128 tokens, q1 | q2 | rope: 3 x 32]  = C Q^T        16 + 4 instructions
+//     O^T [4 x 128 channels, p1 | p2 | p3: 3 x 32] += C^T P^T  4 x 4 instructions
+//
+// The rotary channels are bf16 and have columns of their own.  Both products read
+// the same tile in shared memory, the second as an MN-major operand: a tile is
+// fetched once, 641 bytes a token.  A thread owns a token, so its scale is a
+// thread's number.  The softmax reference of a row bounds P (not p): it moves when
+// some P exceeds it by 2^8, and stands at 2^7, a 2^8 below e5m2's largest power.
+//
+// CTAs have groups of 32 query rows; how the tiles are shared out, and the joining
+// of the pieces, are kda_latent_decode_tc.cu's.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "kda_latent_cache.cuh"
+#include "kda_latent_decode.cuh"
+#include "kda_per_device.h"
+#include "kda_tensor_map.h"
+
+namespace kda {
+
+constexpr int kL8Rows = 32;                                  // query rows of a CTA
+constexpr int kL8Threads = 384;                              // 4 softmax warps, producer, two products, scales, 4 for the queries
+constexpr int kL8Width = latent_row_bytes(kLdRank, kLdWidth - kLdRank);    // bytes of a token's row
+constexpr float kL8Slack = 8.f, kL8Stand = 7.f;              // how far (log2) a weight may exceed its reference; the reference's
+constexpr uint32_t kL8Piece = kLdTile * 128;                 // 128 bytes of each token: 128 codes, or the rotary channels
+constexpr int kL8Pieces = 5, kL8Tiles = 2;
+constexpr uint32_t kL8QPiece = 2 * kL8Rows * 128;            // 128 codes of q1 and q2
+constexpr uint32_t kL8P = kLdTile * kL8Rows;                 // one of p1, p2, p3
+constexpr uint32_t kL8OffQ = kL8Tiles * kL8Pieces * kL8Piece, kL8OffRope = kL8OffQ + 4 * kL8QPiece,
+                   kL8OffP = kL8OffRope + kL8Rows * 128, kL8OffSmall = kL8OffP + 2 * 3 * kL8P;
+constexpr int kL8Scales = 4;                                 // segments whose rows' scales are held
+constexpr uint32_t kL8Smem = 1024 + kL8OffSmall + (3 + 8 + kL8Scales) * kL8Rows * 4 + 2 * kLdTile + 512;
+static_assert(kL8Smem <= 232448, "shared memory of a block");
+constexpr uint32_t kL8O = 3 * kL8Rows;                       // first TMEM column of O^T, 96 a block of 128 channels
+
+struct L8Args {
+    LdArgs a;
+    int64_t q_ts, q_hs, page_stride;
+    const __nv_bfloat16* q;
+    const uint8_t* cache;
+};
+
+// kind::f8f6f4 with fp32 D; A e4m3; B e4m3 or (b_wide) e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn, int b_wide) {
+    return idesc_e4m3(M, N) | ((uint32_t)b_wide << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+}
+// 16-byte piece c of token row r of a P^T (32-byte swizzle).
+__device__ __forceinline__ uint32_t l8_p_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
+
+// Four weights to a word of e5m2 each: p1, what is left of it (times 8) as p2, and of that as p3.
+__device__ __forceinline__ void l8_split(const float (&p)[4], uint32_t& w1, uint32_t& w2, uint32_t& w3) {
+    uint32_t a[3][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (k > 0) h = __hmul2(h, __half2(__float2half(8.f), __float2half(8.f)));
+            const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E5M2);
+            a[k][i] = c;
+            const uint32_t back = __byte_perm(c, 0, 0x1404);       // an e5m2 is the upper byte of a half
+            if (k < 2) h = __hsub2(h, *(const __half2*)&back);
+        }
+    }
+    w1 = a[0][0] | a[0][1] << 16;
+    w2 = a[1][0] | a[1][1] << 16;
+    w3 = a[2][0] | a[2][1] << 16;
+}
+
+__global__ void __launch_bounds__(kL8Threads, 1)
+kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ L8Args b) {
+    constexpr int R = kL8Rows;
+    const LdArgs& a = b.a;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    float* ref = (float*)(mem + kL8OffSmall);          // [R] softmax references (log2)
+    float* fac = ref + R;                              // [R] factors of a moved reference
+    int* query = (int*)(fac + R);                      // [R] query a row belongs to
+    float* across = (float*)(query + R);               // [4][R] one value a warp and row
+    float* sums = across + 4 * R;                      // [4][R]
+    float* worth = sums + 4 * R;                       // [kL8Scales][R] what a unit of a row's q1 is worth (log2 scores)
+    uint8_t* scales = (uint8_t*)(worth + kL8Scales * R);           // [2][128] bytes of a tile's tokens
+    uint64_t* bars = (uint64_t*)(scales + 2 * kLdTile);
+    constexpr int kRing = kL8Tiles * kL8Pieces;
+    uint64_t *full = bars, *empty = full + kRing, *q_full = empty + kRing, *q_empty = q_full + 1, *s_full = q_empty + 1,
+             *s_empty = s_full + 1, *o_full = s_empty + 1, *p_full = o_full + 2, *c_full = p_full + 2, *bars_end = c_full + 2;
+    uint32_t* tmem_at = (uint32_t*)bars_end;
+    int* range = (int*)(tmem_at + 1);                  // first sequence, its first tile, tiles
+    int* fault = range + 3;
+    int64_t* range_at = (int64_t*)(((uintptr_t)(fault + 1) + 7) & ~(uintptr_t)7);   // index of the first tile
+
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int group = blockIdx.x, cta = blockIdx.y;
+    if (warp == 4) {
+        const int len = lane < a.N ? a.lens[lane] : 0;                 // on its way while the barriers are made
+        if (lane < bars_end - bars) {
+            const uint64_t* x = bars + lane;
+            const int arrivals = x == q_full || x == s_empty || x == p_full || x == p_full + 1 ? 4 : 1;
+            mbar_init(bars + lane, arrivals + (a.drop >> lane & 1));
+        }
+        if (lane == 0) prefetch_map(&map);
+        fence_mbar_init();
+        const LdCut cut = ld_cut(a, cta, lane, len);
+        if (lane == 0) {
+            range[0] = cut.n; range[1] = cut.j; range[2] = cut.count;
+            if (cta == 0 && group == 0) a.before[a.N] = cut.total;
+            *fault = cut.bad ? kLdBadLen : 0;
+            *range_at = cut.at;
+        }
+        __syncwarp();
+    } else {
+        if (warp == 0) { tmem_alloc(tmem_at, 512); tmem_relinquish(); }
+        if (threadIdx.x < R) {
+            ref[threadIdx.x] = kLdUnset;
+            query[threadIdx.x] = min((group * R + (int)threadIdx.x) / a.H, a.Lq - 1);
+        }
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
+    LdWalk w;
+    w.start(a, range[0], range[1], range[2]);
+    const int count = w.left;
+    const int row0 = group * R, live = min(R, a.rows - row0);
+
+    if (warp == 4) {                                                   // ---------------- producer
+        const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
+        bool ok = true, bad_page = false;
+        // A lane for each box of tokens: its page and row.  Pages behind the length, and bad ones, read as zeros.
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
+            int row = 0, page = a.num_pages;
+            if (lane < boxes) {
+                const int t = w.j * kLdTile + lane * box;
+                if (t < ld_len(a, w.n)) {
+                    const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
+                    if (p < 0 || p >= a.num_pages) bad_page = true;
+                    else { page = p; row = t % a.page_size; }
+                }
+            }
+            const int at = j % kL8Tiles * kL8Pieces;
+            for (int k = 0; k < kL8Pieces; ++k) {
+                const int u = k == 0 ? 4 : k - 1;                      // the rotary channels first, they are free first
+                if (!(ok = mbar_wait_warp(&empty[at + u], (j / kL8Tiles + 1) & 1))) break;   // (a fresh barrier counts as emptied)
+                if (lane == 0) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, row, page, smem_u32(&full[at + u]));
+                __syncwarp();
+            }
+        }
+        if (bad_page) atomicOr(fault, kLdBadPage);
+        if (!ok) atomicOr(fault, kLdLate);
+    } else if (warp == 5) {                                            // ---------------- S^T
+        constexpr uint32_t codes = idesc_f8(128, 2 * R, 0, 0, 0), rope = idesc_bf16(128, R);
+        const uint64_t dq = sdesc_k_sw128(base + kL8OffQ), dr = sdesc_k_sw128(base + kL8OffRope);
+        uint32_t seg = 0;
+        bool ok = true;
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
+            if (w.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
+            if (ok && j >= 1) ok = mbar_wait_warp(s_empty, (j - 1) & 1);           // S_{j-1} is read
+            const int at = j % kL8Tiles * kL8Pieces;
+            for (int k = 0; k < kL8Pieces && ok; ++k) {
+                const int u = k == 0 ? 4 : k - 1;
+                if (!(ok = mbar_wait_warp(&full[at + u], (j / kL8Tiles) & 1))) break;
+                tc_fence_after_sync();
+                const uint64_t da = sdesc_k_sw128(base + (at + u) * kL8Piece);
+                if (elect_one()) {
+                    if (u == 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_bf16_ss(tmem + 2 * R, da + 2 * i, dr + 2 * i, rope, i > 0);
+                        mma_commit(&empty[at + u]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_f8_ss(tmem, da + 2 * i, dq + u * (kL8QPiece / 16) + 2 * i, codes, u > 0 || i > 0);
+                    }
+                    if (u == 3) {
+                        mma_commit(s_full);
+                        if (w.last()) mma_commit(q_empty);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) atomicOr(fault, kLdLate);
+    } else if (warp == 6) {                                            // ---------------- O^T += C^T P^T
+        constexpr uint32_t wide = idesc_f8(128, 3 * R, 1, 1, 1);
+        bool ok = true;
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
+            if (!(ok = mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
+            tc_fence_after_sync();
+            const int at = j % kL8Tiles * kL8Pieces;
+            // p1, p2 and p3 lie a swizzle atom of 32 rows apart each; 8 tokens 256 bytes
+            const uint64_t dp = sdesc(base + kL8OffP + (j & 1) * 3 * kL8P, kL8P, 256, 6);
+            for (int u = 0; u < 4; ++u) {
+                if (!(ok = mbar_wait_warp(&full[at + u], (j / kL8Tiles) & 1))) break;
+                const uint64_t da = sdesc(base + (at + u) * kL8Piece, kL8Piece, 1024, 2);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_f8_ss(tmem + kL8O + u * 3 * R, da + i * (4096 / 16), dp + i * (1024 / 16), wide, !w.first || i > 0);
+                    mma_commit(&empty[at + u]);
+                    if (u == 3) mma_commit(&o_full[j & 1]);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) atomicOr(fault, kLdLate);
+    } else if (warp == 7) {                                            // ---------------- scales
+        // Four tokens' bytes a lane, fetched a tile ahead; 0 (2^-127) where there is nothing.
+        auto fetch = [&](const LdWalk& x) -> uint32_t {
+            const int t = x.j * kLdTile + 4 * lane;
+            if (x.left <= 0 || t >= ld_len(a, x.n)) return 0;
+            const int p = a.table[(int64_t)x.n * a.max_pages + t / a.page_size];
+            if (p < 0 || p >= a.num_pages) return 0;
+            return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + t % a.page_size);
+        };
+        bool ok = true;
+        uint32_t now = fetch(w);
+        for (int j = 0; j < count && ok; ++j) {
+            w.next(a);
+            const uint32_t ahead = fetch(w);
+            if (j >= 2) ok = mbar_wait_warp(&p_full[j & 1], ((j - 2) >> 1) & 1);    // tile j - 2's bytes are read
+            if (!ok) break;
+            *(uint32_t*)(scales + (j & 1) * kLdTile + 4 * lane) = now;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[j & 1]);
+            now = ahead;
+        }
+        if (!ok) atomicOr(fault, kLdLate);
+    } else if (warp >= 8) {                                            // ---------------- queries
+        const float sc = a.scale * 1.4426950408889634f;
+        uint32_t seg = 0;
+        bool ok = true;
+        for (int j = 0; j < count && ok; ++j, w.next(a)) {
+            if (!w.first) continue;
+            uint4 x[R / 4][2];
+            uint32_t rope[R / 4];
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) {
+                const int r = (warp - 8) + 4 * i;
+                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                rope[i] = 0;
+                if (r < live) {
+                    const int qi = (row0 + r) / a.H, h = (row0 + r) - qi * a.H;
+                    const __nv_bfloat16* from = b.q + ((int64_t)w.n * a.Lq + qi) * b.q_ts + h * b.q_hs;
+                    x[i][0] = ((const uint4*)from)[2 * lane];
+                    x[i][1] = ((const uint4*)from)[2 * lane + 1];
+                    rope[i] = ((const uint32_t*)(from + kLdRank))[lane];
+                }
+            }
+            if (seg > 0 && !(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) {
+                const int r = (warp - 8) + 4 * i;
+                const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                float f[16];
+                uint32_t top = 0;                                      // largest finite channel, as bits
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    f[k] = __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
+                    const uint32_t m = __float_as_uint(f[k]) & 0x7fffffffu;
+                    if (m < 0x7f800000u) top = max(top, m);
+                    else f[k] = __uint_as_float(0x7fc00000u);          // (an infinite channel counts as NaN)
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                const int e = latent_exponent(top);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                uint32_t q1[4], q2[4];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float lo = f[2 * k] * inv, hi = f[2 * k + 1] * inv;
+                    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+                    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
+                    const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2((lo - back.x) * 16.f, (hi - back.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+                    q1[k / 2] = k % 2 ? q1[k / 2] | c << 16 : c;
+                    q2[k / 2] = k % 2 ? q2[k / 2] | d << 16 : d;
+                }
+                const int swz = r & 7;
+                uint8_t* to = mem + kL8OffQ + (lane / 8) * kL8QPiece + r * 128 + ((lane & 7) ^ swz) * 16;
+                *(uint4*)to = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+                *(uint4*)(to + R * 128) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+                *(uint32_t*)(mem + kL8OffRope + r * 128 + ((lane / 4) ^ swz) * 16 + lane % 4 * 4) = rope[i];
+                if (lane == 0) worth[seg % kL8Scales * R + r] = __uint_as_float((uint32_t)(127 + e) << 23) * sc;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            ++seg;
+        }
+        if (!ok) atomicOr(fault, kLdLate);
+    } else {                                                           // ---------------- softmax
+        const uint32_t lanes = tmem_addr(tmem, 32 * warp, 0);
+        const float sc = a.scale * 1.4426950408889634f;
+        float l[R];
+#pragma unroll
+        for (int c = 0; c < R; ++c) l[c] = 0.f;
+        bool ok = true;
+        uint32_t seg = 0;
+        for (int j = 0; j < count; ++j, w.next(a)) {
+            if (w.first) {
+                if (w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+                ++seg;
+            }
+            ok = bar_and(128, mbar_wait_spin(s_full, j & 1) && mbar_wait_spin(&c_full[j & 1], (j >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const int len = ld_len(a, w.n);
+            const int token = w.j * kLdTile + (int)threadIdx.x;
+            const int byte = scales[(j & 1) * kLdTile + threadIdx.x];
+            const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
+            const float* unit = worth + (seg - 1) % kL8Scales * R;
+            // y: log2 of the weight times 2^e
+            float y[R];
+#pragma unroll
+            for (int h = 0; h < R; h += 16) {
+                float d1[16], d2[16], dr[16];
+                tmem_ld16(lanes + h, d1);
+                tmem_ld16(lanes + R + h, d2);
+                tmem_ld16(lanes + 2 * R + h, dr);
+                tmem_wait_ld();
+                tmem_ready(d1);
+                tmem_ready(d2);
+                tmem_ready(dr);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) y[h + c] = fmaf(fmaf(d2[c], 0.0625f, d1[c]), two * unit[h + c], fmaf(dr[c], sc, e));
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty);
+            if ((w.j + 1) * kLdTile > len - a.Lq + 1) {                // some row does not see some token
+#pragma unroll
+                for (int c = 0; c < R; ++c)
+                    if (token > len - a.Lq + query[c]) y[c] = -INFINITY;
+            }
+            bool over = false;
+#pragma unroll
+            for (int c = 0; c < R; c += 4) {
+                const float4 m = *(const float4*)(ref + c);
+                over |= y[c] > m.x + kL8Slack || y[c + 1] > m.y + kL8Slack || y[c + 2] > m.z + kL8Slack ||
+                        y[c + 3] > m.w + kL8Slack;
+            }
+            if (!bar_and(128, !over)) {                                // move the references to the maxima
+                ld_columns<R, true>(y, across + warp * R, lane);
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (threadIdx.x < R) {
+                    const int c = threadIdx.x;
+                    const float old = ref[c];
+                    const float now = fmaxf(old, fmaxf(fmaxf(across[c], across[R + c]),
+                                                       fmaxf(across[2 * R + c], across[3 * R + c])));
+                    ref[c] = now;
+                    fac[c] = ex2(old - now);
+                }
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < R; ++c) l[c] *= fac[c];
+                if (!w.first) {                                        // O^T, once the products into it are complete
+                    ok = bar_and(128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    for (int p = 0; p < 12; ++p) {
+                        for (int h = 0; h < R; h += 16) {
+                            float o[16];
+                            tmem_ld16(lanes + kL8O + p * R + h, o);
+                            tmem_wait_ld();
+                            tmem_ready(o);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[c] *= fac[h + c];
+                            tmem_st16(lanes + kL8O + p * R + h, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+            }
+            if (j >= 2) {                                              // P's buffer: the products that read it are complete
+                ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
+                if (!ok) {                                             // the other warps leave at their next vote, with this one
+                    bar_and(128, false);
+                    break;
+                }
+            }
+            const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
+            uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P;
+#pragma unroll
+            for (int c = 0; c < R; c += 16) {
+                uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 m = *(const float4*)(ref + c + 4 * i);
+                    const float mm[4] = {m.x, m.y, m.z, m.w};
+                    float p[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        p[k] = ex2(y[c + 4 * i + k] - mm[k] + kL8Stand);
+                        l[c + 4 * i + k] = fmaf(p[k], down, l[c + 4 * i + k]);
+                    }
+                    l8_split(p, p1[i], p2[i], p3[i]);
+                }
+                const uint32_t at = l8_p_at(threadIdx.x, c / 16);
+                *(uint4*)(to + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                *(uint4*)(to + kL8P + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                *(uint4*)(to + 2 * kL8P + at) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+            }
+            // Weight 0 times what lies behind the length: make that 0
+            if (token >= len) {
+                uint8_t* at = mem + (j % kL8Tiles) * kL8Pieces * kL8Piece + threadIdx.x * 128;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *(uint4*)(at + u * kL8Piece + ((i + threadIdx.x) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[j & 1]);
+            if (!w.last()) continue;
+
+            // end of a segment: sums across the tokens' threads, then O^T out
+            ld_columns<R, false>(l, sums + warp * R, lane);
+            ok = bar_and(128, mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const bool whole = w.from == 0 && w.j + 1 == w.tiles;
+            float* dst = a.parts + ((size_t)(cta * gridDim.x + group) * 2 + (w.from == 0)) * R * kLdPart;
+            if (threadIdx.x < R) {
+                const int c = threadIdx.x;
+                const float total = (sums[c] + sums[R + c]) + (sums[2 * R + c] + sums[3 * R + c]);
+                if (whole) {
+                    fac[c] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+                    if (c < live && a.lse) a.lse[(size_t)w.n * a.rows + row0 + c] =
+                        total == 0.f ? -INFINITY : (ref[c] - kL8Stand + log2f(total)) * 0.6931471805599453f;
+                } else {
+                    dst[c * kLdPart + kLdRank] = ref[c] - kL8Stand;
+                    dst[c * kLdPart + kLdRank + 1] = total;
+                }
+            }
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+                const int ch = p * 128 + threadIdx.x;
+#pragma unroll
+                for (int h = 0; h < R; h += 16) {
+                    float o[16], o2[16], o3[16];
+                    const uint32_t from = lanes + kL8O + p * 3 * R + h;
+                    tmem_ld16(from, o);
+                    tmem_ld16(from + R, o2);
+                    tmem_ld16(from + 2 * R, o3);
+                    tmem_wait_ld();
+                    tmem_ready(o);
+                    tmem_ready(o2);
+                    tmem_ready(o3);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
+                    if (whole) {
+                        __nv_bfloat16* out = a.out + ((size_t)w.n * a.rows + row0 + h) * kLdRank + ch;
+                        if (h + 16 <= live) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[h + c]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (h + c < live) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[h + c]);
+                        }
+                    } else {                                           // (dead rows too: a condition a store costs more)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) dst[(h + c) * kLdPart + ch] = o[c];
+                    }
+                }
+            }
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+            if (threadIdx.x < R) ref[threadIdx.x] = kLdUnset;
+#pragma unroll
+            for (int c = 0; c < R; ++c) l[c] = 0.f;
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+        }
+        if (!ok) {
+            // The join finds the pieces by where the sequences start, those of the tiles that were left among them.
+            w.start(a, range[0], range[1], range[2]);
+            for (int j = 0; j < count; ++j, w.next(a))
+                if (w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+            atomicOr(fault, kLdLate);
+        }
+    }
+    tc_fence_before_sync();
+    meet_at_end(fault);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0) a.cta_status[cta * gridDim.x + group] = *fault;
+}
+
+// ------------------------------------------------------------------- host
+bool latent_decode8_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_size) {
+    return dtype == KDA_BF16 && dk == kLdRank && dr == kLdWidth - kLdRank && page_size >= 8 &&
+           (page_size & (page_size - 1)) == 0 && (int64_t)Lq * H <= 32 * 1024;
+}
+size_t latent_decode8_tc_bytes(int N, int Lq, int H, int page_size, int max_pages) {
+    return N > 0 ? ld_plan(N, Lq, H, page_size, max_pages, kL8Rows).bytes : 0;
+}
+// What the tensor map and the vectors need of the call's tensors.
+bool latent_decode8_tc_aligned(const LatentDecodeArgs& d) {
+    return (((uintptr_t)d.q | (uintptr_t)d.cache | (uintptr_t)d.out) & 15) == 0 &&
+           (d.q_ts % 8 == 0 || (int64_t)d.N * d.Lq == 1) && (d.q_hs % 8 == 0 || d.H == 1) && d.num_pages > 0 &&
+           d.page_stride < (1ll << 39);
+}
+
+cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {
+    static PerDevice memory_set;
+    int device = 0, set = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = memory_set.get(device, set, [](int& done) {
+        done = 1;
+        return cudaFuncSetAttribute(kda_latent_decode8_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kL8Smem);
+    });
+    if (err != cudaSuccess) return err;
+    const LdPlan p = ld_plan(d.N, d.Lq, d.H, d.page_size, d.max_pages, kL8Rows);
+    L8Args b;
+    LdArgs& a = b.a;
+    a.N = d.N; a.H = d.H; a.Lq = d.Lq; a.rows = d.Lq * d.H; a.page_size = d.page_size; a.num_pages = d.num_pages;
+    a.max_pages = d.max_pages; a.scale = d.scale; a.table = d.table; a.lens = d.lens; a.out = (__nv_bfloat16*)d.out;
+    a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
+    a.before = (int64_t*)((char*)d.scratch + p.before);
+    a.parts = (float*)((char*)d.scratch + p.parts);
+    // the barriers' order: full, empty, q_full, q_empty, s_full, s_empty, o_full [2], p_full [2], c_full [2]
+    constexpr int kAt = 2 * kL8Tiles * kL8Pieces;
+    constexpr uint32_t kDrops[6] = {0, (1u << kAt / 2) - 1, 1u << (kAt + 2), 3u << (kAt + 4), 3u << (kAt + 6), 1u << kAt | 3u << (kAt + 8)};
+    a.drop = kDrops[d.drop];
+    b.q = (const __nv_bfloat16*)d.q; b.q_ts = d.q_ts; b.q_hs = d.q_hs;
+    b.cache = (const uint8_t*)d.cache; b.page_stride = d.page_stride;
+    CUtensorMap map;
+    const uint64_t dims[3] = {(uint64_t)kL8Width, (uint64_t)d.page_size, (uint64_t)d.num_pages};
+    const uint64_t strides[2] = {(uint64_t)kL8Width, (uint64_t)d.page_stride};
+    const uint32_t box[3] = {128, (uint32_t)(d.page_size < kLdTile ? d.page_size : kLdTile), 1};
+    if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, d.cache, dims, strides, box)) return cudaErrorInvalidValue;
+    kda_latent_decode8_tc<<<dim3(p.groups, p.G), kL8Threads, kL8Smem, stream>>>(map, b);
+    err = cudaGetLastError();
+    return err != cudaSuccess ? err : latent_decode_join_launch(a, kL8Rows, p.groups, stream);
+}
+
+}  // namespace kda

@@ -42,22 +42,15 @@
 // order, and what alternates between tiles has a barrier for odd and even ones.
 #include <math.h>
 
-#include "kda_common.cuh"
-#include "kda_paths.h"
+#include "kda_latent_decode.cuh"
 #include "kda_per_device.h"
-#include "kda_sm100_ops.cuh"
 #include "kda_tensor_map.h"
 
 namespace kda {
-using namespace sm100;
 
-constexpr int kLdTile = 128;                  // tokens of a tile
-constexpr int kLdRank = 512, kLdWidth = 576;
 constexpr uint32_t kLdPiece = kLdTile * 128;  // 64 channels of a tile
 constexpr int kLdThreads = 256;               // 4 softmax warps, 2 producers, a warp for each product
-constexpr float kLdUnset = -1e30f;            // reference of a row that has seen no key
 constexpr float kLdSlack = 8.f;               // how far (log2) a score may exceed its reference
-constexpr int kLdLate = 1, kLdBadLen = 2, kLdBadPage = 4;   // bits of a CTA's status
 
 template <int R>
 struct LdShape {
@@ -79,73 +72,6 @@ struct LdShape {
              : R == 32 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 128 + ((c ^ r) & 7) * 16;
     }
 };
-
-struct LdArgs {
-    int N, H, Lq, rows, page_size, num_pages, max_pages;
-    uint32_t drop;                             // barriers, a bit each, that miss an arrival
-    float scale;
-    const int32_t *table, *lens;
-    __nv_bfloat16* out;
-    float* lse;
-    int32_t *status, *cta_status;
-    float* parts;                              // [groups * G][2][R][kLdPart]
-    int64_t* before;                           // [N + 1] tiles ahead of a sequence (where it has tiles); all tiles
-    int G;                                     // CTAs of a group
-};
-constexpr int kLdPart = kLdRank + 4;           // O, ref, sum (rows stay 16-byte aligned)
-
-__device__ __forceinline__ int ld_len(const LdArgs& a, int n) {
-    const int len = a.lens[n];
-    return len < 0 || (int64_t)len > (int64_t)a.max_pages * a.page_size ? 0 : len;
-}
-__device__ __forceinline__ int ld_tiles(const LdArgs& a, int n) { return (ld_len(a, n) + kLdTile - 1) / kLdTile; }
-
-// Position in the tiles of a CTA's range; the same in all lanes of a warp, which call it together.
-struct LdWalk {
-    int n, j, tiles, left;
-    bool first;                                // first tile of a segment
-    int from;                                  // its tile
-    __device__ __forceinline__ bool last() const { return j + 1 == tiles || left == 1; }
-    __device__ __forceinline__ void settle(const LdArgs& a) {      // on to the next sequence that has tiles
-        while (left > 0 && j >= tiles) { ++n; j = 0; tiles = uniform(ld_tiles(a, n)); }
-    }
-    __device__ __forceinline__ void start(const LdArgs& a, int n0, int j0, int count) {
-        n = uniform(n0); j = uniform(j0); left = uniform(count); first = true; from = j;
-        tiles = left > 0 ? uniform(ld_tiles(a, n)) : 0;
-    }
-    __device__ __forceinline__ void next(const LdArgs& a) {
-        first = last();
-        ++j; --left;
-        settle(a);
-        if (first) from = j;
-    }
-};
-
-// Sums (or maxima) over the warp's lanes of R values a lane, to `to`[0 .. R).
-template <int R, bool kMax>
-__device__ __forceinline__ void ld_columns(const float (&x)[R], float* to, int lane) {
-    auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
-    constexpr int W = R < 32 ? R : 32;
-#pragma unroll
-    for (int h = 0; h < R; h += W) {
-        float v[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            v[i] = x[h + i];
-            if (W == 16) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-        }
-#pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) {
-#pragma unroll
-            for (int i = 0; i < o; ++i) {
-                const bool up = lane & o;
-                const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
-            }
-        }
-        if (lane < W) to[h + lane] = v[0];                         // lane l has come to hold column l
-    }
-}
 
 template <int R>
 __global__ void __launch_bounds__(kLdThreads, 1)
@@ -176,8 +102,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (warp == 4) {
         // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
         // warps wait for it at the barrier.
-        const int64_t cap = (int64_t)a.max_pages * a.page_size;
-        int len = lane < a.N ? a.lens[lane] : 0;                       // on its way while the barriers are made
+        const int len = lane < a.N ? a.lens[lane] : 0;                       // on its way while the barriers are made
         if (lane < bars_end - bars) mbar_init(bars + lane, (lane < p_full - bars ? 1 : 4) + (a.drop >> lane & 1));
         if (lane == 0) {
             prefetch_map(&map_s);
@@ -185,55 +110,12 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             prefetch_map(&map_q);
         }
         fence_mbar_init();
-        int64_t total = 0;
-        bool bad = false;
-        int first = 0;                                                 // tiles of sequence `lane`
-        for (int b = 0; b < a.N; b += 32) {
-            if (b > 0) len = b + lane < a.N ? a.lens[b + lane] : 0;
-            bad |= len < 0 || len > cap;
-            const int t = len < 0 || len > cap ? 0 : (len + kLdTile - 1) / kLdTile;
-            if (b == 0) first = t;
-            total += __reduce_add_sync(0xffffffffu, t);
-        }
-        bad = __any_sync(0xffffffffu, bad);
-        const int64_t parts = min64(a.G, total);       // no empty range between two that hold tiles
-        int64_t t0 = 0, t1 = 0;
-        if (cta < parts) {
-            if (total < (1 << 20)) {
-                t0 = (uint32_t)total * cta / (uint32_t)parts;
-                t1 = (uint32_t)total * (cta + 1) / (uint32_t)parts;
-            } else {
-                t0 = total * cta / parts;
-                t1 = total * (cta + 1) / parts;
-            }
-        }
-        int64_t before = 0;
-        int n0 = 0, j0 = 0;
-        if (t1 > t0) {
-            for (int b = 0; b < a.N; b += 32) {
-                const int n = b + lane;
-                const int t = b == 0 ? first : n < a.N ? ld_tiles(a, n) : 0;
-                int x = t;                                             // inclusive scan
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const uint32_t hit = __ballot_sync(0xffffffffu, before + x > t0);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    n0 = b + l;
-                    j0 = (int)(t0 - before - (__shfl_sync(0xffffffffu, x, l) - __shfl_sync(0xffffffffu, t, l)));
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, x, 31);
-            }
-        }
+        const LdCut cut = ld_cut(a, cta, lane, len);
         if (lane == 0) {
-            range[0] = n0; range[1] = j0; range[2] = (int)(t1 - t0);
-            if (cta == 0 && group == 0) a.before[a.N] = total;
-            *fault = bad ? kLdBadLen : 0;
-            *range_at = t0;
+            range[0] = cut.n; range[1] = cut.j; range[2] = cut.count;
+            if (cta == 0 && group == 0) a.before[a.N] = cut.total;
+            *fault = cut.bad ? kLdBadLen : 0;
+            *range_at = cut.at;
         }
         __syncwarp();
         asm volatile("bar.arrive 3, %0;" ::"n"(kLdThreads) : "memory");
@@ -655,22 +537,9 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
 }
 
 // ------------------------------------------------------------------- host
-struct LdPlan { int R, groups, G; size_t before, parts, bytes; };   // offsets behind the CTAs' status
-
-// CTAs and workspace of a call, from its sizes alone.
-static LdPlan ld_plan(int N, int Lq, int H, int page_size, int max_pages) {
-    LdPlan p;
+static int ld_rows(int Lq, int H) {                // rows of a group
     const int64_t rows = (int64_t)Lq * H;
-    p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.groups = (int)((rows + p.R - 1) / p.R);
-    const int64_t tiles = (int64_t)N * (((int64_t)max_pages * page_size + kLdTile - 1) / kLdTile);
-    int64_t g = 152 / p.groups;
-    g = g < 1 ? 1 : g;
-    p.G = (int)(g < tiles ? g : tiles);
-    p.before = ((size_t)p.groups * p.G * 4 + 255) / 256 * 256;
-    p.parts = p.before + ((size_t)(N + 1) * 8 + 255) / 256 * 256;
-    p.bytes = p.parts + (size_t)p.groups * p.G * 2 * p.R * kLdPart * 4;
-    return p;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 bool latent_decode_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_size) {
@@ -678,7 +547,7 @@ bool latent_decode_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_s
            (page_size & (page_size - 1)) == 0 && (int64_t)Lq * H <= 32 * 1024;
 }
 size_t latent_decode_tc_bytes(int N, int Lq, int H, int page_size, int max_pages) {
-    return N > 0 ? ld_plan(N, Lq, H, page_size, max_pages).bytes : 0;
+    return N > 0 ? ld_plan(N, Lq, H, page_size, max_pages, ld_rows(Lq, H)).bytes : 0;
 }
 // What the tensor maps need of the call's tensors.
 bool latent_decode_tc_aligned(const LatentDecodeArgs& d) {
@@ -686,6 +555,29 @@ bool latent_decode_tc_aligned(const LatentDecodeArgs& d) {
     return flat && (((uintptr_t)d.q | (uintptr_t)d.cache | (uintptr_t)d.out) & 15) == 0 && d.q_ts % 8 == 0 &&
            (d.H == 1 || (d.q_hs % 8 == 0 && d.q_hs > 0)) && d.q_ts > 0 && d.page_stride % 8 == 0 && d.num_pages > 0 &&
            d.page_stride < (1ll << 38) && d.q_ts < (1ll << 30);
+}
+
+template <int R>
+static cudaError_t ld_join(const LdArgs& a, int groups, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many).  From 256 rows on as
+    // for many (16 x 2048, 16 heads: 17 us, 21 as for few).
+    const bool many = (int64_t)a.N * a.rows >= 256;
+    const int warps = many ? 2 : 16, per = many ? 4 : 1;
+    cfg.gridDim = dim3(a.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
+    cfg.dynamicSmemBytes = warps * 128 * per * 4;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    // It starts as the last CTAs of the kernel before end (128 x 1024 tokens, 16 heads: 56 us behind them, 52 so);
+    // started with them, its waiting blocks take from it (4 queries x 30000 tokens, 16 heads: 29 us, 26 so).
+    cfg.attrs = at; cfg.numAttrs = 1;
+    return many ? cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 4>, a, groups)
+                : cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 1>, a, groups);
+}
+
+cudaError_t latent_decode_join_launch(const LdArgs& a, int R, int groups, cudaStream_t stream) {
+    return R == 16 ? ld_join<16>(a, groups, stream) : R == 32 ? ld_join<32>(a, groups, stream) : ld_join<64>(a, groups, stream);
 }
 
 template <int R>
@@ -725,25 +617,11 @@ static cudaError_t ld_launch(const LatentDecodeArgs& d, const LdPlan& p, cudaStr
     kda_latent_decode_tc<R><<<dim3(p.groups, p.G), kLdThreads, S::kSmem, stream>>>(mq, ms, mv, a);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    // Few rows: more blocks and warps for each (1 x 30000 tokens, 32 heads: 21 us, 43 as for many).  From 256 rows on as
-    // for many (16 x 2048, 16 heads: 17 us, 21 as for few).
-    const bool many = (int64_t)d.N * a.rows >= 256;
-    const int warps = many ? 2 : 16, per = many ? 4 : 1;
-    cfg.gridDim = dim3(d.N, a.rows, 4 / per); cfg.blockDim = dim3(32 * warps); cfg.stream = stream;
-    cfg.dynamicSmemBytes = warps * 128 * per * 4;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    // It starts as the last CTAs of the kernel before end (128 x 1024 tokens, 16 heads: 56 us behind them, 52 so);
-    // started with them, its waiting blocks take from it (4 queries x 30000 tokens, 16 heads: 29 us, 26 so).
-    cfg.attrs = at; cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 4>, a, p.groups)
-                : cudaLaunchKernelEx(&cfg, kda_latent_decode_join<R, 1>, a, p.groups);
+    return latent_decode_join_launch(a, R, p.groups, stream);
 }
 
 cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {
-    const LdPlan p = ld_plan(d.N, d.Lq, d.H, d.page_size, d.max_pages);
+    const LdPlan p = ld_plan(d.N, d.Lq, d.H, d.page_size, d.max_pages, ld_rows(d.Lq, d.H));
     return p.R == 16 ? ld_launch<16>(d, p, stream) : p.R == 32 ? ld_launch<32>(d, p, stream) : ld_launch<64>(d, p, stream);
 }
 

@@ -83,8 +83,10 @@ static int decode_desc(const kda_latent_desc* d) {
     return KDA_OK;
 }
 static bool decode_tc(const kda_latent_desc* d) {
-    return (d->flags & (KDA_FLAG_CUDA_CORE_PREFILL | KDA_FLAG_CACHE_8)) == 0 &&
-           latent_decode_tc_takes(d->dtype, d->d_k, d->d_rope, d->num_heads, d->num_queries, d->page_size);
+    if (d->flags & KDA_FLAG_CUDA_CORE_PREFILL) return false;
+    if (d->flags & KDA_FLAG_CACHE_8)
+        return latent_decode8_tc_takes(d->dtype, d->d_k, d->d_rope, d->num_heads, d->num_queries, d->page_size);
+    return latent_decode_tc_takes(d->dtype, d->d_k, d->d_rope, d->num_heads, d->num_queries, d->page_size);
 }
 static int workspace_fault(const kda_latent_desc* d, size_t need) {
     return !d->workspace || d->workspace_bytes < need || misaligned(d->workspace, 256);
@@ -239,6 +241,8 @@ size_t kda_latent_prefill_workspace_bytes(const kda_latent_desc* d) {
 size_t kda_latent_decode_workspace_bytes(const kda_latent_desc* d) {
     if (decode_desc(d)) return 0;
     const bool tc = decode_tc(d);
+    if (tc && (d->flags & KDA_FLAG_CACHE_8))
+        return kStatusBytes + latent_decode8_tc_bytes(d->num_seqs, d->num_queries, d->num_heads, d->page_size, d->max_pages);
     return kStatusBytes + (tc ? latent_decode_tc_bytes(d->num_seqs, d->num_queries, d->num_heads, d->page_size, d->max_pages) : 0);
 }
 
@@ -310,7 +314,9 @@ int kda_latent_decode(const kda_latent_desc* d, const void* q, const void* cache
     a.status = (int32_t*)d->workspace; a.scratch = (char*)d->workspace + kStatusBytes;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t err;
-    if (decode_tc(d) && latent_decode_tc_aligned(a)) {
+    if (decode_tc(d) && codes && latent_decode8_tc_aligned(a)) {
+        err = latent_decode8_tc_launch(a, s);
+    } else if (decode_tc(d) && !codes && latent_decode_tc_aligned(a)) {
         err = latent_decode_tc_launch(a, s);
     } else {
         err = cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);

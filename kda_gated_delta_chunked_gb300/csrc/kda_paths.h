@@ -137,6 +137,12 @@ bool latent_decode_tc_aligned(const LatentDecodeArgs& a);
 size_t latent_decode_tc_bytes(int N, int Lq, int H, int page_size, int max_pages);
 cudaError_t latent_decode_tc_launch(const LatentDecodeArgs& a, cudaStream_t stream);
 
+// The same over the quantised cache.
+bool latent_decode8_tc_takes(int dtype, int dk, int dr, int H, int Lq, int page_size);
+bool latent_decode8_tc_aligned(const LatentDecodeArgs& a);
+size_t latent_decode8_tc_bytes(int N, int Lq, int H, int page_size, int max_pages);
+cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& a, cudaStream_t stream);
+
 // The quantised cache: rows into pages (write) and out of them.
 struct LatentCacheArgs {
     int dtype, N, rank, d_rope, page_size, num_pages, max_pages;

@@ -66,9 +66,10 @@ def attention_bounds(q, keys, rank, want, lse, weight, ds, scale, dtype, tensor_
       puts its row's largest within 224 .. 448: exact for the 8 bits of bf16,
       below that half of e4m3's smallest step, 2^-10 / 16, so 2^-14 / 224 of the
       largest channel;
-    - a weight is an e4m3 value (off by 2^-4) and an e5m2 one for the rest (2^-3
-      of that), so off by 2^-7, or by half of e5m2's smallest step, 2^-17, over
-      2^12; the reference keeps the largest weight at 1 or more.
+    - a weight is rounded to half precision (2^-11) and then the sum of three e5m2
+      values, each the rest of the one before (2^-3 of it), so off by 2^-8.6, or by
+      half of the third one's smallest step, 2^-23, where the reference keeps the
+      largest weight at 2^7 or more.
     - the exponent of a token's scale is added to its score: 2^-24 of both."""
     n = keys.shape[0]
     bo, bl = ref.attention_bounds(want, lse, weight, ds, n, dtype, False)
@@ -77,8 +78,8 @@ def attention_bounds(q, keys, rank, want, lse, weight, ds, scale, dtype, tensor_
     more = scale * 2.0 ** -21.8 * float(q.abs().to(F).max()) * float(keys[:, :rank].abs().sum(1).max())
     more += 4 * 2.0 ** -24 * (130 + abs(lse))
     p = torch.exp((keys.to(F) @ q.to(F)) * scale - lse)
-    floor = n * 2.0 ** -29 * float((p * keys[:, :rank].abs().amax(1)).max()) * 2
-    return bo + (2 * more + 2.0 ** -7) * weight * (1 + HALF[dtype]) + floor, bl + more
+    floor = n * 2.0 ** -30 * float((p * keys[:, :rank].abs().amax(1)).max()) * 2
+    return bo + (2 * more + 2.0 ** -8.6) * weight * (1 + HALF[dtype]) + floor, bl + more
 
 
 def rotary(x, positions, frequencies, dim, offset, interleaved, inverse, scale):
