@@ -39,7 +39,8 @@
 namespace kda {
 
 constexpr int kL8Rows = 32;                                  // query rows of a CTA
-constexpr int kL8Threads = 384;                              // 4 softmax warps, producer, two products, scales, 4 for the queries
+constexpr int kL8Threads = 512;                              // 8 softmax warps, producer, two products, scales, 4 for the queries
+constexpr int kL8Half = 16;                                  // rows of a softmax warp
 constexpr int kL8Width = latent_row_bytes(kLdRank, kLdWidth - kLdRank);    // bytes of a token's row
 constexpr float kL8Slack = 8.f, kL8Stand = 7.f;              // how far (log2) a weight may exceed its reference; the reference's
 constexpr uint32_t kL8Piece = kLdTile * 128;                 // 128 bytes of each token: 128 codes, or the rotary channels
@@ -112,11 +113,14 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
-    if (warp == 4) {
+    LdWalk w;
+    if (warp == 8) {
+        // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
+        // warps wait for it at the barrier.
         const int len = lane < a.N ? a.lens[lane] : 0;                 // on its way while the barriers are made
         if (lane < bars_end - bars) {
             const uint64_t* x = bars + lane;
-            const int arrivals = x == q_full || x == s_empty || x == p_full || x == p_full + 1 ? 4 : 1;
+            const int arrivals = x == s_empty || x == p_full || x == p_full + 1 ? 8 : x == q_full ? 4 : 1;
             mbar_init(bars + lane, arrivals + (a.drop >> lane & 1));
         }
         if (lane == 0) prefetch_map(&map);
@@ -129,6 +133,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             *range_at = cut.at;
         }
         __syncwarp();
+        asm volatile("bar.arrive 5, %0;" ::"n"(kL8Threads) : "memory");
+        w.start(a, cut.n, cut.j, cut.count);
     } else {
         if (warp == 0) { tmem_alloc(tmem_at, 512); tmem_relinquish(); }
         if (threadIdx.x < R) {
@@ -136,29 +142,35 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             query[threadIdx.x] = min((group * R + (int)threadIdx.x) / a.H, a.Lq - 1);
         }
         tc_fence_before_sync();
+        asm volatile("bar.sync 5, %0;" ::"n"(kL8Threads) : "memory");
+        tc_fence_after_sync();
+        w.start(a, range[0], range[1], range[2]);
     }
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
-    LdWalk w;
-    w.start(a, range[0], range[1], range[2]);
+    const uint32_t tmem = warp == 8 ? 0 : __shfl_sync(0xffffffffu, *tmem_at, 0);
     const int count = w.left;
     const int row0 = group * R, live = min(R, a.rows - row0);
 
-    if (warp == 4) {                                                   // ---------------- producer
+    if (warp == 8) {                                                   // ---------------- producer
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
         bool ok = true, bad_page = false;
-        // A lane for each box of tokens: its page and row.  Pages behind the length, and bad ones, read as zeros.
-        for (int j = 0; j < count && ok; ++j, w.next(a)) {
-            int row = 0, page = a.num_pages;
-            if (lane < boxes) {
-                const int t = w.j * kLdTile + lane * box;
-                if (t < ld_len(a, w.n)) {
-                    const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
-                    if (p < 0 || p >= a.num_pages) bad_page = true;
-                    else { page = p; row = t % a.page_size; }
-                }
-            }
+        // A lane for each box of tokens: its page and row, found a tile ahead.  Pages behind the length, and bad ones,
+        // read as zeros.
+        int row = 0, page = a.num_pages;
+        auto find = [&]() {
+            row = 0;
+            page = a.num_pages;
+            if (w.left <= 0 || lane >= boxes) return;
+            const int t = w.j * kLdTile + lane * box;
+            if (t >= ld_len(a, w.n)) return;
+            const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
+            if (p < 0 || p >= a.num_pages) bad_page = true;
+            else { page = p; row = t % a.page_size; }
+        };
+        find();
+        for (int j = 0; j < count && ok; ++j) {
+            const int here = page, at_row = row;
+            w.next(a);
+            find();
             const int at = j % kL8Tiles * kL8Pieces;
             for (int k = 0; k < kL8Pieces; ++k) {
                 const int u = k == 0 ? 4 : k - 1;                      // the rotary channels first, they are free first
@@ -166,13 +178,13 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 if (lane == 0) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
                 __syncwarp();
                 if (lane < boxes)
-                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, row, page, smem_u32(&full[at + u]));
+                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, at_row, here, smem_u32(&full[at + u]));
                 __syncwarp();
             }
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
         if (!ok) atomicOr(fault, kLdLate);
-    } else if (warp == 5) {                                            // ---------------- S^T
+    } else if (warp == 9) {                                            // ---------------- S^T
         constexpr uint32_t codes = idesc_f8(128, 2 * R, 0, 0, 0), rope = idesc_bf16(128, R);
         const uint64_t dq = sdesc_k_sw128(base + kL8OffQ), dr = sdesc_k_sw128(base + kL8OffRope);
         uint32_t seg = 0;
@@ -204,7 +216,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
         }
         if (!ok) atomicOr(fault, kLdLate);
-    } else if (warp == 6) {                                            // ---------------- O^T += C^T P^T
+    } else if (warp == 10) {                                           // ---------------- O^T += C^T P^T
         constexpr uint32_t wide = idesc_f8(128, 3 * R, 1, 1, 1);
         bool ok = true;
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
@@ -227,7 +239,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
         }
         if (!ok) atomicOr(fault, kLdLate);
-    } else if (warp == 7) {                                            // ---------------- scales
+    } else if (warp == 11) {                                           // ---------------- scales
         // Four tokens' bytes a lane, fetched a tile ahead; 0 (2^-127) where there is nothing.
         auto fetch = [&](const LdWalk& x) -> uint32_t {
             const int t = x.j * kLdTile + 4 * lane;
@@ -249,7 +261,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             now = ahead;
         }
         if (!ok) atomicOr(fault, kLdLate);
-    } else if (warp >= 8) {                                            // ---------------- queries
+    } else if (warp >= 12) {                                           // ---------------- queries
         const float sc = a.scale * 1.4426950408889634f;
         uint32_t seg = 0;
         bool ok = true;
@@ -259,7 +271,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             uint32_t rope[R / 4];
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) {
-                const int r = (warp - 8) + 4 * i;
+                const int r = (warp - 12) + 4 * i;
                 x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
                 rope[i] = 0;
                 if (r < live) {
@@ -273,27 +285,35 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             if (seg > 0 && !(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) {
-                const int r = (warp - 8) + 4 * i;
-                const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-                float f[16];
-                uint32_t top = 0;                                      // largest finite channel, as bits
+                const int r = (warp - 12) + 4 * i;
+                uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                uint32_t top = 0;                                      // largest channel's bits, in each half
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    f[k] = __uint_as_float(k % 2 ? u[k / 2] & 0xffff0000u : u[k / 2] << 16);
-                    const uint32_t m = __float_as_uint(f[k]) & 0x7fffffffu;
-                    if (m < 0x7f800000u) top = max(top, m);
-                    else f[k] = __uint_as_float(0x7fc00000u);          // (an infinite channel counts as NaN)
+                for (int k = 0; k < 8; ++k) top = __vmaxu2(top, u[k] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                if (__any_sync(0xffffffffu, top >= 0x7f80u)) {         // infinite channels count as NaN, neither in the maximum
+                    top = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t lo = u[k] & 0x7fffu, hi = u[k] >> 16 & 0x7fffu;
+                        if (lo >= 0x7f80u) u[k] |= 0x7fffu;
+                        else top = max(top, lo);
+                        if (hi >= 0x7f80u) u[k] |= 0x7fff0000u;
+                        else top = max(top, hi);
+                    }
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
-                const int e = latent_exponent(top);
+                const int e = latent_exponent(top << 16);
                 const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
                 uint32_t q1[4], q2[4];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float lo = f[2 * k] * inv, hi = f[2 * k + 1] * inv;
-                    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-                    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
-                    const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2((lo - back.x) * 16.f, (hi - back.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+                    // (in half precision: exact where a step of q2 is more than 2^-24, its smallest number)
+                    const __half2 v = __floats2half2_rn(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xffff0000u) * inv);
+                    const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3));
+                    const __half2 rest = __hmul2(__hsub2(v, back), __half2(__float2half(16.f), __float2half(16.f)));
+                    const uint32_t d = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
                     q1[k / 2] = k % 2 ? q1[k / 2] | c << 16 : c;
                     q2[k / 2] = k % 2 ? q2[k / 2] | d << 16 : d;
                 }
@@ -311,84 +331,104 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else {                                                           // ---------------- softmax
-        const uint32_t lanes = tmem_addr(tmem, 32 * warp, 0);
+        const int half = warp >> 2, part = warp & 3, r0 = half * kL8Half, thread = threadIdx.x & 127;
+        const bool idle = r0 >= live;                                  // rows that are none: nothing of theirs is read
+        const uint32_t vote = half ? 3 : 1, meet = half ? 4 : 2;
+        auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(meet) : "memory"); };
+        const uint32_t lanes = tmem_addr(tmem, 32 * part, 0);
         const float sc = a.scale * 1.4426950408889634f;
-        float l[R];
+        float l[kL8Half];
 #pragma unroll
-        for (int c = 0; c < R; ++c) l[c] = 0.f;
+        for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
         bool ok = true;
         uint32_t seg = 0;
+        int len = 0;
         for (int j = 0; j < count; ++j, w.next(a)) {
             if (w.first) {
                 if (w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
+                len = ld_len(a, w.n);
                 ++seg;
             }
-            ok = bar_and(128, mbar_wait_spin(s_full, j & 1) && mbar_wait_spin(&c_full[j & 1], (j >> 1) & 1));
+            ok = bar_and_id(vote, 128, mbar_wait_spin(s_full, j & 1) && mbar_wait_spin(&c_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
-            const int len = ld_len(a, w.n);
-            const int token = w.j * kLdTile + (int)threadIdx.x;
-            const int byte = scales[(j & 1) * kLdTile + threadIdx.x];
-            const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
-            const float* unit = worth + (seg - 1) % kL8Scales * R;
+            const int token = w.j * kLdTile + thread;
+            const int byte = scales[(j & 1) * kLdTile + thread];
             // y: log2 of the weight times 2^e
-            float y[R];
-#pragma unroll
-            for (int h = 0; h < R; h += 16) {
-                float d1[16], d2[16], dr[16];
-                tmem_ld16(lanes + h, d1);
-                tmem_ld16(lanes + R + h, d2);
-                tmem_ld16(lanes + 2 * R + h, dr);
+            float y[kL8Half];
+            if (!idle) {
+                const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
+                const float* unit = worth + (seg - 1) % kL8Scales * R + r0;
+                float d2[kL8Half], dr[kL8Half];
+                tmem_ld16(lanes + r0, y);
+                tmem_ld16(lanes + R + r0, d2);
+                tmem_ld16(lanes + 2 * R + r0, dr);
                 tmem_wait_ld();
-                tmem_ready(d1);
+                tmem_ready(y);
                 tmem_ready(d2);
                 tmem_ready(dr);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) y[h + c] = fmaf(fmaf(d2[c], 0.0625f, d1[c]), two * unit[h + c], fmaf(dr[c], sc, e));
+                for (int c = 0; c < kL8Half; ++c) y[c] = fmaf(fmaf(d2[c], 0.0625f, y[c]), two * unit[c], fmaf(dr[c], sc, e));
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty);
-            if ((w.j + 1) * kLdTile > len - a.Lq + 1) {                // some row does not see some token
-#pragma unroll
-                for (int c = 0; c < R; ++c)
-                    if (token > len - a.Lq + query[c]) y[c] = -INFINITY;
-            }
             bool over = false;
+            if (!idle) {
+                if ((w.j + 1) * kLdTile > len - a.Lq + 1) {            // some row does not see some token
 #pragma unroll
-            for (int c = 0; c < R; c += 4) {
-                const float4 m = *(const float4*)(ref + c);
-                over |= y[c] > m.x + kL8Slack || y[c + 1] > m.y + kL8Slack || y[c + 2] > m.z + kL8Slack ||
-                        y[c + 3] > m.w + kL8Slack;
+                    for (int c = 0; c < kL8Half; ++c)
+                        if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < kL8Half; c += 4) {
+                    const float4 m = *(const float4*)(ref + r0 + c);
+                    over |= y[c] > m.x + kL8Slack || y[c + 1] > m.y + kL8Slack || y[c + 2] > m.z + kL8Slack ||
+                            y[c + 3] > m.w + kL8Slack;
+                }
             }
-            if (!bar_and(128, !over)) {                                // move the references to the maxima
-                ld_columns<R, true>(y, across + warp * R, lane);
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-                if (threadIdx.x < R) {
-                    const int c = threadIdx.x;
+            if (!bar_and_id(vote, 128, !over)) {                       // move the references to the maxima
+                ld_columns<kL8Half, true>(y, across + part * R + r0, lane);
+                sync();
+                if (thread < kL8Half) {
+                    const int c = r0 + thread;
                     const float old = ref[c];
                     const float now = fmaxf(old, fmaxf(fmaxf(across[c], across[R + c]),
                                                        fmaxf(across[2 * R + c], across[3 * R + c])));
                     ref[c] = now;
                     fac[c] = ex2(old - now);
                 }
-                asm volatile("bar.sync 2, 128;" ::: "memory");
+                sync();
+                float f[kL8Half];
 #pragma unroll
-                for (int c = 0; c < R; ++c) l[c] *= fac[c];
+                for (int c = 0; c < kL8Half; ++c) {
+                    f[c] = fac[r0 + c];
+                    l[c] *= f[c];
+                }
                 if (!w.first) {                                        // O^T, once the products into it are complete
-                    ok = bar_and(128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
+                    ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    for (int p = 0; p < 12; ++p) {
-                        for (int h = 0; h < R; h += 16) {
-                            float o[16];
-                            tmem_ld16(lanes + kL8O + p * R + h, o);
-                            tmem_wait_ld();
-                            tmem_ready(o);
+#pragma unroll 1
+                    for (int p = 0; p < 4; ++p) {
+                        const uint32_t at = lanes + kL8O + p * 3 * R + r0;
+                        float o1[kL8Half], o2[kL8Half], o3[kL8Half];
+                        tmem_ld16(at, o1);
+                        tmem_ld16(at + R, o2);
+                        tmem_ld16(at + 2 * R, o3);
+                        tmem_wait_ld();
+                        tmem_ready(o1);
+                        tmem_ready(o2);
+                        tmem_ready(o3);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= fac[h + c];
-                            tmem_st16(lanes + kL8O + p * R + h, o);
+                        for (int c = 0; c < kL8Half; ++c) {
+                            o1[c] *= f[c];
+                            o2[c] *= f[c];
+                            o3[c] *= f[c];
                         }
+                        tmem_st16(at, o1);
+                        tmem_st16(at + R, o2);
+                        tmem_st16(at + 2 * R, o3);
                     }
                     tmem_wait_st();
                 }
@@ -396,39 +436,37 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             if (j >= 2) {                                              // P's buffer: the products that read it are complete
                 ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
                 if (!ok) {                                             // the other warps leave at their next vote, with this one
-                    bar_and(128, false);
+                    bar_and_id(vote, 128, false);
                     break;
                 }
             }
-            const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
-            uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P;
-#pragma unroll
-            for (int c = 0; c < R; c += 16) {
+            if (!idle) {
+                const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
                 uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 m = *(const float4*)(ref + c + 4 * i);
+                    const float4 m = *(const float4*)(ref + r0 + 4 * i);
                     const float mm[4] = {m.x, m.y, m.z, m.w};
                     float p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(y[c + 4 * i + k] - mm[k] + kL8Stand);
-                        l[c + 4 * i + k] = fmaf(p[k], down, l[c + 4 * i + k]);
+                        p[k] = ex2(y[4 * i + k] - mm[k] + kL8Stand);
+                        l[4 * i + k] = fmaf(p[k], down, l[4 * i + k]);
                     }
                     l8_split(p, p1[i], p2[i], p3[i]);
                 }
-                const uint32_t at = l8_p_at(threadIdx.x, c / 16);
-                *(uint4*)(to + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                *(uint4*)(to + kL8P + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                *(uint4*)(to + 2 * kL8P + at) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+                uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P + l8_p_at(thread, half);
+                *(uint4*)to = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                *(uint4*)(to + kL8P) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                *(uint4*)(to + 2 * kL8P) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
-            // Weight 0 times what lies behind the length: make that 0
+            // Weight 0 times what lies behind the length: make that 0, half of the codes each half of the warps
             if (token >= len) {
-                uint8_t* at = mem + (j % kL8Tiles) * kL8Pieces * kL8Piece + threadIdx.x * 128;
+                uint8_t* at = mem + ((j % kL8Tiles) * kL8Pieces + 2 * half) * kL8Piece + thread * 128;
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) *(uint4*)(at + u * kL8Piece + ((i + threadIdx.x) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 8; ++i) *(uint4*)(at + u * kL8Piece + ((i + thread) & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
@@ -437,14 +475,14 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             if (!w.last()) continue;
 
             // end of a segment: sums across the tokens' threads, then O^T out
-            ld_columns<R, false>(l, sums + warp * R, lane);
-            ok = bar_and(128, mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
+            ld_columns<kL8Half, false>(l, sums + part * R + r0, lane);
+            ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
             const bool whole = w.from == 0 && w.j + 1 == w.tiles;
             float* dst = a.parts + ((size_t)(cta * gridDim.x + group) * 2 + (w.from == 0)) * R * kLdPart;
-            if (threadIdx.x < R) {
-                const int c = threadIdx.x;
+            if (thread < kL8Half) {
+                const int c = r0 + thread;
                 const float total = (sums[c] + sums[R + c]) + (sums[2 * R + c] + sums[3 * R + c]);
                 if (whole) {
                     fac[c] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
@@ -455,44 +493,41 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     dst[c * kLdPart + kLdRank + 1] = total;
                 }
             }
-            asm volatile("bar.sync 2, 128;" ::: "memory");
+            sync();
 #pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
-                const int ch = p * 128 + threadIdx.x;
+            for (int p = 0; p < 4 && !idle; ++p) {
+                const int ch = p * 128 + thread;
+                float o[kL8Half], o2[kL8Half], o3[kL8Half];
+                const uint32_t from = lanes + kL8O + p * 3 * R + r0;
+                tmem_ld16(from, o);
+                tmem_ld16(from + R, o2);
+                tmem_ld16(from + 2 * R, o3);
+                tmem_wait_ld();
+                tmem_ready(o);
+                tmem_ready(o2);
+                tmem_ready(o3);
 #pragma unroll
-                for (int h = 0; h < R; h += 16) {
-                    float o[16], o2[16], o3[16];
-                    const uint32_t from = lanes + kL8O + p * 3 * R + h;
-                    tmem_ld16(from, o);
-                    tmem_ld16(from + R, o2);
-                    tmem_ld16(from + 2 * R, o3);
-                    tmem_wait_ld();
-                    tmem_ready(o);
-                    tmem_ready(o2);
-                    tmem_ready(o3);
+                for (int c = 0; c < kL8Half; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
+                if (whole) {
+                    __nv_bfloat16* out = a.out + ((size_t)w.n * a.rows + row0 + r0) * kLdRank + ch;
+                    if (r0 + kL8Half <= live) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
-                    if (whole) {
-                        __nv_bfloat16* out = a.out + ((size_t)w.n * a.rows + row0 + h) * kLdRank + ch;
-                        if (h + 16 <= live) {
+                        for (int c = 0; c < kL8Half; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
+                    } else {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[h + c]);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                if (h + c < live) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[h + c]);
-                        }
-                    } else {                                           // (dead rows too: a condition a store costs more)
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) dst[(h + c) * kLdPart + ch] = o[c];
+                        for (int c = 0; c < kL8Half; ++c)
+                            if (r0 + c < live) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
                     }
+                } else {                                               // (dead rows too: a condition a store costs more)
+#pragma unroll
+                    for (int c = 0; c < kL8Half; ++c) dst[(r0 + c) * kLdPart + ch] = o[c];
                 }
             }
-            asm volatile("bar.sync 2, 128;" ::: "memory");
-            if (threadIdx.x < R) ref[threadIdx.x] = kLdUnset;
+            sync();
+            if (thread < kL8Half) ref[r0 + thread] = kLdUnset;
 #pragma unroll
-            for (int c = 0; c < R; ++c) l[c] = 0.f;
-            asm volatile("bar.sync 2, 128;" ::: "memory");
+            for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
+            sync();
         }
         if (!ok) {
             // The join finds the pieces by where the sequences start, those of the tiles that were left among them.
