@@ -451,9 +451,9 @@ KDA_API int kda_latent_prefill(const kda_latent_desc *desc, const void *q, const
  * on the tensor cores, on the codes themselves: there a query is the sum of two
  * e4m3 values under one power of two for its row (exact down to 2^-22 of its
  * largest channel; infinite channels count as NaN) and a softmax weight the sum of
- * three e5m2 values (off by 2^-8.6 of it at most, and by 2^-30 of the row's largest
- * weight); sums are fp32.  Everything else, and
- * fp32 queries, run on CUDA cores in fp32. */
+ * three e5m2 values (off by 2^-8.6 of it at most, or by 2^-26 of the row's largest
+ * weight, whichever is more); sums are fp32.  Everything else, and fp32 queries,
+ * run on CUDA cores in fp32. */
 KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const void *cache,
                               const int32_t *page_table, const int32_t *lengths, void *out, float *lse,
                               kda_stream_t stream);

@@ -12,9 +12,9 @@
 //     8 bits of a bf16 exactly, down to 2^-14 of steps where the row's largest is
 //     224 to 448 (e4m3's subnormals).  q1 and q2 are columns of one product.
 //   - a weight P = p 2^e is p1 + p2 / 8 + p3 / 64 in e5m2, each the rest of the one
-//     before: three bits each, off by 2^-8.7 (bf16: 2^-8), for weights down to 2^-21
-//     of the largest and 2^-30 of that below.  e5m2 for its range: the tokens behind
-//     a dominant one are many and small, and would be lost in e4m3's.
+//     before: three bits each, off by 2^-8.6 (bf16: 2^-8) for weights down to 2^-17
+//     of the largest, below that by 2^-26 of the largest.  e5m2 for its range: the
+//     tokens behind a dominant one are many and small, and would be lost in e4m3's.
 //
 //     S^T [128 tokens, q1 | q2 | rope: 3 x 32]  = C Q^T        16 + 4 instructions
 //     O^T [4 x 128 channels, p1 | p2 | p3: 3 x 32] += C^T P^T  4 x 4 instructions
@@ -23,13 +23,14 @@
 // the same tile in shared memory, the second as an MN-major operand: a tile is
 // fetched once, 641 bytes a token.  A thread owns a token, so its scale is a
 // thread's number.  The softmax reference of a row bounds P (not p): it moves when
-// some P exceeds it by 2^8, and stands at 2^7, a 2^8 below e5m2's largest power.
+// some P exceeds it by 2^12, and stands at 2^3, so that P stays below 2^15, e5m2's
+// largest power of two.
 //
 // CTAs have groups of 32 query rows; how the tiles are shared out, and the joining
 // of the pieces, are kda_latent_decode_tc.cu's.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
+#include <string.h>
 
 #include "kda_latent_cache.cuh"
 #include "kda_latent_decode.cuh"
@@ -42,7 +43,7 @@ constexpr int kL8Rows = 32;                                  // query rows of a 
 constexpr int kL8Threads = 512;                              // 8 softmax warps, producer, two products, scales, 4 for the queries
 constexpr int kL8Half = 16;                                  // rows of a softmax warp
 constexpr int kL8Width = latent_row_bytes(kLdRank, kLdWidth - kLdRank);    // bytes of a token's row
-constexpr float kL8Slack = 8.f, kL8Stand = 7.f;              // how far (log2) a weight may exceed its reference; the reference's
+constexpr float kL8Slack = 12.f, kL8Stand = 3.f;              // how far (log2) a weight may exceed its reference; the reference's
 constexpr uint32_t kL8Piece = kLdTile * 128;                 // 128 bytes of each token: 128 codes, or the rotary channels
 constexpr int kL8Pieces = 5, kL8Tiles = 2;
 constexpr uint32_t kL8QPiece = 2 * kL8Rows * 128;            // 128 codes of q1 and q2
@@ -68,24 +69,96 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn
 // 16-byte piece c of token row r of a P^T (32-byte swizzle).
 __device__ __forceinline__ uint32_t l8_p_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
 
-// Four weights to a word of e5m2 each: p1, what is left of it (times 8) as p2, and of that as p3.
-__device__ __forceinline__ void l8_split(const float (&p)[4], uint32_t& w1, uint32_t& w2, uint32_t& w3) {
-    uint32_t a[3][2];
+// Conversions to eight bits by masks and shifts: the conversion instructions take eight cycles of a scheduler each.
+
+template <typename T> __device__ __forceinline__ uint32_t bits_of(T x) {
+    uint32_t b;
+    memcpy(&b, &x, 4);
+    return b;
+}
+template <typename T> __device__ __forceinline__ T of_bits(uint32_t b) {
+    T x;
+    memcpy(&x, &b, 4);
+    return x;
+}
+
+// Four weights to a word each of e5m2 p1, p2, p3.  An e5m2 is the upper byte of a half: rounded to nine significant bits
+// (multiples of 2^-22 below 2^-14), a half is the sum of its upper byte, that of the rest times 8, and what is left of
+// that.  (A NaN is lost here; it is in the row's sum.)
+__device__ __forceinline__ void l8_split(const float* p, uint32_t& w1, uint32_t& w2, uint32_t& w3) {
+    const __half2 eight = __half2(__float2half(8.f), __float2half(8.f));
+    uint32_t x[2], y[2], z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            if (k > 0) h = __hmul2(h, __half2(__float2half(8.f), __float2half(8.f)));
-            const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E5M2);
-            a[k][i] = c;
-            const uint32_t back = __byte_perm(c, 0, 0x1404);       // an e5m2 is the upper byte of a half
-            if (k < 2) h = __hsub2(h, *(const __half2*)&back);
-        }
+        const uint32_t h = (bits_of(__floats2half2_rn(p[2 * i], p[2 * i + 1])) + 0x00020002u) & 0xfffcfffcu;
+        x[i] = h & 0xff00ff00u;
+        const __half2 r = __hmul2(__hsub2(of_bits<__half2>(h), of_bits<__half2>(x[i])), eight);
+        y[i] = bits_of(r) & 0xff00ff00u;
+        z[i] = bits_of(__hmul2(__hsub2(r, of_bits<__half2>(y[i])), eight));
     }
-    w1 = a[0][0] | a[0][1] << 16;
-    w2 = a[1][0] | a[1][1] << 16;
-    w3 = a[2][0] | a[2][1] << 16;
+    w1 = __byte_perm(x[0], x[1], 0x7531);
+    w2 = __byte_perm(y[0], y[1], 0x7531);
+    w3 = __byte_perm(z[0], z[1], 0x7531);
+}
+
+// Two bf16 channels, 448 at most, times 2^-120, to e4m3 q1 and 16 times the rest q2 (each code in the lower byte of its
+// half).  The factor makes e4m3's exponents bf16's, its subnormals too: a code is sign, exponent and three mantissa bits.
+// q1 is rounded to nearest, so that the rest is at most 8 of the 128 steps of a bf16 and its code 256 at most.
+__device__ __forceinline__ void l8_codes(__nv_bfloat162 t, uint32_t& q1, uint32_t& q2) {
+    const __nv_bfloat162 sixteen = __nv_bfloat162(__float2bfloat16(16.f), __float2bfloat16(16.f));
+    auto code = [](uint32_t x) { return (x >> 4 & 0x007f007fu) | (x >> 8 & 0x00800080u); };
+    const uint32_t top = (bits_of(t) + 0x00080008u) & 0xfff0fff0u;
+    q1 = code(top);
+    q2 = code(bits_of(__hmul2(__hsub2(t, of_bits<__nv_bfloat162>(top)), sixteen)));
+}
+
+// Query row `row` (query, head) of sequence n.
+__device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n, int row) {
+    const int i = row / b.a.H;
+    return b.q + ((int64_t)n * b.a.Lq + i) * b.q_ts + (row - i * b.a.H) * b.q_hs;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Query row r in registers (16 channels a lane, two rotary ones) to q1, q2 and the rotary part in shared memory, by a warp.
+__device__ __forceinline__ void l8_convert(uint8_t* mem, float* worth, int r, int lane, float sc, uint4 x0, uint4 x1, uint32_t rope) {
+    constexpr int R = kL8Rows;
+    uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    uint32_t top = 0;                                      // largest channel's bits, in each half
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = __vmaxu2(top, u[k] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
+    const bool strange = __any_sync(0xffffffffu, top >= 0x7f80u);
+    if (strange) {                                         // infinities and NaN: left out here, the row's unit is NaN
+        top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if ((u[k] & 0x7fffu) >= 0x7f80u) u[k] &= 0xffff0000u;
+            if ((u[k] >> 16 & 0x7fffu) >= 0x7f80u) u[k] &= 0xffffu;
+            top = __vmaxu2(top, u[k] & 0x7fff7fffu);
+        }
+        top = max(top & 0xffffu, top >> 16);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = latent_exponent(top << 16);
+    const __nv_bfloat16 inv = __float2bfloat16(__uint_as_float((uint32_t)(127 - e) << 23));
+    const __nv_bfloat162 down = __nv_bfloat162(inv, inv),
+                         far = __nv_bfloat162(__float2bfloat16(0x1p-120f), __float2bfloat16(0x1p-120f));
+    uint32_t q1[4], q2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t lo[2], hi[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            l8_codes(__hmul2(__hmul2(of_bits<__nv_bfloat162>(u[2 * k + h]), down), far), lo[h], hi[h]);
+        q1[k] = __byte_perm(lo[0], lo[1], 0x6420);
+        q2[k] = __byte_perm(hi[0], hi[1], 0x6420);
+    }
+    const int swz = r & 7;
+    uint8_t* to = mem + kL8OffQ + (lane / 8) * kL8QPiece + r * 128 + ((lane & 7) ^ swz) * 16;
+    *(uint4*)to = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    *(uint4*)(to + R * 128) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+    *(uint32_t*)(mem + kL8OffRope + r * 128 + ((lane / 4) ^ swz) * 16 + lane % 4 * 4) = rope;
+    if (lane == 0) worth[r] = strange ? NAN : __uint_as_float((uint32_t)(127 + e) << 23) * sc;
 }
 
 __global__ void __launch_bounds__(kL8Threads, 1)
@@ -105,14 +178,25 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
     uint64_t* bars = (uint64_t*)(scales + 2 * kLdTile);
     constexpr int kRing = kL8Tiles * kL8Pieces;
     uint64_t *full = bars, *empty = full + kRing, *q_full = empty + kRing, *q_empty = q_full + 1, *s_full = q_empty + 1,
-             *s_empty = s_full + 1, *o_full = s_empty + 1, *p_full = o_full + 2, *c_full = p_full + 2, *bars_end = c_full + 2;
+             *s_empty = s_full + 1, *o_full = s_empty + 1, *p_full = o_full + 2, *c_full = p_full + 2, *q_first = c_full + 2, *bars_end = q_first + 1;
     uint32_t* tmem_at = (uint32_t*)bars_end;
     int* range = (int*)(tmem_at + 1);                  // first sequence, its first tile, tiles
     int* fault = range + 3;
-    int64_t* range_at = (int64_t*)(((uintptr_t)(fault + 1) + 7) & ~(uintptr_t)7);   // index of the first tile
+    int* gave = fault + 1;                             // [2] a wait of this half of the softmax's warps gave up
+    int64_t* range_at = (int64_t*)(((uintptr_t)(gave + 2) + 7) & ~(uintptr_t)7);   // index of the first tile
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
+    // What the range's start hangs on next, were the sequences equally long: the translations at least are then there.
+    if (warp >= 11) {
+        const int n = (int)((int64_t)cta * a.N / gridDim.y);
+        if (warp == 11) {
+            if (lane == 0) prefetch_l2(a.table + (int64_t)n * a.max_pages);
+        } else {
+            for (int r = warp - 12; r < R && group * R + r < a.rows; r += 4)
+                if (lane < 9) prefetch_l2(l8_query(b, n, group * R + r) + lane * 64);
+        }
+    }
     LdWalk w;
     if (warp == 8) {
         // This CTA's range of the tiles of all sequences.  The producer finds it and starts copying; the other
@@ -120,7 +204,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         const int len = lane < a.N ? a.lens[lane] : 0;                 // on its way while the barriers are made
         if (lane < bars_end - bars) {
             const uint64_t* x = bars + lane;
-            const int arrivals = x == s_empty || x == p_full || x == p_full + 1 ? 8 : x == q_full ? 4 : 1;
+            const int arrivals = x == s_empty || x == p_full || x == p_full + 1 ? 8 : x == q_full ? 4 : x == q_first ? 12 : 1;
             mbar_init(bars + lane, arrivals + (a.drop >> lane & 1));
         }
         if (lane == 0) prefetch_map(&map);
@@ -131,6 +215,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             if (cta == 0 && group == 0) a.before[a.N] = cut.total;
             *fault = cut.bad ? kLdBadLen : 0;
             *range_at = cut.at;
+            gave[0] = gave[1] = 0;
         }
         __syncwarp();
         asm volatile("bar.arrive 5, %0;" ::"n"(kL8Threads) : "memory");
@@ -150,27 +235,60 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
     const int count = w.left;
     const int row0 = group * R, live = min(R, a.rows - row0);
 
+    auto load_row = [&](int r, uint4& x0, uint4& x1, uint32_t& rope) {
+        x0 = x1 = make_uint4(0, 0, 0, 0);
+        rope = 0;
+        if (r < live) {
+            const __nv_bfloat16* from = l8_query(b, w.n, row0 + r);
+            x0 = ((const uint4*)from)[2 * lane];
+            x1 = ((const uint4*)from)[2 * lane + 1];
+            rope = ((const uint32_t*)(from + kLdRank))[lane];
+        }
+    };
+    if (count > 0 && (warp < 8 || warp >= 12)) {                       // the first queries, by twelve warps (by four: 1.5 us later)
+        uint4 x[3][2];
+        uint32_t rope[3];
+        const int first = warp < 8 ? warp : warp - 4;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) load_row(first + 12 * i, x[i][0], x[i][1], rope[i]);
+#pragma unroll 1
+        for (int r = first; r < R; r += 12) {
+            l8_convert(mem, worth, r, lane, a.scale * 1.4426950408889634f, x[0][0], x[0][1], rope[0]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[i][0] = x[i + 1][0];
+                x[i][1] = x[i + 1][1];
+                rope[i] = rope[i + 1];
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_first);
+    }
+
     if (warp == 8) {                                                   // ---------------- producer
         const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
         bool ok = true, bad_page = false;
-        // A lane for each box of tokens: its page and row, found a tile ahead.  Pages behind the length, and bad ones,
-        // read as zeros.
-        int row = 0, page = a.num_pages;
-        auto find = [&]() {
-            row = 0;
-            page = a.num_pages;
-            if (w.left <= 0 || lane >= boxes) return;
+        // A lane for each box of tokens: its page, asked for a tile ahead.  Pages behind the length, and bad ones, read
+        // as zeros.
+        int len = 0, row = 0, page = a.num_pages;
+        bool some = false;
+        auto ask = [&]() {
+            if (w.left <= 0) return;
+            if (w.first) len = ld_len(a, w.n);
             const int t = w.j * kLdTile + lane * box;
-            if (t >= ld_len(a, w.n)) return;
-            const int p = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
-            if (p < 0 || p >= a.num_pages) bad_page = true;
-            else { page = p; row = t % a.page_size; }
+            some = lane < boxes && t < len;
+            row = t % a.page_size;
+            if (some) page = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
         };
-        find();
+        ask();
         for (int j = 0; j < count && ok; ++j) {
-            const int here = page, at_row = row;
+            const int p = page, here = some ? p : a.num_pages, at_row = some ? row : 0;
+            const bool asked = some;
             w.next(a);
-            find();
+            ask();
+            const bool bad = asked && (here < 0 || here >= a.num_pages);
+            bad_page |= bad;
             const int at = j % kL8Tiles * kL8Pieces;
             for (int k = 0; k < kL8Pieces; ++k) {
                 const int u = k == 0 ? 4 : k - 1;                      // the rotary channels first, they are free first
@@ -178,7 +296,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 if (lane == 0) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
                 __syncwarp();
                 if (lane < boxes)
-                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, at_row, here, smem_u32(&full[at + u]));
+                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, at_row, bad ? a.num_pages : here, smem_u32(&full[at + u]));
                 __syncwarp();
             }
         }
@@ -190,7 +308,10 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         uint32_t seg = 0;
         bool ok = true;
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
-            if (w.first) { ok = mbar_wait_warp(q_full, seg & 1); ++seg; }
+            if (w.first) {
+                ok = seg == 0 ? mbar_wait_warp(q_first, 0) : mbar_wait_warp(q_full, (seg - 1) & 1);
+                ++seg;
+            }
             if (ok && j >= 1) ok = mbar_wait_warp(s_empty, (j - 1) & 1);           // S_{j-1} is read
             const int at = j % kL8Tiles * kL8Pieces;
             for (int k = 0; k < kL8Pieces && ok; ++k) {
@@ -220,30 +341,35 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         constexpr uint32_t wide = idesc_f8(128, 3 * R, 1, 1, 1);
         bool ok = true;
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
-            if (!(ok = mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
-            tc_fence_after_sync();
             const int at = j % kL8Tiles * kL8Pieces;
+            const uint32_t here = (j / kL8Tiles) & 1;                  // (the first product has awaited them too: no time is lost)
+            uint64_t* const pieces[4] = {&full[at], &full[at + 1], &full[at + 2], &full[at + 3]};
+            if (!(ok = mbar_wait_all(pieces, {here, here, here, here}) && mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
+            tc_fence_after_sync();
             // p1, p2 and p3 lie a swizzle atom of 32 rows apart each; 8 tokens 256 bytes
             const uint64_t dp = sdesc(base + kL8OffP + (j & 1) * 3 * kL8P, kL8P, 256, 6);
-            for (int u = 0; u < 4; ++u) {
-                if (!(ok = mbar_wait_warp(&full[at + u], (j / kL8Tiles) & 1))) break;
-                const uint64_t da = sdesc(base + (at + u) * kL8Piece, kL8Piece, 1024, 2);
-                if (elect_one()) {
+            if (elect_one()) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint64_t da = sdesc(base + (at + u) * kL8Piece, kL8Piece, 1024, 2);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mma_f8_ss(tmem + kL8O + u * 3 * R, da + i * (4096 / 16), dp + i * (1024 / 16), wide, !w.first || i > 0);
                     mma_commit(&empty[at + u]);
-                    if (u == 3) mma_commit(&o_full[j & 1]);
                 }
-                __syncwarp();
+                mma_commit(&o_full[j & 1]);
             }
+            __syncwarp();
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 11) {                                           // ---------------- scales
         // Four tokens' bytes a lane, fetched a tile ahead; 0 (2^-127) where there is nothing.
+        int len = 0;
         auto fetch = [&](const LdWalk& x) -> uint32_t {
             const int t = x.j * kLdTile + 4 * lane;
-            if (x.left <= 0 || t >= ld_len(a, x.n)) return 0;
+            if (x.left <= 0) return 0;
+            if (x.first) len = ld_len(a, x.n);
+            if (t >= len) return 0;
             const int p = a.table[(int64_t)x.n * a.max_pages + t / a.page_size];
             if (p < 0 || p >= a.num_pages) return 0;
             return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + t % a.page_size);
@@ -263,66 +389,29 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp >= 12) {                                           // ---------------- queries
         const float sc = a.scale * 1.4426950408889634f;
-        uint32_t seg = 0;
+        uint32_t seg = 1;
         bool ok = true;
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
-            if (!w.first) continue;
+            if (!w.first || j == 0) continue;                          // (the first segment's are done)
+            // All rows' loads at once; then two rows after two by the same instructions (four times as many are cold).
             uint4 x[R / 4][2];
             uint32_t rope[R / 4];
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
-                const int r = (warp - 12) + 4 * i;
-                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-                rope[i] = 0;
-                if (r < live) {
-                    const int qi = (row0 + r) / a.H, h = (row0 + r) - qi * a.H;
-                    const __nv_bfloat16* from = b.q + ((int64_t)w.n * a.Lq + qi) * b.q_ts + h * b.q_hs;
-                    x[i][0] = ((const uint4*)from)[2 * lane];
-                    x[i][1] = ((const uint4*)from)[2 * lane + 1];
-                    rope[i] = ((const uint32_t*)(from + kLdRank))[lane];
+            for (int i = 0; i < R / 4; ++i) load_row(warp - 12 + 4 * i, x[i][0], x[i][1], rope[i]);
+            if (!(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
+#pragma unroll 1
+            for (int i0 = 0; i0 < R / 4; i0 += 2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = warp - 12 + 4 * (i0 + i);
+                    l8_convert(mem, worth + seg % kL8Scales * R, r, lane, sc, x[i][0], x[i][1], rope[i]);
                 }
-            }
-            if (seg > 0 && !(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
-                const int r = (warp - 12) + 4 * i;
-                uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-                uint32_t top = 0;                                      // largest channel's bits, in each half
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = __vmaxu2(top, u[k] & 0x7fff7fffu);
-                top = max(top & 0xffffu, top >> 16);
-                if (__any_sync(0xffffffffu, top >= 0x7f80u)) {         // infinite channels count as NaN, neither in the maximum
-                    top = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t lo = u[k] & 0x7fffu, hi = u[k] >> 16 & 0x7fffu;
-                        if (lo >= 0x7f80u) u[k] |= 0x7fffu;
-                        else top = max(top, lo);
-                        if (hi >= 0x7f80u) u[k] |= 0x7fff0000u;
-                        else top = max(top, hi);
-                    }
+                for (int i = 0; i + 2 < R / 4; ++i) {
+                    x[i][0] = x[i + 2][0];
+                    x[i][1] = x[i + 2][1];
+                    rope[i] = rope[i + 2];
                 }
-                top = __reduce_max_sync(0xffffffffu, top);
-                const int e = latent_exponent(top << 16);
-                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                uint32_t q1[4], q2[4];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    // (in half precision: exact where a step of q2 is more than 2^-24, its smallest number)
-                    const __half2 v = __floats2half2_rn(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xffff0000u) * inv);
-                    const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-                    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3));
-                    const __half2 rest = __hmul2(__hsub2(v, back), __half2(__float2half(16.f), __float2half(16.f)));
-                    const uint32_t d = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
-                    q1[k / 2] = k % 2 ? q1[k / 2] | c << 16 : c;
-                    q2[k / 2] = k % 2 ? q2[k / 2] | d << 16 : d;
-                }
-                const int swz = r & 7;
-                uint8_t* to = mem + kL8OffQ + (lane / 8) * kL8QPiece + r * 128 + ((lane & 7) ^ swz) * 16;
-                *(uint4*)to = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-                *(uint4*)(to + R * 128) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
-                *(uint32_t*)(mem + kL8OffRope + r * 128 + ((lane / 4) ^ swz) * 16 + lane % 4 * 4) = rope[i];
-                if (lane == 0) worth[seg % kL8Scales * R + r] = __uint_as_float((uint32_t)(127 + e) << 23) * sc;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -334,6 +423,12 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         const int half = warp >> 2, part = warp & 3, r0 = half * kL8Half, thread = threadIdx.x & 127;
         const bool idle = r0 >= live;                                  // rows that are none: nothing of theirs is read
         const uint32_t vote = half ? 3 : 1, meet = half ? 4 : 2;
+        // A warp whose wait gave up says so at a vote that the others come to next, and all four leave there.
+        auto leave = [&]() {
+            if (lane == 0) *(volatile int*)(gave + half) = 1;
+            __syncwarp();
+            bar_and_id(vote, 128, false);
+        };
         auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(meet) : "memory"); };
         const uint32_t lanes = tmem_addr(tmem, 32 * part, 0);
         const float sc = a.scale * 1.4426950408889634f;
@@ -349,8 +444,11 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 len = ld_len(a, w.n);
                 ++seg;
             }
-            ok = bar_and_id(vote, 128, mbar_wait_spin(s_full, j & 1) && mbar_wait_spin(&c_full[j & 1], (j >> 1) & 1));
-            if (!ok) break;
+            ok = mbar_wait_warp(s_full, j & 1) && mbar_wait_warp(&c_full[j & 1], (j >> 1) & 1);
+            if (!ok) {
+                leave();
+                break;
+            }
             tc_fence_after_sync();
             const int token = w.j * kLdTile + thread;
             const int byte = scales[(j & 1) * kLdTile + thread];
@@ -373,21 +471,32 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty);
-            bool over = false;
-            if (!idle) {
-                if ((w.j + 1) * kLdTile > len - a.Lq + 1) {            // some row does not see some token
+            if (!idle && (w.j + 1) * kLdTile > len - a.Lq + 1) {       // some row does not see some token
 #pragma unroll
-                    for (int c = 0; c < kL8Half; ++c)
-                        if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
-                }
+                for (int c = 0; c < kL8Half; ++c)
+                    if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
+            }
+            // The weights under the references as they are; under new ones, where some weight is too large for that.
+            float p[kL8Half];
+            bool over = false;
+            auto weigh = [&]() {
 #pragma unroll
                 for (int c = 0; c < kL8Half; c += 4) {
                     const float4 m = *(const float4*)(ref + r0 + c);
-                    over |= y[c] > m.x + kL8Slack || y[c + 1] > m.y + kL8Slack || y[c + 2] > m.z + kL8Slack ||
-                            y[c + 3] > m.w + kL8Slack;
+                    const float d[4] = {y[c] - m.x, y[c + 1] - m.y, y[c + 2] - m.z, y[c + 3] - m.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        over |= d[k] > kL8Slack;
+                        p[c + k] = ex2(d[k] + kL8Stand);
+                    }
                 }
-            }
+            };
+            if (!idle) weigh();
             if (!bar_and_id(vote, 128, !over)) {                       // move the references to the maxima
+                if (*(volatile int*)(gave + half)) {
+                    ok = false;
+                    break;
+                }
                 ld_columns<kL8Half, true>(y, across + part * R + r0, lane);
                 sync();
                 if (thread < kL8Half) {
@@ -432,11 +541,12 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     }
                     tmem_wait_st();
                 }
+                if (!idle) weigh();
             }
             if (j >= 2) {                                              // P's buffer: the products that read it are complete
                 ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
-                if (!ok) {                                             // the other warps leave at their next vote, with this one
-                    bar_and_id(vote, 128, false);
+                if (!ok) {
+                    leave();
                     break;
                 }
             }
@@ -445,15 +555,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 m = *(const float4*)(ref + r0 + 4 * i);
-                    const float mm[4] = {m.x, m.y, m.z, m.w};
-                    float p[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(y[4 * i + k] - mm[k] + kL8Stand);
-                        l[4 * i + k] = fmaf(p[k], down, l[4 * i + k]);
-                    }
-                    l8_split(p, p1[i], p2[i], p3[i]);
+                    for (int k = 0; k < 4; ++k) l[4 * i + k] = fmaf(p[4 * i + k], down, l[4 * i + k]);
+                    l8_split(p + 4 * i, p1[i], p2[i], p3[i]);
                 }
                 uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P + l8_p_at(thread, half);
                 *(uint4*)to = make_uint4(p1[0], p1[1], p1[2], p1[3]);
@@ -576,9 +680,9 @@ cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t str
     a.lse = d.lse; a.status = d.status; a.cta_status = (int32_t*)d.scratch; a.G = p.G;
     a.before = (int64_t*)((char*)d.scratch + p.before);
     a.parts = (float*)((char*)d.scratch + p.parts);
-    // the barriers' order: full, empty, q_full, q_empty, s_full, s_empty, o_full [2], p_full [2], c_full [2]
+    // the barriers' order: full, empty, q_full, q_empty, s_full, s_empty, o_full [2], p_full [2], c_full [2], q_first
     constexpr int kAt = 2 * kL8Tiles * kL8Pieces;
-    constexpr uint32_t kDrops[6] = {0, (1u << kAt / 2) - 1, 1u << (kAt + 2), 3u << (kAt + 4), 3u << (kAt + 6), 1u << kAt | 3u << (kAt + 8)};
+    constexpr uint32_t kDrops[6] = {0, (1u << kAt / 2) - 1, 1u << (kAt + 2), 3u << (kAt + 4), 3u << (kAt + 6), 1u << kAt | 7u << (kAt + 8)};
     a.drop = kDrops[d.drop];
     b.q = (const __nv_bfloat16*)d.q; b.q_ts = d.q_ts; b.q_hs = d.q_hs;
     b.cache = (const uint8_t*)d.cache; b.page_stride = d.page_stride;

@@ -69,7 +69,7 @@ def attention_bounds(q, keys, rank, want, lse, weight, ds, scale, dtype, tensor_
     - a weight is rounded to half precision (2^-11) and then the sum of three e5m2
       values, each the rest of the one before (2^-3 of it), so off by 2^-8.6, or by
       half of the third one's smallest step, 2^-23, where the reference keeps the
-      largest weight at 2^7 or more.
+      largest weight at 2^3 or more.
     - the exponent of a token's scale is added to its score: 2^-24 of both."""
     n = keys.shape[0]
     bo, bl = ref.attention_bounds(want, lse, weight, ds, n, dtype, False)
@@ -78,7 +78,7 @@ def attention_bounds(q, keys, rank, want, lse, weight, ds, scale, dtype, tensor_
     more = scale * 2.0 ** -21.8 * float(q.abs().to(F).max()) * float(keys[:, :rank].abs().sum(1).max())
     more += 4 * 2.0 ** -24 * (130 + abs(lse))
     p = torch.exp((keys.to(F) @ q.to(F)) * scale - lse)
-    floor = n * 2.0 ** -30 * float((p * keys[:, :rank].abs().amax(1)).max()) * 2
+    floor = n * 2.0 ** -26 * float((p * keys[:, :rank].abs().amax(1)).max()) * 2
     return bo + (2 * more + 2.0 ** -8.6) * weight * (1 + HALF[dtype]) + floor, bl + more
 
 
