@@ -3,12 +3,13 @@
 //
 //     e = min { e : max |c| <= 448 2^e },   code = e4m3(c / 2^e)
 //
-// A warp owns a token, a lane 16 of its channels: the maximum is one reduction,
-// a lane's codes are one 16-byte access.  Division by a power of two is exact, so
-// the code is the latent rounded once.  Bound by HBM bytes (1152 and 641 of them
-// a token in bf16 at rank 512); a warp takes kTokens neighbouring tokens, whose
-// rows it loads before it looks for their places (write), or whose places it
-// finds before it loads any (read).
+// A warp owns a token, a lane every 32nd vector of 16 bytes of its channels: the
+// maximum is one reduction, and the warp's accesses lie side by side (16 channels in
+// a row a lane: fp32 rows read in 41 us instead of @@ for 65536 tokens).  Division
+// by a power of two is exact, so the code is the latent rounded once.  Bound by HBM
+// bytes (1152 and 641 of them a token in bf16 at rank 512); a warp takes kTokens
+// neighbouring tokens, whose rows it loads before it looks for their places
+// (write), or whose places it finds before it loads any (read).
 //
 // Errors in lengths and pages are found by a block of its own, if there is a
 // status word: it alone writes it.  The others leave out what is wrong.
@@ -23,31 +24,37 @@ namespace kda {
 
 constexpr int kLcWarps = 8;
 
-// 16 channels of a row, as they lie in memory.
-template <typename T> struct Lc16 { uint4 v[sizeof(T)]; };
+// A lane's channels of a row: kVecs vectors of kVec, 32 kVec channels apart; and its pairs of rotary channels.
+template <typename T> struct LcRow {
+    static constexpr int kVec = 16 / (int)sizeof(T), kVecs = 512 / (32 * kVec);
+    uint4 v[kVecs];
+    T rope[2][2];
+};
+template <typename T>
+__device__ __forceinline__ int lc_channel(int i, int lane) { return (i * 32 + lane) * LcRow<T>::kVec; }
 
 template <typename T, bool kWide>
-__device__ __forceinline__ void lc_load(Lc16<T>& x, const T* p) {
-    if constexpr (kWide) {
+__device__ __forceinline__ void lc_load(const LatentCacheArgs& a, int64_t t, int lane, LcRow<T>& x) {
+    const T* p = (const T*)a.latents + t * a.latent_stride;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) x.v[i] = ((const uint4*)p)[i];
-    } else {
-        T e[16];
+    for (int i = 0; i < LcRow<T>::kVecs; ++i) {
+        const int c = lc_channel<T>(i, lane);
+        x.v[i] = make_uint4(0, 0, 0, 0);
+        if (c >= a.rank) continue;
+        if constexpr (kWide) {
+            x.v[i] = *(const uint4*)(p + c);
+        } else {
+            T e[LcRow<T>::kVec];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = p[i];
-        memcpy(&x, e, sizeof(x));
+            for (int k = 0; k < LcRow<T>::kVec; ++k) e[k] = p[c + k];
+            memcpy(&x.v[i], e, 16);
+        }
     }
-}
-template <typename T, bool kWide>
-__device__ __forceinline__ void lc_store(const Lc16<T>& x, T* p) {
-    if constexpr (kWide) {
+    const T* r = (const T*)a.rope + t * a.rope_stride;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) ((uint4*)p)[i] = x.v[i];
-    } else {
-        T e[16];
-        memcpy(e, &x, sizeof(x));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = e[i];
+    for (int i = 0; i < 2; ++i) {
+        const int c = 64 * i + 2 * lane;
+        if (c < a.d_rope) { x.rope[i][0] = r[c]; x.rope[i][1] = r[c + 1]; }
     }
 }
 
@@ -131,57 +138,68 @@ __device__ __forceinline__ void lc_check(const LatentCacheArgs& a) {
     if (threadIdx.x == 0) *a.status = bad_page ? KDA_ERR_BAD_PAGE : bad_len ? KDA_ERR_BAD_SEQLENS : KDA_OK;
 }
 
+// The codes of one vector, a byte each, from its first.
+template <int kVec> struct LcCodes { uint32_t w[kVec / 4]; };
+
 template <typename T, bool kWide, int kTokens>
 __global__ void __launch_bounds__(32 * kLcWarps)
 kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
+    constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
     const int lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * kTokens;
     if (t0 >= a.T) return;
-    const bool codes = lane * 16 < a.rank;
-    Lc16<T> x[kTokens];
+    LcRow<T> x[kTokens];
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-        x[i] = {};
-        if (codes && t0 + i < a.T) lc_load<T, kWide>(x[i], (const T*)a.latents + (t0 + i) * a.latent_stride + lane * 16);
-    }
+    for (int i = 0; i < kTokens; ++i)
+        if (t0 + i < a.T) lc_load<T, kWide>(a, t0 + i, lane, x[i]);
     int page, row;
     lc_places<kTokens>(a, t0, page, row);
+    const int width = latent_row_bytes(a.rank, a.d_rope);
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
         if (p < 0) continue;
-        T v[16];
-        memcpy(v, &x[i], sizeof(x[i]));
-        float c[16];
+        float c[kVecs][kVec];
         uint32_t top = 0;                                          // |c| as bits: ordered like the values
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            c[k] = to_f32(v[k]);
-            const uint32_t b = __float_as_uint(c[k]) & 0x7fffffffu;
-            if (b < 0x7f800000u) top = max(top, b);
-            else c[k] = __uint_as_float(0x7fc00000u);
+        for (int k = 0; k < kVecs; ++k) {
+            T v[kVec];
+            memcpy(v, &x[i].v[k], 16);
+#pragma unroll
+            for (int m = 0; m < kVec; ++m) {
+                c[k][m] = to_f32(v[m]);
+                const uint32_t b = __float_as_uint(c[k][m]) & 0x7fffffffu;
+                if (b < 0x7f800000u) top = max(top, b);
+                else c[k][m] = __uint_as_float(0x7fc00000u);
+            }
         }
         top = __reduce_max_sync(0xffffffffu, top);
         const int e = latent_exponent(top);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t* base = a.cache + p * a.page_stride;
-        const int width = latent_row_bytes(a.rank, a.d_rope);
         uint8_t* to = base + (int64_t)r * width;
-        if (codes) {
-            uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * k] * inv, c[4 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * k + 2] * inv, c[4 * k + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-                w[k] = lo | hi << 16;
+        for (int k = 0; k < kVecs; ++k) {
+            LcCodes<kVec> w;
+#pragma unroll
+            for (int m = 0; m < kVec / 4; ++m) {
+                const float* f = c[k] + 4 * m;
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * inv, f[1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * inv, f[3] * inv), __NV_SATFINITE, __NV_E4M3);
+                w.w[m] = lo | hi << 16;
             }
-            *(uint4*)(to + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            const int ch = lc_channel<T>(k, lane);
+            if (ch >= a.rank) continue;
+            if constexpr (kVec == 8) *(uint2*)(to + ch) = make_uint2(w.w[0], w.w[1]);
+            else *(uint32_t*)(to + ch) = w.w[0];
         }
-        const T* rope = (const T*)a.rope + (t0 + i) * a.rope_stride;
-        for (int k = 2 * lane; k < a.d_rope; k += 64) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(to_f32(rope[k]), to_f32(rope[k + 1]));
-            *(uint32_t*)(to + a.rank + 2 * k) = *(const uint32_t*)&h;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int ch = 64 * k + 2 * lane;
+            if (ch >= a.d_rope) continue;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(to_f32(x[i].rope[k][0]), to_f32(x[i].rope[k][1]));
+            *(uint32_t*)(to + a.rank + 2 * ch) = *(const uint32_t*)&h;
         }
         if (lane == 0) base[(int64_t)a.page_size * width + r] = (uint8_t)(e + kScaleBias);
     }
@@ -191,14 +209,14 @@ template <typename T, bool kWide, int kTokens>
 __global__ void __launch_bounds__(32 * kLcWarps)
 kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
+    constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
     const int lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * kTokens;
     if (t0 >= a.T) return;
     int page, row;
     lc_places<kTokens>(a, t0, page, row);
-    const bool codes = lane * 16 < a.rank;
     const int width = latent_row_bytes(a.rank, a.d_rope);
-    uint4 w[kTokens];
+    LcCodes<kVec> w[kTokens][kVecs];
     uint32_t rope[kTokens][2], e[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
@@ -206,7 +224,18 @@ kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
         if (p < 0) continue;
         const uint8_t* base = a.cache + p * a.page_stride;
         const uint8_t* from = base + (int64_t)r * width;
-        if (codes) w[i] = *(const uint4*)(from + lane * 16);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int ch = lc_channel<T>(k, lane);
+            if (ch >= a.rank) continue;
+            if constexpr (kVec == 8) {
+                const uint2 u = *(const uint2*)(from + ch);
+                w[i][k].w[0] = u.x;
+                w[i][k].w[1] = u.y;
+            } else {
+                w[i][k].w[0] = *(const uint32_t*)(from + ch);
+            }
+        }
         e[i] = base[(int64_t)a.page_size * width + r];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -216,19 +245,27 @@ kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
     for (int i = 0; i < kTokens; ++i) {
         if (__shfl_sync(0xffffffffu, page, i) < 0) continue;
         const float s = __uint_as_float(e[i] << 23);               // 2^e
-        if (codes) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            T v[16];
+        T* out = (T*)a.latents + (t0 + i) * a.latent_stride;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[k / 2] >> 16 * (k % 2)), __NV_E4M3));
+        for (int k = 0; k < kVecs; ++k) {
+            const int ch = lc_channel<T>(k, lane);
+            if (ch >= a.rank) continue;
+            T v[kVec];
+#pragma unroll
+            for (int m = 0; m < kVec / 2; ++m) {
+                const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i][k].w[m / 2] >> 16 * (m % 2)), __NV_E4M3));
                 const float2 f = __half22float2(h);
-                v[2 * k] = from_f32<T>(f.x * s);
-                v[2 * k + 1] = from_f32<T>(f.y * s);
+                v[2 * m] = from_f32<T>(f.x * s);
+                v[2 * m + 1] = from_f32<T>(f.y * s);
             }
-            Lc16<T> x;
-            memcpy(&x, v, sizeof(x));
-            lc_store<T, kWide>(x, (T*)a.latents + (t0 + i) * a.latent_stride + lane * 16);
+            if constexpr (kWide) {
+                uint4 u;
+                memcpy(&u, v, 16);
+                *(uint4*)(out + ch) = u;
+            } else {
+#pragma unroll
+                for (int m = 0; m < kVec; ++m) out[ch + m] = v[m];
+            }
         }
         T* to = (T*)a.rope + (t0 + i) * a.rope_stride;
 #pragma unroll

@@ -4,35 +4,40 @@
 //
 // Bound by HBM bytes (every channel read once and written once; in place the
 // channels beside the turned ones are not touched).  A block takes some rows
-// (token and head) and forms their tokens' sines and cosines once, in shared
-// memory, while its loads are on their way; a thread takes `kRotSteps` vectors.
+// (token and head) of the queries or of the keys and forms their tokens' sines and
+// cosines once, in shared memory, while its loads are on their way.  A thread has a
+// few vectors, the turned ones of all rows before the copied ones, so that a warp
+// does one of the two.
 //
 // The angle: f / (2 pi) turns a position, as a 64-bit fraction of a turn, times
-// the position in 64-bit integers that wrap at whole turns.  What is left is off
-// by 2^-53 of f / (2 pi), times the position, whatever the position; its first 32
-// bits go to sincospi in fp32.
+// the position in 64-bit integers that wrap at whole turns: off by 2^-63 of f / (2 pi)
+// and by 2^-64, times the position.  Its first 32 bits go to sincospi in fp32.
+#include <string.h>
+
 #include "kda_common.cuh"
 #include "kda_paths.h"
 
 namespace kda {
 
-constexpr int kRotThreads = 256, kRotSteps = 4;
+constexpr int kRotThreads = 256;
 constexpr int kRotTable = 2048;                     // pairs of a block's tokens
-constexpr int kRotDim = 1024;
+constexpr int kRotTurns = 4;
 
 struct RotPart {
     const char* in;
     char* out;
     int64_t its, ihs, ots, ohs;                     // bytes
     int heads, offset;                              // offset: elements
-    int turned, units;                              // vectors (half layout: pairs of them) that are turned; all
+    int turned, copied;                             // a row's vectors (half layout: pairs of them) that are turned; the others
+    uint32_t by_turned, by_copied, by_heads;        // 2^32 over them, rounded up
+    int tokens_block, rows_block;                   // of a block: tokens (then all heads), or rows of one token
+    int64_t blocks;
+    int across;                                     // blocks of a token
 };
 struct RotArgs {
     RotPart part[2];
     int64_t tokens;
-    int dim, rows, units, tokens_block, rows_block; // rows of a token, vectors of a row (of both parts)
-    uint32_t by_rows, by_units;                     // 2^32 / rows, 2^32 / units, rounded up
-    int flags;
+    int dim, flags;
     float scale;
     const void* positions;
     const double* frequencies;
@@ -40,6 +45,23 @@ struct RotArgs {
 
 // u / d with m = 2^32 / d rounded up: exact while u d < 2^32.
 __device__ __forceinline__ int rot_divide(int u, int d, uint32_t m) { return d == 1 ? u : (int)__umulhi((uint32_t)u, m); }
+
+// f / (2 pi) as a 64-bit fraction of a turn (f finite), from the double's bits: 53 of them times 2^64 / pi, shifted to
+// where f's exponent says.  (In fp64, of which the SM has little, this took longer than the sines.)
+__device__ __forceinline__ unsigned long long rot_turns(double f) {
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
+    const int exponent = (int)(bits >> 52 & 0x7ff);
+    const unsigned long long m = (bits & 0xfffffffffffffull) | (exponent ? 1ull << 52 : 0ull);
+    const unsigned long long k = 5871781006564002453ull;           // 2^64 / pi
+    const unsigned long long lo = m * k, hi = __umul64hi(m, k);
+    const int down = 1076 - (exponent ? exponent : 1);             // turns 2^64 = (hi, lo) 2^-down
+    unsigned long long t;
+    if (down >= 128) t = 0;
+    else if (down >= 64) t = hi >> (down - 64);
+    else if (down > 0) t = hi << (64 - down) | lo >> down;
+    else t = down > -64 ? lo << -down : 0;
+    return bits >> 63 ? 0 - t : t;
+}
 
 template <int B> struct RotVec;
 template <> struct RotVec<16> { uint4 v; };
@@ -75,73 +97,90 @@ __device__ __forceinline__ void rot_turn(float& a, float& b, float2 w) {
 // neighbouring pairs one vector, else the two vectors of the same pairs (of a
 // single element each where B is an element's size, in both layouts).
 template <typename T, int B, bool kNear>
-__global__ void __launch_bounds__(kRotThreads)
+struct RotShape {
+    static constexpr int V = B / (int)sizeof(T);
+    static constexpr bool kTwo = !kNear || V == 1;                 // two vectors a unit
+    static constexpr int kPairs = kTwo ? V : V / 2;
+    static constexpr int kSteps = (B == 16 ? 2 : 4) / (kTwo ? 2 : 1);   // units of a thread at once
+};
+
+template <typename T, int B, bool kNear>
+__global__ void __launch_bounds__(kRotThreads, 8)
 kda_rotary_kernel(const __grid_constant__ RotArgs a) {
-    constexpr int V = B / (int)sizeof(T);
-    constexpr bool kTwo = !kNear || V == 1;                        // two vectors a unit
-    constexpr int kPairs = kTwo ? V : V / 2;
-    __shared__ unsigned long long turn[kRotDim / 2];
+    using S = RotShape<T, B, kNear>;
+    constexpr int V = S::V, kPairs = S::kPairs, kSteps = S::kSteps;
     __shared__ __align__(16) float2 table[kRotTable];
     const int half = a.dim / 2;
-    const int64_t token0 = (int64_t)blockIdx.x * a.tokens_block;
-    const int row0 = blockIdx.y * a.rows_block;                    // (more than one y: one token a block)
-    const int tokens = (int)min64(a.tokens_block, a.tokens - token0);
-    const int rows = a.tokens_block > 1 ? tokens * a.rows : min(a.rows_block, a.rows - row0);
-    const int total = rows * a.units;
-    for (int base = 0; base < total; base += kRotThreads * kRotSteps) {
-        RotVec<B> va[kRotSteps], vb[kRotSteps];
-        char* to[kRotSteps];
-        int at[kRotSteps];                                         // first pair in the table, -1: a copy
+    const bool key = blockIdx.x >= a.part[0].blocks;
+    const RotPart& p = a.part[key];
+    const uint32_t block = blockIdx.x - (key ? (uint32_t)a.part[0].blocks : 0);
+    const int64_t token0 = p.across > 1 ? block / (uint32_t)p.across : (int64_t)block * p.tokens_block;
+    const int row0 = p.across > 1 ? (int)(block % (uint32_t)p.across) * p.rows_block : 0;
+    const int tokens = (int)min64(p.tokens_block, a.tokens - token0);
+    const int rows = p.across > 1 ? min(p.rows_block, p.heads - row0) : tokens * p.heads;
+    const int turned = rows * p.turned, total = turned + rows * p.copied;
+    const char* in = p.in + token0 * p.its + row0 * p.ihs;
+    char* out = p.out + token0 * p.ots + row0 * p.ohs;
+    const int apart = kNear ? (int)sizeof(T) : half * (int)sizeof(T);
+    for (int base = 0; base < total; base += kRotThreads * kSteps) {
+        RotVec<B> va[kSteps], vb[kSteps];
+        char* to[kSteps];
+        int at[kSteps];                                            // first pair in the table, -1: a copy
 #pragma unroll
-        for (int k = 0; k < kRotSteps; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
             to[k] = nullptr;
             const int u = base + k * kRotThreads + (int)threadIdx.x;
             if (u >= total) continue;
-            const int r = rot_divide(u, a.units, a.by_units), unit = u - r * a.units;
-            const int token = a.tokens_block > 1 ? rot_divide(r, a.rows, a.by_rows) : 0;
-            int head = r - token * a.rows + row0;
-            const bool key = head >= a.part[0].heads;
-            const RotPart& p = a.part[key];
-            if (key) head -= a.part[0].heads;
-            if (unit >= p.units) continue;
-            const char* from = p.in + (token0 + token) * p.its + head * p.ihs;
-            to[k] = p.out + (token0 + token) * p.ots + head * p.ohs;
-            int e;
-            if (unit < p.turned) {
-                at[k] = token * half + unit * kPairs;
-                e = p.offset + (kNear ? (V == 1 ? 2 * unit : unit * V) : unit * V);
+            int r, e;
+            if (u < turned) {
+                r = rot_divide(u, p.turned, p.by_turned);
+                const int unit = u - r * p.turned;
+                e = p.offset + (kNear && V == 1 ? 2 * unit : unit * V);
+                at[k] = unit * kPairs;
             } else {
-                at[k] = -1;
-                e = (unit - p.turned) * V;
+                const int v = u - turned;
+                r = rot_divide(v, p.copied, p.by_copied);
+                e = (v - r * p.copied) * V;
                 if (e >= p.offset) e += a.dim;
+                at[k] = -1;
             }
-            from += (int64_t)e * (int)sizeof(T);
-            to[k] += (int64_t)e * (int)sizeof(T);
+            int token = 0;
+            if (p.tokens_block > 1) {
+                token = rot_divide(r, p.heads, p.by_heads);
+                r -= token * p.heads;
+                if (at[k] >= 0) at[k] += token * half;
+            }
+            const char* from = in + token * p.its + r * p.ihs + e * (int)sizeof(T);
+            to[k] = out + token * p.ots + r * p.ohs + e * (int)sizeof(T);
             va[k] = *(const RotVec<B>*)from;
-            if (kTwo && at[k] >= 0) vb[k] = *(const RotVec<B>*)(from + (kNear ? 1 : half) * (int)sizeof(T));
+            if (S::kTwo && at[k] >= 0) vb[k] = *(const RotVec<B>*)(from + apart);
         }
         if (base == 0) {
-            for (int i = threadIdx.x; i < half; i += kRotThreads) {
-                double t = a.frequencies[i] * 0.15915494309189533577;      // 1 / (2 pi)
-                t -= rint(t);
-                turn[i] = (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
-            }
-            __syncthreads();
             const float sign = a.flags & KDA_FLAG_INVERSE ? -a.scale : a.scale;
-            for (int e = threadIdx.x; e < tokens * half; e += kRotThreads) {
-                const int token = e / half;
-                const long long pos = a.flags & KDA_FLAG_POSITIONS_64 ? ((const int64_t*)a.positions)[token0 + token]
-                                                                     : ((const int32_t*)a.positions)[token0 + token];
-                const unsigned long long whole = (unsigned long long)pos * turn[e - token * half];
-                float s, c;
-                sincospif((float)(int)(whole >> 32) * 0x1p-31f, &s, &c);
-                table[e] = make_float2(a.scale * c, sign * s);
+            // A thread's pairs are of one frequency (of one at a time, where there are more frequencies than threads)
+            const int each = half < kRotThreads ? kRotThreads / half : 1;      // tokens at once
+            const int first = half < kRotThreads ? (int)threadIdx.x / half : 0;
+            for (int i = (int)threadIdx.x - first * half; i < half && first < each; i += kRotThreads) {
+                const unsigned long long turns = rot_turns(a.frequencies[i]);
+                for (int token = first; token < tokens; token += each) {
+                    const long long pos = a.flags & KDA_FLAG_POSITIONS_64 ? ((const int64_t*)a.positions)[token0 + token]
+                                                                         : ((const int32_t*)a.positions)[token0 + token];
+                    const float angle = (float)(int)((unsigned long long)pos * turns >> 32) * 0x1p-31f;    // half turns
+                    float s, c;
+                    if constexpr (sizeof(T) == 2) {
+                        // 2^-21 off, in outputs of 8 bits (sincospi: 65536 tokens of one head 15 us, @@ so)
+                        s = __sinf(angle * 3.14159265f);
+                        c = __cosf(angle * 3.14159265f);
+                    } else {
+                        sincospif(angle, &s, &c);
+                    }
+                    table[token * half + i] = make_float2(a.scale * c, sign * s);
+                }
             }
             __syncthreads();
         }
-        constexpr int64_t kApart = kNear ? sizeof(T) : 0;
 #pragma unroll
-        for (int k = 0; k < kRotSteps; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
             if (!to[k]) continue;
             if (at[k] < 0) {
                 *(RotVec<B>*)to[k] = va[k];
@@ -160,21 +199,16 @@ kda_rotary_kernel(const __grid_constant__ RotArgs a) {
             }
             float x[V], y[V];
             rot_get<T, B>(va[k], x);
-            if constexpr (kTwo) {
+            if constexpr (S::kTwo) {
                 rot_get<T, B>(vb[k], y);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    rot_turn(x[i], y[i], cs[i]);
-                }
-                *(RotVec<B>*)to[k] = rot_set<T, B>(x);
-                *(RotVec<B>*)(to[k] + (kNear ? kApart : (int64_t)half * (int)sizeof(T))) = rot_set<T, B>(y);
+                for (int i = 0; i < V; ++i) rot_turn(x[i], y[i], cs[i]);
+                *(RotVec<B>*)(to[k] + apart) = rot_set<T, B>(y);
             } else {
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                    rot_turn(x[2 * i], x[2 * i + 1], cs[i]);
-                }
-                *(RotVec<B>*)to[k] = rot_set<T, B>(x);
+                for (int i = 0; i < V / 2; ++i) rot_turn(x[2 * i], x[2 * i + 1], cs[i]);
             }
+            *(RotVec<B>*)to[k] = rot_set<T, B>(x);
         }
     }
 }
@@ -182,29 +216,33 @@ kda_rotary_kernel(const __grid_constant__ RotArgs a) {
 // ------------------------------------------------------------------- host
 template <typename T, int B, bool kNear>
 static cudaError_t rotary_launch_as(RotArgs a, cudaStream_t stream) {
-    constexpr int V = B / (int)sizeof(T);
-    a.units = 1;
-    a.rows = 0;
+    using S = RotShape<T, B, kNear>;
+    const int half = a.dim / 2, block = kRotThreads * S::kSteps;
+    auto over = [](int d) { return (uint32_t)((0x100000000ull + d - 1) / (d < 1 ? 1 : d)); };
     for (RotPart& p : a.part) {
-        if (!p.in) { p.heads = 0; continue; }
-        p.turned = kNear && V > 1 ? a.dim / V : a.dim / 2 / V;
-        p.units = p.turned + p.units / V;                          // (units: channels to copy so far)
-        a.units = p.units > a.units ? p.units : a.units;
-        a.rows += p.heads;
+        if (!p.in) continue;
+        p.turned = half / S::kPairs;
+        p.copied /= S::V;                                          // (channels so far)
+        p.by_turned = over(p.turned);
+        p.by_copied = over(p.copied);
+        p.by_heads = over(p.heads);
+        // Rows of a block, of one token or of several (as the table holds): up to kRotTurns vectors after one another a
+        // thread, while that leaves each SM twice the blocks that it runs at once
+        const int units = p.turned + p.copied;
+        const int64_t turns = a.tokens * p.heads * units / ((int64_t)block * 152 * 16);
+        const int fit = block * (int)(turns < 1 ? 1 : turns > kRotTurns ? kRotTurns : turns) / units;
+        p.rows_block = fit < 1 ? 1 : fit;
+        p.tokens_block = 1;
+        p.across = (p.heads + p.rows_block - 1) / p.rows_block;
+        if (p.across == 1) {
+            p.tokens_block = p.rows_block / p.heads;
+            if (p.tokens_block > kRotTable / half) p.tokens_block = kRotTable / half;
+        }
+        p.blocks = p.across > 1 ? a.tokens * p.across : (a.tokens + p.tokens_block - 1) / p.tokens_block;
     }
-    // As many rows as give each thread its vectors, of one token or of several (as the table holds)
-    const int fit = kRotThreads * kRotSteps / a.units, half = a.dim / 2;
-    a.rows_block = fit < 1 ? 1 + a.rows / 65536 : fit;             // (at most 65535 blocks in y)
-    a.tokens_block = 1;
-    if (a.rows_block >= a.rows) {
-        a.tokens_block = a.rows_block / a.rows;
-        if (a.tokens_block > kRotTable / half) a.tokens_block = kRotTable / half;
-        a.rows_block = a.rows;
-    }
-    a.by_rows = (uint32_t)((0x100000000ull + a.rows - 1) / a.rows);
-    a.by_units = (uint32_t)((0x100000000ull + a.units - 1) / a.units);
-    const dim3 grid((unsigned)((a.tokens + a.tokens_block - 1) / a.tokens_block), (unsigned)((a.rows + a.rows_block - 1) / a.rows_block));
-    kda_rotary_kernel<T, B, kNear><<<grid, kRotThreads, 0, stream>>>(a);
+    const int64_t blocks = a.part[0].blocks + a.part[1].blocks;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kda_rotary_kernel<T, B, kNear><<<(unsigned)blocks, kRotThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -229,11 +267,11 @@ cudaError_t rotary_launch(const kda_rotary_desc& d, const void* x, const void* k
         if (!p.in) continue;
         p.its = s.token_stride * e; p.ihs = s.head_stride * e; p.ots = s.out_token_stride * e; p.ohs = s.out_head_stride * e;
         p.heads = s.heads; p.offset = s.offset;
-        p.units = p.in == p.out ? 0 : s.width - d.dim;
+        p.copied = p.in == p.out ? 0 : s.width - d.dim;
         bits |= (uint64_t)(uintptr_t)p.in | (uint64_t)(uintptr_t)p.out | (uint64_t)(s.offset * e);
         if (d.tokens > 1) bits |= (uint64_t)(p.its | p.ots);
         if (s.heads > 1) bits |= (uint64_t)(p.ihs | p.ohs);
-        if (p.units) bits |= (uint64_t)(s.width * e);
+        if (p.copied) bits |= (uint64_t)(s.width * e);
     }
     if (d.dtype == KDA_BF16) {
         if ((bits & 15) == 0) return rotary_launch_near<__nv_bfloat16, 16>(a, stream);
