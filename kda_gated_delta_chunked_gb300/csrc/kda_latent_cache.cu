@@ -4,16 +4,21 @@
 //     e = min { e : max |c| <= 448 2^e },   code = e4m3(c / 2^e)
 //
 // A warp owns a token, a lane every 32nd vector of 16 bytes of its channels: the
-// maximum is one reduction, and the warp's accesses lie side by side (16 channels in
-// a row a lane: fp32 rows read in 41 us instead of @@ for 65536 tokens).  Division
-// by a power of two is exact, so the code is the latent rounded once.  Bound by HBM
-// bytes (1152 and 641 of them a token in bf16 at rank 512); a warp takes kTokens
-// neighbouring tokens, whose rows it loads before it looks for their places
-// (write), or whose places it finds before it loads any (read).
+// maximum is one reduction, and the warp's accesses lie side by side (with 16
+// channels in a row a lane, fp32 rows were read in 42 us instead of 33, for 65536
+// tokens).  Division by a power of two is exact, so the code is the latent rounded
+// once.  A warp takes one or two neighbouring tokens, whose rows it loads before it
+// looks for their places (write), or whose places it finds before it loads any
+// (read).
+//
+// Bound by HBM bytes: 1152 and 641 of them a token in bf16 at rank 512.  65536
+// tokens, us in a graph of ten (floor 17 in bf16, 28 in fp32): written 20 and 31,
+// read 19 and 33; one token each of 48 sequences 2.3.
 //
 // Errors in lengths and pages are found by a block of its own, if there is a
 // status word: it alone writes it.  The others leave out what is wrong.
 #include <cuda_fp8.h>
+#include <math.h>
 #include <string.h>
 
 #include "kda_common.cuh"
@@ -66,7 +71,7 @@ __device__ __forceinline__ LcSequence lc_sequence(const LatentCacheArgs& a, int6
     const int lane = threadIdx.x & 31;
     LcSequence s = {0, 0, 0, 0};
     if (!a.cu) {
-        s.n = (int)(t / a.rows_each);
+        s.n = (int)((uint32_t)t / (uint32_t)a.rows_each);              // (rows are below 2^31)
         s.from = s.n * a.rows_each;
         s.to = s.from + a.rows_each;
     } else {
@@ -108,10 +113,11 @@ __device__ __forceinline__ void lc_places(const LatentCacheArgs& a, int64_t t, i
         i = (int)min64(kTokens, end - t);
     }
     if (lane < kTokens && t + lane < a.T && place >= 0) {
-        const int p = a.table[(int64_t)n * a.max_pages + place / a.page_size];
+        const uint32_t at = (uint32_t)place, size = (uint32_t)a.page_size;   // (places are below 2^31)
+        const int p = a.table[(int64_t)n * a.max_pages + at / size];
         if (p >= 0 && p < a.num_pages) {
             page = p;
-            row = (int)(place % a.page_size);
+            row = (int)(at % size);
         }
     }
 }
@@ -141,8 +147,72 @@ __device__ __forceinline__ void lc_check(const LatentCacheArgs& a) {
 // The codes of one vector, a byte each, from its first.
 template <int kVec> struct LcCodes { uint32_t w[kVec / 4]; };
 
+__device__ __forceinline__ uint32_t lc_code4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+// A lane's channels as words: their largest |finite| one (as a float's bits), and their codes under 2^e.  Two of 16 bits
+// at once; infinities, which rarely are, are looked for again where the maximum shows one, and become NaN.
+__device__ __forceinline__ uint32_t lc_top(uint4 (&v)[2], const __nv_bfloat16*) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        top = __vmaxu2(__vmaxu2(__vmaxu2(top, v[k].x & 0x7fff7fffu), __vmaxu2(v[k].y & 0x7fff7fffu, v[k].z & 0x7fff7fffu)),
+                       v[k].w & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
+    if (top >= 0x7f80u) {
+        top = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t* u = (uint32_t*)&v[k];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t lo = u[m] & 0x7fffu, hi = u[m] >> 16 & 0x7fffu;
+                if (lo >= 0x7f80u) u[m] |= 0x7fffu;
+                else top = max(top, lo);
+                if (hi >= 0x7f80u) u[m] |= 0x7fff0000u;
+                else top = max(top, hi);
+            }
+        }
+    }
+    return top << 16;
+}
+__device__ __forceinline__ uint32_t lc_top(uint4 (&v)[4], const float*) {
+    float top = 0.f;
+    const float* f = (const float*)v;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(f[k]));        // (leaves NaN out)
+    if (top == INFINITY) {
+        top = 0.f;
+        float* g = (float*)v;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (fabsf(g[k]) == INFINITY) g[k] = __uint_as_float(0x7fc00000u);
+            top = fmaxf(top, fabsf(g[k]));
+        }
+    }
+    return __float_as_uint(top);
+}
+__device__ __forceinline__ LcCodes<8> lc_codes(const uint4& v, float inv, const __nv_bfloat16*) {
+    // (products with powers of two: exact in bf16 where the code is not 0)
+    const __nv_bfloat162 by = __nv_bfloat162(__float2bfloat16(inv), __float2bfloat16(inv));
+    float2 f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        __nv_bfloat162 x;
+        memcpy(&x, (const uint32_t*)&v + k, 4);
+        f[k] = __bfloat1622float2(__hmul2(x, by));
+    }
+    return {{lc_code4(f[0].x, f[0].y, f[1].x, f[1].y), lc_code4(f[2].x, f[2].y, f[3].x, f[3].y)}};
+}
+__device__ __forceinline__ LcCodes<4> lc_codes(const uint4& v, float inv, const float*) {
+    return {{lc_code4(__uint_as_float(v.x) * inv, __uint_as_float(v.y) * inv, __uint_as_float(v.z) * inv, __uint_as_float(v.w) * inv)}};
+}
+
 template <typename T, bool kWide, int kTokens>
-__global__ void __launch_bounds__(32 * kLcWarps)
+__global__ void __launch_bounds__(32 * kLcWarps, sizeof(T) == 2 ? 5 : 4)
 kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
     constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
@@ -160,35 +230,14 @@ kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
     for (int i = 0; i < kTokens; ++i) {
         const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
         if (p < 0) continue;
-        float c[kVecs][kVec];
-        uint32_t top = 0;                                          // |c| as bits: ordered like the values
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            T v[kVec];
-            memcpy(v, &x[i].v[k], 16);
-#pragma unroll
-            for (int m = 0; m < kVec; ++m) {
-                c[k][m] = to_f32(v[m]);
-                const uint32_t b = __float_as_uint(c[k][m]) & 0x7fffffffu;
-                if (b < 0x7f800000u) top = max(top, b);
-                else c[k][m] = __uint_as_float(0x7fc00000u);
-            }
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, lc_top(x[i].v, (const T*)nullptr));
         const int e = latent_exponent(top);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t* base = a.cache + p * a.page_stride;
         uint8_t* to = base + (int64_t)r * width;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            LcCodes<kVec> w;
-#pragma unroll
-            for (int m = 0; m < kVec / 4; ++m) {
-                const float* f = c[k] + 4 * m;
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * inv, f[1] * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * inv, f[3] * inv), __NV_SATFINITE, __NV_E4M3);
-                w.w[m] = lo | hi << 16;
-            }
+            const LcCodes<kVec> w = lc_codes(x[i].v[k], inv, (const T*)nullptr);
             const int ch = lc_channel<T>(k, lane);
             if (ch >= a.rank) continue;
             if constexpr (kVec == 8) *(uint2*)(to + ch) = make_uint2(w.w[0], w.w[1]);
@@ -206,7 +255,7 @@ kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
 }
 
 template <typename T, bool kWide, int kTokens>
-__global__ void __launch_bounds__(32 * kLcWarps)
+__global__ void __launch_bounds__(32 * kLcWarps, 8)
 kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
     constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
@@ -290,9 +339,9 @@ static cudaError_t lc_launch_as(const LatentCacheArgs& a, bool write, cudaStream
 template <typename T>
 static cudaError_t lc_launch(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
     const bool wide = (((uintptr_t)a.latents | (uintptr_t)(a.latent_stride * (int64_t)sizeof(T))) & 15) == 0;
-    // One token a warp until every SM has eight warps, four behind that
+    // One token a warp while every SM has 32 warps for them, two behind that (65536 tokens, us: one 23, two 20, four 24)
     if (a.T <= 152 * 32) return wide ? lc_launch_as<T, true, 1>(a, write, stream) : lc_launch_as<T, false, 1>(a, write, stream);
-    return wide ? lc_launch_as<T, true, 4>(a, write, stream) : lc_launch_as<T, false, 4>(a, write, stream);
+    return wide ? lc_launch_as<T, true, 2>(a, write, stream) : lc_launch_as<T, false, 2>(a, write, stream);
 }
 
 cudaError_t latent_cache_launch(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
