@@ -486,6 +486,18 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     float o[4 * Q];
 #pragma unroll
     for (int i = 0; i < 4 * Q; ++i) o[i] = 0.f;
+    // With few rows, the warp's first two pieces of each 32 (all, with sixteen warps) on their way beside what weighs them
+    // (8-bit cache, 1 x 30000 tokens, 32 heads, with the kernel before: 19.3 us, 17.6 so; with many rows it takes a
+    // microsecond more).
+    constexpr int kAhead = Q == 1 ? 2 : 0;
+    float4 ahead[5][2];
+#pragma unroll
+    for (int g = 0; g < 5; ++g)
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) {
+            const int k = warp + t * warps;
+            if (k < 32 && cf + 32 * g + k <= cl) ahead[g][t] = *(const float4*)(piece(cf + 32 * g + k) + ch0 + lane * 4);
+        }
     // Every warp weighs all pieces (152 at most), a lane each, and adds up its share of them.
     float2 ml[5];
     float top = kLdUnset, sum = 0.f;
@@ -503,8 +515,16 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
         const float wgt = ex2(ml[g].x - top);
         sum += wgt * ml[g].y;
         const int here = min(32, cl - cf - 32 * g + 1);
+        int k = warp;
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) {
+            if (k >= here) break;
+            const float x = __shfl_sync(0xffffffffu, wgt, k);
+            o[0] += x * ahead[g][t].x; o[1] += x * ahead[g][t].y; o[2] += x * ahead[g][t].z; o[3] += x * ahead[g][t].w;
+            k += warps;
+        }
 #pragma unroll 4
-        for (int k = warp; k < here; k += warps) {
+        for (; k < here; k += warps) {
             const float x = __shfl_sync(0xffffffffu, wgt, k);
             const float* p = piece(cf + 32 * g + k);
 #pragma unroll
