@@ -314,21 +314,26 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
             if (ok && j >= 1) ok = mbar_wait_warp(s_empty, (j - 1) & 1);           // S_{j-1} is read
             const int at = j % kL8Tiles * kL8Pieces;
-            for (int k = 0; k < kL8Pieces && ok; ++k) {
-                const int u = k == 0 ? 4 : k - 1;
-                if (!(ok = mbar_wait_warp(&full[at + u], (j / kL8Tiles) & 1))) break;
+            const uint32_t here = (j / kL8Tiles) & 1;
+            // The rotary channels and the first codes, two more pieces, the last: a wait each
+#pragma unroll
+            for (int k = 0; k < 3 && ok; ++k) {
+                uint64_t* const two[2] = {&full[at + (k == 0 ? 4 : k == 1 ? 1 : 3)], &full[at + (k == 0 ? 0 : k == 1 ? 2 : 3)]};
+                if (!(ok = mbar_wait_all(two, {here, here}))) break;
                 tc_fence_after_sync();
-                const uint64_t da = sdesc_k_sw128(base + (at + u) * kL8Piece);
+                const uint64_t da = sdesc_k_sw128(base + at * kL8Piece);
                 if (elect_one()) {
-                    if (u == 4) {
+                    if (k == 0) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_bf16_ss(tmem + 2 * R, da + 2 * i, dr + 2 * i, rope, i > 0);
-                        mma_commit(&empty[at + u]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f8_ss(tmem, da + 2 * i, dq + u * (kL8QPiece / 16) + 2 * i, codes, u > 0 || i > 0);
+                        for (int i = 0; i < 4; ++i) mma_bf16_ss(tmem + 2 * R, da + 4 * (kL8Piece / 16) + 2 * i, dr + 2 * i, rope, i > 0);
+                        mma_commit(&empty[at + 4]);
                     }
-                    if (u == 3) {
+#pragma unroll
+                    for (int u = k == 0 ? 0 : 2 * k - 1; u < (k == 0 ? 1 : k == 1 ? 3 : 4); ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_f8_ss(tmem, da + u * (kL8Piece / 16) + 2 * i, dq + u * (kL8QPiece / 16) + 2 * i, codes, u > 0 || i > 0);
+                    if (k == 2) {
                         mma_commit(s_full);
                         if (w.last()) mma_commit(q_empty);
                     }
@@ -444,18 +449,24 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 len = ld_len(a, w.n);
                 ++seg;
             }
-            ok = mbar_wait_warp(s_full, j & 1) && mbar_wait_warp(&c_full[j & 1], (j >> 1) & 1);
-            if (!ok) {
+            if (!(ok = mbar_wait_warp(&c_full[j & 1], (j >> 1) & 1))) {
+                leave();
+                break;
+            }
+            const int token = w.j * kLdTile + thread;
+            const int byte = scales[(j & 1) * kLdTile + thread];
+            const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
+            // (also the products of the tile before last are complete then, whose weights this tile's replace: its codes
+            // came to where theirs were)
+            static_assert(kL8Tiles == 2, "as many buffers for the weights");
+            if (!(ok = mbar_wait_warp(s_full, j & 1))) {
                 leave();
                 break;
             }
             tc_fence_after_sync();
-            const int token = w.j * kLdTile + thread;
-            const int byte = scales[(j & 1) * kLdTile + thread];
             // y: log2 of the weight times 2^e
             float y[kL8Half];
             if (!idle) {
-                const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
                 const float* unit = worth + (seg - 1) % kL8Scales * R + r0;
                 float d2[kL8Half], dr[kL8Half];
                 tmem_ld16(lanes + r0, y);
@@ -542,13 +553,6 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     tmem_wait_st();
                 }
                 if (!idle) weigh();
-            }
-            if (j >= 2) {                                              // P's buffer: the products that read it are complete
-                ok = mbar_wait_warp(&o_full[j & 1], ((j - 2) >> 1) & 1);
-                if (!ok) {
-                    leave();
-                    break;
-                }
             }
             if (!idle) {
                 const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
