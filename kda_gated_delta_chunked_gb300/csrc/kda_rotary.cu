@@ -5,9 +5,13 @@
 // Bound by HBM bytes (every channel read once and written once; in place the
 // channels beside the turned ones are not touched).  A block takes some rows
 // (token and head) of the queries or of the keys and forms their tokens' sines and
-// cosines once, in shared memory, while its loads are on their way.  A thread has a
-// few vectors, the turned ones of all rows before the copied ones, so that a warp
-// does one of the two.
+// cosines once, in shared memory, while its first loads are on their way.  A thread
+// has a vector or two at a time, the turned ones of all rows before the copied
+// ones, so that a warp does one of the two; 32 registers, so that an SM is full of
+// them (with four vectors and 64 registers: 32768 tokens of 32 x 192 in 154 us).
+// Measured, us in a graph of ten (floor): that 122 (120); 65536 tokens of 8 + 8
+// heads of 128 56 (45); 65536 of one head of 64 9 (2.5: two million sines and as
+// many cosines); one token of 32 heads 2.5.
 //
 // The angle: f / (2 pi) turns a position, as a 64-bit fraction of a turn, times
 // the position in 64-bit integers that wrap at whole turns: off by 2^-63 of f / (2 pi)
@@ -167,13 +171,7 @@ kda_rotary_kernel(const __grid_constant__ RotArgs a) {
                                                                          : ((const int32_t*)a.positions)[token0 + token];
                     const float angle = (float)(int)((unsigned long long)pos * turns >> 32) * 0x1p-31f;    // half turns
                     float s, c;
-                    if constexpr (sizeof(T) == 2) {
-                        // 2^-21 off, in outputs of 8 bits (sincospi: 65536 tokens of one head 15 us, @@ so)
-                        s = __sinf(angle * 3.14159265f);
-                        c = __cosf(angle * 3.14159265f);
-                    } else {
-                        sincospif(angle, &s, &c);
-                    }
+                    sincospif(angle, &s, &c);
                     table[token * half + i] = make_float2(a.scale * c, sign * s);
                 }
             }

@@ -98,14 +98,12 @@ def rotary(x, positions, frequencies, dim, offset, interleaved, inverse, scale):
 
 
 # cos and sin: the angle in half turns is rounded to 24 bits (pi 2^-25), sincospi is off by 2 ulp (2^-23), then the
-# scale, the product and the sum are rounded (3 2^-24).  For 16-bit outputs the angle times pi is rounded twice more
-# (2 pi 2^-24) and the sine and cosine units are off by 2^-21.19.
+# scale, the product and the sum are rounded (3 2^-24)
 ROTARY = math.pi * 2.0 ** -25 + 2.0 ** -23 + 3 * 2.0 ** -24
-ROTARY16 = math.pi * 2.0 ** -25 + 2 * math.pi * 2.0 ** -24 + 2.0 ** -21.19 + 3 * 2.0 ** -24
 
 
 def rotary_bound(y, size, positions, frequencies, dtype):
     """Element-wise bound; the turn fraction of a position is off by 2^-52 of position times frequency."""
     angle = 2 * float(positions.abs().max() if positions.numel() else 0) * float(frequencies.abs().max()) * 2.0 ** -52
-    rel = (ROTARY16 if dtype == torch.bfloat16 else ROTARY) * 1.01 + angle
+    rel = ROTARY * 1.01 + angle
     return rel * size + HALF[dtype] * (y.abs() + rel * size) * (size > 0)
