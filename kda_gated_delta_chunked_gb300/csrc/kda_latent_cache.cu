@@ -23,6 +23,7 @@
 
 #include "kda_common.cuh"
 #include "kda_latent_cache.cuh"
+#include "kda_launch.cuh"
 #include "kda_paths.h"
 
 namespace kda {
@@ -214,6 +215,8 @@ __device__ __forceinline__ LcCodes<4> lc_codes(const uint4& v, float inv, const 
 template <typename T, bool kWide, int kTokens>
 __global__ void __launch_bounds__(32 * kLcWarps, sizeof(T) == 2 ? 5 : 4)
 kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
+    wait_before();
+    follow_me();
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
     constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
     const int lane = threadIdx.x & 31;
@@ -257,6 +260,8 @@ kda_latent_cache_write_kernel(const __grid_constant__ LatentCacheArgs a) {
 template <typename T, bool kWide, int kTokens>
 __global__ void __launch_bounds__(32 * kLcWarps, 8)
 kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
+    wait_before();
+    follow_me();
     if (a.status && blockIdx.x == gridDim.x - 1) return lc_check(a);
     constexpr int kVec = LcRow<T>::kVec, kVecs = LcRow<T>::kVecs;
     const int lane = threadIdx.x & 31;
@@ -331,9 +336,8 @@ kda_latent_cache_read_kernel(const __grid_constant__ LatentCacheArgs a) {
 template <typename T, bool kWide, int kTokens>
 static cudaError_t lc_launch_as(const LatentCacheArgs& a, bool write, cudaStream_t stream) {
     const int64_t blocks = (a.T + kLcWarps * kTokens - 1) / (kLcWarps * kTokens) + (a.status != nullptr);
-    if (write) kda_latent_cache_write_kernel<T, kWide, kTokens><<<(unsigned)blocks, 32 * kLcWarps, 0, stream>>>(a);
-    else kda_latent_cache_read_kernel<T, kWide, kTokens><<<(unsigned)blocks, 32 * kLcWarps, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(write ? kda_latent_cache_write_kernel<T, kWide, kTokens> : kda_latent_cache_read_kernel<T, kWide, kTokens>,
+                         dim3((unsigned)blocks), 32 * kLcWarps, 0, stream, a);
 }
 
 template <typename T>

@@ -34,6 +34,7 @@
 
 #include "kda_latent_cache.cuh"
 #include "kda_latent_decode.cuh"
+#include "kda_launch.cuh"
 #include "kda_per_device.h"
 #include "kda_tensor_map.h"
 
@@ -187,6 +188,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int group = blockIdx.x, cta = blockIdx.y;
+    wait_before();
     // What the range's start hangs on next, were the sequences equally long: the translations at least are then there.
     if (warp >= 11) {
         const int n = (int)((int64_t)cta * a.N / gridDim.y);
@@ -647,7 +649,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
     }
     tc_fence_before_sync();
     meet_at_end(fault);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    follow_me();
     if (warp == 0) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0) a.cta_status[cta * gridDim.x + group] = *fault;
 }
@@ -695,8 +697,7 @@ cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t str
     const uint64_t strides[2] = {(uint64_t)kL8Width, (uint64_t)d.page_stride};
     const uint32_t box[3] = {128, (uint32_t)(d.page_size < kLdTile ? d.page_size : kLdTile), 1};
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, d.cache, dims, strides, box)) return cudaErrorInvalidValue;
-    kda_latent_decode8_tc<<<dim3(p.groups, p.G), kL8Threads, kL8Smem, stream>>>(map, b);
-    err = cudaGetLastError();
+    err = launch_behind(kda_latent_decode8_tc, dim3(p.groups, p.G), kL8Threads, kL8Smem, stream, map, b);
     return err != cudaSuccess ? err : latent_decode_join_launch(a, kL8Rows, p.groups, stream);
 }
 

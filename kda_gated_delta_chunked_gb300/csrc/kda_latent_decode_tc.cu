@@ -43,6 +43,7 @@
 #include <math.h>
 
 #include "kda_latent_decode.cuh"
+#include "kda_launch.cuh"
 #include "kda_per_device.h"
 #include "kda_tensor_map.h"
 
@@ -456,7 +457,8 @@ kda_latent_decode_join(const LdArgs a, const int groups) {
     const int warps = blockDim.x >> 5;
     const int ch0 = blockIdx.z * 128 * Q;
     const int tiles = ld_tiles(a, n);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
+    follow_me();
     if (n == 0 && row == 0 && blockIdx.z == 0) {
         int st = 0;
         for (int i = threadIdx.x; i < a.G * groups; i += blockDim.x) st |= a.cta_status[i];

@@ -19,6 +19,7 @@
 #include <string.h>
 
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 #include "kda_paths.h"
 
 namespace kda {
@@ -114,6 +115,8 @@ kda_rotary_kernel(const __grid_constant__ RotArgs a) {
     using S = RotShape<T, B, kNear>;
     constexpr int V = S::V, kPairs = S::kPairs, kSteps = S::kSteps;
     __shared__ __align__(16) float2 table[kRotTable];
+    wait_before();
+    follow_me();
     const int half = a.dim / 2;
     const bool key = blockIdx.x >= a.part[0].blocks;
     const RotPart& p = a.part[key];
@@ -240,8 +243,7 @@ static cudaError_t rotary_launch_as(RotArgs a, cudaStream_t stream) {
     }
     const int64_t blocks = a.part[0].blocks + a.part[1].blocks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kda_rotary_kernel<T, B, kNear><<<(unsigned)blocks, kRotThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(kda_rotary_kernel<T, B, kNear>, dim3((unsigned)blocks), kRotThreads, 0, stream, a);
 }
 
 template <typename T, int B>
