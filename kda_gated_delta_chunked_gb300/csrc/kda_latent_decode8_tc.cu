@@ -314,14 +314,18 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 ok = seg == 0 ? mbar_wait_warp(q_first, 0) : mbar_wait_warp(q_full, (seg - 1) & 1);
                 ++seg;
             }
-            if (ok && j >= 1) ok = mbar_wait_warp(s_empty, (j - 1) & 1);           // S_{j-1} is read
             const int at = j % kL8Tiles * kL8Pieces;
             const uint32_t here = (j / kL8Tiles) & 1;
-            // The rotary channels and the first codes, two more pieces, the last: a wait each
+            bool ready = true;                                         // the tile is there: no waits behind that for S
+#pragma unroll
+            for (int k = 0; k < kL8Pieces; ++k) ready &= mbar_test_wait(&full[at + k], here);
+            ready = __all_sync(0xffffffffu, ready);
+            if (ok && j >= 1) ok = mbar_wait_warp(s_empty, (j - 1) & 1);           // S_{j-1} is read
+            // Otherwise the rotary channels and the first codes, two more pieces, the last: a wait each
 #pragma unroll
             for (int k = 0; k < 3 && ok; ++k) {
                 uint64_t* const two[2] = {&full[at + (k == 0 ? 4 : k == 1 ? 1 : 3)], &full[at + (k == 0 ? 0 : k == 1 ? 2 : 3)]};
-                if (!(ok = mbar_wait_all(two, {here, here}))) break;
+                if (!ready && !(ok = mbar_wait_all(two, {here, here}))) break;
                 tc_fence_after_sync();
                 const uint64_t da = sdesc_k_sw128(base + at * kL8Piece);
                 if (elect_one()) {
@@ -478,12 +482,14 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 tmem_ready(y);
                 tmem_ready(d2);
                 tmem_ready(dr);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty);
 #pragma unroll
                 for (int c = 0; c < kL8Half; ++c) y[c] = fmaf(fmaf(d2[c], 0.0625f, y[c]), two * unit[c], fmaf(dr[c], sc, e));
+            } else if (lane == 0) {
+                mbar_arrive(s_empty);
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty);
             if (!idle && (w.j + 1) * kLdTile > len - a.Lq + 1) {       // some row does not see some token
 #pragma unroll
                 for (int c = 0; c < kL8Half; ++c)

@@ -167,3 +167,13 @@ def test_python_refusals():
                  lambda: kda.latent_cache_read(x, x, x, total_tokens=1, page_size=64)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_nothing_of_a_device_is_kept_for_the_process():
+    """Functions' plain statics would be the first device's: attributes of kernels, blocks that run at once."""
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for name in ("kda_latent_decode8_tc.cu", "kda_latent_cache.cu", "kda_rotary.cu", "kda_launch.cuh", "kda_latent_decode.cuh"):
+        text = open(os.path.join(root, "kda_gated_delta_chunked_gb300", "csrc", name)).read()
+        found = re.findall(r"^ {4,}static (?!constexpr|__device__)(\w+)", text, re.M)
+        assert set(found) <= {"PerDevice"}, (name, found)
