@@ -450,7 +450,7 @@ KDA_API int kda_latent_prefill(const kda_latent_desc *desc, const void *q, const
  * quantised cache below, each exactly.  bf16 queries, rank 512 and d_rope 64 run
  * on the tensor cores, on the codes themselves: there a query is the sum of two
  * e4m3 values under one power of two for its row (exact down to 2^-22 of its
- * largest channel; infinite channels count as NaN) and a softmax weight the sum of
+ * largest channel; infinite ones count as NaN) and a softmax weight the sum of
  * three e5m2 values (off by 2^-8.6 of it at most, or by 2^-26 of the row's largest
  * weight, whichever is more); sums are fp32.  Everything else, and fp32 queries,
  * run on CUDA cores in fp32. */

@@ -21,13 +21,30 @@
 //
 // The rotary channels are bf16 and have columns of their own.  Both products read
 // the same tile in shared memory, the second as an MN-major operand: a tile is
-// fetched once, 641 bytes a token.  A thread owns a token, so its scale is a
-// thread's number.  The softmax reference of a row bounds P (not p): it moves when
-// some P exceeds it by 2^12, and stands at 2^3, so that P stays below 2^15, e5m2's
-// largest power of two.
+// fetched once, 641 bytes a token.  A thread owns a token and half of the rows, so
+// the token's scale is a thread's number, and the halves need not wait for one
+// another.  The softmax reference of a row bounds P (not p): it moves when some P
+// exceeds it by 2^12, and stands at 2^3, so that P stays below 2^15, e5m2's largest
+// power of two.
 //
 // CTAs have groups of 32 query rows; how the tiles are shared out, and the joining
-// of the pieces, are kda_latent_decode_tc.cu's.
+// of the pieces, are kda_latent_decode_tc.cu's.  A warp each copies, issues the one
+// product and the other, and fetches the tokens' scales; eight do the softmax, four
+// the queries of the sequence that comes next.
+//
+// One group: bound by HBM.  A tile's 82 KB take an SM 3650 cycles at 6.78 TB/s.
+// Several groups, which share a tile in L2: 2700 a tile.  An instruction takes as
+// long as its operands at 128 bytes a cycle (32, 64, 96 columns: 40, 48, 56 cycles),
+// a tile's 1830, and the copies' 82 KB, the weights and the softmax use the same
+// shared memory.  (A tile of 96 tokens, three in shared memory: 64 x up to 16384
+// tokens, 32 heads 75 us instead of 77, but 64 x 4096, 128 heads 121 instead of 108.)
+// The first scores come 4 us after the start, a sequence's end costs 3, the join 3
+// to 9.
+// Measured, us in a graph of ten / one behind a flush of L2 (the join included):
+//   64 x 16384 tokens, 16 heads  117 (5.7 TB/s) / 131       64 x 4096, 64 heads   64 / 72
+//   64 x up to 16384, 32 heads   77 / 89                    64 x 4096, 128 heads  108 / 112
+//   128 x 1024, 16 heads         27 / 37                    3 x 8192, 128 heads   26 / 31
+//   1 x 30000, 32 heads          17 / 25                    1 x 700, 32 heads     12 / 18
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -413,10 +430,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 #pragma unroll 1
             for (int i0 = 0; i0 < R / 4; i0 += 2) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = warp - 12 + 4 * (i0 + i);
-                    l8_convert(mem, worth + seg % kL8Scales * R, r, lane, sc, x[i][0], x[i][1], rope[i]);
-                }
+                for (int i = 0; i < 2; ++i)
+                    l8_convert(mem, worth + seg % kL8Scales * R, warp - 12 + 4 * (i0 + i), lane, sc, x[i][0], x[i][1], rope[i]);
 #pragma unroll
                 for (int i = 0; i + 2 < R / 4; ++i) {
                     x[i][0] = x[i + 2][0];
