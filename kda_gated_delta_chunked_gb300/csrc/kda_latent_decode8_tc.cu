@@ -33,17 +33,20 @@
 // the queries of the sequence that comes next.
 //
 // One group: bound by HBM.  A tile's 82 KB take an SM 3650 cycles at 6.78 TB/s.
-// Several groups, which share a tile in L2: 2700 a tile.  An instruction takes as
-// long as its operands at 128 bytes a cycle (32, 64, 96 columns: 40, 48, 56 cycles),
-// a tile's 1830, and the copies' 82 KB, the weights and the softmax use the same
-// shared memory.  (A tile of 96 tokens, three in shared memory: 64 x up to 16384
-// tokens, 32 heads 75 us instead of 77, but 64 x 4096, 128 heads 121 instead of 108.)
+// Several groups, which share a tile in L2: 2700 a tile.  The tensor core takes 1830
+// of them (an instruction lasts as long as its operands at 128 bytes a cycle: 32, 64,
+// 96 columns 40, 48, 56 cycles).  What bounds it is how long a piece stays: 1900 to
+// arrive, 930 the scores, 1500 the softmax, 900 the second product, with room for two
+// tiles.  Measured beside it: tiles of 96 tokens, three in shared memory (64 x up to
+// 16384 tokens, 32 heads 75 us instead of 77; 64 x 4096, 128 heads 121 instead of
+// 108); one place for the weights and a ring of nine or ten pieces of codes instead of
+// eight (114 and 117 instead of 109).
 // The first scores come 4 us after the start, a sequence's end costs 3, the join 3
 // to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  117 (5.7 TB/s) / 131       64 x 4096, 64 heads   64 / 72
-//   64 x up to 16384, 32 heads   77 / 89                    64 x 4096, 128 heads  108 / 112
-//   128 x 1024, 16 heads         27 / 37                    3 x 8192, 128 heads   26 / 31
+//   64 x 16384 tokens, 16 heads  116 (5.8 TB/s) / 131       64 x 4096, 64 heads   64 / 72
+//   64 x up to 16384, 32 heads   77 / 89                    64 x 4096, 128 heads  106 / 111
+//   128 x 1024, 16 heads         27 / 37                    3 x 8192, 128 heads   25 / 31
 //   1 x 30000, 32 heads          17 / 25                    1 x 700, 32 heads     12 / 18
 #include <cuda_fp16.h>
 #include <math.h>
@@ -286,7 +289,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
     }
 
     if (warp == 8) {                                                   // ---------------- producer
-        const int box = min(a.page_size, kLdTile), boxes = kLdTile / box;
+        const int box = min(a.page_size, kLdTile), boxes = kLdTile / box, shift = __ffs(a.page_size) - 1;
         bool ok = true, bad_page = false;
         // A lane for each box of tokens: its page, asked for a tile ahead.  Pages behind the length, and bad ones, read
         // as zeros.
@@ -297,8 +300,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             if (w.first) len = ld_len(a, w.n);
             const int t = w.j * kLdTile + lane * box;
             some = lane < boxes && t < len;
-            row = t % a.page_size;
-            if (some) page = a.table[(int64_t)w.n * a.max_pages + t / a.page_size];
+            row = t & (a.page_size - 1);
+            if (some) page = a.table[(int64_t)w.n * a.max_pages + (t >> shift)];
         };
         ask();
         for (int j = 0; j < count && ok; ++j) {
@@ -392,15 +395,16 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 11) {                                           // ---------------- scales
         // Four tokens' bytes a lane, fetched a tile ahead; 0 (2^-127) where there is nothing.
+        const int shift = __ffs(a.page_size) - 1;
         int len = 0;
         auto fetch = [&](const LdWalk& x) -> uint32_t {
             const int t = x.j * kLdTile + 4 * lane;
             if (x.left <= 0) return 0;
             if (x.first) len = ld_len(a, x.n);
             if (t >= len) return 0;
-            const int p = a.table[(int64_t)x.n * a.max_pages + t / a.page_size];
+            const int p = a.table[(int64_t)x.n * a.max_pages + (t >> shift)];
             if (p < 0 || p >= a.num_pages) return 0;
-            return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + t % a.page_size);
+            return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + (t & (a.page_size - 1)));
         };
         bool ok = true;
         uint32_t now = fetch(w);
