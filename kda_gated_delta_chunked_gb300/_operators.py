@@ -284,8 +284,8 @@ def latent_decode(q, cache, page_table, lengths, *, scale: float, rank: Optional
 
     A uint8 cache ``[pages, latent_cache_page_bytes(...)]`` with its
     ``page_size`` is a quantised one (``latent_cache_write``).  In bf16, queries
-    and softmax weights then meet its codes as sums of two 8-bit values each
-    (include/kda.h); fp32 queries stay in fp32."""
+    and softmax weights then meet its codes as sums of two and three 8-bit
+    values (include/kda.h); fp32 queries stay in fp32."""
     return _call("latent_decode", stream, q, cache, page_table, lengths, scale, -1 if rank is None else rank, flags, out,
                  lse, workspace, page_size)
 

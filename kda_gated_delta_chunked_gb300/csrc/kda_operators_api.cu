@@ -368,11 +368,11 @@ int kda_rotary(const kda_rotary_desc* d, const void* x, const void* key, const v
     if (!d || d->tokens < 0 || d->dim < 2 || d->dim % 2 != 0 || !dtype_ok(d->dtype) || !isfinite(d->scale)) return KDA_ERR_INVALID_ARGUMENT;
     if (d->flags & ~(KDA_FLAG_INTERLEAVED | KDA_FLAG_INVERSE | KDA_FLAG_POSITIONS_64)) return KDA_ERR_INVALID_ARGUMENT;
     if ((key == nullptr) != (key_out == nullptr) && d->tokens > 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (d->dim > 1024 || d->tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     const bool two = key != nullptr || key_out != nullptr;
     for (int i = 0; i < (two ? 2 : 1); ++i) {
         if (int rc = rotary_part(i ? d->key : d->x, d->tokens, d->dim)) return rc;
     }
-    if (d->dim > 1024 || d->tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     if (d->tokens == 0) return KDA_OK;
     if (!x || !out || !positions || !frequencies) return KDA_ERR_INVALID_ARGUMENT;
     const size_t e = esize(d->dtype), pos = d->flags & KDA_FLAG_POSITIONS_64 ? 8 : 4;
