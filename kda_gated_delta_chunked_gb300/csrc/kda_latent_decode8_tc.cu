@@ -35,17 +35,18 @@
 // One group: bound by HBM.  A tile's 82 KB take an SM 3650 cycles at 6.78 TB/s.
 // Several groups, which share a tile in L2: 2700 a tile.  The tensor core takes 1830
 // of them (an instruction lasts as long as its operands at 128 bytes a cycle: 32, 64,
-// 96 columns 40, 48, 56 cycles).  What bounds it is how long a piece stays: 1900 to
-// arrive, 930 the scores, 1500 the softmax, 900 the second product, with room for two
-// tiles.  Measured beside it: tiles of 96 tokens, three in shared memory (64 x up to
-// 16384 tokens, 32 heads 75 us instead of 77; 64 x 4096, 128 heads 121 instead of
-// 108); one place for the weights and a ring of nine or ten pieces of codes instead of
-// eight (114 and 117 instead of 109).
+// 96 columns 40, 48, 56 cycles).  What bounds it is how long a piece stays: 900 to
+// arrive (1900 from HBM), 930 the scores, 1500 the softmax, 900 the second product,
+// with room for two tiles, and the pieces come one after another.  Measured beside
+// it: tiles of 96 tokens, three in shared memory (64 x up to 16384 tokens, 32 heads
+// 75 us instead of 77; 64 x 4096, 128 heads 121 instead of 108); one place for the
+// weights and a ring of nine or ten pieces of codes instead of eight (114 and 117
+// instead of 109).
 // The first scores come 4 us after the start, a sequence's end costs 3, the join 3
 // to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  116 (5.8 TB/s) / 131       64 x 4096, 64 heads   64 / 72
-//   64 x up to 16384, 32 heads   77 / 89                    64 x 4096, 128 heads  106 / 111
+//   64 x 16384 tokens, 16 heads  112 (6.0 TB/s) / 129       64 x 4096, 64 heads   63 / 68
+//   64 x up to 16384, 32 heads   74 / 86                    64 x 4096, 128 heads  106 / 107
 //   128 x 1024, 16 heads         27 / 37                    3 x 8192, 128 heads   25 / 31
 //   1 x 30000, 32 heads          17 / 25                    1 x 700, 32 heads     12 / 18
 #include <cuda_fp16.h>
@@ -139,6 +140,10 @@ __device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n,
     return b.q + ((int64_t)n * b.a.Lq + i) * b.q_ts + (row - i * b.a.H) * b.q_hs;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__device__ __forceinline__ void prefetch_l2_rows(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 // Query row r in registers (16 channels a lane, two rotary ones) to q1, q2 and the rotary part in shared memory, by a warp.
 __device__ __forceinline__ void l8_convert(uint8_t* mem, float* worth, int r, int lane, float sc, uint4 x0, uint4 x1, uint32_t rope) {
@@ -321,6 +326,10 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, at_row, bad ? a.num_pages : here, smem_u32(&full[at + u]));
                 __syncwarp();
             }
+            // The next tile's rows, dense in a page, to L2: there is no place in shared memory for them yet (64 x up to
+            // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80)
+            if (w.left > 0 && some && page >= 0 && page < a.num_pages)
+                prefetch_l2_rows(b.cache + page * b.page_stride + row * kL8Width, box * kL8Width);
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
         if (!ok) atomicOr(fault, kLdLate);
