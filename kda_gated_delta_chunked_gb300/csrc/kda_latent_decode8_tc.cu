@@ -33,15 +33,15 @@
 // the queries of the sequence that comes next.
 //
 // One group: bound by HBM.  A tile's 82 KB take an SM 3650 cycles at 6.78 TB/s.
-// Several groups, which share a tile in L2: 2700 a tile.  The tensor core takes 1830
-// of them (an instruction lasts as long as its operands at 128 bytes a cycle: 32, 64,
-// 96 columns 40, 48, 56 cycles).  What bounds it is how long a piece stays: 900 to
-// arrive (1900 from HBM), 930 the scores, 1500 the softmax, 900 the second product,
-// with room for two tiles, and the pieces come one after another.  Measured beside
-// it: tiles of 96 tokens, three in shared memory (64 x up to 16384 tokens, 32 heads
-// 75 us instead of 77; 64 x 4096, 128 heads 121 instead of 108); one place for the
-// weights and a ring of nine or ten pieces of codes instead of eight (114 and 117
-// instead of 109).
+// Several groups, which share a tile in L2: 2500 a tile, and shared memory is busy
+// for about as long at its 128 bytes a cycle: 1830 with the operands (an instruction
+// of 32, 64, 96 columns takes 40, 48, 56 cycles), 640 with the copies, 100 with the
+// weights.  A piece stays for 4200, 900 to arrive (1900 from HBM), 930 the scores,
+// 1500 the softmax, 900 the second product, and there is room for two tiles.
+// Measured beside it: tiles of 96 tokens, three in shared memory (64 x up to 16384
+// tokens, 32 heads 75 us instead of 77; 64 x 4096, 128 heads 121 instead of 108); one
+// place for the weights and a ring of nine or ten pieces of codes instead of eight
+// (114 and 117 instead of 109).
 // The first scores come 4 us after the start, a sequence's end costs 3, the join 3
 // to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
