@@ -145,9 +145,9 @@ __device__ __forceinline__ void prefetch_l2_rows(const void* p, uint32_t bytes) 
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// Query row r in registers (16 channels a lane, two rotary ones) to q1, q2 and the rotary part in shared memory, by a warp.
-__device__ __forceinline__ void l8_convert(uint8_t* mem, float* worth, int r, int lane, float sc, uint4 x0, uint4 x1, uint32_t rope) {
-    constexpr int R = kL8Rows;
+// A query row in registers (16 channels a lane in two vectors) to q1 and q2 there, by a warp, and what a unit of q1 is
+// worth.
+__device__ __forceinline__ float l8_convert(uint4& x0, uint4& x1, float sc) {
     uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     uint32_t top = 0;                                      // largest channel's bits, in each half
 #pragma unroll
@@ -179,12 +179,32 @@ __device__ __forceinline__ void l8_convert(uint8_t* mem, float* worth, int r, in
         q1[k] = __byte_perm(lo[0], lo[1], 0x6420);
         q2[k] = __byte_perm(hi[0], hi[1], 0x6420);
     }
+    x0 = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    x1 = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+    return strange ? NAN : __uint_as_float((uint32_t)(127 + e) << 23) * sc;
+}
+// To shared memory, with two rotary channels a lane.
+__device__ __forceinline__ void l8_put(uint8_t* mem, int r, int lane, uint4 q1, uint4 q2, uint32_t rope) {
     const int swz = r & 7;
     uint8_t* to = mem + kL8OffQ + (lane / 8) * kL8QPiece + r * 128 + ((lane & 7) ^ swz) * 16;
-    *(uint4*)to = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-    *(uint4*)(to + R * 128) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+    *(uint4*)to = q1;
+    *(uint4*)(to + kL8Rows * 128) = q2;
     *(uint32_t*)(mem + kL8OffRope + r * 128 + ((lane / 4) ^ swz) * 16 + lane % 4 * 4) = rope;
-    if (lane == 0) worth[r] = strange ? NAN : __uint_as_float((uint32_t)(127 + e) << 23) * sc;
+}
+
+// The boxes of a piece, B at once, by a warp: operands in uniform registers (a lane for each box: 80 cycles a box).
+template <int B>
+__device__ __forceinline__ void l8_boxes(uint32_t to, const CUtensorMap* map, int x, int row, int page, int boxes, int box, uint64_t* bar) {
+    for (int b0 = 0; b0 < boxes; b0 += B) {
+        int z[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) z[i] = __shfl_sync(0xffffffffu, page, b0 + i);
+        if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) tma_load_3d_at(to + (b0 + i) * box * 128, map, x, row, z[i], smem_u32(bar));
+        }
+        __syncwarp();
+    }
 }
 
 __global__ void __launch_bounds__(kL8Threads, 1)
@@ -280,7 +300,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         for (int i = 0; i < 3; ++i) load_row(first + 12 * i, x[i][0], x[i][1], rope[i]);
 #pragma unroll 1
         for (int r = first; r < R; r += 12) {
-            l8_convert(mem, worth, r, lane, a.scale * 1.4426950408889634f, x[0][0], x[0][1], rope[0]);
+            const float unit = l8_convert(x[0][0], x[0][1], a.scale * 1.4426950408889634f);
+            l8_put(mem, r, lane, x[0][0], x[0][1], rope[0]);
+            if (lane == 0) worth[r] = unit;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 x[i][0] = x[i + 1][0];
@@ -316,15 +338,18 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             ask();
             const bool bad = asked && (here < 0 || here >= a.num_pages);
             bad_page |= bad;
+            const int from_page = bad ? a.num_pages : here, in_page = uniform(at_row);     // (not 0: a single box)
             const int at = j % kL8Tiles * kL8Pieces;
             for (int k = 0; k < kL8Pieces; ++k) {
                 const int u = k == 0 ? 4 : k - 1;                      // the rotary channels first, they are free first
                 if (!(ok = mbar_wait_warp(&empty[at + u], (j / kL8Tiles + 1) & 1))) break;   // (a fresh barrier counts as emptied)
-                if (lane == 0) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
+                if (elect_one()) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_3d_at(base + (at + u) * kL8Piece + lane * box * 128, &map, u * 128, at_row, bad ? a.num_pages : here, smem_u32(&full[at + u]));
-                __syncwarp();
+                const uint32_t to = base + (at + u) * kL8Piece;
+                if (boxes == 1) l8_boxes<1>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
+                else if (boxes == 2) l8_boxes<2>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
+                else if (boxes == 4) l8_boxes<4>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
+                else l8_boxes<8>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
             }
             // The next tile's rows, dense in a page, to L2: there is no place in shared memory for them yet (64 x up to
             // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80)
@@ -434,24 +459,32 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         bool ok = true;
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
             if (!w.first || j == 0) continue;                          // (the first segment's are done)
-            // All rows' loads at once; then two rows after two by the same instructions (four times as many are cold).
+            // All rows' loads at once; then one after another by the same instructions (others would be cold), in registers
+            // until the last segment's products are done.
             uint4 x[R / 4][2];
             uint32_t rope[R / 4];
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) load_row(warp - 12 + 4 * i, x[i][0], x[i][1], rope[i]);
-            if (!(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
+            // (worth: that of the segment four before was read before its last scores were replaced)
 #pragma unroll 1
-            for (int i0 = 0; i0 < R / 4; i0 += 2) {
+            for (int k = 0; k < R / 4; ++k) {
+                const float unit = l8_convert(x[0][0], x[0][1], sc);
+                if (lane == 0) worth[seg % kL8Scales * R + warp - 12 + 4 * k] = unit;
+                const uint4 q1 = x[0][0], q2 = x[0][1];
+                const uint32_t same = rope[0];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    l8_convert(mem, worth + seg % kL8Scales * R, warp - 12 + 4 * (i0 + i), lane, sc, x[i][0], x[i][1], rope[i]);
-#pragma unroll
-                for (int i = 0; i + 2 < R / 4; ++i) {
-                    x[i][0] = x[i + 2][0];
-                    x[i][1] = x[i + 2][1];
-                    rope[i] = rope[i + 2];
+                for (int i = 0; i + 1 < R / 4; ++i) {                  // (round by one: in order again at the end)
+                    x[i][0] = x[i + 1][0];
+                    x[i][1] = x[i + 1][1];
+                    rope[i] = rope[i + 1];
                 }
+                x[R / 4 - 1][0] = q1;
+                x[R / 4 - 1][1] = q2;
+                rope[R / 4 - 1] = same;
             }
+            if (!(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) l8_put(mem, warp - 12 + 4 * i, lane, x[i][0], x[i][1], rope[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
@@ -477,10 +510,10 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         bool ok = true;
         uint32_t seg = 0;
         int len = 0;
-        for (int j = 0; j < count; ++j, w.next(a)) {
+        if (count > 0) len = ld_len(a, w.n);
+        for (int j = 0; j < count; ++j) {
             if (w.first) {
                 if (w.j == 0 && threadIdx.x == 0 && group == 0) a.before[w.n] = *range_at + j;
-                len = ld_len(a, w.n);
                 ++seg;
             }
             if (!(ok = mbar_wait_warp(&c_full[j & 1], (j >> 1) & 1))) {
@@ -523,23 +556,29 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 for (int c = 0; c < kL8Half; ++c)
                     if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
             }
-            // The weights under the references as they are; under new ones, where some weight is too large for that.
+            // The weights under the references as they are, and under new ones where some weight is too large for that or
+            // there are none yet: the same instructions, others would be cold.
             float p[kL8Half];
-            bool over = false;
-            auto weigh = [&]() {
+#pragma unroll 1
+            for (bool moved = false;; moved = true) {
+                bool over = w.first && !moved && !idle;
+                if (!idle && !over) {
 #pragma unroll
-                for (int c = 0; c < kL8Half; c += 4) {
-                    const float4 m = *(const float4*)(ref + r0 + c);
-                    const float d[4] = {y[c] - m.x, y[c + 1] - m.y, y[c + 2] - m.z, y[c + 3] - m.w};
+                    for (int c = 0; c < kL8Half; c += 4) {
+                        const float4 m = *(const float4*)(ref + r0 + c);
+                        const float d[4] = {y[c] - m.x, y[c + 1] - m.y, y[c + 2] - m.z, y[c + 3] - m.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        over |= d[k] > kL8Slack;
-                        p[c + k] = ex2(d[k] + kL8Stand);
+                        for (int k = 0; k < 4; ++k) {
+                            over |= d[k] > kL8Slack;
+                            p[c + k] = ex2(d[k] + kL8Stand);
+                        }
                     }
+                } else {                                               // (no register is held for the ones before)
+#pragma unroll
+                    for (int c = 0; c < kL8Half; ++c) p[c] = 0.f;
                 }
-            };
-            if (!idle) weigh();
-            if (!bar_and_id(vote, 128, !over)) {                       // move the references to the maxima
+                if (moved || bar_and_id(vote, 128, !over)) break;
+                // Move the references to the maxima
                 if (*(volatile int*)(gave + half)) {
                     ok = false;
                     break;
@@ -548,48 +587,48 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 sync();
                 if (thread < kL8Half) {
                     const int c = r0 + thread;
-                    const float old = ref[c];
+                    const float old = w.first ? kLdUnset : ref[c];
                     const float now = fmaxf(old, fmaxf(fmaxf(across[c], across[R + c]),
                                                        fmaxf(across[2 * R + c], across[3 * R + c])));
                     ref[c] = now;
                     fac[c] = ex2(old - now);
                 }
                 sync();
+                if (w.first) continue;                                 // (no sums and no O^T yet)
                 float f[kL8Half];
 #pragma unroll
                 for (int c = 0; c < kL8Half; ++c) {
                     f[c] = fac[r0 + c];
                     l[c] *= f[c];
                 }
-                if (!w.first) {                                        // O^T, once the products into it are complete
-                    ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after_sync();
+                // O^T, once the products into it are complete
+                ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1));
+                if (!ok) break;
+                tc_fence_after_sync();
 #pragma unroll 1
-                    for (int p = 0; p < 4; ++p) {
-                        const uint32_t at = lanes + kL8O + p * 3 * R + r0;
-                        float o1[kL8Half], o2[kL8Half], o3[kL8Half];
-                        tmem_ld16(at, o1);
-                        tmem_ld16(at + R, o2);
-                        tmem_ld16(at + 2 * R, o3);
-                        tmem_wait_ld();
-                        tmem_ready(o1);
-                        tmem_ready(o2);
-                        tmem_ready(o3);
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t at = lanes + kL8O + b * 3 * R + r0;
+                    float o1[kL8Half], o2[kL8Half], o3[kL8Half];
+                    tmem_ld16(at, o1);
+                    tmem_ld16(at + R, o2);
+                    tmem_ld16(at + 2 * R, o3);
+                    tmem_wait_ld();
+                    tmem_ready(o1);
+                    tmem_ready(o2);
+                    tmem_ready(o3);
 #pragma unroll
-                        for (int c = 0; c < kL8Half; ++c) {
-                            o1[c] *= f[c];
-                            o2[c] *= f[c];
-                            o3[c] *= f[c];
-                        }
-                        tmem_st16(at, o1);
-                        tmem_st16(at + R, o2);
-                        tmem_st16(at + 2 * R, o3);
+                    for (int c = 0; c < kL8Half; ++c) {
+                        o1[c] *= f[c];
+                        o2[c] *= f[c];
+                        o3[c] *= f[c];
                     }
-                    tmem_wait_st();
+                    tmem_st16(at, o1);
+                    tmem_st16(at + R, o2);
+                    tmem_st16(at + 2 * R, o3);
                 }
-                if (!idle) weigh();
+                tmem_wait_st();
             }
+            if (!ok) break;
             if (!idle) {
                 const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
                 uint32_t p1[4], p2[4], p3[4];
@@ -616,21 +655,26 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[j & 1]);
-            if (!w.last()) continue;
+            const LdWalk at = w;
+            w.next(a);
+            if (!at.last()) continue;
 
             // end of a segment: sums across the tokens' threads, then O^T out
+            if (w.left > 0) len = ld_len(a, w.n);
             ld_columns<kL8Half, false>(l, sums + part * R + r0, lane);
+#pragma unroll
+            for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
             ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
-            const bool whole = w.from == 0 && w.j + 1 == w.tiles;
-            float* dst = a.parts + ((size_t)(cta * gridDim.x + group) * 2 + (w.from == 0)) * R * kLdPart;
+            const bool whole = at.from == 0 && at.j + 1 == at.tiles;
+            float* dst = a.parts + ((size_t)(cta * gridDim.x + group) * 2 + (at.from == 0)) * R * kLdPart;
             if (thread < kL8Half) {
                 const int c = r0 + thread;
                 const float total = (sums[c] + sums[R + c]) + (sums[2 * R + c] + sums[3 * R + c]);
                 if (whole) {
                     fac[c] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
-                    if (c < live && a.lse) a.lse[(size_t)w.n * a.rows + row0 + c] =
+                    if (c < live && a.lse) a.lse[(size_t)at.n * a.rows + row0 + c] =
                         total == 0.f ? -INFINITY : (ref[c] - kL8Stand + log2f(total)) * 0.6931471805599453f;
                 } else {
                     dst[c * kLdPart + kLdRank] = ref[c] - kL8Stand;
@@ -639,10 +683,10 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
             sync();
 #pragma unroll 1
-            for (int p = 0; p < 4 && !idle; ++p) {
-                const int ch = p * 128 + thread;
+            for (int b = 0; b < 4 && !idle; ++b) {
+                const int ch = b * 128 + thread;
                 float o[kL8Half], o2[kL8Half], o3[kL8Half];
-                const uint32_t from = lanes + kL8O + p * 3 * R + r0;
+                const uint32_t from = lanes + kL8O + b * 3 * R + r0;
                 tmem_ld16(from, o);
                 tmem_ld16(from + R, o2);
                 tmem_ld16(from + 2 * R, o3);
@@ -653,7 +697,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 #pragma unroll
                 for (int c = 0; c < kL8Half; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
                 if (whole) {
-                    __nv_bfloat16* out = a.out + ((size_t)w.n * a.rows + row0 + r0) * kLdRank + ch;
+                    __nv_bfloat16* out = a.out + ((size_t)at.n * a.rows + row0 + r0) * kLdRank + ch;
                     if (r0 + kL8Half <= live) {
 #pragma unroll
                         for (int c = 0; c < kL8Half; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
@@ -667,11 +711,6 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     for (int c = 0; c < kL8Half; ++c) dst[(r0 + c) * kLdPart + ch] = o[c];
                 }
             }
-            sync();
-            if (thread < kL8Half) ref[r0 + thread] = kLdUnset;
-#pragma unroll
-            for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
-            sync();
         }
         if (!ok) {
             // The join finds the pieces by where the sequences start, those of the tiles that were left among them.
