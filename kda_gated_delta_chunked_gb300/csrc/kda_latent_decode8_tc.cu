@@ -45,10 +45,11 @@
 // The first scores come 4 us after the start, a sequence's end costs 3, the join 3
 // to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  112 (6.0 TB/s) / 129       64 x 4096, 64 heads   63 / 68
-//   64 x up to 16384, 32 heads   74 / 86                    64 x 4096, 128 heads  106 / 107
-//   128 x 1024, 16 heads         27 / 37                    3 x 8192, 128 heads   25 / 31
+//   64 x 16384 tokens, 16 heads  112 (6.0 TB/s) / 127       64 x 4096, 64 heads   61 / 68
+//   64 x up to 16384, 32 heads   73 / 86                    64 x 4096, 128 heads  104 / 107
+//   128 x 1024, 16 heads         25 / 35                    3 x 8192, 128 heads   24 / 29
 //   1 x 30000, 32 heads          17 / 25                    1 x 700, 32 heads     12 / 18
+//   64 x 8192, 16 heads, pages of 8, 16, 32 and more: 69, 68, 64.5 (copies are issued a box of a page at a time)
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -352,8 +353,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 else l8_boxes<8>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
             }
             // The next tile's rows, dense in a page, to L2: there is no place in shared memory for them yet (64 x up to
-            // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80)
-            if (w.left > 0 && some && page >= 0 && page < a.num_pages)
+            // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80).  Not where issuing many small
+            // copies bounds the tiles (64 x 4096 tokens, 64 heads, pages of 8: 81 with them, 73 without)
+            if (boxes <= 4 && w.left > 0 && some && page >= 0 && page < a.num_pages)
                 prefetch_l2_rows(b.cache + page * b.page_stride + row * kL8Width, box * kL8Width);
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
