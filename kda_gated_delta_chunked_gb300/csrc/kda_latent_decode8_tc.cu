@@ -142,6 +142,17 @@ __device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n,
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// The warp's maximum of each column to `to`[column].
+__device__ __forceinline__ void l8_maxima(const float (&x)[kL8Half], float* to, int lane) {
+    float mine = 0.f;
+#pragma unroll
+    for (int c = 0; c < kL8Half; ++c) {
+        float top;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(x[c]));
+        if (lane == c) mine = top;
+    }
+    if (lane < kL8Half) to[lane] = mine;
+}
 __device__ __forceinline__ void prefetch_l2_rows(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -585,7 +596,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     ok = false;
                     break;
                 }
-                ld_columns<kL8Half, true>(y, across + part * R + r0, lane);
+                l8_maxima(y, across + part * R + r0, lane);
                 sync();
                 if (thread < kL8Half) {
                     const int c = r0 + thread;
