@@ -81,6 +81,7 @@ constexpr uint32_t kL8O = 3 * kL8Rows;                       // first TMEM colum
 struct L8Args {
     LdArgs a;
     int64_t q_ts, q_hs, page_stride;
+    uint32_t by_heads;                          // 2^31 / H, rounded up
     const __nv_bfloat16* q;
     const uint8_t* cache;
 };
@@ -137,7 +138,7 @@ __device__ __forceinline__ void l8_codes(__nv_bfloat162 t, uint32_t& q1, uint32_
 
 // Query row `row` (query, head) of sequence n.
 __device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n, int row) {
-    const int i = row / b.a.H;
+    const int i = (int)((uint64_t)row * b.by_heads >> 31);             // row / H: exact while row H < 2^31
     return b.q + ((int64_t)n * b.a.Lq + i) * b.q_ts + (row - i * b.a.H) * b.q_hs;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -312,7 +313,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         for (int i = 0; i < 3; ++i) load_row(first + 12 * i, x[i][0], x[i][1], rope[i]);
 #pragma unroll 1
         for (int r = first; r < R; r += 12) {
-            const float unit = l8_convert(x[0][0], x[0][1], a.scale * 1.4426950408889634f);
+            float unit = 0.f;                                          // (rows that are none are zeros already)
+            if (r < live) unit = l8_convert(x[0][0], x[0][1], a.scale * 1.4426950408889634f);
             l8_put(mem, r, lane, x[0][0], x[0][1], rope[0]);
             if (lane == 0) worth[r] = unit;
 #pragma unroll
@@ -481,7 +483,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             // (worth: that of the segment four before was read before its last scores were replaced)
 #pragma unroll 1
             for (int k = 0; k < R / 4; ++k) {
-                const float unit = l8_convert(x[0][0], x[0][1], sc);
+                float unit = 0.f;
+                if (warp - 12 + 4 * k < live) unit = l8_convert(x[0][0], x[0][1], sc);
                 if (lane == 0) worth[seg % kL8Scales * R + warp - 12 + 4 * k] = unit;
                 const uint4 q1 = x[0][0], q2 = x[0][1];
                 const uint32_t same = rope[0];
@@ -776,6 +779,7 @@ cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t str
     constexpr int kAt = 2 * kL8Tiles * kL8Pieces;
     constexpr uint32_t kDrops[6] = {0, (1u << kAt / 2) - 1, 1u << (kAt + 2), 3u << (kAt + 4), 3u << (kAt + 6), 1u << kAt | 7u << (kAt + 8)};
     a.drop = kDrops[d.drop];
+    b.by_heads = (uint32_t)(((1ull << 31) + d.H - 1) / d.H);
     b.q = (const __nv_bfloat16*)d.q; b.q_ts = d.q_ts; b.q_hs = d.q_hs;
     b.cache = (const uint8_t*)d.cache; b.page_stride = d.page_stride;
     CUtensorMap map;
