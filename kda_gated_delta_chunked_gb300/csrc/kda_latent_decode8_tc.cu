@@ -42,13 +42,13 @@
 // tokens, 32 heads 75 us instead of 77; 64 x 4096, 128 heads 121 instead of 108); one
 // place for the weights and a ring of nine or ten pieces of codes instead of eight
 // (114 and 117 instead of 109).
-// The first scores come 4 us after the start, a sequence's end costs 3, the join 3
-// to 9.
+// The first scores come 3.5 us after the start and their weights 1.2 later, in
+// instructions not used before; a sequence's end costs 3, the join 3 to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  112 (6.0 TB/s) / 127       64 x 4096, 64 heads   61 / 68
-//   64 x up to 16384, 32 heads   73 / 86                    64 x 4096, 128 heads  104 / 107
-//   128 x 1024, 16 heads         25 / 35                    3 x 8192, 128 heads   24 / 29
-//   1 x 30000, 32 heads          17 / 25                    1 x 700, 32 heads     12 / 18
+//   64 x 16384 tokens, 16 heads  110 (6.1 TB/s) / 127       64 x 4096, 64 heads   61 / 68
+//   64 x up to 16384, 32 heads   72 / 86                    64 x 4096, 128 heads  102 / 107
+//   128 x 1024, 16 heads         24 / 35                    3 x 8192, 128 heads   23 / 29
+//   1 x 30000, 32 heads          16 / 25                    1 x 700, 32 heads     11 / 16
 //   64 x 8192, 16 heads, pages of 8, 16, 32 and more: 69, 68, 64.5 (copies are issued a box of a page at a time)
 #include <cuda_fp16.h>
 #include <math.h>
