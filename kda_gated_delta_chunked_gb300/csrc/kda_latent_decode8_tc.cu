@@ -49,7 +49,7 @@
 //   64 x up to 16384, 32 heads   72 / 86                    64 x 4096, 128 heads  102 / 107
 //   128 x 1024, 16 heads         24 / 35                    3 x 8192, 128 heads   23 / 29
 //   1 x 30000, 32 heads          16 / 25                    1 x 700, 32 heads     11 / 16
-//   64 x 8192, 16 heads, pages of 8, 16, 32 and more: 69, 68, 64.5 (copies are issued a box of a page at a time)
+//   64 x 8192, 16 heads, pages of 8, of 16 and more: 68, 64 (copies are issued a box of a page at a time)
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -205,20 +205,29 @@ __device__ __forceinline__ void l8_put(uint8_t* mem, int r, int lane, uint4 q1, 
     *(uint32_t*)(mem + kL8OffRope + r * 128 + ((lane / 4) ^ swz) * 16 + lane % 4 * 4) = rope;
 }
 
-// The boxes of a piece, B at once, by a warp: operands in uniform registers (a lane for each box: 80 cycles a box).
+// Boxes [from, from + count) of a piece, by a warp: operands in uniform registers, 57 cycles a box (80 with a lane for
+// each).  Box b's page is in lane b * step.
 template <int B>
-__device__ __forceinline__ void l8_boxes(uint32_t to, const CUtensorMap* map, int x, int row, int page, int boxes, int box, uint64_t* bar) {
-    for (int b0 = 0; b0 < boxes; b0 += B) {
-        int z[B];
+__device__ __forceinline__ void l8_issue(uint32_t to, const CUtensorMap* map, int x, int row, int page, int step, int from, int box, uint64_t* bar) {
+    int z[B];
 #pragma unroll
-        for (int i = 0; i < B; ++i) z[i] = __shfl_sync(0xffffffffu, page, b0 + i);
-        if (elect_one()) {
+    for (int i = 0; i < B; ++i) z[i] = __shfl_sync(0xffffffffu, page, (from + i) * step);
+    if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < B; ++i) tma_load_3d_at(to + (b0 + i) * box * 128, map, x, row, z[i], smem_u32(bar));
-        }
-        __syncwarp();
+        for (int i = 0; i < B; ++i) tma_load_3d_at(to + (from + i) * box * 128, map, x, row, z[i], smem_u32(bar));
     }
+    __syncwarp();
 }
+__device__ __forceinline__ void l8_boxes(uint32_t to, const CUtensorMap* map, int x, int row, int page, int step, int from, int count, int box,
+                                         uint64_t* bar) {
+    if (count == 1) l8_issue<1>(to, map, x, row, page, step, from, box, bar);
+    else if (count == 2) l8_issue<2>(to, map, x, row, page, step, from, box, bar);
+    else if (count == 4) l8_issue<4>(to, map, x, row, page, step, from, box, bar);
+    else l8_issue<8>(to, map, x, row, page, step, from, box, bar);
+}
+// Small pages' boxes are issued by two warps, half of them each (64 x 4096 tokens, 64 heads,
+// pages of 8 and 16: 73 and 66 us, 64 and 62 so; 37 x 3 queries, 16 heads, pages of 16: 25.0 and 24.1).
+__device__ __forceinline__ bool l8_shared(int boxes) { return boxes >= 8; }
 
 __global__ void __launch_bounds__(kL8Threads, 1)
 kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ L8Args b) {
@@ -359,16 +368,12 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 if (!(ok = mbar_wait_warp(&empty[at + u], (j / kL8Tiles + 1) & 1))) break;   // (a fresh barrier counts as emptied)
                 if (elect_one()) mbar_arrive_expect_tx(&full[at + u], kL8Piece);
                 __syncwarp();
-                const uint32_t to = base + (at + u) * kL8Piece;
-                if (boxes == 1) l8_boxes<1>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
-                else if (boxes == 2) l8_boxes<2>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
-                else if (boxes == 4) l8_boxes<4>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
-                else l8_boxes<8>(to, &map, u * 128, in_page, from_page, boxes, box, &full[at + u]);
+                l8_boxes(base + (at + u) * kL8Piece, &map, u * 128, in_page, from_page, 1, 0, l8_shared(boxes) ? boxes / 2 : boxes, box, &full[at + u]);
             }
             // The next tile's rows, dense in a page, to L2: there is no place in shared memory for them yet (64 x up to
-            // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80).  Not where issuing many small
-            // copies bounds the tiles (64 x 4096 tokens, 64 heads, pages of 8: 81 with them, 73 without)
-            if (boxes <= 4 && w.left > 0 && some && page >= 0 && page < a.num_pages)
+            // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80; 64 x 4096, 64 heads,
+            // pages of 16: 62.4 -> 60.5).  Not where issuing many small copies bounds the tiles (pages of 8)
+            if (boxes <= 8 && w.left > 0 && some && page >= 0 && page < a.num_pages)
                 prefetch_l2_rows(b.cache + page * b.page_stride + row * kL8Width, box * kL8Width);
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
@@ -443,29 +448,39 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 11) {                                           // ---------------- scales
-        // Four tokens' bytes a lane, fetched a tile ahead; 0 (2^-127) where there is nothing.
-        const int shift = __ffs(a.page_size) - 1;
-        int len = 0;
+        // Four tokens' bytes a lane, 0 (2^-127) where there is nothing; and half of small pages' boxes.
+        const int shift = __ffs(a.page_size) - 1, box = min(a.page_size, kLdTile), boxes = kLdTile / box;
+        int len = 0, page = a.num_pages;
         auto fetch = [&](const LdWalk& x) -> uint32_t {
             const int t = x.j * kLdTile + 4 * lane;
+            page = a.num_pages;
             if (x.left <= 0) return 0;
             if (x.first) len = ld_len(a, x.n);
             if (t >= len) return 0;
             const int p = a.table[(int64_t)x.n * a.max_pages + (t >> shift)];
             if (p < 0 || p >= a.num_pages) return 0;
+            page = p;
             return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + (t & (a.page_size - 1)));
         };
         bool ok = true;
         uint32_t now = fetch(w);
         for (int j = 0; j < count && ok; ++j) {
-            w.next(a);
-            const uint32_t ahead = fetch(w);
+            if (l8_shared(boxes)) {
+                const int at = j % kL8Tiles * kL8Pieces;
+                for (int k = 0; k < kL8Pieces; ++k) {                  // as the producer
+                    const int u = k == 0 ? 4 : k - 1;
+                    if (!(ok = mbar_wait_warp(&empty[at + u], (j / kL8Tiles + 1) & 1))) break;
+                    l8_boxes(base + (at + u) * kL8Piece, &map, u * 128, 0, page, box / 4, boxes / 2, boxes / 2, box, &full[at + u]);
+                }
+                if (!ok) break;
+            }
             if (j >= 2) ok = mbar_wait_warp(&p_full[j & 1], ((j - 2) >> 1) & 1);    // tile j - 2's bytes are read
             if (!ok) break;
             *(uint32_t*)(scales + (j & 1) * kLdTile + 4 * lane) = now;
             __syncwarp();
             if (lane == 0) mbar_arrive(&c_full[j & 1]);
-            now = ahead;
+            w.next(a);
+            now = fetch(w);
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp >= 12) {                                           // ---------------- queries
