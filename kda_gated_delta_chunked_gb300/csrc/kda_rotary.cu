@@ -257,7 +257,8 @@ cudaError_t rotary_launch(const kda_rotary_desc& d, const void* x, const void* k
     a.tokens = d.tokens; a.dim = d.dim; a.flags = d.flags; a.scale = d.scale;
     a.positions = positions; a.frequencies = frequencies;
     const int64_t e = d.dtype == KDA_BF16 ? 2 : 4;
-    // 16-byte vectors, or the widest on whose boundaries everything starts that a vector of its own covers
+    // 16-byte vectors, or the widest on whose boundaries everything starts that a vector of its own covers (20000 x 4 rows
+    // of 100 bf16, 64 turned: 11.7 us with 8 bytes, 15.9 with 4; 98: 15.7; of 100, 50 turned: 28.8 with 2)
     uint64_t bits = (uint64_t)((d.flags & KDA_FLAG_INTERLEAVED ? d.dim : d.dim / 2) * e);
     for (int i = 0; i < 2; ++i) {
         const kda_rotary_part& s = i ? d.key : d.x;
@@ -275,10 +276,12 @@ cudaError_t rotary_launch(const kda_rotary_desc& d, const void* x, const void* k
     }
     if (d.dtype == KDA_BF16) {
         if ((bits & 15) == 0) return rotary_launch_near<__nv_bfloat16, 16>(a, stream);
+        if ((bits & 7) == 0) return rotary_launch_near<__nv_bfloat16, 8>(a, stream);
         if ((bits & 3) == 0) return rotary_launch_near<__nv_bfloat16, 4>(a, stream);
         return rotary_launch_near<__nv_bfloat16, 2>(a, stream);
     }
-    return (bits & 15) == 0 ? rotary_launch_near<float, 16>(a, stream) : rotary_launch_near<float, 4>(a, stream);
+    if ((bits & 15) == 0) return rotary_launch_near<float, 16>(a, stream);
+    return (bits & 7) == 0 ? rotary_launch_near<float, 8>(a, stream) : rotary_launch_near<float, 4>(a, stream);
 }
 
 }  // namespace kda
