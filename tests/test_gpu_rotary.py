@@ -181,3 +181,22 @@ def test_rotary_refusals(kda):  # noqa: F811
                dict(out=x[:1].expand(4, 2, 64))):
         with pytest.raises(kda.KdaError):
             kda.rotary(flat[:512].view(4, 2, 64), pos, f, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lead,row", [(8, 104), (4, 104), (4, 100), (2, 106), (1, 100), (0, 97)])
+def test_rotary_of_every_alignment_gives_the_same_bits(kda, dtype, interleaved, lead, row):  # noqa: F811
+    """Rows of 96 channels, 64 turned, that start on 16, 8, 4 or 2 bytes; what lies between them stays."""
+    x = normal(19, 130, 5, 96, dtype=dtype).cuda()
+    f, pos = kda.rotary_frequencies(64), places(20, 130, 70000)
+    want = check(kda, x, pos, f, offset=16, interleaved=interleaved)[0]
+    wide = lambda: torch.full((lead + 130 * 5 * row,), 5.0, dtype=dtype, device="cuda")  # noqa: E731
+    of = lambda b: b[lead:].view(130, 5, row)[..., :96]  # noqa: E731
+    a, b = wide(), wide()
+    of(a).copy_(x)
+    kda.rotary(of(a), pos, f, offset=16, interleaved=interleaved, out=of(b))
+    assert torch.equal(of(b), want)
+    assert (b[:lead] == 5).all() and (b[lead:].view(130, 5, row)[..., 96:] == 5).all()
+    kda.rotary(of(a), pos, f, offset=16, interleaved=interleaved, out=of(a))
+    assert torch.equal(a, b)
