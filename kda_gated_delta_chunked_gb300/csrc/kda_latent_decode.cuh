@@ -67,7 +67,8 @@ __device__ __forceinline__ void ld_columns(const float (&x)[R], float* to, int l
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             v[i] = x[h + i];
-            if (W == 16) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
+#pragma unroll
+            for (int o = 16; o >= W; o >>= 1) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
         }
 #pragma unroll
         for (int o = W / 2; o > 0; o >>= 1) {

@@ -45,9 +45,9 @@
 // The first scores come 3.5 us after the start and their weights 1.2 later, in
 // instructions not used before; a sequence's end costs 3, the join 3 to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  110 (6.1 TB/s) / 127       64 x 4096, 64 heads   61 / 68
+//   64 x 16384 tokens, 16 heads  108 (6.2 TB/s) / 125       64 x 4096, 64 heads   61 / 68
 //   64 x up to 16384, 32 heads   72 / 86                    64 x 4096, 128 heads  102 / 107
-//   128 x 1024, 16 heads         24 / 35                    3 x 8192, 128 heads   23 / 29
+//   128 x 1024, 16 heads         23 / 35                    3 x 8192, 128 heads   23 / 29
 //   1 x 30000, 32 heads          16 / 25                    1 x 700, 32 heads     11 / 16
 //   64 x 8192, 16 heads, pages of 8, of 16 and more: 68, 64 (copies are issued a box of a page at a time)
 #include <cuda_fp16.h>
@@ -64,7 +64,6 @@ namespace kda {
 
 constexpr int kL8Rows = 32;                                  // query rows of a CTA
 constexpr int kL8Threads = 512;                              // 8 softmax warps, producer, two products, scales, 4 for the queries
-constexpr int kL8Half = 16;                                  // rows of a softmax warp
 constexpr int kL8Width = latent_row_bytes(kLdRank, kLdWidth - kLdRank);    // bytes of a token's row
 constexpr float kL8Slack = 12.f, kL8Stand = 3.f;              // how far (log2) a weight may exceed its reference; the reference's
 constexpr uint32_t kL8Piece = kLdTile * 128;                 // 128 bytes of each token: 128 codes, or the rotary channels
@@ -92,6 +91,20 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn
 }
 // 16-byte piece c of token row r of a P^T (32-byte swizzle).
 __device__ __forceinline__ uint32_t l8_p_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
+
+// 8 or 16 columns of a warp's TMEM lanes.
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&f)[16]) { tmem_ld16(at, f); }
+__device__ __forceinline__ void tmem_st(uint32_t at, const float (&f)[16]) { tmem_st16(at, f); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&f)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_st(uint32_t at, const float (&f)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(at), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                 : "memory");
+}
 
 // Conversions to eight bits by masks and shifts: the conversion instructions take eight cycles of a scheduler each.
 
@@ -144,19 +157,23 @@ __device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n,
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The warp's maximum of each column to `to`[column].
-__device__ __forceinline__ void l8_maxima(const float (&x)[kL8Half], float* to, int lane) {
+template <int N>
+__device__ __forceinline__ void l8_maxima(const float (&x)[N], float* to, int lane) {
     float mine = 0.f;
 #pragma unroll
-    for (int c = 0; c < kL8Half; ++c) {
+    for (int c = 0; c < N; ++c) {
         float top;
         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(x[c]));
         if (lane == c) mine = top;
     }
-    if (lane < kL8Half) to[lane] = mine;
+    if (lane < N) to[lane] = mine;
 }
 __device__ __forceinline__ void prefetch_l2_rows(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
+
+__device__ __forceinline__ void l8_store(uint8_t* to, const uint32_t (&w)[4]) { *(uint4*)to = make_uint4(w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ void l8_store(uint8_t* to, const uint32_t (&w)[2]) { *(uint2*)to = make_uint2(w[0], w[1]); }
 
 // A query row in registers (16 channels a lane in two vectors) to q1 and q2 there, by a warp, and what a unit of q1 is
 // worth.
@@ -229,6 +246,9 @@ __device__ __forceinline__ void l8_boxes(uint32_t to, const CUtensorMap* map, in
 // pages of 8 and 16: 73 and 66 us, 64 and 62 so; 37 x 3 queries, 16 heads, pages of 16: 25.0 and 24.1).
 __device__ __forceinline__ bool l8_shared(int boxes) { return boxes >= 8; }
 
+// kHalf: rows of a softmax warp, 16, or 8 where there are no more than 16 rows (16 heads, 256 x 200 tokens: 22.2 us, with
+// half of the warps idle 23.8; 64 x 16384: 108 and 110.5).
+template <int kHalf>
 __global__ void __launch_bounds__(kL8Threads, 1)
 kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ L8Args b) {
     constexpr int R = kL8Rows;
@@ -523,7 +543,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else {                                                           // ---------------- softmax
-        const int half = warp >> 2, part = warp & 3, r0 = half * kL8Half, thread = threadIdx.x & 127;
+        const int half = warp >> 2, part = warp & 3, r0 = half * kHalf, thread = threadIdx.x & 127;
         const bool idle = r0 >= live;                                  // rows that are none: nothing of theirs is read
         const uint32_t vote = half ? 3 : 1, meet = half ? 4 : 2;
         // A warp whose wait gave up says so at a vote that the others come to next, and all four leave there.
@@ -535,9 +555,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(meet) : "memory"); };
         const uint32_t lanes = tmem_addr(tmem, 32 * part, 0);
         const float sc = a.scale * 1.4426950408889634f;
-        float l[kL8Half];
+        float l[kHalf];
 #pragma unroll
-        for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
+        for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
         bool ok = true;
         uint32_t seg = 0;
         int len = 0;
@@ -563,13 +583,13 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
             tc_fence_after_sync();
             // y: log2 of the weight times 2^e
-            float y[kL8Half];
+            float y[kHalf];
             if (!idle) {
                 const float* unit = worth + (seg - 1) % kL8Scales * R + r0;
-                float d2[kL8Half], dr[kL8Half];
-                tmem_ld16(lanes + r0, y);
-                tmem_ld16(lanes + R + r0, d2);
-                tmem_ld16(lanes + 2 * R + r0, dr);
+                float d2[kHalf], dr[kHalf];
+                tmem_ld(lanes + r0, y);
+                tmem_ld(lanes + R + r0, d2);
+                tmem_ld(lanes + 2 * R + r0, dr);
                 tmem_wait_ld();
                 tmem_ready(y);
                 tmem_ready(d2);
@@ -578,24 +598,24 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty);
 #pragma unroll
-                for (int c = 0; c < kL8Half; ++c) y[c] = fmaf(fmaf(d2[c], 0.0625f, y[c]), two * unit[c], fmaf(dr[c], sc, e));
+                for (int c = 0; c < kHalf; ++c) y[c] = fmaf(fmaf(d2[c], 0.0625f, y[c]), two * unit[c], fmaf(dr[c], sc, e));
             } else if (lane == 0) {
                 mbar_arrive(s_empty);
             }
             if (!idle && (w.j + 1) * kLdTile > len - a.Lq + 1) {       // some row does not see some token
 #pragma unroll
-                for (int c = 0; c < kL8Half; ++c)
+                for (int c = 0; c < kHalf; ++c)
                     if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
             }
             // The weights under the references as they are, and under new ones where some weight is too large for that or
             // there are none yet: the same instructions, others would be cold.
-            float p[kL8Half];
+            float p[kHalf];
 #pragma unroll 1
             for (bool moved = false;; moved = true) {
                 bool over = w.first && !moved && !idle;
                 if (!idle && !over) {
 #pragma unroll
-                    for (int c = 0; c < kL8Half; c += 4) {
+                    for (int c = 0; c < kHalf; c += 4) {
                         const float4 m = *(const float4*)(ref + r0 + c);
                         const float d[4] = {y[c] - m.x, y[c + 1] - m.y, y[c + 2] - m.z, y[c + 3] - m.w};
 #pragma unroll
@@ -606,7 +626,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                     }
                 } else {                                               // (no register is held for the ones before)
 #pragma unroll
-                    for (int c = 0; c < kL8Half; ++c) p[c] = 0.f;
+                    for (int c = 0; c < kHalf; ++c) p[c] = 0.f;
                 }
                 if (moved || bar_and_id(vote, 128, !over)) break;
                 // Move the references to the maxima
@@ -616,7 +636,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 }
                 l8_maxima(y, across + part * R + r0, lane);
                 sync();
-                if (thread < kL8Half) {
+                if (thread < kHalf) {
                     const int c = r0 + thread;
                     const float old = w.first ? kLdUnset : ref[c];
                     const float now = fmaxf(old, fmaxf(fmaxf(across[c], across[R + c]),
@@ -626,9 +646,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 }
                 sync();
                 if (w.first) continue;                                 // (no sums and no O^T yet)
-                float f[kL8Half];
+                float f[kHalf];
 #pragma unroll
-                for (int c = 0; c < kL8Half; ++c) {
+                for (int c = 0; c < kHalf; ++c) {
                     f[c] = fac[r0 + c];
                     l[c] *= f[c];
                 }
@@ -639,40 +659,40 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     const uint32_t at = lanes + kL8O + b * 3 * R + r0;
-                    float o1[kL8Half], o2[kL8Half], o3[kL8Half];
-                    tmem_ld16(at, o1);
-                    tmem_ld16(at + R, o2);
-                    tmem_ld16(at + 2 * R, o3);
+                    float o1[kHalf], o2[kHalf], o3[kHalf];
+                    tmem_ld(at, o1);
+                    tmem_ld(at + R, o2);
+                    tmem_ld(at + 2 * R, o3);
                     tmem_wait_ld();
                     tmem_ready(o1);
                     tmem_ready(o2);
                     tmem_ready(o3);
 #pragma unroll
-                    for (int c = 0; c < kL8Half; ++c) {
+                    for (int c = 0; c < kHalf; ++c) {
                         o1[c] *= f[c];
                         o2[c] *= f[c];
                         o3[c] *= f[c];
                     }
-                    tmem_st16(at, o1);
-                    tmem_st16(at + R, o2);
-                    tmem_st16(at + 2 * R, o3);
+                    tmem_st(at, o1);
+                    tmem_st(at + R, o2);
+                    tmem_st(at + 2 * R, o3);
                 }
                 tmem_wait_st();
             }
             if (!ok) break;
             if (!idle) {
                 const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
-                uint32_t p1[4], p2[4], p3[4];
+                uint32_t p1[kHalf / 4], p2[kHalf / 4], p3[kHalf / 4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kHalf / 4; ++i) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) l[4 * i + k] = fmaf(p[4 * i + k], down, l[4 * i + k]);
                     l8_split(p + 4 * i, p1[i], p2[i], p3[i]);
                 }
-                uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P + l8_p_at(thread, half);
-                *(uint4*)to = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                *(uint4*)(to + kL8P) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                *(uint4*)(to + 2 * kL8P) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+                uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P + l8_p_at(thread, r0 / 16) + r0 % 16;
+                l8_store(to, p1);
+                l8_store(to + kL8P, p2);
+                l8_store(to + 2 * kL8P, p3);
             }
             // Weight 0 times what lies behind the length: make that 0, half of the codes each half of the warps
             if (token >= len) {
@@ -692,15 +712,15 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 
             // end of a segment: sums across the tokens' threads, then O^T out
             if (w.left > 0) len = ld_len(a, w.n);
-            ld_columns<kL8Half, false>(l, sums + part * R + r0, lane);
+            ld_columns<kHalf, false>(l, sums + part * R + r0, lane);
 #pragma unroll
-            for (int c = 0; c < kL8Half; ++c) l[c] = 0.f;
+            for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
             ok = bar_and_id(vote, 128, mbar_wait_spin(&o_full[j & 1], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after_sync();
             const bool whole = at.from == 0 && at.j + 1 == at.tiles;
             float* dst = a.parts + ((size_t)(cta * gridDim.x + group) * 2 + (at.from == 0)) * R * kLdPart;
-            if (thread < kL8Half) {
+            if (thread < kHalf) {
                 const int c = r0 + thread;
                 const float total = (sums[c] + sums[R + c]) + (sums[2 * R + c] + sums[3 * R + c]);
                 if (whole) {
@@ -716,30 +736,30 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 #pragma unroll 1
             for (int b = 0; b < 4 && !idle; ++b) {
                 const int ch = b * 128 + thread;
-                float o[kL8Half], o2[kL8Half], o3[kL8Half];
+                float o[kHalf], o2[kHalf], o3[kHalf];
                 const uint32_t from = lanes + kL8O + b * 3 * R + r0;
-                tmem_ld16(from, o);
-                tmem_ld16(from + R, o2);
-                tmem_ld16(from + 2 * R, o3);
+                tmem_ld(from, o);
+                tmem_ld(from + R, o2);
+                tmem_ld(from + 2 * R, o3);
                 tmem_wait_ld();
                 tmem_ready(o);
                 tmem_ready(o2);
                 tmem_ready(o3);
 #pragma unroll
-                for (int c = 0; c < kL8Half; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
+                for (int c = 0; c < kHalf; ++c) o[c] = fmaf(fmaf(o3[c], 0.125f, o2[c]), 0.125f, o[c]);
                 if (whole) {
                     __nv_bfloat16* out = a.out + ((size_t)at.n * a.rows + row0 + r0) * kLdRank + ch;
-                    if (r0 + kL8Half <= live) {
+                    if (r0 + kHalf <= live) {
 #pragma unroll
-                        for (int c = 0; c < kL8Half; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
+                        for (int c = 0; c < kHalf; ++c) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < kL8Half; ++c)
+                        for (int c = 0; c < kHalf; ++c)
                             if (r0 + c < live) out[(size_t)c * kLdRank] = __float2bfloat16_rn(o[c] * fac[r0 + c]);
                     }
                 } else {                                               // (dead rows too: a condition a store costs more)
 #pragma unroll
-                    for (int c = 0; c < kL8Half; ++c) dst[(r0 + c) * kLdPart + ch] = o[c];
+                    for (int c = 0; c < kHalf; ++c) dst[(r0 + c) * kLdPart + ch] = o[c];
                 }
             }
         }
@@ -773,15 +793,20 @@ bool latent_decode8_tc_aligned(const LatentDecodeArgs& d) {
            d.page_stride < (1ll << 39);
 }
 
-cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {
+template <int kHalf>
+static cudaError_t l8_launch(const LdPlan& p, const CUtensorMap& map, const L8Args& b, cudaStream_t stream) {
     static PerDevice memory_set;
     int device = 0, set = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err == cudaSuccess) err = memory_set.get(device, set, [](int& done) {
         done = 1;
-        return cudaFuncSetAttribute(kda_latent_decode8_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kL8Smem);
+        return cudaFuncSetAttribute(kda_latent_decode8_tc<kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kL8Smem);
     });
     if (err != cudaSuccess) return err;
+    return launch_behind(kda_latent_decode8_tc<kHalf>, dim3(p.groups, p.G), kL8Threads, kL8Smem, stream, map, b);
+}
+
+cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t stream) {
     const LdPlan p = ld_plan(d.N, d.Lq, d.H, d.page_size, d.max_pages, kL8Rows);
     L8Args b;
     LdArgs& a = b.a;
@@ -802,7 +827,7 @@ cudaError_t latent_decode8_tc_launch(const LatentDecodeArgs& d, cudaStream_t str
     const uint64_t strides[2] = {(uint64_t)kL8Width, (uint64_t)d.page_stride};
     const uint32_t box[3] = {128, (uint32_t)(d.page_size < kLdTile ? d.page_size : kLdTile), 1};
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, d.cache, dims, strides, box)) return cudaErrorInvalidValue;
-    err = launch_behind(kda_latent_decode8_tc, dim3(p.groups, p.G), kL8Threads, kL8Smem, stream, map, b);
+    const cudaError_t err = a.rows <= 16 ? l8_launch<8>(p, map, b, stream) : l8_launch<16>(p, map, b, stream);
     return err != cudaSuccess ? err : latent_decode_join_launch(a, kL8Rows, p.groups, stream);
 }
 
