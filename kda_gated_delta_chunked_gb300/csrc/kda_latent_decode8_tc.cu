@@ -468,7 +468,9 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
         }
         if (!ok) atomicOr(fault, kLdLate);
     } else if (warp == 11) {                                           // ---------------- scales
-        // Four tokens' bytes a lane, 0 (2^-127) where there is nothing; and half of small pages' boxes.
+        // Four tokens' bytes a lane, 0 (2^-127) where there is nothing, also behind the length in the same four (a byte of
+        // 255 there, as memory that nothing has cleared holds, would be 2^128, and 0 times that); and half of small pages'
+        // boxes.
         const int shift = __ffs(a.page_size) - 1, box = min(a.page_size, kLdTile), boxes = kLdTile / box;
         int len = 0, page = a.num_pages;
         auto fetch = [&](const LdWalk& x) -> uint32_t {
@@ -480,7 +482,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             const int p = a.table[(int64_t)x.n * a.max_pages + (t >> shift)];
             if (p < 0 || p >= a.num_pages) return 0;
             page = p;
-            return *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + (t & (a.page_size - 1)));
+            const uint32_t word = *(const uint32_t*)(b.cache + p * b.page_stride + (int64_t)a.page_size * kL8Width + (t & (a.page_size - 1)));
+            return len - t < 4 ? word & ((1u << 8 * (len - t)) - 1) : word;
         };
         bool ok = true;
         uint32_t now = fetch(w);
