@@ -394,7 +394,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             // 16384 tokens, 32 heads 76.5 -> 74.2 us; two or three tiles ahead 77 and 80; 64 x 4096, 64 heads,
             // pages of 16: 62.4 -> 60.5).  Not where issuing many small copies bounds the tiles (pages of 8)
             if (boxes <= 8 && w.left > 0 && some && page >= 0 && page < a.num_pages)
-                prefetch_l2_rows(b.cache + page * b.page_stride + row * kL8Width, box * kL8Width);
+                prefetch_l2_rows(b.cache + page * b.page_stride + (int64_t)row * kL8Width, box * kL8Width);
         }
         if (bad_page) atomicOr(fault, kLdBadPage);
         if (!ok) atomicOr(fault, kLdLate);
