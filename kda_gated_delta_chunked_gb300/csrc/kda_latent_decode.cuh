@@ -33,7 +33,8 @@ __device__ __forceinline__ int ld_len(const LdArgs& a, int n) {
     const int len = a.lens[n];
     return len < 0 || (int64_t)len > (int64_t)a.max_pages * a.page_size ? 0 : len;
 }
-__device__ __forceinline__ int ld_tiles(const LdArgs& a, int n) { return (ld_len(a, n) + kLdTile - 1) / kLdTile; }
+__device__ __forceinline__ int ld_tiles_of(int len) { return (int)(((uint32_t)len + kLdTile - 1) / kLdTile); }   // (up to 2^31 - 1)
+__device__ __forceinline__ int ld_tiles(const LdArgs& a, int n) { return ld_tiles_of(ld_len(a, n)); }
 
 // Position in the tiles of a CTA's range; the same in all lanes of a warp, which call it together.
 struct LdWalk {
@@ -41,6 +42,7 @@ struct LdWalk {
     bool first;                                // first tile of a segment
     int from;                                  // its tile
     __device__ __forceinline__ bool last() const { return j + 1 == tiles || left == 1; }
+    __device__ __forceinline__ int end() const { return j * kLdTile + (kLdTile - 1); }   // its last token (one more may be 2^31)
     __device__ __forceinline__ void settle(const LdArgs& a) {      // on to the next sequence that has tiles
         while (left > 0 && j >= tiles) { ++n; j = 0; tiles = uniform(ld_tiles(a, n)); }
     }
@@ -94,7 +96,7 @@ __device__ __forceinline__ LdCut ld_cut(const LdArgs& a, int cta, int lane, int 
     for (int b = 0; b < a.N; b += 32) {
         if (b > 0) len = b + lane < a.N ? a.lens[b + lane] : 0;
         bad |= len < 0 || len > cap;
-        const int t = len < 0 || len > cap ? 0 : (len + kLdTile - 1) / kLdTile;
+        const int t = len < 0 || len > cap ? 0 : ld_tiles_of(len);
         if (b == 0) first = t;
         total += __reduce_add_sync(0xffffffffu, t);
     }

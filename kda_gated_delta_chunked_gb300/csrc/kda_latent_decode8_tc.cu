@@ -605,7 +605,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             } else if (lane == 0) {
                 mbar_arrive(s_empty);
             }
-            if (!idle && (w.j + 1) * kLdTile > len - a.Lq + 1) {       // some row does not see some token
+            if (!idle && w.end() > len - a.Lq) {                          // some row does not see some token
 #pragma unroll
                 for (int c = 0; c < kHalf; ++c)
                     if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;

@@ -235,7 +235,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (int j = 0; j < count && ok; ++j, w.next(a)) {
             if (!(ok = mbar_wait_warp(&p_full[j & 1], (j >> 1) & 1))) break;
             const uint64_t dp = sdesc(base + S::kOffP + j % S::kBufP * S::kP, 16, 8 * S::kRow, S::kSwz);
-            const bool ragged = uniform((w.j + 1) * kLdTile > ld_len(a, w.n));
+            const bool ragged = uniform(w.end() >= ld_len(a, w.n));
             for (int p = 0; p < 4; ++p) {
                 ok = mbar_wait_warp(&full_v[s], ph);
                 if (ok && ragged) ok = mbar_wait_warp(&zeroed[p], zero & 1);
@@ -287,7 +287,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             tmem_ready(x);
 #pragma unroll
             for (int c = 0; c < R; ++c) x[c] *= sc;
-            if ((w.j + 1) * kLdTile > len - a.Lq + 1) {                // some row does not see some token
+            if (w.end() > len - a.Lq) {                                // some row does not see some token
 #pragma unroll
                 for (int c = 0; c < R; ++c)
                     if (token > len - a.Lq + query[c]) x[c] = -INFINITY;
@@ -360,7 +360,7 @@ kda_latent_decode_tc(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (lane == 0) mbar_arrive(&p_full[j & 1]);
             // Weight 0 times what lies behind the length: make that 0, each pair of pieces as it comes (once the
             // products of the tile before are complete, the ring is at this tile's).
-            if ((w.j + 1) * kLdTile > len) {
+            if (w.end() >= len) {
                 if (j > 0) ok = mbar_wait_warp(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
                 for (int p = 0; p < 4 && ok; ++p) {
                     const uint32_t u = 4 * j + p, s = u % S::kSlotsV;
