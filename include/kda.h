@@ -384,7 +384,8 @@ enum {
  * do values behind the end of a sequence.  Values that a row does not see inside
  * its sequence (behind the causal limit) may: on the tensor cores they are
  * multiplied by 0, so an infinity or NaN in one makes rows NaN that see keys of
- * the same 128. */
+ * the same 128 (not so with KDA_FLAG_CACHE_8, where no value does that its row
+ * does not see). */
 typedef struct kda_latent_desc {
     int32_t num_seqs;        /* N >= 0 */
     int32_t num_heads;       /* H >= 1 */

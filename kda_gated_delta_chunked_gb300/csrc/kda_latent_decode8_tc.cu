@@ -149,6 +149,12 @@ __device__ __forceinline__ void l8_codes(__nv_bfloat162 t, uint32_t& q1, uint32_
     q2 = code(bits_of(__hmul2(__hsub2(t, of_bits<__nv_bfloat162>(top)), sixteen)));
 }
 
+// Sixteen codes with 0 in place of those that are NaN (all bits but the sign set).
+__device__ __forceinline__ uint4 l8_no_nan(uint4 x) {
+    auto keep = [](uint32_t u) { return u & ~((((u & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 255u); };
+    return make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
+}
+
 // Query row `row` (query, head) of sequence n.
 __device__ __forceinline__ const __nv_bfloat16* l8_query(const L8Args& b, int n, int row) {
     const int i = (int)((uint64_t)row * b.by_heads >> 31);             // row / H: exact while row H < 2^31
@@ -606,6 +612,26 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 mbar_arrive(s_empty);
             }
             if (!idle && w.end() > len - a.Lq) {                          // some row does not see some token
+                // Weight 0 times a NaN code of a token that other rows see: make that 0 too.  Those have it in their sums.
+                // (A NaN code makes the scores of every row NaN, so that they tell where to look.)
+                const bool strange = token > len - a.Lq && token < len && !(y[0] == y[0]);
+                if (__any_sync(0xffffffffu, strange)) {
+                    const int from = 2 * half, pieces = live <= kHalf ? 4 : 2;     // the other half is idle: all of them
+                    const int at = j % kL8Tiles * kL8Pieces + from;
+#pragma unroll 1
+                    for (int u = 0; u < pieces && ok; ++u) {           // (complete; awaited for the copies to be seen here)
+                        ok = mbar_wait_warp(&full[at + u], (j / kL8Tiles) & 1);
+#pragma unroll 1
+                        for (int i = 0; i < 8 && strange; ++i) {
+                            uint4* x = (uint4*)(mem + (at + u) * kL8Piece + thread * 128 + i * 16);
+                            *x = l8_no_nan(*x);
+                        }
+                    }
+                    if (!ok) {
+                        leave();
+                        break;
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < kHalf; ++c)
                     if (token > len - a.Lq + query[r0 + c]) y[c] = -INFINITY;
