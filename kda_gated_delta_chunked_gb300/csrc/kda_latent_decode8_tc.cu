@@ -66,6 +66,11 @@ constexpr int kL8Rows = 32;                                  // query rows of a 
 constexpr int kL8Threads = 512;                              // 8 softmax warps, producer, two products, scales, 4 for the queries
 constexpr int kL8Width = latent_row_bytes(kLdRank, kLdWidth - kLdRank);    // bytes of a token's row
 constexpr float kL8Slack = 12.f, kL8Stand = 3.f;              // how far (log2) a weight may exceed its reference; the reference's
+// Tokens of scales below 2^-30 (latents of 0: 2^-100).  Beside latents of 2^30 and more their P would be lost in fp32, and
+// with it their weight in the row's sum: it is held 2^100 times as large until the sum has it (64 x 4096 tokens, 128 heads:
+// 102.9 -> 103.9 us).
+constexpr int kL8Small = kScaleBias - 30;
+constexpr int kL8Lift = 100;                                 // (log2)
 constexpr uint32_t kL8Piece = kLdTile * 128;                 // 128 bytes of each token: 128 codes, or the rotary channels
 constexpr int kL8Pieces = 5, kL8Tiles = 2;
 constexpr uint32_t kL8QPiece = 2 * kL8Rows * 128;            // 128 codes of q1 and q2
@@ -583,6 +588,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             const int token = w.j * kLdTile + thread;
             const int byte = scales[(j & 1) * kLdTile + thread];
             const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
+            const bool small = byte < kL8Small;
+            const float stand = kL8Stand + (small ? kL8Lift : 0);
             // (also the products of the tile before last are complete then, whose weights this tile's replace: its codes
             // came to where theirs were)
             static_assert(kL8Tiles == 2, "as many buffers for the weights");
@@ -650,7 +657,7 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             over |= d[k] > kL8Slack;
-                            p[c + k] = ex2(d[k] + kL8Stand);
+                            p[c + k] = ex2(d[k] + stand);
                         }
                     }
                 } else {                                               // (no register is held for the ones before)
@@ -710,12 +717,16 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
             }
             if (!ok) break;
             if (!idle) {
-                const float down = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: back from P to p
+                const float down = __uint_as_float((uint32_t)((small ? 254 - kL8Lift : 254) - byte) << 23);   // 2^-e: back from P to p
+                const float back = small ? 0x1p-100f : 1.f;
                 uint32_t p1[kHalf / 4], p2[kHalf / 4], p3[kHalf / 4];
 #pragma unroll
                 for (int i = 0; i < kHalf / 4; ++i) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) l[4 * i + k] = fmaf(p[4 * i + k], down, l[4 * i + k]);
+                    for (int k = 0; k < 4; ++k) {
+                        l[4 * i + k] = fmaf(p[4 * i + k], down, l[4 * i + k]);
+                        p[4 * i + k] *= back;
+                    }
                     l8_split(p + 4 * i, p1[i], p2[i], p3[i]);
                 }
                 uint8_t* to = mem + kL8OffP + (j & 1) * 3 * kL8P + l8_p_at(thread, r0 / 16) + r0 % 16;
