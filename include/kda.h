@@ -451,12 +451,12 @@ KDA_API int kda_latent_prefill(const kda_latent_desc *desc, const void *q, const
  * quantised cache below, each exactly.  bf16 queries, rank 512 and d_rope 64 run
  * on the tensor cores, on the codes themselves: there a query is the sum of two
  * e4m3 values under one power of two for its row (exact down to 2^-22 of its
- * largest channel; infinite ones count as NaN) and a softmax weight the sum of
- * three e5m2 values (off by 2^-8.6 of it at most, or by 2^-26 of the row's largest
- * weight, whichever is more).  Sums are fp32; a
+ * largest channel; infinite ones count as NaN) and a softmax weight times its
+ * token's 2^e the sum of three e5m2 values (off by 2^-8.6 of it at most, or by
+ * 2^-26 of the row's largest such product, whichever is more).  Sums are fp32; a
  * weight may be missing from its row's if it is below 2^(x - 99) of another one's,
- * 2^x the row's largest scale.  Everything else, and fp32 queries,
- * run on CUDA cores in fp32. */
+ * 2^x the row's largest scale.  Everything else, and fp32 queries, run on CUDA
+ * cores in fp32. */
 KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const void *cache,
                               const int32_t *page_table, const int32_t *lengths, void *out, float *lse,
                               kda_stream_t stream);

@@ -12,9 +12,9 @@
 //     8 bits of a bf16 exactly, down to 2^-14 of steps where the row's largest is
 //     224 to 448 (e4m3's subnormals).  q1 and q2 are columns of one product.
 //   - a weight P = p 2^e is p1 + p2 / 8 + p3 / 64 in e5m2, each the rest of the one
-//     before: three bits each, off by 2^-8.6 (bf16: 2^-8) for weights down to 2^-17
-//     of the largest, below that by 2^-26 of the largest.  e5m2 for its range: the
-//     tokens behind a dominant one are many and small, and would be lost in e4m3's.
+//     before: three bits each, off by 2^-8.6 (bf16: 2^-8) for P down to 2^-17 of the
+//     row's largest P, below that by 2^-26 of it.  e5m2 for its range: the tokens
+//     behind a dominant one are many and small, and would be lost in e4m3's.
 //
 //     S^T [128 tokens, q1 | q2 | rope: 3 x 32]  = C Q^T        16 + 4 instructions
 //     O^T [4 x 128 channels, p1 | p2 | p3: 3 x 32] += C^T P^T  4 x 4 instructions
