@@ -502,7 +502,8 @@ KDA_API size_t kda_latent_cache_page_bytes(int32_t page_size, int32_t rank, int3
  *              sequences, packed; read by _write, written by _read
  *   cu_seqlens int32 [N+1], device: rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 are
  *              sequence n's; NULL: T / N rows each (N divides T).  cu_seqlens[N]
- *              may be less than T: rows behind it are not read, or left as they were
+ *              may be less than T: rows behind it are not written to the cache, or
+ *              left as they were
  *   page_table int32 [N, max_pages], lengths int32 [N] as for kda_latent_decode:
  *              row i of the L rows of sequence n is its cached token
  *              lengths[n] - L + i (lengths count the new tokens).  Rows whose
@@ -512,9 +513,11 @@ KDA_API size_t kda_latent_cache_page_bytes(int32_t page_size, int32_t rank, int3
  *
  * A malformed cu_seqlens or a length outside 0 .. max_pages * page_size
  * (KDA_ERR_BAD_SEQLENS) and page numbers outside the cache (KDA_ERR_BAD_PAGE)
- * are recorded in the status word (kda_latent_status), if there is one; the rows
- * concerned are left out, never dereferenced.  Two rows of one call in the same
- * place of the cache leave that place unspecified. */
+ * are recorded in the status word (kda_latent_status), if there is one.  Left out,
+ * and never dereferenced, are the rows of a sequence with such a length or with
+ * bounds that are not 0 <= c_n <= c_n+1 <= T (c_0 = 0), and the rows of a page with
+ * such a number; rows that several sequences claim are one's of them.  Two rows of
+ * one call in the same place of the cache leave that place unspecified. */
 KDA_API int kda_latent_cache_write(const kda_latent_cache_desc *desc, const void *latents, const void *rope,
                                    const int32_t *cu_seqlens, const int32_t *page_table, const int32_t *lengths,
                                    uint8_t *cache, kda_stream_t stream);

@@ -67,7 +67,7 @@ __device__ __forceinline__ void lc_load(const LatentCacheArgs& a, int64_t t, int
 // Rows [from, to) of a sequence and the place of its first one.
 struct LcSequence { int n; int64_t from, to, place; };
 
-// The sequence of row t, by a whole warp; from == to: there is none, or its lengths are no lengths.
+// The sequence of row t, by a whole warp; from == to: there is none, or its bounds or its length are none.
 __device__ __forceinline__ LcSequence lc_sequence(const LatentCacheArgs& a, int64_t t) {
     const int lane = threadIdx.x & 31;
     LcSequence s = {0, 0, 0, 0};
@@ -85,9 +85,9 @@ __device__ __forceinline__ LcSequence lc_sequence(const LatentCacheArgs& a, int6
             hi = min(lo + step, hi);
         }
         s.n = lo;
-        s.from = a.cu[lo];
-        s.to = a.cu[lo + 1];
-        if (t < s.from || t >= s.to) s.to = s.from;
+        const int from = a.cu[lo], to = a.cu[lo + 1];
+        s.from = from;
+        s.to = t < from || t >= to || to > (int)a.T || (lo == 0 ? from != 0 : from < 0) ? from : to;
     }
     const int64_t len = a.lens[s.n];
     if (len < 0 || len > (int64_t)a.max_pages * a.page_size) s.to = s.from;
