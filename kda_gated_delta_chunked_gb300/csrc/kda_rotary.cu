@@ -16,6 +16,7 @@
 // The angle: f / (2 pi) turns a position, as a 64-bit fraction of a turn, times
 // the position in 64-bit integers that wrap at whole turns: off by 2^-63 of f / (2 pi)
 // and by 2^-64, times the position.  Its first 32 bits go to sincospi in fp32.
+#include <math.h>
 #include <string.h>
 
 #include "kda_common.cuh"
@@ -163,19 +164,21 @@ kda_rotary_kernel(const __grid_constant__ RotArgs a) {
             if (S::kTwo && at[k] >= 0) vb[k] = *(const RotVec<B>*)(from + apart);
         }
         if (base == 0) {
-            const float sign = a.flags & KDA_FLAG_INVERSE ? -a.scale : a.scale;
             // A thread's pairs are of one frequency (of one at a time, where there are more frequencies than threads)
             const int each = half < kRotThreads ? kRotThreads / half : 1;      // tokens at once
             const int first = half < kRotThreads ? (int)threadIdx.x / half : 0;
             for (int i = (int)threadIdx.x - first * half; i < half && first < each; i += kRotThreads) {
-                const unsigned long long turns = rot_turns(a.frequencies[i]);
+                const double f = a.frequencies[i];
+                const unsigned long long turns = rot_turns(f);
+                const bool none = (__double2hiint(f) & 0x7ff00000) == 0x7ff00000;      // infinite or NaN
+                const float scale = none ? NAN : a.scale;
                 for (int token = first; token < tokens; token += each) {
                     const long long pos = a.flags & KDA_FLAG_POSITIONS_64 ? ((const int64_t*)a.positions)[token0 + token]
                                                                          : ((const int32_t*)a.positions)[token0 + token];
                     const float angle = (float)(int)((unsigned long long)pos * turns >> 32) * 0x1p-31f;    // half turns
                     float s, c;
                     sincospif(angle, &s, &c);
-                    table[token * half + i] = make_float2(a.scale * c, sign * s);
+                    table[token * half + i] = make_float2(scale * c, (a.flags & KDA_FLAG_INVERSE ? -scale : scale) * s);
                 }
             }
             __syncthreads();
