@@ -561,9 +561,9 @@ typedef struct kda_rotary_desc {
 /* x, and key or NULL (the keys of the same tokens, in the same launch), to out
  * and key_out.  An output may be its own input, with the same strides, and
  * overlaps nothing else (rows of both inside one wider row, like queries and keys
- * of one projection, do not overlap).  positions int32 or int64 [tokens],
- * frequencies fp64 [dim / 2] (radians a position), device; the pairs of one that is
- * infinite or NaN become NaN. */
+ * of one projection, a token's or each head's side by side, do not overlap).
+ * positions int32 or int64 [tokens], frequencies fp64 [dim / 2] (radians a
+ * position), device; the pairs of one that is infinite or NaN become NaN. */
 KDA_API int kda_rotary(const kda_rotary_desc *desc, const void *x, const void *key, const void *positions,
                        const double *frequencies, void *out, void *key_out, kda_stream_t stream);
 

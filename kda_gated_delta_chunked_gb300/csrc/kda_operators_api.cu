@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <numeric>
 #include <stdint.h>
 #include <string.h>
 
@@ -107,22 +108,30 @@ static int nothing_to_compute(const kda_latent_desc* d, const int32_t* cu_q, con
 }
 
 // Rows of several heads a token, for the rotary positions (bytes).
-struct Rows { const void* p; int64_t token, head; size_t row, span; };      // row: from a token's first byte behind its last
+struct Rows { const void* p; int64_t token, head; size_t row, span, width; };    // row: from a token's first byte behind its last
 static Rows rows_of(const void* p, const kda_rotary_part& s, int64_t tokens, size_t e, bool out) {
     const int64_t token = out ? s.out_token_stride : s.token_stride, head = out ? s.out_head_stride : s.head_stride;
-    Rows r = {p, token * (int64_t)e, head * (int64_t)e, 0, 0};
+    // (one token or one head: no stride)
+    Rows r = {p, tokens > 1 ? token * (int64_t)e : 0, s.heads > 1 ? head * (int64_t)e : 0, 0, 0, s.width * e};
     if (!p) return r;
-    r.row = ((size_t)(s.heads - 1) * (size_t)head + (size_t)s.width) * e;
+    r.row = (size_t)(s.heads - 1) * (size_t)r.head + r.width;
     r.span = (size_t)(tokens - 1) * (size_t)r.token + r.row;
     return r;
 }
+// Whether [x, x + a) and [y, y + b) meet, both repeated every s bytes.
+static bool meet_modulo(const void* x, size_t a, const void* y, size_t b, size_t s) {
+    if (s < a || s < b) return true;
+    const uintptr_t u = (uintptr_t)x, v = (uintptr_t)y;
+    const size_t d = v >= u ? (v - u) % s : (s - (u - v) % s) % s;     // where b's begins behind a's
+    return d < a || d + b > s;
+}
 static bool rows_meet(const Rows& a, const Rows& b) {
     if (!overlap({a.p, a.span}, {b.p, b.span})) return false;
-    if (a.token != b.token || (size_t)a.token < a.row || (size_t)a.token < b.row) return true;
-    // Parts of the same wider rows: where b's begins behind a's, modulo those
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p, s = (uintptr_t)a.token;
-    const uintptr_t d = y >= x ? (y - x) % s : (s - (x - y) % s) % s;
-    return d < a.row || d + b.row > s;
+    // Parts of the same wider rows, a token's all together; or of wider rows that repeat by a divisor of all strides, as
+    // where queries and keys lie side by side in each head
+    if (a.token == b.token && a.token > 0 && !meet_modulo(a.p, a.row, b.p, b.row, a.token)) return false;
+    const int64_t every = std::gcd(std::gcd(a.token, b.token), std::gcd(a.head, b.head));
+    return every == 0 || meet_modulo(a.p, a.width, b.p, b.width, every);
 }
 static int rotary_part(const kda_rotary_part& p, int64_t tokens, int dim) {
     if (p.heads < 1 || p.reserved != 0 || p.offset < 0 || p.width < dim || p.offset > p.width - dim) return KDA_ERR_INVALID_ARGUMENT;
@@ -155,8 +164,8 @@ static int cache_call(const kda_latent_cache_desc* d, bool write, void* latents,
     const size_t e = esize(d->dtype);
     if (misaligned(latents, e) || misaligned(rope, e) || misaligned(cu, 4) || misaligned(table, 4) || misaligned(lens, 4) ||
         misaligned(cache, 16)) return KDA_ERR_INVALID_ARGUMENT;
-    const Rows c = {latents, d->latent_stride * (int64_t)e, 0, d->rank * e, span(T, d->latent_stride, d->rank, e)};
-    const Rows r = {rope, d->rope_stride * (int64_t)e, 0, d->d_rope * e, span(T, d->rope_stride, d->d_rope, e)};
+    const Rows c = {latents, d->latent_stride * (int64_t)e, 0, d->rank * e, span(T, d->latent_stride, d->rank, e), d->rank * e};
+    const Rows r = {rope, d->rope_stride * (int64_t)e, 0, d->d_rope * e, span(T, d->rope_stride, d->d_rope, e), d->d_rope * e};
     const Range pages = {cache, span(d->num_pages, d->page_stride, page, 1)}, status = {d->workspace, d->workspace ? kStatusBytes : 0};
     const Range ints[3] = {{cu, cu ? ((size_t)N + 1) * 4 : 0}, {table, (size_t)N * d->max_pages * 4}, {lens, (size_t)N * 4}};
     const Range lat = {latents, c.span}, rop = {rope, r.span};
