@@ -282,9 +282,7 @@ def run(s):
         if s["op"] == "write":
             kda.latent_cache_write(s["latent"], s["rope"], s["cache"], s["table"], s["lens"], None if s["steps"] else s["cu"],
                                    page_size=s["page"])
-            if "views" not in s:                # of the cache, made once: the call itself returns nothing
-                s["views"] = dict(zip(("codes", "rope", "scales"), _views(s["cache"], s["page"])))
-            return s["views"]
+            return dict(zip(("codes", "rope", "scales"), _views(s["cache"], s["page"])))
         if s["op"] == "read":
             c, r = kda.latent_cache_read(s["cache"], s["table"], s["lens"], s["cu"], total_tokens=s["tokens"],
                                          page_size=s["page"], rank=RANK, d_rope=ROPE, dtype=_dtype(s["dtype"]))
