@@ -574,7 +574,9 @@ typedef enum {
     KDA_ROTARY_LINEAR = 1,       /* all divided by factor */
     KDA_ROTARY_BASE = 2,         /* with base * factor^(dim / (dim - 2)): the slowest divided by factor, the fastest kept */
     KDA_ROTARY_BY_PARTS = 3      /* f (w + (1 - w) / factor), w = (turns - slow) / (fast - slow) within 0 .. 1, of the
-                                    turns original_length f / (2 pi) that a pair made in training */
+                                    turns original_length f / (2 pi) that a pair made in training.  (w goes by the turns;
+                                    frequencies whose w goes by the pair's index i between those of `fast` and `slow`
+                                    turns are others, to be made by the caller) */
 } kda_rotary_method;
 KDA_API int kda_rotary_frequencies(int32_t dim, double base, int32_t method, double factor, double original_length,
                                    double slow, double fast, double *frequencies);

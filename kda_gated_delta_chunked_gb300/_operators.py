@@ -334,7 +334,9 @@ def rotary_frequencies(dim: int, *, base: float = 10000.0, method: int = KDA_ROT
                        original_length: float = 4096, slow: float = 1.0, fast: float = 32.0, device=None) -> torch.Tensor:
     """Frequencies fp64 ``[dim / 2]`` for ``rotary``, in radians a position:
     base^(-2 i / dim), scaled for contexts ``factor`` times as long as
-    ``original_length`` by a KDA_ROTARY_* method (kda_rotary_frequencies)."""
+    ``original_length`` by a KDA_ROTARY_* method (kda_rotary_frequencies).
+    KDA_ROTARY_BY_PARTS blends by the turns that a pair made in training, not by
+    its index: frequencies of models that do so are the caller's to make."""
     host = (ctypes.c_double * max(1, dim // 2))()
     status = kda_rotary_frequencies(dim, base, method, factor, original_length, slow, fast, host)
     if status != B.KDA_OK:
