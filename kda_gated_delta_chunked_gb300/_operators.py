@@ -363,7 +363,7 @@ def rotary(x, positions, frequencies, *, key=None, offset: Optional[int] = None,
 
 def latent_status(workspace, stream=None) -> int:
     """Device status (KDA_OK, KDA_ERR_BAD_SEQLENS, KDA_ERR_BAD_PAGE, KDA_ERR_TIMEOUT) that the last
-    latent_prefill or latent_decode on this workspace recorded; synchronises the stream."""
+    latent_* call on this workspace recorded; synchronises the stream."""
     desc = KdaLatentDesc()
     desc.workspace = workspace.data_ptr()
     desc.workspace_bytes = workspace.numel() * workspace.element_size()

@@ -12,8 +12,8 @@
 // (read).
 //
 // Bound by HBM bytes: 1152 and 641 of them a token in bf16 at rank 512.  65536
-// tokens, us in a graph of ten (floor 17 in bf16, 28 in fp32): written 20 and 31,
-// read 19 and 33; one token each of 48 sequences 2.3.
+// tokens, us in a graph of ten (floor 17 in bf16, 28 in fp32): written 20 and 30,
+// read 18 and 32; one token each of 48 sequences 2.0.
 //
 // Errors in lengths and pages are found by a block of its own, if there is a
 // status word: it alone writes it.  The others leave out what is wrong.

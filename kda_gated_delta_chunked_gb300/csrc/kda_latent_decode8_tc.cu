@@ -45,11 +45,11 @@
 // The first scores come 3.5 us after the start and their weights 1.2 later, in
 // instructions not used before; a sequence's end costs 3, the join 3 to 9.
 // Measured, us in a graph of ten / one behind a flush of L2 (the join included):
-//   64 x 16384 tokens, 16 heads  108 (6.2 TB/s) / 125       64 x 4096, 64 heads   61 / 68
-//   64 x up to 16384, 32 heads   72 / 86                    64 x 4096, 128 heads  102 / 107
-//   128 x 1024, 16 heads         23 / 35                    3 x 8192, 128 heads   23 / 29
+//   64 x 16384 tokens, 16 heads  110 (6.1 TB/s) / 126       64 x 4096, 64 heads   61 / 68
+//   64 x up to 16384, 32 heads   72 / 86                    64 x 4096, 128 heads  103 / 107
+//   128 x 1024, 16 heads         23 / 35                    3 x 8192, 128 heads   24 / 29
 //   1 x 30000, 32 heads          16 / 25                    1 x 700, 32 heads     11 / 16
-//   64 x 8192, 16 heads, pages of 8, of 16 and more: 68, 64 (copies are issued a box of a page at a time)
+//   64 x 8192, 16 heads, pages of 8, of 16 and more: 67, 63 (copies are issued a box of a page at a time)
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>

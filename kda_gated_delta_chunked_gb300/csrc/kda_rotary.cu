@@ -9,9 +9,9 @@
 // has a vector or two at a time, the turned ones of all rows before the copied
 // ones, so that a warp does one of the two; 32 registers, so that an SM is full of
 // them (with four vectors and 64 registers: 32768 tokens of 32 x 192 in 154 us).
-// Measured, us in a graph of ten (floor): that 122 (120); 65536 tokens of 8 + 8
-// heads of 128 56 (45); 65536 of one head of 64 9 (2.5: two million sines and as
-// many cosines); one token of 32 heads 2.5.
+// Measured, us in a graph of ten (floor): that 120 (120); 65536 tokens of 8 heads
+// of 128 and a key 56 (45); 65536 of one head of 64 9 (2.5: two million sines and
+// as many cosines); one token of 32 heads 2.5.
 //
 // The angle: f / (2 pi) turns a position, as a 64-bit fraction of a turn, times
 // the position in 64-bit integers that wrap at whole turns: off by 2^-63 of f / (2 pi)
@@ -261,7 +261,7 @@ cudaError_t rotary_launch(const kda_rotary_desc& d, const void* x, const void* k
     a.positions = positions; a.frequencies = frequencies;
     const int64_t e = d.dtype == KDA_BF16 ? 2 : 4;
     // 16-byte vectors, or the widest on whose boundaries everything starts that a vector of its own covers (20000 x 4 rows
-    // of 100 bf16, 64 turned: 11.7 us with 8 bytes, 15.9 with 4; 98: 15.7; of 100, 50 turned: 28.8 with 2)
+    // of 100 bf16, 64 turned: 11.7 us with 8 bytes, 15.9 with 4; 98: 15.7; of 100, 50 turned: 27.2 with 2)
     uint64_t bits = (uint64_t)((d.flags & KDA_FLAG_INTERLEAVED ? d.dim : d.dim / 2) * e);
     for (int i = 0; i < 2; ++i) {
         const kda_rotary_part& s = i ? d.key : d.x;
