@@ -550,7 +550,11 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 x[R / 4 - 1][1] = q2;
                 rope[R / 4 - 1] = same;
             }
-            if (!(ok = mbar_wait_warp(q_empty, (seg - 1) & 1))) break;
+            // (a whole segment, which may take seconds: up to 40, unless another warp gave up)
+            ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
+#pragma unroll 1
+            for (int k = 1; k < 20 && !ok && !(uniform(*(volatile int*)fault) & kLdLate); ++k) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
+            if (!ok) break;
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) l8_put(mem, warp - 12 + 4 * i, lane, x[i][0], x[i][1], rope[i]);
             fence_proxy_async_smem();

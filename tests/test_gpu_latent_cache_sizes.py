@@ -74,3 +74,20 @@ def test_the_longest_sequences(kda, quantized):  # noqa: F811
             bound = 1.1 * rel * (p @ keys[:, :512].abs()) + HALF[BF16] * (p @ keys[:, :512]).abs()
             within(out[i, c], p @ keys[:, :512], bound, (i, c))
             assert abs(float(lse[i, c]) - float(torch.logsumexp(s, 0)) - math.log(reps)) < 1.1 * (scores + (sums if i == 0 else 0)) + 1e-4
+
+
+@pytest.mark.parametrize("quantized", [True, False])
+def test_a_sequence_that_takes_a_thread_block_seconds(kda, quantized):  # noqa: F811
+    """2^28 tokens, one page over and over, by 4096 query rows: a thread block has all tiles of a group (over the cache in
+    16 bits half of them), and the queries of the short sequence behind them wait for seconds."""
+    cache, _ = repeated(kda, quantized)
+    kw = dict(page_size=64) if quantized else {}
+    lq, h, pages = 32, 128, 2 ** 22
+    table = torch.zeros(2, pages, dtype=torch.int32, device="cuda")
+    q = normal(7, 2, lq, h, 576, dtype=BF16, scale=0.2).cuda()
+    size = kda.latent_decode_workspace_bytes(2, lq, h, 512, 64, BF16, 64, pages, quantized=quantized)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out, lse = kda.latent_decode(q, cache, table, ints(64 * pages, 64), scale=0.07, workspace=ws, **kw)
+    assert kda.latent_status(ws) == kda.KDA_OK
+    want, wl = kda.latent_decode(q[1:], cache, table[1:], ints(64), scale=0.07, **kw)
+    assert torch.equal(out[1:], want) and torch.equal(lse[1:], wl) and torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
