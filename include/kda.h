@@ -474,7 +474,9 @@ KDA_API int kda_latent_decode(const kda_latent_desc *desc, const void *q, const 
  * maximum is over the token's finite channels), so that no code saturates and the
  * values are exact in bf16.  One scale a token does: behind a channel's own
  * exponent of four bits, scales of shorter groups would change only values below
- * 2^-14 of the token's largest.  Channels that are infinite or NaN become NaN. */
+ * 2^-14 of the token's largest.  Channels that are infinite or NaN become NaN.
+ * Memory need not be cleared before it is written.  Pages of zeros hold tokens of
+ * zeros. */
 typedef struct kda_latent_cache_desc {
     int32_t num_seqs;        /* N >= 0 */
     int32_t dtype;           /* kda_dtype of latents and rope */

@@ -593,7 +593,8 @@ kda_latent_decode8_tc(const __grid_constant__ CUtensorMap map, const __grid_cons
                 break;
             }
             const int token = w.j * kLdTile + thread;
-            const int byte = scales[(j & 1) * kLdTile + thread];
+            // (0 in pages that were cleared, not written: 2^127 for `down` would be too much for the sum)
+            const int byte = max((int)scales[(j & 1) * kLdTile + thread], kScaleLow + kScaleBias);
             const float two = __uint_as_float((uint32_t)byte << 23), e = (float)(byte - kScaleBias);
             const bool small = byte < kL8Small;
             const float stand = kL8Stand + (small ? kL8Lift : 0);

@@ -60,3 +60,19 @@ def test_a_cache_of_memory_that_held_something_else(kda, new):  # noqa: F811
         got.append(kda.latent_decode(q, cache, ints(1).view(1, 1), ints(new), scale=0.07, page_size=64))
     assert torch.isfinite(got[0][0].float()).all() and torch.isfinite(got[0][1]).all()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("dtype,simt", FORMS)
+@pytest.mark.parametrize("lens,lq,h,page", [([1, 1, 64], 1, 16, 64), ([700, 2], 3, 32, 16), ([9000], 1, 100, 64)])
+def test_a_cleared_cache_holds_tokens_of_zeros(kda, dtype, simt, lens, lq, h, page):  # noqa: F811
+    """Pages of zeros, as batches are padded with: all scores are 0, so lse is the logarithm of the tokens seen."""
+    _, table, _ = cached(kda, lens, page, 512, 64, 86)
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache = torch.zeros(pages, kda.latent_cache_page_bytes(page), dtype=torch.uint8, device="cuda")
+    q = normal(87, len(lens), lq, h, 576, dtype=dtype).cuda()
+    out, lse = kda.latent_decode(q, cache, table, ints(*lens), scale=0.07, page_size=page, flags=kda.KDA_FLAG_CUDA_CORE_PREFILL if simt else 0)
+    assert (out == 0).all()
+    seen = torch.tensor([[max(0, n - lq + 1 + i) for i in range(lq)] for n in lens], dtype=torch.float64)
+    # the exponent of a scale stands in the sum's logarithm: 2^-24 of 130 four times, and the sum's own additions
+    assert float((lse.cpu().double() - seen.log()[:, :, None]).abs().nan_to_num().max()) < 4 * 2.0 ** -24 * 140 + 9000 * 2.0 ** -23
+    assert torch.equal(torch.isinf(lse.cpu()), (seen == 0)[:, :, None].expand(lse.shape))
